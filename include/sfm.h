@@ -345,6 +345,91 @@ sfm_status sfm_pick_b1(int64_t B, int64_t L, int64_t D, int64_t N, int64_t* B1_o
 sfm_status sfm_scan_plan_string(int64_t B1, int64_t B2, int64_t D, int64_t N, int64_t L, int conv_k,
                                 int io_dtype, int flags, char* buf, int64_t cap);
 
+/*
+ * The gated delta rule: a linear recurrence next to the scan above whose state
+ * is a matrix per head.  For a token of a row, with key k, query q (dk values),
+ * value v (dv values), log decay g and gate beta of its head,
+ *   S <- exp(g) S;  u = beta (v - S^T k);  S <- S + k u^T;  o = scale S^T q,
+ * S [dk, dv] float32, zero (or h0) before the row's first token.
+ *
+ * sfm_gated_delta_fwd -- whole rows.
+ *   q, k     [tokens, Hk, dk] io   token strides ldq, ldk (elements, >= Hk dk)
+ *   v        [tokens, H, dv] io    token stride ldv (>= H dv)
+ *   g, beta  [tokens, H] io        g normally <= 0; minus infinity resets the state
+ *   h0       [rows, H, dk, dv] f32 or NULL (zero)
+ *   o        [tokens, H, dv] io
+ *   hT       [rows, H, dk, dv] f32 or NULL: the states after each row (a row
+ *            without tokens: its h0); hT == h0 is allowed
+ *   offsets  NULL: row r is tokens r L .. (r + 1) L - 1, tokens == rows * L;
+ *            else int32 [rows + 1] on the device, rising from 0 to tokens: row r
+ *            is tokens offsets[r] .. offsets[r + 1] - 1 (possibly none), at most
+ *            L of them (L bounds the longest row; offsets outside the tokens are
+ *            cut to them, tokens of no row and those past L keep their old o)
+ *   H must be a multiple of Hk: value head h uses key head h / (H / Hk).
+ *   dk 1..128, dv 1..256.  Tensors need their element's alignment only; rows on
+ *   16 bytes are loaded 16 bytes at a time.
+ *   flags & SFM_DELTA_L2NORM: q and k are divided by sqrt(sum of squares + 1e-6)
+ *            of their head first.
+ * States and sums are float32.  A non-finite value reaches no token of another
+ * row, nor any earlier 64-token chunk of its own.  Repeated calls give the same bits.
+ * workspace: device memory of at least sfm_gated_delta_fwd_ws_size() bytes
+ *   (may be NULL when that is 0), 16-byte aligned, owned by the caller.
+ * Returns SFM_OK, or NULL/SHAPE/DTYPE/ALIAS/ALIGN (nothing launched), HIP.
+ */
+#define SFM_DELTA_L2NORM 1
+sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                               const float* h0, void* o, float* hT, const int32_t* offsets, int64_t rows,
+                               int64_t L, int64_t tokens, int64_t Hk, int64_t H, int64_t dk, int64_t dv,
+                               int64_t ldq, int64_t ldk, int64_t ldv, float scale, int io_dtype, int flags,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes sfm_gated_delta_fwd needs (host only); want_state: hT != NULL.
+ * Returns SFM_OK or NULL/SHAPE/DTYPE. */
+sfm_status sfm_gated_delta_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk,
+                                       int64_t dv, int want_state, int io_dtype, int64_t* bytes);
+
+/*
+ * sfm_gated_delta_step -- one token of each of `rows` requests (serving): the
+ * recurrence above on a pool of states, updated in place.
+ *   q, k [rows, Hk, dk], v [rows, H, dv] io with strides as above; g, beta
+ *   [rows, H] io; state [pool, H, dk, dv] f32; o [rows, H, dv] io
+ *   slots  int32 [rows] on the device: row r uses state number slots[r]; two
+ *          rows must not share one.  A slot outside 0..pool-1 marks a row of
+ *          padding: its o is zero and no state changes.  NULL: state r (pool >= rows).
+ */
+sfm_status sfm_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                float* state, const int32_t* slots, void* o, int64_t rows, int64_t pool,
+                                int64_t Hk, int64_t H, int64_t dk, int64_t dv, int64_t ldq, int64_t ldk,
+                                int64_t ldv, float scale, int io_dtype, int flags, void* stream);
+
+/*
+ * Group norm of channel-last tokens with an activation.  The channels of a
+ * sample are G groups of C / G neighbours; mean and variance (over count) are
+ * taken over a group's channels and all L tokens:
+ *   xh = (x - mean) / sqrt(var + eps);  y = act(w xh + b).
+ * L = 1 norms every token by itself.
+ *
+ * sfm_group_norm_fwd:  x, y [N, L, C] io (y must not overlap x);  w, b [C] f32
+ *   or NULL (1, 0);  mean, rstd [N, G] f32 out (rstd = 1 / sqrt(var + eps));
+ *   act sfm_act.  Tensors need their element's alignment; 16-byte aligned ones
+ *   with C a multiple of 16 bytes are faster.
+ * sfm_group_norm_bwd:  dy, x as above with the forward's mean and rstd;  dx
+ *   [N, L, C] io;  dw, db [C] f32 or NULL (not wanted).
+ * workspace: at least the _ws_size() bytes (want_weights: dw or db given), may
+ *   be NULL when that is 0; 16-byte aligned.  Sums are float32 in a fixed order:
+ *   repeated calls give the same bits.
+ */
+sfm_status sfm_group_norm_fwd(const void* x, const float* w, const float* b, void* y, float* mean, float* rstd,
+                              int64_t N, int64_t L, int64_t C, int64_t G, float eps, int act, int io_dtype,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+sfm_status sfm_group_norm_fwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G, int io_dtype, int64_t* bytes);
+sfm_status sfm_group_norm_bwd(const void* dy, const void* x, const float* mean, const float* rstd, const float* w,
+                              const float* b, void* dx, float* dw, float* db, int64_t N, int64_t L, int64_t C,
+                              int64_t G, int act, int io_dtype, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G, int want_weights, int io_dtype,
+                                      int64_t* bytes);
+
 /* Static text for a status code. */
 const char* sfm_status_string(sfm_status s);
 

@@ -8,7 +8,8 @@ the library's kernels; there is no fallback -- if ``libsfm.so`` is missing the
 first call raises.
 
 Functions keep the C names:
-  sfm_selective_scan_fwd, sfm_dwconv1d_fold, sfm_aux_pad_swap, sfm_pick_b1
+  sfm_selective_scan_fwd, sfm_dwconv1d_fold, sfm_aux_pad_swap, sfm_pick_b1,
+  sfm_gated_delta_fwd, sfm_gated_delta_step, sfm_group_norm_fwd, sfm_group_norm_bwd
 """
 from __future__ import annotations
 
@@ -19,6 +20,8 @@ __all__ = ["sfm_selective_scan_fwd", "sfm_selective_scan_fwd_ex", "sfm_selective
            "sfm_selective_scan_fwd_ws_size", "sfm_selective_scan_bwd",
            "sfm_selective_scan_bwd_workspace_size", "sfm_dwconv1d_fold", "sfm_aux_pad_swap", "sfm_aux_pad_bwd",
            "sfm_aux_pad_bwd_ex",
+           "sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_step", "sfm_group_norm_fwd",
+           "sfm_group_norm_bwd", "sfm_group_norm_ws_size",
            "sfm_pick_b1", "sfm_scan_plan_string", "sfm_version", "library_path", "load_library", "SFMError"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +72,18 @@ def load_library():
     lib.sfm_aux_pad_swap.argtypes = [vp, vp, i64, i64, i64, ci, ci, vp]
     lib.sfm_pick_b1.argtypes = [i64, i64, i64, i64, ctypes.POINTER(ctypes.c_int64)]
     lib.sfm_scan_plan_string.argtypes = [i64, i64, i64, i64, i64, ci, ci, ci, ctypes.c_char_p, i64]
+    f32 = ctypes.c_float
+    pi64 = ctypes.POINTER(ctypes.c_int64)
+    lib.sfm_gated_delta_fwd.argtypes = [vp] * 9 + [i64] * 10 + [f32, ci, ci, vp, i64, vp]
+    lib.sfm_gated_delta_fwd_ws_size.argtypes = [i64] * 6 + [ci, ci, pi64]
+    lib.sfm_gated_delta_step.argtypes = [vp] * 8 + [i64] * 9 + [f32, ci, ci, vp]
+    lib.sfm_group_norm_fwd.argtypes = [vp] * 6 + [i64] * 4 + [f32, ci, ci, vp, i64, vp]
+    lib.sfm_group_norm_bwd.argtypes = [vp] * 9 + [i64] * 4 + [ci, ci, vp, i64, vp]
+    lib.sfm_group_norm_fwd_ws_size.argtypes = [i64] * 4 + [ci, pi64]
+    lib.sfm_group_norm_bwd_ws_size.argtypes = [i64] * 4 + [ci, ci, pi64]
+    for f in ("sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_step", "sfm_group_norm_fwd",
+              "sfm_group_norm_bwd", "sfm_group_norm_fwd_ws_size", "sfm_group_norm_bwd_ws_size"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("sfm_selective_scan_fwd", "sfm_selective_scan_fwd_ex", "sfm_selective_scan_fwd_ws",
               "sfm_selective_scan_fwd_ws_size", "sfm_dwconv1d_fold", "sfm_aux_pad_swap",
               "sfm_pick_b1", "sfm_version", "sfm_scan_plan_string", "sfm_selective_scan_bwd",
@@ -406,3 +421,211 @@ def sfm_pick_b1(B: int, L: int, D: int, N: int) -> int:
     out = ctypes.c_int64(0)
     _check(load_library().sfm_pick_b1(B, L, D, N, ctypes.byref(out)), "sfm_pick_b1")
     return int(out.value)
+
+
+# ---------------------------------------------------------------- the gated delta rule
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream`: memory that the caching allocator hands out again only after it."""
+    t = _torch().empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+SFM_DELTA_L2NORM = 1
+
+
+def _tokens(t, name, heads, width, dtype, lead):
+    """Checks a [*lead, heads, width] tensor whose heads are contiguous and whose tokens
+    are evenly strided (a slice of a wider projection is fine); returns the token stride."""
+    if t.device.type != "cuda":
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != lead + (heads, width):
+        raise ValueError(f"{name} must have shape {lead + (heads, width)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return heads * width
+    st = t.stride()
+    ld = st[-3]
+    if (width > 1 and st[-1] != 1) or (heads > 1 and st[-2] != width) or \
+            (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * ld) or (ld < heads * width and lead[-1] > 1):
+        raise ValueError(f"{name}: heads must be contiguous and tokens evenly strided, got strides {st}")
+    return max(ld, heads * width)
+
+
+def _delta_args(q, k, v, g, beta, packed):
+    """Checks shared by the gated delta rule's functions; returns the sizes and strides."""
+    io = _io_code(q)
+    lead = tuple(q.shape[:-2])
+    Hk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    if packed and lead[0] != 1:
+        raise ValueError("packed rows (offsets) are one batch entry: [1, tokens, heads, size]")
+    ldq = _tokens(q, "q", Hk, dk, q.dtype, lead)
+    ldk = _tokens(k, "k", Hk, dk, q.dtype, lead)
+    ldv = _tokens(v, "v", H, dv, q.dtype, lead)
+    _dev(g, "g", q.dtype, lead + (H,))
+    _dev(beta, "beta", q.dtype, lead + (H,))
+    return io, lead, Hk, H, dk, dv, ldq, ldk, ldv
+
+
+def _rows(lead, offsets, max_len):
+    if offsets is None:
+        return lead[0], lead[1], lead[0] * lead[1]
+    torch = _torch()
+    _dev(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be int32 [rows + 1]")
+    return offsets.numel() - 1, lead[1] if max_len is None else int(max_len), lead[1]
+
+
+def sfm_gated_delta_fwd_ws_size(rows: int, L: int, tokens: int, H: int, dk: int, dv: int, want_state: bool = False,
+                                io: str = "bf16") -> int:
+    """Workspace bytes sfm_gated_delta_fwd needs (host only)."""
+    out = ctypes.c_int64(0)
+    _check(load_library().sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, int(bool(want_state)),
+                                                      SFM_BF16 if io == "bf16" else SFM_F32, ctypes.byref(out)),
+           "sfm_gated_delta_fwd_ws_size")
+    return int(out.value)
+
+
+def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, scale=None, l2norm=False, o=None,
+                        return_state=False, state=None, workspace=None, stream=None):
+    """The gated delta rule over whole rows (see include/sfm.h).
+
+    q, k: [B, L, Hk, dk]; v: [B, L, H, dv]; g (log decay), beta: [B, L, H]; float32 or bfloat16.
+    h0: [B, H, dk, dv] float32 states before the rows, or None.  offsets (int32 [rows + 1] on the
+    GPU): packed rows, tensors [1, tokens, ...]; max_len bounds the longest row.  scale defaults to
+    dk ** -0.5; l2norm divides q and k by their length.  Returns o [B, L, H, dv], and with
+    return_state the states after the rows (written to `state` if given; h0 itself is allowed)."""
+    torch = _torch()
+    io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
+    rows, L, tokens = _rows(lead, offsets, max_len)
+    _dev(h0, "h0", torch.float32, (rows, H, dk, dv))
+    if o is None:
+        o = _new(lead + (H, dv), q.dtype, q.device, stream)
+    _dev(o, "o", q.dtype, lead + (H, dv))
+    if return_state and state is None:
+        state = _new((rows, H, dk, dv), torch.float32, q.device, stream)
+    if not return_state:
+        state = None
+    _dev(state, "state", torch.float32, (rows, H, dk, dv))
+    need = sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, return_state, "bf16" if io else "f32")
+    if workspace is None and need:
+        workspace = _new(need, torch.uint8, q.device, stream)
+    _dev(workspace, "workspace")
+    rc = load_library().sfm_gated_delta_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(o), _ptr(state), _ptr(offsets), rows, L,
+        tokens, Hk, H, dk, dv, ldq, ldk, ldv, dk ** -0.5 if scale is None else scale, io,
+        SFM_DELTA_L2NORM if l2norm else 0, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "sfm_gated_delta_fwd")
+    return (o, state) if return_state else o
+
+
+def sfm_gated_delta_step(q, k, v, g, beta, state, slots=None, scale=None, l2norm=False, o=None, stream=None):
+    """One token of each request: q, k [R, Hk, dk]; v [R, H, dv]; g, beta [R, H]; state [pool, H, dk, dv]
+    float32, updated in place; slots int32 [R] (row r's state; outside the pool: padding) or None
+    (state r).  Returns o [R, H, dv]."""
+    torch = _torch()
+    io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, False)
+    rows = lead[0]
+    _dev(state, "state", torch.float32)
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+        raise ValueError(f"state must have shape (pool, {H}, {dk}, {dv}), got {tuple(state.shape)}")
+    _dev(slots, "slots", torch.int32, (rows,))
+    if o is None:
+        o = _new((rows, H, dv), q.dtype, q.device, stream)
+    _dev(o, "o", q.dtype, (rows, H, dv))
+    rc = load_library().sfm_gated_delta_step(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots), _ptr(o), rows, state.shape[0],
+        Hk, H, dk, dv, ldq, ldk, ldv, dk ** -0.5 if scale is None else scale, io,
+        SFM_DELTA_L2NORM if l2norm else 0, _stream(stream))
+    _check(rc, "sfm_gated_delta_step")
+    return o
+
+
+# ---------------------------------------------------------------- group norm, channels last
+def sfm_group_norm_ws_size(N: int, L: int, C: int, G: int, io: str = "bf16", backward: bool = False,
+                           want_weights: bool = True) -> int:
+    """Workspace bytes of sfm_group_norm_fwd, or with `backward` of sfm_group_norm_bwd (host only)."""
+    out = ctypes.c_int64(0)
+    code = SFM_BF16 if io == "bf16" else SFM_F32
+    lib = load_library()
+    _check(lib.sfm_group_norm_bwd_ws_size(N, L, C, G, int(bool(want_weights)), code, ctypes.byref(out)) if backward
+           else lib.sfm_group_norm_fwd_ws_size(N, L, C, G, code, ctypes.byref(out)), "sfm_group_norm_ws_size")
+    return int(out.value)
+
+
+def _norm_sizes(x):
+    """[N, ..., C] -> N, tokens, C."""
+    if x.dim() < 2:
+        raise ValueError("x must be [N, ..., C]")
+    N, C = x.shape[0], x.shape[-1]
+    return N, x.numel() // max(1, N * C), C
+
+
+def sfm_group_norm_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, act=None, y=None, mean=None, rstd=None,
+                       workspace=None, stream=None):
+    """Group norm of channel-last x [N, ..., C] over num_groups groups of neighbouring channels, then
+    act (None or 'silu').  weight, bias: [C] float32 or None.  Returns y and the float32 [N, G]
+    mean and rstd that sfm_group_norm_bwd takes."""
+    torch = _torch()
+    io = _io_code(x)
+    N, L, C = _norm_sizes(x)
+    _dev(x, "x")
+    _dev(weight, "weight", torch.float32, (C,))
+    _dev(bias, "bias", torch.float32, (C,))
+    if y is None:
+        y = _new(x.shape, x.dtype, x.device, stream)
+    _dev(y, "y", x.dtype, x.shape)
+    if mean is None:
+        mean = _new((N, num_groups), torch.float32, x.device, stream)
+    if rstd is None:
+        rstd = _new((N, num_groups), torch.float32, x.device, stream)
+    _dev(mean, "mean", torch.float32, (N, num_groups))
+    _dev(rstd, "rstd", torch.float32, (N, num_groups))
+    need = sfm_group_norm_ws_size(N, L, C, num_groups, "bf16" if io else "f32")
+    if workspace is None and need:
+        workspace = _new(need, torch.uint8, x.device, stream)
+    _dev(workspace, "workspace")
+    rc = load_library().sfm_group_norm_fwd(
+        _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), N, L, C, num_groups, eps, _ACT[act], io,
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "sfm_group_norm_fwd")
+    return y, mean, rstd
+
+
+def sfm_group_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, act=None, grads=None, workspace=None, stream=None):
+    """Gradients of sfm_group_norm_fwd for upstream dy: a dict with dx and, for the weight and bias
+    given, dw and db (float32).  `grads` may hold preallocated tensors under those names."""
+    torch = _torch()
+    io = _io_code(x)
+    N, L, C = _norm_sizes(x)
+    _dev(x, "x")
+    _dev(dy, "dy", x.dtype, x.shape)
+    _dev(mean, "mean", torch.float32)
+    if mean.dim() != 2 or mean.shape[0] != N:
+        raise ValueError(f"mean must be [{N}, groups], got {tuple(mean.shape)}")
+    G = mean.shape[1]
+    _dev(rstd, "rstd", torch.float32, (N, G))
+    _dev(weight, "weight", torch.float32, (C,))
+    _dev(bias, "bias", torch.float32, (C,))
+    out = dict(grads or {})
+    for name, given, shape, dt in (("dx", True, x.shape, x.dtype), ("dw", weight is not None, (C,), torch.float32),
+                                   ("db", bias is not None, (C,), torch.float32)):
+        if given and out.get(name) is None:
+            out[name] = _new(shape, dt, x.device, stream)
+        _dev(out.get(name), name, dt, shape)
+    need = sfm_group_norm_ws_size(N, L, C, G, "bf16" if io else "f32", True,
+                                  out.get("dw") is not None or out.get("db") is not None)
+    if workspace is None and need:
+        workspace = _new(need, torch.uint8, x.device, stream)
+    _dev(workspace, "workspace")
+    rc = load_library().sfm_group_norm_bwd(
+        _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(out["dx"]), _ptr(out.get("dw")),
+        _ptr(out.get("db")), N, L, C, G, _ACT[act], io, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "sfm_group_norm_bwd")
+    return out

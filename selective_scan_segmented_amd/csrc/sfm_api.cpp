@@ -14,55 +14,14 @@
 #include <string>
 #include <vector>
 
+#include "sfm_api_util.h"
 #include "sfm_bwd.h"
 #include "sfm_cl.h"
 #include "sfm_internal.h"
 
-namespace {
+thread_local std::string sfm::api::g_last_error;
 
-thread_local std::string g_last_error;
-
-sfm_status fail(sfm_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return s;
-}
-
-sfm_status ok() {
-    g_last_error.clear();
-    return SFM_OK;
-}
-
-sfm_status hip_status(hipError_t e, const char* what) {
-    if (e == hipSuccess) return ok();
-    return fail(SFM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-int io_bytes(int io_dtype) { return io_dtype == SFM_F32 ? 4 : 2; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    const char* name;
-    uintptr_t lo, hi;
-};
-
-Range rng(const char* name, const void* p, int64_t bytes) {
-    uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, lo + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// products of positive sizes that must stay well inside int32 indexing of one
-// (sample, channel) row and int64 element counts overall
-bool sane(int64_t v, int64_t hi) { return v >= 1 && v <= hi; }
-
-}  // namespace
+using namespace sfm::api;
 
 extern "C" {
 

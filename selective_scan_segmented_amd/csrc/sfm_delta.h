@@ -1,0 +1,55 @@
+// sfm_delta.h -- host/device contract of the gated delta rule's kernels.  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace sfm {
+
+constexpr int kDeltaChunk = 64;        // tokens to a chunk of the chunked kernels
+constexpr int kDeltaMaxK = 128;        // largest key head
+constexpr int kDeltaMaxV = 256;        // largest value head
+
+// One call's rows, heads and strides (forward, backward and the token-by-token form).
+struct DeltaParams {
+    const void* q;       // token t, key head j: q + t * ldq + j * dk (elements)
+    const void* k;
+    const void* v;       // token t, head h: v + t * ldv + h * dv
+    const void* g;       // [tokens][H]
+    const void* beta;
+    const float* h0;     // [rows][H][dk][dv] or null (zero states); the pool with slots
+    void* o;             // [tokens][H][dv]
+    float* hT;           // [rows][H][dk][dv] or null; the pool with slots
+    const int32_t* offsets;  // [rows + 1] or null: row s is tokens s * L .. + L - 1
+    const int32_t* slots;    // [rows] or null: the state of row s is number slots[s] of `pool` in h0 and hT
+    int64_t ldq, ldk, ldv, tokens, pool;
+    int rows, L, Hk, H, dk, dv;
+    float scale;
+    int l2norm;
+    int vec_k, vec_v;    // q and k (v) rows may be loaded 16 bytes at a time
+    int vec_s;           // states likewise
+};
+
+// first token and length of row s; offsets outside the tokens (a caller's mistake) are cut to them
+__device__ __forceinline__ void delta_row(const DeltaParams& p, int s, int64_t& first, int& len) {
+    if (!p.offsets) {
+        first = (int64_t)s * p.L;
+        len = p.L;
+        return;
+    }
+    int64_t lo = p.offsets[s], hi = p.offsets[s + 1];
+    lo = lo < 0 ? 0 : (lo > p.tokens ? p.tokens : lo);
+    hi = hi < lo ? lo : (hi > p.tokens ? p.tokens : hi);
+    first = lo;
+    len = hi - lo > p.L ? p.L : (int)(hi - lo);
+}
+
+// unit-length rows: x / sqrt(sum x^2 + this)
+constexpr float kDeltaNormEps = 1e-6f;
+// Log decays are taken as at least -110: exp of that is already zero in float32 (2^-158), and minus infinity
+// (the state's reset) then keeps the differences of a chunk's running sums finite.
+constexpr float kDeltaMinGate = -110.0f;
+
+hipError_t launch_delta_recurrent(const DeltaParams& p, int io_dtype, hipStream_t s);
+
+}  // namespace sfm

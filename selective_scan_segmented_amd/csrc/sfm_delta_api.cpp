@@ -1,0 +1,177 @@
+// sfm_delta_api.cpp -- the C ABI of the gated delta rule (declared in include/sfm.h): argument checks and dispatch.
+#include "sfm.h"
+
+#include <hip/hip_runtime.h>
+
+#include "sfm_api_util.h"
+#include "sfm_delta.h"
+
+using namespace sfm::api;
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Sizes, strides and types every entry point of the rule shares.
+sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, bool packed, int64_t Hk, int64_t H,
+                       int64_t dk, int64_t dv, int io_dtype, int flags) {
+    if (io_dtype != SFM_F32 && io_dtype != SFM_BF16) return fail(SFM_ERR_DTYPE, "%s: io_dtype %d", fn, io_dtype);
+    if (flags & ~SFM_DELTA_L2NORM) return fail(SFM_ERR_SHAPE, "%s: unknown flags 0x%x", fn, flags);
+    if (!sane(rows, 1 << 24) || !sane(L, 1 << 24) || tokens < 0 || tokens > (1LL << 31) - 1)
+        return fail(SFM_ERR_SHAPE, "%s: rows=%lld L=%lld tokens=%lld out of range", fn, (long long)rows, (long long)L,
+                    (long long)tokens);
+    if (!packed && tokens != rows * L)
+        return fail(SFM_ERR_SHAPE, "%s: %lld tokens are not rows=%lld of L=%lld", fn, (long long)tokens,
+                    (long long)rows, (long long)L);
+    if (!sane(Hk, 4096) || !sane(H, 4096) || H % Hk)
+        return fail(SFM_ERR_SHAPE, "%s: %lld value heads over %lld key heads", fn, (long long)H, (long long)Hk);
+    if (!sane(dk, sfm::kDeltaMaxK) || !sane(dv, sfm::kDeltaMaxV))
+        return fail(SFM_ERR_SHAPE, "%s: head sizes dk=%lld (1 to %d), dv=%lld (1 to %d)", fn, (long long)dk,
+                    sfm::kDeltaMaxK, (long long)dv, sfm::kDeltaMaxV);
+    const int64_t widest = dk > dv ? dk : dv;
+    if (tokens * H > (1LL << 40) / widest || rows * H > (1LL << 28))
+        return fail(SFM_ERR_SHAPE, "%s: tensor too large", fn);
+    return SFM_OK;
+}
+
+sfm_status check_inputs(const char* fn, const void* q, const void* k, const void* v, const void* g, const void* beta,
+                        int64_t tokens, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int64_t ldq, int64_t ldk,
+                        int64_t ldv, int io_dtype) {
+    if (tokens > 0 && (!q || !k || !v || !g || !beta))
+        return fail(SFM_ERR_NULL, "%s: q, k, v, g and beta are required", fn);
+    if (ldq < Hk * dk || ldk < Hk * dk || ldv < H * dv || ldq > (1 << 24) || ldk > (1 << 24) || ldv > (1 << 24))
+        return fail(SFM_ERR_SHAPE, "%s: token strides %lld, %lld, %lld below the heads' widths (or too large)", fn,
+                    (long long)ldq, (long long)ldk, (long long)ldv);
+    const uintptr_t e = io_bytes(io_dtype);
+    if (!aligned_to(q, e) || !aligned_to(k, e) || !aligned_to(v, e) || !aligned_to(g, e) || !aligned_to(beta, e))
+        return fail(SFM_ERR_ALIGN, "%s: an input is not aligned to its element", fn);
+    return SFM_OK;
+}
+
+struct Ranges {
+    Range ins[8];
+    int n = 0;
+    void add(const char* name, const void* p, int64_t bytes) {
+        if (p && bytes > 0) ins[n++] = rng(name, p, bytes);
+    }
+    void add_inputs(const void* q, const void* k, const void* v, const void* g, const void* beta, int64_t tokens,
+                    int64_t Hk, int64_t H, int64_t dk, int64_t dv, int64_t ldq, int64_t ldk, int64_t ldv, int e) {
+        if (tokens <= 0) return;
+        add("q", q, ((tokens - 1) * ldq + Hk * dk) * e);
+        add("k", k, ((tokens - 1) * ldk + Hk * dk) * e);
+        add("v", v, ((tokens - 1) * ldv + H * dv) * e);
+        add("g", g, tokens * H * e);
+        add("beta", beta, tokens * H * e);
+    }
+    const char* hit(const Range& r) const {
+        for (int i = 0; i < n; ++i)
+            if (overlap(r, ins[i])) return ins[i].name;
+        return nullptr;
+    }
+};
+
+sfm::DeltaParams params(const void* q, const void* k, const void* v, const void* g, const void* beta, int64_t rows,
+                        int64_t L, int64_t tokens, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int64_t ldq,
+                        int64_t ldk, int64_t ldv, float scale, int flags, int io_dtype) {
+    sfm::DeltaParams p{};
+    const int e = io_bytes(io_dtype);
+    p.q = q, p.k = k, p.v = v, p.g = g, p.beta = beta;
+    p.ldq = ldq, p.ldk = ldk, p.ldv = ldv, p.tokens = tokens;
+    p.rows = (int)rows, p.L = (int)L, p.Hk = (int)Hk, p.H = (int)H, p.dk = (int)dk, p.dv = (int)dv;
+    p.scale = scale;
+    p.l2norm = flags & SFM_DELTA_L2NORM ? 1 : 0;
+    // 16-byte loads of whole rows need every row to start on 16 bytes
+    p.vec_k = aligned16(q) && aligned16(k) && dk * e % 16 == 0 && ldq * e % 16 == 0 && ldk * e % 16 == 0;
+    p.vec_v = aligned16(v) && dv * e % 16 == 0 && ldv * e % 16 == 0;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+sfm_status sfm_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                float* state, const int32_t* slots, void* o, int64_t rows, int64_t pool, int64_t Hk,
+                                int64_t H, int64_t dk, int64_t dv, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
+                                int io_dtype, int flags, void* stream) {
+    static const char* fn = "sfm_gated_delta_step";
+    sfm_status st = check_sizes(fn, rows, 1, rows, false, Hk, H, dk, dv, io_dtype, flags);
+    if (st != SFM_OK) return st;
+    st = check_inputs(fn, q, k, v, g, beta, rows, Hk, H, dk, dv, ldq, ldk, ldv, io_dtype);
+    if (st != SFM_OK) return st;
+    if (!state || !o) return fail(SFM_ERR_NULL, "%s: state and o are required", fn);
+    if (!sane(pool, 1 << 24) || pool * H > (1LL << 40) / (dk * dv))
+        return fail(SFM_ERR_SHAPE, "%s: a pool of %lld states", fn, (long long)pool);
+    if (!slots && pool < rows)
+        return fail(SFM_ERR_SHAPE, "%s: %lld states for %lld rows (no slots)", fn, (long long)pool, (long long)rows);
+    const int e = io_bytes(io_dtype);
+    if (!aligned_to(state, 4) || !aligned_to(slots, 4) || !aligned_to(o, e))
+        return fail(SFM_ERR_ALIGN, "%s: state, slots or o not aligned to its element", fn);
+    Ranges in;
+    in.add_inputs(q, k, v, g, beta, rows, Hk, H, dk, dv, ldq, ldk, ldv, e);
+    in.add("slots", slots, rows * 4);
+    const Range rs = rng("state", state, pool * H * dk * dv * 4), ro = rng("o", o, rows * H * dv * e);
+    if (const char* n = in.hit(rs)) return fail(SFM_ERR_ALIAS, "%s: state overlaps %s", fn, n);
+    if (const char* n = in.hit(ro)) return fail(SFM_ERR_ALIAS, "%s: o overlaps %s", fn, n);
+    if (overlap(rs, ro)) return fail(SFM_ERR_ALIAS, "%s: o overlaps state", fn);
+    sfm::DeltaParams p = params(q, k, v, g, beta, rows, 1, rows, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
+    p.h0 = state, p.hT = state, p.slots = slots, p.pool = pool, p.o = o;
+    p.vec_s = dv % 4 == 0 && aligned16(state);
+    return hip_status(sfm::launch_delta_recurrent(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
+}
+
+sfm_status sfm_gated_delta_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv,
+                                       int want_state, int io_dtype, int64_t* bytes) {
+    static const char* fn = "sfm_gated_delta_fwd_ws_size";
+    if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
+    const sfm_status st = check_sizes(fn, rows, L, tokens, true, 1, H, dk, dv, io_dtype, 0);
+    if (st != SFM_OK) return st;
+    *bytes = 0;
+    return ok();
+}
+
+sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                               const float* h0, void* o, float* hT, const int32_t* offsets, int64_t rows, int64_t L,
+                               int64_t tokens, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int64_t ldq,
+                               int64_t ldk, int64_t ldv, float scale, int io_dtype, int flags, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+    static const char* fn = "sfm_gated_delta_fwd";
+    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, Hk, H, dk, dv, io_dtype, flags);
+    if (st != SFM_OK) return st;
+    st = check_inputs(fn, q, k, v, g, beta, tokens, Hk, H, dk, dv, ldq, ldk, ldv, io_dtype);
+    if (st != SFM_OK) return st;
+    if (tokens > 0 && !o) return fail(SFM_ERR_NULL, "%s: o is required", fn);
+    const int e = io_bytes(io_dtype);
+    if (!aligned_to(h0, 4) || !aligned_to(hT, 4) || !aligned_to(offsets, 4) || !aligned_to(o, e))
+        return fail(SFM_ERR_ALIGN, "%s: h0, hT, offsets or o not aligned to its element", fn);
+    int64_t need = 0;
+    st = sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, hT != nullptr, io_dtype, &need);
+    if (st != SFM_OK) return st;
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(SFM_ERR_SHAPE, "%s: workspace of %lld bytes needed, %lld given", fn, (long long)need,
+                    (long long)(workspace ? workspace_bytes : 0));
+    if (need > 0 && !aligned16(workspace)) return fail(SFM_ERR_ALIGN, "%s: workspace not 16-byte aligned", fn);
+    const int64_t sb = rows * H * dk * dv * 4;
+    Ranges in;
+    in.add_inputs(q, k, v, g, beta, tokens, Hk, H, dk, dv, ldq, ldk, ldv, e);
+    in.add("offsets", offsets, (rows + 1) * 4);
+    in.add("h0", h0, sb);
+    Ranges out;
+    out.add("o", o, tokens * H * dv * e);
+    out.add("workspace", workspace, need);
+    for (int i = 0; i < out.n; ++i)
+        if (const char* n = in.hit(out.ins[i])) return fail(SFM_ERR_ALIAS, "%s: %s overlaps %s", fn, out.ins[i].name, n);
+    if (out.n == 2 && overlap(out.ins[0], out.ins[1])) return fail(SFM_ERR_ALIAS, "%s: o overlaps workspace", fn);
+    if (hT) {
+        const Range r = rng("hT", hT, sb);
+        const char* n = in.hit(r);
+        if (n && !(hT == h0 && n[0] == 'h')) return fail(SFM_ERR_ALIAS, "%s: hT overlaps %s", fn, n);
+        if (const char* m = out.hit(r)) return fail(SFM_ERR_ALIAS, "%s: hT overlaps %s", fn, m);
+    }
+    sfm::DeltaParams p = params(q, k, v, g, beta, rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
+    p.h0 = h0, p.hT = hT, p.offsets = offsets, p.o = o;
+    p.vec_s = dv % 4 == 0 && aligned16(h0) && aligned16(hT);
+    return hip_status(sfm::launch_delta_recurrent(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
+}
+
+}  // extern "C"
