@@ -1,0 +1,10 @@
+// delta_fwd_f32.hip -- the chunked forward of the gated delta rule for float32 tensors (delta_fwd.h).
+#include "delta_fwd.h"
+
+namespace sfm {
+
+hipError_t launch_delta_fwd_f32(const DeltaParams& p, hipStream_t s) {
+    return p.dk <= 64 ? launch_delta_fwd_one<float, 64, 1, 1>(p, s) : launch_delta_fwd_one<float, 128, 1, 1>(p, s);
+}
+
+}  // namespace sfm

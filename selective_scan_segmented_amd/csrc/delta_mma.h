@@ -96,19 +96,20 @@ template <int P> __device__ __forceinline__ void store_parts(f32x4 x, float* p, 
     *reinterpret_cast<f32x4*>(p) = x;
 }
 
-// c += a b with a in PA planes of an LDS operand at `a`, b in PB parts: the part products that are not below the
-// smaller count's last part
-template <int PA, int PB, typename T>
-__device__ __forceinline__ f32x4 mma_parts(const T* a, int plane, const Parts<T, PB>& b, f32x4 c) {
+// c[n] += a b[n] for NC column tiles, a in PA planes of an LDS operand, b in PB parts: the products of parts that
+// are not below the last part of the finer operand, smallest first
+template <int PA, int PB, int NC, typename T>
+__device__ __forceinline__ void mma_columns(const T* a, int plane, const Parts<T, PB> (&b)[NC], f32x4 (&c)[NC]) {
     constexpr int top = PA > PB ? PA : PB;
 #pragma unroll
     for (int p = PA - 1; p >= 0; --p) {
         const Frag<T> fa = Frag<T>::load(a + p * plane);
 #pragma unroll
-        for (int q = PB - 1; q >= 0; --q)
-            if (p + q < top) c = mma(fa, b.p[q], c);
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int q = PB - 1; q >= 0; --q)
+                if (p + q < top) c[n] = mma(fa, b[n].p[q], c[n]);
     }
-    return c;
 }
 
 }  // namespace sfm

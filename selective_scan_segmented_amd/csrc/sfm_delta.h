@@ -50,6 +50,9 @@ constexpr float kDeltaNormEps = 1e-6f;
 // (the state's reset) then keeps the differences of a chunk's running sums finite.
 constexpr float kDeltaMinGate = -110.0f;
 
+// chunked forward, one translation unit per io type
+hipError_t launch_delta_fwd_f32(const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_fwd_bf16(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_recurrent(const DeltaParams& p, int io_dtype, hipStream_t s);
 
 }  // namespace sfm

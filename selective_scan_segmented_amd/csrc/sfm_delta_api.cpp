@@ -48,6 +48,9 @@ sfm_status check_inputs(const char* fn, const void* q, const void* k, const void
     return SFM_OK;
 }
 
+// Rows up to this long go token by token.
+constexpr int64_t kRecurrentMax = 4;
+
 struct Ranges {
     Range ins[8];
     int n = 0;
@@ -171,7 +174,9 @@ sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
     sfm::DeltaParams p = params(q, k, v, g, beta, rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
     p.h0 = h0, p.hT = hT, p.offsets = offsets, p.o = o;
     p.vec_s = dv % 4 == 0 && aligned16(h0) && aligned16(hT);
-    return hip_status(sfm::launch_delta_recurrent(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (L <= kRecurrentMax) return hip_status(sfm::launch_delta_recurrent(p, io_dtype, hs), fn);
+    return hip_status(io_dtype == SFM_F32 ? sfm::launch_delta_fwd_f32(p, hs) : sfm::launch_delta_fwd_bf16(p, hs), fn);
 }
 
 }  // extern "C"
