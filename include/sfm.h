@@ -353,8 +353,8 @@ sfm_status sfm_scan_plan_string(int64_t B1, int64_t B2, int64_t D, int64_t N, in
  * S [dk, dv] float32, zero (or h0) before the row's first token.
  *
  * sfm_gated_delta_fwd -- whole rows.
- *   q, k     [tokens, Hk, dk] io   token strides ldq, ldk (elements, >= Hk dk)
- *   v        [tokens, H, dv] io    token stride ldv (>= H dv)
+ *   q, k     [tokens, Hk, dk] io   token strides ldq, ldk (elements, Hk dk to 2^22)
+ *   v        [tokens, H, dv] io    token stride ldv (H dv to 2^22)
  *   g, beta  [tokens, H] io        g normally <= 0; minus infinity resets the state
  *   h0       [rows, H, dk, dv] f32 or NULL (zero)
  *   o        [tokens, H, dv] io

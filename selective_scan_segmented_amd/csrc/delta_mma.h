@@ -6,7 +6,7 @@
 // long as both operands agree, and it is chosen so that results become operands without leaving their lanes: an
 // accumulator tile has column l % 16 and rows 4 (l / 16) .. + 3 in lane l, so slot 8 g + 4 h + j stands for index
 // 16 h + 4 g + j, and two accumulator tiles that lie one above the other are, lane by lane, the right operand of
-// the next product (slot_of below).
+// the next product.
 //
 // bfloat16 tensors use v_mfma_f32_16x16x32_bf16.  What is computed (states, the chunk's inverse, the updates) is
 // float32; as an operand it is a sum of two or three bfloat16 parts (8 bits each: relative error 2^-17 or 2^-25)
@@ -23,9 +23,38 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
-// slot of contraction index i within its block of 32 (and of the 4-aligned run it starts, if i % 4 == 0)
-__device__ __forceinline__ constexpr int slot_of(int i) {
-    return (i & ~31) | (((i >> 2) & 3) << 3) | (((i >> 4) & 1) << 2) | (i & 3);
+// this wave's number in its workgroup, known to the compiler as one value for all lanes
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// ---------------------------------------------------------------- bounded memory
+// A run of device memory as a buffer: loads past its end give zero and stores there are dropped, so rows behind the
+// end of a chunk and columns behind a head's need no branch (a branch round every load makes them wait in turn).
+struct Buf {
+    __amdgpu_buffer_rsrc_t r;
+};
+constexpr unsigned kNowhere = 0x80000000u;  // an offset past every buffer (they end below 2^30, offsets add less)
+__device__ __forceinline__ Buf make_buf(const void* p, int64_t bytes) {
+    return Buf{__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000)};
+}
+// The value as one the compiler must take afresh: sums of it with each of a loop's constants are then made where
+// they are used, not all kept in registers across the loop.
+__device__ __forceinline__ unsigned fresh(unsigned v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+template <typename T> __device__ __forceinline__ T buf_load(const Buf& b, unsigned at) {
+    if constexpr (sizeof(T) == 2)
+        return __builtin_bit_cast(T, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(b.r, at, 0, 0));
+    else if constexpr (sizeof(T) == 4)
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(b.r, at, 0, 0));
+    else
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b128(b.r, at, 0, 0));
+}
+template <typename T> __device__ __forceinline__ void buf_store(const Buf& b, unsigned at, T v) {
+    if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), b.r, at, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), b.r, at, 0, 0);
 }
 
 template <typename T> struct Frag;
@@ -79,37 +108,88 @@ template <int P> __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Parts
     out.p[0] = Frag<float>{lo, hi};
 }
 
-// four values into P planes of an LDS operand (plane stride `plane` elements)
-template <int P> __device__ __forceinline__ void store_parts(f32x4 x, __bf16* p, int plane) {
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-        bf16x4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = (__bf16)x[j];
-            x[j] -= (float)v[j];
-        }
-        *reinterpret_cast<bf16x4*>(p + q * plane) = v;
-    }
-}
-template <int P> __device__ __forceinline__ void store_parts(f32x4 x, float* p, int) {
-    *reinterpret_cast<f32x4*>(p) = x;
+// Fragment of a [token][key] array whose keys lie in their own order: slots 0..3 and 4..7 of a lane are the runs at
+// 4 (l / 16) and 16 further on.
+template <typename T> __device__ __forceinline__ Frag<T> load_runs(const T* p) {
+    typedef T quad __attribute__((ext_vector_type(4)));
+    const quad lo = *reinterpret_cast<const quad*>(p), hi = *reinterpret_cast<const quad*>(p + 16);
+    if constexpr (sizeof(T) == 4)
+        return Frag<T>{lo, hi};
+    else
+        return Frag<T>{__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)};
 }
 
-// c[n] += a b[n] for NC column tiles, a in PA planes of an LDS operand, b in PB parts: the products of parts that
-// are not below the last part of the finer operand, smallest first
+// Fragment of the transpose of a [token][key] array: rows are the 16 keys from `keys` on (p points at the array's
+// element [32 tokens' first][keys' first]), the contraction runs over 32 tokens.  bfloat16: the LDS read that
+// transposes 4 x 16 values among 16 lanes (lane i gives the address of token i / 4, keys 4 (i % 4) .. + 3, and
+// receives key i of the four tokens); float32: element by element.
+template <typename T> __device__ __forceinline__ Frag<T> load_transposed(const T* p, int pitch) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
+    if constexpr (sizeof(T) == 4) {
+        Frag<T> f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f.lo[j] = p[(g4 + j) * pitch + l16];
+            f.hi[j] = p[(g4 + 16 + j) * pitch + l16];
+        }
+        return f;
+    } else {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+        const T* at = p + (g4 + (l16 >> 2)) * pitch + (l16 & 3) * 4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 16 * pitch));
+        return Frag<T>{__builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7))};
+    }
+}
+
+// Computed operands [64][64], lower triangle of tiles: fragment by fragment, 64 lanes x 8 slots each, so a lane
+// writes what the same lane of any wave reads.  Row tile rt, step kb of 32 columns:
+__device__ __forceinline__ constexpr int lower_frag(int rt, int kb) { return rt < 2 ? rt : 2 * rt - 2 + kb; }
+constexpr int kLowerFrags = 6;
+constexpr int kFragSize = 64 * 8;
+
+// tile (rt, tj)'s four values of this lane (row l % 16, columns 4 (l / 16) .. + 3) into P planes
+template <int P, typename T> __device__ __forceinline__ void store_tile(f32x4 x, T* base, int rt, int tj) {
+    const int lane = threadIdx.x & 63;
+    T* p = base + lower_frag(rt, tj >> 1) * kFragSize + lane * 8 + (tj & 1) * 4;
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<f32x4*>(p) = x;
+    } else {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            bf16x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = (__bf16)x[j];
+                x[j] -= (float)v[j];
+            }
+            *reinterpret_cast<bf16x4*>(p + q * kLowerFrags * kFragSize) = v;
+        }
+    }
+}
+
+// c[n] += a b[n] for NC column tiles, a given by its PA parts, b in PB: the products of parts that are not below
+// the last part of the finer operand, smallest first
 template <int PA, int PB, int NC, typename T>
-__device__ __forceinline__ void mma_columns(const T* a, int plane, const Parts<T, PB> (&b)[NC], f32x4 (&c)[NC]) {
+__device__ __forceinline__ void mma_parts(const Parts<T, PA>& a, const Parts<T, PB> (&b)[NC], f32x4 (&c)[NC]) {
     constexpr int top = PA > PB ? PA : PB;
 #pragma unroll
-    for (int p = PA - 1; p >= 0; --p) {
-        const Frag<T> fa = Frag<T>::load(a + p * plane);
+    for (int p = PA - 1; p >= 0; --p)
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+        for (int q = PB - 1; q >= 0; --q)
+            if (p + q < top)
 #pragma unroll
-            for (int q = PB - 1; q >= 0; --q)
-                if (p + q < top) c[n] = mma(fa, b[n].p[q], c[n]);
-    }
+                for (int n = 0; n < NC; ++n) c[n] = mma(a.p[p], b[n].p[q], c[n]);
+}
+
+// parts of fragment `f` of a computed operand
+template <int P, typename T> __device__ __forceinline__ Parts<T, P> load_parts(const T* base, int f) {
+    const int lane = threadIdx.x & 63;
+    Parts<T, P> a;
+#pragma unroll
+    for (int q = 0; q < P; ++q) a.p[q] = Frag<T>::load(base + (q * kLowerFrags + f) * kFragSize + lane * 8);
+    return a;
 }
 
 }  // namespace sfm

@@ -19,12 +19,12 @@ constexpr int kCols = 64;    // columns to a workgroup
 constexpr int kGroups = 16;  // row groups
 
 template <typename T, int RPT, bool VEC>
-__global__ __launch_bounds__(256) void delta_recurrent_kernel(const DeltaParams p, int tiles) {
+__global__ __launch_bounds__(256) void delta_recurrent_kernel(const DeltaParams p, unsigned tiles) {
     __shared__ float red[2][2][4][kCols];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t unit = blockIdx.x / tiles;
+    const unsigned unit = blockIdx.x / tiles;
     const int c0 = (int)(blockIdx.x - unit * tiles) * kCols + (tid & 15) * 4;
-    const int s = (int)(unit / p.H), h = (int)(unit - (int64_t)s * p.H);
+    const int s = (int)(unit / (unsigned)p.H), h = (int)(unit - (unsigned)s * p.H);
     const int rg = tid >> 4;
     int64_t first;
     int len;
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void delta_recurrent_kernel(const DeltaParams 
         if (slot < 0 || slot >= p.pool) slot = -1;
     }
     const int64_t sbase = (slot * p.H + h) * (int64_t)p.dk * p.dv;
-    const int hk = h / (p.H / p.Hk);
+    const int hk = (int)((unsigned)h / (unsigned)p.share);
     const bool full = VEC && c0 + 4 <= p.dv;
 
     float S[RPT][4];
@@ -156,8 +156,8 @@ __global__ __launch_bounds__(256) void delta_recurrent_kernel(const DeltaParams 
 
 template <typename T, int RPT>
 hipError_t launch_rpt(const DeltaParams& p, hipStream_t s) {
-    const int tiles = (p.dv + kCols - 1) / kCols;
-    const dim3 grid((unsigned)((int64_t)p.rows * p.H * tiles));
+    const unsigned tiles = (p.dv + kCols - 1) / kCols;
+    const dim3 grid((unsigned)p.rows * p.H * tiles);
     if (p.vec_s)
         hipLaunchKernelGGL((delta_recurrent_kernel<T, RPT, true>), grid, dim3(256), 0, s, p, tiles);
     else

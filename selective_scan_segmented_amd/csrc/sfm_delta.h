@@ -9,6 +9,7 @@ namespace sfm {
 constexpr int kDeltaChunk = 64;        // tokens to a chunk of the chunked kernels
 constexpr int kDeltaMaxK = 128;        // largest key head
 constexpr int kDeltaMaxV = 256;        // largest value head
+constexpr int64_t kDeltaMaxUnits = 1LL << 28;  // rows x heads (each is at most four workgroups wide)
 
 // One call's rows, heads and strides (forward, backward and the token-by-token form).
 struct DeltaParams {
@@ -23,7 +24,7 @@ struct DeltaParams {
     const int32_t* offsets;  // [rows + 1] or null: row s is tokens s * L .. + L - 1
     const int32_t* slots;    // [rows] or null: the state of row s is number slots[s] of `pool` in h0 and hT
     int64_t ldq, ldk, ldv, tokens, pool;
-    int rows, L, Hk, H, dk, dv;
+    int rows, L, Hk, H, share, dk, dv;  // share = H / Hk
     float scale;
     int l2norm;
     int vec_k, vec_v;    // q and k (v) rows may be loaded 16 bytes at a time

@@ -29,7 +29,7 @@ sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, 
         return fail(SFM_ERR_SHAPE, "%s: head sizes dk=%lld (1 to %d), dv=%lld (1 to %d)", fn, (long long)dk,
                     sfm::kDeltaMaxK, (long long)dv, sfm::kDeltaMaxV);
     const int64_t widest = dk > dv ? dk : dv;
-    if (tokens * H > (1LL << 40) / widest || rows * H > (1LL << 28))
+    if (tokens * H > (1LL << 40) / widest || rows * H > sfm::kDeltaMaxUnits)
         return fail(SFM_ERR_SHAPE, "%s: tensor too large", fn);
     return SFM_OK;
 }
@@ -39,7 +39,7 @@ sfm_status check_inputs(const char* fn, const void* q, const void* k, const void
                         int64_t ldv, int io_dtype) {
     if (tokens > 0 && (!q || !k || !v || !g || !beta))
         return fail(SFM_ERR_NULL, "%s: q, k, v, g and beta are required", fn);
-    if (ldq < Hk * dk || ldk < Hk * dk || ldv < H * dv || ldq > (1 << 24) || ldk > (1 << 24) || ldv > (1 << 24))
+    if (ldq < Hk * dk || ldk < Hk * dk || ldv < H * dv || ldq > (1 << 22) || ldk > (1 << 22) || ldv > (1 << 22))
         return fail(SFM_ERR_SHAPE, "%s: token strides %lld, %lld, %lld below the heads' widths (or too large)", fn,
                     (long long)ldq, (long long)ldk, (long long)ldv);
     const uintptr_t e = io_bytes(io_dtype);
@@ -80,7 +80,7 @@ sfm::DeltaParams params(const void* q, const void* k, const void* v, const void*
     const int e = io_bytes(io_dtype);
     p.q = q, p.k = k, p.v = v, p.g = g, p.beta = beta;
     p.ldq = ldq, p.ldk = ldk, p.ldv = ldv, p.tokens = tokens;
-    p.rows = (int)rows, p.L = (int)L, p.Hk = (int)Hk, p.H = (int)H, p.dk = (int)dk, p.dv = (int)dv;
+    p.rows = (int)rows, p.L = (int)L, p.Hk = (int)Hk, p.H = (int)H, p.share = (int)(H / Hk), p.dk = (int)dk, p.dv = (int)dv;
     p.scale = scale;
     p.l2norm = flags & SFM_DELTA_L2NORM ? 1 : 0;
     // 16-byte loads of whole rows need every row to start on 16 bytes
