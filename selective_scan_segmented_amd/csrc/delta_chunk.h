@@ -28,7 +28,7 @@ struct ChunkRows {
     float eg[kC];            // e^G
     float er[kC];            // e^(G_C - G)
     float beta[kC];
-    float rk[kC], rq[kC];    // 1 / key length; scale / query length
+    float rk[kC], rq[kC];    // 1 / length of the key and of the query (1 without l2norm)
 };
 
 template <typename T, int DK> struct ChunkShape {
@@ -89,8 +89,8 @@ template <typename T, int DK> struct RowShare {
         }
     }
 
-    // into LDS: the rows and, if wanted, their factors (scale over the row's length)
-    __device__ __forceinline__ void store(T* rows, float* factor, float scale, int l2norm) const {
+    // into LDS: the rows and, if wanted, one over their lengths
+    __device__ __forceinline__ void store(T* rows, float* factor, int l2norm) const {
         using Sh = ChunkShape<T, DK>;
         const int t0 = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
 #pragma unroll
@@ -98,7 +98,7 @@ template <typename T, int DK> struct RowShare {
         if (!factor) return;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            float f = scale;
+            float f = 1.0f;
             if (l2norm) {
                 float s = 0.0f;
 #pragma unroll
@@ -106,7 +106,7 @@ template <typename T, int DK> struct RowShare {
                     const float x = to_f32((T)a[i][e]);
                     s = __builtin_fmaf(x, x, s);
                 }
-                f *= __builtin_amdgcn_rsqf(lanes_sum<kPer>(s) + kDeltaNormEps);
+                f = __builtin_amdgcn_rsqf(lanes_sum<kPer>(s) + kDeltaNormEps);
             }
             if (c == 0) factor[t0 + i * kStep] = f;
         }
@@ -161,7 +161,7 @@ template <typename T, int DK> __device__ __forceinline__ f32x4 rows_product(cons
 // The twenty lower tiles of M and A, five to a wave: task w + 4 n, M's ten first.  M goes to LDS; A's stay in
 // registers (a[n - 2]; lane: row i = l % 16, columns 4 (l / 16) .. + 3) until M's place is free.
 template <typename T, int DK>
-__device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const ChunkRows* rows, float* mt, f32x4 (&a)[3]) {
+__device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const ChunkRows* rows, float scale, float* mt, f32x4 (&a)[3]) {
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
     f32x4 c[5];
 #pragma unroll
@@ -188,7 +188,7 @@ __device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const C
             *reinterpret_cast<f32x4*>(mt + tile_at(ti, tj) + l16 * 20 + g4) = m;
         } else {
             const int i = ti * 16 + l16, j0 = tj * 16 + g4;
-            const float ri = rows->rq[i], hi = rows->ghi[i], lo = rows->glo[i];
+            const float ri = scale * rows->rq[i], hi = rows->ghi[i], lo = rows->glo[i];
             const f32x4 hj = four(rows->ghi + j0), lj = four(rows->glo + j0), rj = four(rows->rk + j0);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -265,6 +265,62 @@ template <int PT, typename T> __device__ __forceinline__ void store_t(const f32x
     for (int j = 0; j < 4; ++j)
         if (j <= (wave | 1)) store_tile<PT>(t[j], ts, wave, j);
 }
+
+// Gates, K and Q (in registers) to LDS, then M, T and A, all by the whole workgroup: T (PT parts) at ts and A (PA
+// parts) at as, where M lies before.  Ends with T and A visible to all.
+template <typename T, int DK, int PT, int PA, typename Between>
+__device__ __forceinline__ void build_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const DeltaParams& p,
+                                            const T* g, const T* beta, int n, ChunkRows* rows, T* ks, T* qs, T* as,
+                                            T* ts, Between between) {
+    float* mt = reinterpret_cast<float*>(as);
+    kr.store(ks, rows->rk, p.l2norm);
+    qr.store(qs, rows->rq, p.l2norm);
+    if (wave_id() == 0) chunk_gates<T>(g, beta, p.H, n, rows);
+    lds_barrier();
+    f32x4 a[3], t[4];
+    chunk_products<T, DK>(ks, qs, rows, p.scale, mt, a);
+    lds_barrier();
+    invert_diagonal(mt);
+    lds_barrier();
+    inverse_rows(mt, t);
+    store_t<PT>(t, ts);
+    between();       // what needs K and Q only
+    lds_barrier();  // M is done with
+    store_a<PA>(a, as);
+    lds_barrier();
+}
+
+// A row's place in the arrays that hold something for every chunk: chunk c of row s is entry first + c.  Packed
+// rows: first = start / 64 + s leaves every row room for its chunks without a count of those before it.
+__device__ __forceinline__ unsigned chunk_entry(const DeltaParams& p, int s, int64_t first) {
+    return p.offsets ? (unsigned)(first / kC) + s : (unsigned)s * ((p.L + kC - 1) / kC);
+}
+
+// What the preparing kernel leaves of a chunk and head: the row scalars, T and A (P parts each).
+template <typename T, int P> struct ChunkOperands {
+    static constexpr int frag_bytes = kLowerFrags * kFragSize * (int)sizeof(T);
+    static constexpr int t = (int)sizeof(ChunkRows), a = t + P * frag_bytes, bytes = a + P * frag_bytes;
+    static_assert(sizeof(ChunkRows) % 16 == 0 && frag_bytes % 16 == 0, "whole 16-byte units");
+};
+
+// One thread's share of such a run of 16-byte units, N bytes long
+template <int N> struct Linear {
+    typedef unsigned unit __attribute__((ext_vector_type(4)));
+    static constexpr int kUnits = (N / 16 + kDeltaThreads - 1) / kDeltaThreads;
+    unit x[kUnits];
+    __device__ __forceinline__ void load(const char* p) {
+        const Buf b = make_buf(p, N);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) x[i] = buf_load<unit>(b, (threadIdx.x + i * kDeltaThreads) * 16u);
+    }
+    __device__ __forceinline__ void store(char* p) const {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = threadIdx.x + i * kDeltaThreads;
+            if (N % (kDeltaThreads * 16) == 0 || u < N / 16) *reinterpret_cast<unit*>(p + u * 16) = x[i];
+        }
+    }
+};
 
 // Workgroup -> unit of work: workgroups go to the eight dies in turn, and neighbouring units (the column tiles and
 // heads that read the same keys) stay on one die, so its L2 serves them.

@@ -1,42 +1,48 @@
-// delta_fwd.h -- the chunked forward of the gated delta rule (kernels; one translation unit per io type).
+// delta_fwd.h -- the walk over a row's chunks: the gated delta rule's forward, and the states that its backward needs
+// (kernels; one translation unit per io type).
+//
+// A workgroup takes one (row, head) and 64 columns of its values, 16 to a wave, and walks the row's chunks; the
+// state's columns stay in the wave's accumulators (float32) all the way.  S0, R and U pass from product to product
+// inside a lane (delta_mma.h), so waves meet only over K, Q, T and A in LDS.
 #pragma once
 
 #include "delta_chunk.h"
 
 namespace sfm {
 
-// LDS of the forward, in bytes from the start.
-template <typename T, int DK, int PS> struct FwdLds {
+// kWhole: T and A of a chunk are made on the way (rows of few chunks, or enough rows to fill the card while some
+// workgroups do that).  kPrepared: they come from the preparing kernel.  kStates: likewise, and instead of outputs
+// the states before the chunks and U are written down, for the backward.
+enum Walk { kWhole, kPrepared, kStates };
+
+template <typename T, int DK, int P> struct WalkLds {
     using Sh = ChunkShape<T, DK>;
-    static constexpr int PT = PS;                                  // parts of T
-    static constexpr int PA = sizeof(T) == 4 ? 1 : 2;              // parts of A
     static constexpr int frag_bytes = kLowerFrags * kFragSize * (int)sizeof(T);
     static constexpr int rows = 0;
-    static constexpr int ks = (int)sizeof(ChunkRows);
+    static constexpr int ts = (int)sizeof(ChunkRows);              // T, A: as ChunkOperands has them
+    static constexpr int as = ts + P * frag_bytes;                 // (M before A)
+    static constexpr int ks = as + (P * frag_bytes > kBytesM ? P * frag_bytes : kBytesM);
     static constexpr int qs = ks + Sh::row_bytes;
-    static constexpr int as = qs + Sh::row_bytes;                  // A; M before it
-    static constexpr int ts = as + (PA * frag_bytes > kBytesM ? PA * frag_bytes : kBytesM);
-    static constexpr int bytes = ts + PT * frag_bytes;
+    static constexpr int bytes = qs + Sh::row_bytes;
     static constexpr int groups = 160 * 1024 / bytes < 2 ? 1 : 2;  // workgroups to a compute unit
 };
 
-// A workgroup takes one (row, head) and 64 NC columns of its values, NC tiles of 16 to a wave, and walks the
-// row's chunks; the state's columns stay in the wave's accumulators (float32) all the way.
-template <typename T, int DK, int NC, int PS>
-__global__ __launch_bounds__(kDeltaThreads, (FwdLds<T, DK, PS>::groups)) void delta_fwd_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+template <typename T, int DK, int P, Walk W>
+__global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
     using Sh = ChunkShape<T, DK>;
-    using L = FwdLds<T, DK, PS>;
-    constexpr int PA = L::PA, PT = L::PT, PY = PS < 2 ? PS : 2;
+    using L = WalkLds<T, DK, P>;
+    using Ops = ChunkOperands<T, P>;
+    constexpr int PY = P < 2 ? P : 2;  // parts that only the outputs see: their type's rounding is far above the third
+    constexpr int E = (int)sizeof(T);
     extern __shared__ char lds[];
     ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs),
       *as = reinterpret_cast<T*>(lds + L::as), *ts = reinterpret_cast<T*>(lds + L::ts);
-    float* mt = reinterpret_cast<float*>(lds + L::as);
 
     const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
-    const int col0 = (int)(unit - rh * tiles) * 64 * NC + wave * 16 * NC + l16;
+    const int col = (int)(unit - rh * tiles) * 64 + wave * 16 + l16;
     int64_t first;
     int len;
     delta_row(p, s, first, len);
@@ -46,178 +52,249 @@ __global__ __launch_bounds__(kDeltaThreads, (FwdLds<T, DK, PS>::groups)) void de
     const T* gp = static_cast<const T*>(p.g) + first * p.H + h;
     const T* bp = static_cast<const T*>(p.beta) + first * p.H + h;
     T* op = static_cast<T*>(p.o) + (first * p.H + h) * p.dv;
-    constexpr int E = (int)sizeof(T);
     const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
-    unsigned soff[NC], voff[NC], ooff[NC];  // this lane's columns in a state, in the values and in the output
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int c = col0 + n * 16;
-        soff[n] = c < p.dv ? (unsigned)(g4 * p.dv + c) * 4u : kNowhere;
-        voff[n] = c < p.dv ? (unsigned)(g4 * p.ldv + c) * E : kNowhere;
-        ooff[n] = c < p.dv ? (unsigned)(g4 * p.H * p.dv + c) * E : kNowhere;
-    }
+    // this lane's column in a state, in the values and in the output
+    const unsigned soff = col < p.dv ? (unsigned)(g4 * p.dv + col) * 4u : kNowhere;
+    const unsigned voff = col < p.dv ? (unsigned)(g4 * p.ldv + col) * E : kNowhere;
+    const unsigned ooff = col < p.dv ? (unsigned)(g4 * p.H * p.dv + col) * E : kNowhere;
+    int64_t entry = (int64_t)chunk_entry(p, s, first) * p.H + h;
+    const int vals = (int)tiles * 64;  // values in the workspace: whole tiles
 
-    f32x4 S[DK / 16][NC];
+    f32x4 S[DK / 16];
 #pragma unroll
-    for (int d = 0; d < DK / 16; ++d)
-#pragma unroll
-        for (int n = 0; n < NC; ++n) S[d][n] = f32x4{0, 0, 0, 0};
+    for (int d = 0; d < DK / 16; ++d) S[d] = f32x4{0, 0, 0, 0};
     if (p.h0) {
         const Buf b = make_buf(p.h0 + sbase, (int64_t)p.dk * p.dv * 4);
 #pragma unroll
         for (int d = 0; d < DK / 16; ++d)
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[d][n][r] = buf_load<float>(b, fresh(soff[n]) + (unsigned)((d * 16 + r) * p.dv) * 4u);
+            for (int r = 0; r < 4; ++r) S[d][r] = buf_load<float>(b, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u);
     }
     bool zero = !p.h0;  // the state is zero: its products are left out
 
+    RowShare<T, DK> kr, qr;
+    Linear<Ops::a> ops;                // row scalars and T
+    Linear<PY * L::frag_bytes> opa;    // A
+    unsigned v[4][4];                  // values' bits
+    auto fetch = [&](int64_t t0) {
+        const int64_t n = min((int64_t)kC, len - t0);
+        kr.load(make_buf(kp + t0 * p.ldk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
+        if (W != kStates) qr.load(make_buf(qp + t0 * p.ldq, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
+        if (W != kWhole) {
+            const char* o = p.w_ops + entry * Ops::bytes;
+            ops.load(o);
+            if (W == kPrepared) opa.load(o + Ops::a);
+        }
+        const Buf vb = make_buf(vp + t0 * p.ldv, n * p.ldv * E);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(vb, fresh(voff) + (unsigned)((rt * 16 + r) * p.ldv) * E);
+    };
+    if (W != kWhole && len > 0) fetch(0);  // ahead of its use by a chunk
+
     for (int64_t t0 = 0; t0 < len; t0 += kC) {
         const int64_t n_tok = min((int64_t)kC, len - t0);
-        RowShare<T, DK> kr, qr;
-        kr.load(make_buf(kp + t0 * p.ldk, n_tok * p.ldk * E), p.ldk, p.dk, p.vec_k);
-        qr.load(make_buf(qp + t0 * p.ldq, n_tok * p.ldq * E), p.ldq, p.dk, p.vec_k);
-        const Buf vb = make_buf(vp + t0 * p.ldv, n_tok * p.ldv * E);
-        T v[4][NC][4];
+        const int64_t here = entry;
+        entry += p.H;
+        f32x4 X[4], Y[4];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
+        for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = f32x4{0, 0, 0, 0};
+        // X = K S, Y = Q S; then R = beta (V - e^G X) in X's place
+        auto state_products = [&] {
+            if (!zero || W == kStates) {
+                Frag<T> fk[2][4], fq[2][4];
+                auto load = [&](int kb) {
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[rt][n][r] = buf_load<T>(vb, fresh(voff[n]) + (unsigned)((rt * 16 + r) * p.ldv) * E);
-        __syncthreads();  // the chunk before is done with LDS
-        kr.store(ks, rows->rk, 1.0f, p.l2norm);
-        qr.store(qs, rows->rq, p.scale, p.l2norm);
-        if (wave == 0) chunk_gates<T>(gp + t0 * p.H, bp + t0 * p.H, p.H, (int)n_tok, rows);
-        __syncthreads();
-        f32x4 a[3];
-        chunk_products<T, DK>(ks, qs, rows, mt, a);
-        __syncthreads();
-        invert_diagonal(mt);
-        __syncthreads();
-        f32x4 t[4];
-        inverse_rows(mt, t);
-        store_t<PT>(t, ts);
-        // the state's products: X = K S, Y = Q S
-        f32x4 X[4][NC], Y[4][NC];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-            for (int n = 0; n < NC; ++n) X[rt][n] = Y[rt][n] = f32x4{0, 0, 0, 0};
-        if (!zero) {
-#pragma unroll
-            for (int kb = 0; kb < DK / 32; ++kb) {
-                Parts<T, PS> sp[NC];
-#pragma unroll
-                for (int n = 0; n < NC; ++n) split<PS>(S[2 * kb][n], S[2 * kb + 1][n], sp[n]);
-#pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    const int at = (rt * 16 + l16) * Sh::KS + kb * 32 + g4;
-                    const Frag<T> fk = load_runs<T>(ks + at), fq = load_runs<T>(qs + at);
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-#pragma unroll
-                        for (int q = PS - 1; q >= 0; --q) X[rt][n] = mma(fk, sp[n].p[q], X[rt][n]);
-#pragma unroll
-                        for (int q = PY - 1; q >= 0; --q) Y[rt][n] = mma(fq, sp[n].p[q], Y[rt][n]);
+                    for (int rt = 0; rt < 4; ++rt) {
+                        const int at = (rt * 16 + l16) * Sh::KS + kb * 32 + g4;
+                        fk[kb & 1][rt] = load_runs<T>(ks + at);
+                        if constexpr (W != kStates) fq[kb & 1][rt] = load_runs<T>(qs + at);
                     }
+                };
+                load(0);
+#pragma unroll
+                for (int kb = 0; kb < DK / 32; ++kb) {
+                    if (kb + 1 < DK / 32) load(kb + 1);
+                    loads_end();
+                    Parts<T, P> sp;
+                    split<P>(S[2 * kb], S[2 * kb + 1], sp);
+                    if constexpr (W == kStates)
+                        store_planes<P>(sp, reinterpret_cast<T*>(p.w_s) + here * P * vals * DK + (int64_t)col * DK + kb * 32 + g4,
+                                        (int64_t)vals * DK);
+#pragma unroll
+                    for (int q = P - 1; q >= 0; --q)
+#pragma unroll
+                        for (int rt = 0; rt < 4; ++rt) {
+                            X[rt] = mma(fk[kb & 1][rt], sp.p[q], X[rt]);
+                            if constexpr (W != kStates)
+                                if (q < PY) Y[rt] = mma(fq[kb & 1][rt], sp.p[q], Y[rt]);
+                        }
                 }
             }
-        }
-        // R = beta (V - e^G X), in X's place
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            const f32x4 be = four(rows->beta + rt * 16 + g4), eg = four(rows->eg + rt * 16 + g4),
-                        rk = four(rows->rk + rt * 16 + g4);
+            for (int rt = 0; rt < 4; ++rt) {
+                const f32x4 be = four(rows->beta + rt * 16 + g4), f = four(rows->eg + rt * 16 + g4) * four(rows->rk + rt * 16 + g4);
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    X[rt][n][r] = be[r] * __builtin_fmaf(-(eg[r] * rk[r]), X[rt][n][r], to_f32(v[rt][n][r]));
-        }
-        __syncthreads();  // T is there; M is done with
-        store_a<PA>(a, as);
-        f32x4 U[4][NC];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-            for (int n = 0; n < NC; ++n) U[rt][n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            Parts<T, PS> rp[NC];
-#pragma unroll
-            for (int n = 0; n < NC; ++n) split<PS>(X[2 * kb][n], X[2 * kb + 1][n], rp[n]);
-#pragma unroll
-            for (int rt = 2 * kb; rt < 4; ++rt)
-                mma_parts<PT, PS, NC>(load_parts<PT>(ts, lower_frag(rt, kb)), rp, U[rt]);
-        }
-        __syncthreads();  // A is there
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            const f32x4 f = four(rows->eg + rt * 16 + g4) * four(rows->rq + rt * 16 + g4);
-#pragma unroll
-            for (int n = 0; n < NC; ++n) Y[rt][n] *= f;
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            Parts<T, PA> up[NC];
-#pragma unroll
-            for (int n = 0; n < NC; ++n) split<PA>(U[2 * kb][n], U[2 * kb + 1][n], up[n]);
-#pragma unroll
-            for (int rt = 2 * kb; rt < 4; ++rt)
-                mma_parts<PA, PA, NC>(load_parts<PA>(as, lower_frag(rt, kb)), up, Y[rt]);
-        }
-        const Buf ob = make_buf(op + (int64_t)t0 * p.H * p.dv, (int64_t)n_tok * p.H * p.dv * E);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    buf_store<T>(ob, fresh(ooff[n]) + (unsigned)((rt * 16 + r) * p.H * p.dv) * E, from_f32<T>(Y[rt][n][r]));
-        zero = false;
-        if (t0 + kC >= len && !p.hT) break;  // nobody asks for the state after the last chunk
-        const float ec = rows->eg[kC - 1];
-#pragma unroll
-        for (int d = 0; d < DK / 16; ++d)
-#pragma unroll
-            for (int n = 0; n < NC; ++n) S[d][n] *= ec;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            Parts<T, PS> up[NC];
-#pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                const int r0 = kb * 32 + g4;
-                split<PS>(U[2 * kb][n] * (four(rows->er + r0) * four(rows->rk + r0)),
-                          U[2 * kb + 1][n] * (four(rows->er + r0 + 16) * four(rows->rk + r0 + 16)), up[n]);
+                for (int r = 0; r < 4; ++r) X[rt][r] = be[r] * __builtin_fmaf(-f[r], X[rt][r], Io<T>::of_bits(v[rt][r]));
             }
+        };
+        if (W == kWhole) fetch(t0);  // (registers that other workgroups on the unit can use better)
+        lds_barrier();  // the chunk before is done with LDS
+        if constexpr (W == kWhole) {
+            build_chunk<T, DK, P, PY>(kr, qr, p, gp + t0 * p.H, bp + t0 * p.H, (int)n_tok, rows, ks, qs, as, ts, state_products);
+        } else {
+            kr.store(ks, nullptr, 0);
+            ops.store(lds);
+            if (W == kPrepared) {
+                qr.store(qs, nullptr, 0);
+                opa.store(lds + L::as);
+            }
+            lds_barrier();
+            state_products();
+            if (t0 + kC < len) fetch(t0 + kC);
+        }
+        f32x4 U[4];
+        {
+            Parts<T, P> tp[kLowerFrags], rp[2];
 #pragma unroll
-            for (int d = 0; d < DK / 16; ++d)
-                mma_parts<1, PS, NC>(Parts<T, 1>{load_transposed<T>(ks + kb * 32 * Sh::KS + d * 16, Sh::KS)}, up, S[d]);
+            for (int f = 0; f < kLowerFrags; ++f) tp[f] = load_parts<P>(ts, f);
+            loads_end();
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) split<P>(X[2 * kb], X[2 * kb + 1], rp[kb]);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) U[rt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) mma_lower<P, P>(tp, rp[kb], kb, U);
+        }
+        if constexpr (W == kStates) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                Parts<T, P> up;
+                split<P>(U[2 * kb], U[2 * kb + 1], up);
+                store_planes<P>(up, reinterpret_cast<T*>(p.w_u) + here * P * vals * kC + (int64_t)col * kC + kb * 32 + g4, (int64_t)vals * kC);
+            }
+        } else {
+            Parts<T, PY> ap[kLowerFrags], up[2];
+#pragma unroll
+            for (int f = 0; f < kLowerFrags; ++f) ap[f] = load_parts<PY>(as, f);
+            loads_end();
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) Y[rt] *= four(rows->eg + rt * 16 + g4) * four(rows->rq + rt * 16 + g4) * p.scale;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) split<PY>(U[2 * kb], U[2 * kb + 1], up[kb]);
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) mma_lower<PY, PY>(ap, up[kb], kb, Y);
+            const Buf ob = make_buf(op + t0 * p.H * p.dv, n_tok * p.H * p.dv * E);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    buf_store<T>(ob, fresh(ooff) + (unsigned)((rt * 16 + r) * p.H * p.dv) * E, from_f32<T>(Y[rt][r]));
+        }
+        zero = false;
+        if (t0 + kC >= len && (W == kStates || !p.hT)) break;  // nobody asks for the state after the last chunk
+        const float ec = rows->eg[kC - 1];
+        Parts<T, P> up[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const int r0 = kb * 32 + g4;
+            split<P>(U[2 * kb] * (four(rows->er + r0) * four(rows->rk + r0)),
+                     U[2 * kb + 1] * (four(rows->er + r0 + 16) * four(rows->rk + r0 + 16)), up[kb]);
+        }
+#pragma unroll
+        for (int d = 0; d < DK / 16; ++d) S[d] *= ec;
+        constexpr int kHalf = DK / 32;  // key tiles to a group
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            Frag<T> f[kHalf][2];
+#pragma unroll
+            for (int d = 0; d < kHalf; ++d)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) f[d][kb] = load_transposed<T>(ks + kb * 32 * Sh::KS + (half * kHalf + d) * 16, Sh::KS);
+            loads_end();
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int q = P - 1; q >= 0; --q)
+#pragma unroll
+                    for (int d = 0; d < kHalf; ++d) S[half * kHalf + d] = mma(f[d][kb], up[kb].p[q], S[half * kHalf + d]);
         }
     }
-    if (!p.hT) return;
+    if (W == kStates || !p.hT) return;
     const Buf sb = make_buf(p.hT + sbase, (int64_t)p.dk * p.dv * 4);
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d)
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) buf_store<float>(sb, fresh(soff[n]) + (unsigned)((d * 16 + r) * p.dv) * 4u, S[d][n][r]);
+        for (int r = 0; r < 4; ++r) buf_store<float>(sb, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u, S[d][r]);
 }
 
-template <typename T, int DK, int NC, int PS> hipError_t launch_delta_fwd_one(const DeltaParams& p, hipStream_t s) {
-    auto kern = delta_fwd_kernel<T, DK, NC, PS>;
-    constexpr int bytes = FwdLds<T, DK, PS>::bytes;
-    if (bytes > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != hipSuccess) return e;
-    }
-    const unsigned tiles = (p.dv + 64 * NC - 1) / (64 * NC), units = (unsigned)p.rows * p.H * tiles;
+// T, A and the row scalars of every chunk and head, a workgroup to each.
+template <typename T, int DK, int P>
+__global__ __launch_bounds__(kDeltaThreads, (WalkLds<T, DK, P>::groups)) void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) {
+    using L = WalkLds<T, DK, P>;
+    using Ops = ChunkOperands<T, P>;
+    constexpr int E = (int)sizeof(T);
+    extern __shared__ char lds[];
+    ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
+    T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs),
+      *as = reinterpret_cast<T*>(lds + L::as), *ts = reinterpret_cast<T*>(lds + L::ts);
+    const unsigned unit = die_local(blockIdx.x, units);
+    const int h = (int)(unit % (unsigned)p.H), hk = (int)((unsigned)h / (unsigned)p.share);
+    const unsigned sc = unit / (unsigned)p.H;
+    const int s = (int)(sc / chunks);
+    int64_t first;
+    int len;
+    delta_row(p, s, first, len);
+    const int64_t t0 = (int64_t)(sc - s * chunks) * kC;
+    if (t0 >= len) return;
+    const int64_t n = min((int64_t)kC, len - t0);
+    first += t0;
+    RowShare<T, DK> kr, qr;
+    kr.load(make_buf(static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
+    qr.load(make_buf(static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
+    const int64_t at = first * p.H + h;
+    build_chunk<T, DK, P, P>(kr, qr, p, static_cast<const T*>(p.g) + at, static_cast<const T*>(p.beta) + at, (int)n, rows,
+                             ks, qs, as, ts, [] {});
+    char* o = p.w_ops + ((int64_t)(chunk_entry(p, s, first - t0) + (unsigned)(t0 / kC)) * p.H + h) * Ops::bytes;
+    for (int u = threadIdx.x * 16; u < Ops::a; u += kDeltaThreads * 16) *reinterpret_cast<uint4*>(o + u) = *reinterpret_cast<const uint4*>(lds + u);
+    for (int u = threadIdx.x * 16; u < P * L::frag_bytes; u += kDeltaThreads * 16)
+        *reinterpret_cast<uint4*>(o + Ops::a + u) = *reinterpret_cast<const uint4*>(lds + L::as + u);
+}
+
+static_assert(ChunkOperands<float, 1>::bytes == 7 * kC * 4 + 2 * 6 * 64 * 8 * 4 &&
+              ChunkOperands<__bf16, 3>::bytes == 7 * kC * 4 + 2 * 6 * 64 * 8 * 2 * 3, "delta_operand_bytes");
+
+// dynamic LDS above the default limit has to be asked for
+template <typename K> hipError_t allow_lds(K kern, int bytes) {
+    if (bytes <= 64 * 1024) return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename T, int DK, int P, Walk W> hipError_t launch_walk(const DeltaParams& p, hipStream_t s) {
+    auto kern = delta_walk_kernel<T, DK, P, W>;
+    constexpr int bytes = WalkLds<T, DK, P>::bytes;
+    const hipError_t e = allow_lds(kern, bytes);
+    if (e != hipSuccess) return e;
+    const unsigned tiles = (p.dv + 63) / 64, units = (unsigned)p.rows * p.H * tiles;
     hipLaunchKernelGGL(kern, dim3(units), dim3(kDeltaThreads), bytes, s, p, tiles, units);
     return hipGetLastError();
+}
+
+template <typename T, int DK, int P> hipError_t launch_prepare(const DeltaParams& p, hipStream_t s) {
+    auto kern = delta_prepare_kernel<T, DK, P>;
+    constexpr int bytes = WalkLds<T, DK, P>::bytes;
+    const hipError_t e = allow_lds(kern, bytes);
+    if (e != hipSuccess) return e;
+    const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), units = (unsigned)p.rows * chunks * p.H;
+    hipLaunchKernelGGL(kern, dim3(units), dim3(kDeltaThreads), bytes, s, p, chunks, units);
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int P> hipError_t launch_forward(const DeltaParams& p, hipStream_t s) {
+    if (!p.w_ops) return launch_walk<T, DK, P, kWhole>(p, s);
+    const hipError_t e = launch_prepare<T, DK, P>(p, s);
+    return e != hipSuccess ? e : launch_walk<T, DK, P, kPrepared>(p, s);
 }
 
 }  // namespace sfm

@@ -4,7 +4,7 @@
 namespace sfm {
 
 hipError_t launch_delta_fwd_f32(const DeltaParams& p, hipStream_t s) {
-    return p.dk <= 64 ? launch_delta_fwd_one<float, 64, 1, 1>(p, s) : launch_delta_fwd_one<float, 128, 1, 1>(p, s);
+    return p.dk <= 64 ? launch_forward<float, 64, 1>(p, s) : launch_forward<float, 128, 1>(p, s);
 }
 
 }  // namespace sfm

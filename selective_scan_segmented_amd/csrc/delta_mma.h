@@ -26,6 +26,9 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 // this wave's number in its workgroup, known to the compiler as one value for all lanes
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// Operand loads above stay above: issued together, they are in flight while the instructions between run.
+__device__ __forceinline__ void loads_end() { __builtin_amdgcn_sched_barrier(0); }
+
 // ---------------------------------------------------------------- bounded memory
 // A run of device memory as a buffer: loads past its end give zero and stores there are dropped, so rows behind the
 // end of a chunk and columns behind a head's need no branch (a branch round every load makes them wait in turn).
@@ -41,6 +44,13 @@ __device__ __forceinline__ Buf make_buf(const void* p, int64_t bytes) {
 __device__ __forceinline__ unsigned fresh(unsigned v) {
     asm volatile("" : "+v"(v));
     return v;
+}
+// one element's bits in a register of its own (neighbours are not packed, which would wait for both), and its value
+template <typename T> __device__ __forceinline__ unsigned buf_load_bits(const Buf& b, unsigned at) {
+    if constexpr (sizeof(T) == 2)
+        return (unsigned)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(b.r, at, 0, 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b32(b.r, at, 0, 0);
 }
 template <typename T> __device__ __forceinline__ T buf_load(const Buf& b, unsigned at) {
     if constexpr (sizeof(T) == 2)
@@ -169,10 +179,23 @@ template <int P, typename T> __device__ __forceinline__ void store_tile(f32x4 x,
     }
 }
 
-// c[n] += a b[n] for NC column tiles, a given by its PA parts, b in PB: the products of parts that are not below
-// the last part of the finer operand, smallest first
-template <int PA, int PB, int NC, typename T>
-__device__ __forceinline__ void mma_parts(const Parts<T, PA>& a, const Parts<T, PB> (&b)[NC], f32x4 (&c)[NC]) {
+// c += a b, a given by its PA parts and b by its PB: the products of parts that are not below the last part of the
+// finer operand, smallest first
+template <int PA, int PB, typename T>
+__device__ __forceinline__ f32x4 mma_parts(const Parts<T, PA>& a, const Parts<T, PB>& b, f32x4 c) {
+    constexpr int top = PA > PB ? PA : PB;
+#pragma unroll
+    for (int p = PA - 1; p >= 0; --p)
+#pragma unroll
+        for (int q = PB - 1; q >= 0; --q)
+            if (p + q < top) c = mma(a.p[p], b.p[q], c);
+    return c;
+}
+
+// c[rt] += the step kb of 32 columns of a lower triangular operand (its fragments' parts) times b; products of like
+// size follow one another, so that no accumulator waits for itself
+template <int PA, int PB, typename T>
+__device__ __forceinline__ void mma_lower(const Parts<T, PA> (&a)[kLowerFrags], const Parts<T, PB>& b, int kb, f32x4 (&c)[4]) {
     constexpr int top = PA > PB ? PA : PB;
 #pragma unroll
     for (int p = PA - 1; p >= 0; --p)
@@ -180,7 +203,7 @@ __device__ __forceinline__ void mma_parts(const Parts<T, PA>& a, const Parts<T, 
         for (int q = PB - 1; q >= 0; --q)
             if (p + q < top)
 #pragma unroll
-                for (int n = 0; n < NC; ++n) c[n] = mma(a.p[p], b[n].p[q], c[n]);
+                for (int rt = 2 * kb; rt < 4; ++rt) c[rt] = mma(a[lower_frag(rt, kb)].p[p], b.p[q], c[rt]);
 }
 
 // parts of fragment `f` of a computed operand
@@ -190,6 +213,57 @@ template <int P, typename T> __device__ __forceinline__ Parts<T, P> load_parts(c
 #pragma unroll
     for (int q = 0; q < P; ++q) a.p[q] = Frag<T>::load(base + (q * kLowerFrags + f) * kFragSize + lane * 8);
     return a;
+}
+
+// The same of the operand's transpose: row tile jt, contraction over its rows 32 kb .. + 31; row tiles above the
+// diagonal (below jt) are zero.
+template <int P, typename T> __device__ __forceinline__ Parts<T, P> load_parts_transposed(const T* base, int jt, int kb) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
+    Parts<T, P> a;
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        const T* plane = base + q * kLowerFrags * kFragSize + (jt & 1) * 4;
+        if constexpr (sizeof(T) == 4) {
+            // column l16 of the tile lies with lanes 16 (l16 / 4) + row
+            auto get = [&](int it) {
+                f32x4 v = {0, 0, 0, 0};
+                if (it >= jt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = plane[lower_frag(it, jt >> 1) * kFragSize + ((l16 >> 2) * 16 + g4 + j) * 8 + (l16 & 3)];
+                return v;
+            };
+            a.p[q] = Frag<T>{get(2 * kb), get(2 * kb + 1)};
+        } else {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+            auto get = [&](int it) {
+                s16x4 v = {0, 0, 0, 0};
+                if (it >= jt)
+                    v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_ptr)(plane + lower_frag(it, jt >> 1) * kFragSize + ((l16 & 3) * 16 + g4 + (l16 >> 2)) * 8));
+                return v;
+            };
+            a.p[q].v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(get(2 * kb), get(2 * kb + 1), 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+    return a;
+}
+
+// halves of a fragment's parts as P planes of a [row][16-aligned run] array in memory: slots 0..3 go to `at`, 4..7 to
+// `at` + 16 elements (the next tile's rows)
+template <int P, typename T> __device__ __forceinline__ void store_planes(const Parts<T, P>& x, T* at, int64_t plane) {
+    typedef T quad __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<quad*>(at + q * plane) = x.p[q].lo;
+            *reinterpret_cast<quad*>(at + q * plane + 16) = x.p[q].hi;
+        } else {
+            *reinterpret_cast<quad*>(at + q * plane) = __builtin_shufflevector(x.p[q].v, x.p[q].v, 0, 1, 2, 3);
+            *reinterpret_cast<quad*>(at + q * plane + 16) = __builtin_shufflevector(x.p[q].v, x.p[q].v, 4, 5, 6, 7);
+        }
+    }
 }
 
 }  // namespace sfm

@@ -29,6 +29,16 @@ struct DeltaParams {
     int l2norm;
     int vec_k, vec_v;    // q and k (v) rows may be loaded 16 bytes at a time
     int vec_s;           // states likewise
+    // backward
+    const void* dout;    // [tokens][H][dv]
+    const float* dhT;    // [rows][H][dk][dv] or null (zero)
+    void *dq, *dk_, *dv_, *dg, *dbeta;
+    float* dh0;          // or null
+    // workspace: for every chunk (chunk_entry) and head
+    char* w_ops;         // ChunkOperands
+    char *w_s, *w_ds;    // states before the chunk and gradients of those after it, [parts][values][keys]
+    char *w_u, *w_dr;    // U and dR, [parts][values][64 tokens]
+    float *w_dq, *w_dk;  // [tokens][H][dk]: gradients by value head, where heads share keys
 };
 
 // first token and length of row s; offsets outside the tokens (a caller's mistake) are cut to them
@@ -51,6 +61,14 @@ constexpr float kDeltaNormEps = 1e-6f;
 // (the state's reset) then keeps the differences of a chunk's running sums finite.
 constexpr float kDeltaMinGate = -110.0f;
 
+// Workspace of the chunked forward in bytes: 0 where a chunk's T and A are made on the way (delta_fwd.h).
+int64_t plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dv, bool want_state, int io_dtype);
+// entries of the arrays that hold something for every chunk (chunk_entry): enough for packed and for equal rows
+inline int64_t delta_chunk_entries(int64_t rows, int64_t tokens) { return tokens / kDeltaChunk + rows; }
+// bytes of a chunk and head's prepared operands (ChunkOperands), P parts to bfloat16 ones
+inline int64_t delta_operand_bytes(int io_dtype, int parts) {
+    return 7 * kDeltaChunk * 4 + 2 * 6 * 64 * 8 * (io_dtype == 0 ? 4 : 2 * (int64_t)parts);
+}
 // chunked forward, one translation unit per io type
 hipError_t launch_delta_fwd_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_fwd_bf16(const DeltaParams& p, hipStream_t s);

@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cstdlib>
+
 #include "sfm_api_util.h"
 #include "sfm_delta.h"
 
@@ -91,6 +93,17 @@ sfm::DeltaParams params(const void* q, const void* k, const void* v, const void*
 
 }  // namespace
 
+// Few (row, head, column tile) workgroups walk long rows: the chunks' triangular inverses, which need no state, are
+// then made beforehand by the whole card (two launches) instead of inside the walk.
+// SFM_DELTA_WALK=whole|prepared overrides (tuning and tests).
+int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dv, bool want_state, int io_dtype) {
+    const int64_t chunks = (L + kDeltaChunk - 1) / kDeltaChunk;
+    if (rows * H > INT32_MAX / chunks) return 0;
+    bool prepared = chunks > 1 && rows * H * ((dv + 63) / 64) <= 1024;
+    if (const char* e = std::getenv("SFM_DELTA_WALK")) prepared = e[0] == 'p' || (e[0] != 'w' && prepared);
+    return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2) : 0;
+}
+
 extern "C" {
 
 sfm_status sfm_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -129,7 +142,7 @@ sfm_status sfm_gated_delta_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, 
     if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
     const sfm_status st = check_sizes(fn, rows, L, tokens, true, 1, H, dk, dv, io_dtype, 0);
     if (st != SFM_OK) return st;
-    *bytes = 0;
+    *bytes = L <= kRecurrentMax ? 0 : sfm::plan_delta_fwd(rows, L, tokens, H, dv, want_state != 0, io_dtype);
     return ok();
 }
 
@@ -173,6 +186,7 @@ sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
     }
     sfm::DeltaParams p = params(q, k, v, g, beta, rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
     p.h0 = h0, p.hT = hT, p.offsets = offsets, p.o = o;
+    p.w_ops = need > 0 ? static_cast<char*>(workspace) : nullptr;
     p.vec_s = dv % 4 == 0 && aligned16(h0) && aligned16(hT);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     if (L <= kRecurrentMax) return hip_status(sfm::launch_delta_recurrent(p, io_dtype, hs), fn);
