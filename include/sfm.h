@@ -389,6 +389,27 @@ sfm_status sfm_gated_delta_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, 
                                        int64_t dv, int want_state, int io_dtype, int64_t* bytes);
 
 /*
+ * sfm_gated_delta_bwd -- gradients of sfm_gated_delta_fwd (same inputs, sizes and
+ * flags) for the gradients dout [tokens, H, dv] io of o and dhT [rows, H, dk, dv]
+ * f32 (or NULL: zero) of the states after the rows.
+ *   dq, dk [tokens, Hk, dk], dv [tokens, H, dv], dg, dbeta [tokens, H] io, all
+ *   contiguous (dq, dk summed over the value heads of a key head, in order);
+ *   dh0 [rows, H, dk, dv] f32 or NULL (not wanted).  Tokens of no row keep their old
+ *   gradients.  workspace: at least sfm_gated_delta_bwd_ws_size() bytes (want_dh0:
+ *   dh0 != NULL), 16-byte aligned: for every 64 tokens of a row and head the states
+ *   before them, their gradients after them and what passes between them.  No
+ *   atomics: repeated calls give the same bits.
+ */
+sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                               const float* h0, const void* dout, const float* dhT, void* dq, void* dk_out,
+                               void* dv_out, void* dg, void* dbeta, float* dh0, const int32_t* offsets,
+                               int64_t rows, int64_t L, int64_t tokens, int64_t Hk, int64_t H, int64_t dk,
+                               int64_t dv, int64_t ldq, int64_t ldk, int64_t ldv, float scale, int io_dtype,
+                               int flags, void* workspace, int64_t workspace_bytes, void* stream);
+sfm_status sfm_gated_delta_bwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t Hk, int64_t H,
+                                       int64_t dk, int64_t dv, int want_dh0, int io_dtype, int64_t* bytes);
+
+/*
  * sfm_gated_delta_step -- one token of each of `rows` requests (serving): the
  * recurrence above on a pool of states, updated in place.
  *   q, k [rows, Hk, dk], v [rows, H, dv] io with strides as above; g, beta

@@ -20,7 +20,8 @@ __all__ = ["sfm_selective_scan_fwd", "sfm_selective_scan_fwd_ex", "sfm_selective
            "sfm_selective_scan_fwd_ws_size", "sfm_selective_scan_bwd",
            "sfm_selective_scan_bwd_workspace_size", "sfm_dwconv1d_fold", "sfm_aux_pad_swap", "sfm_aux_pad_bwd",
            "sfm_aux_pad_bwd_ex",
-           "sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_step", "sfm_group_norm_fwd",
+           "sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_bwd",
+           "sfm_gated_delta_bwd_ws_size", "sfm_gated_delta_step", "sfm_group_norm_fwd",
            "sfm_group_norm_bwd", "sfm_group_norm_ws_size",
            "sfm_pick_b1", "sfm_scan_plan_string", "sfm_version", "library_path", "load_library", "SFMError"]
 
@@ -81,7 +82,10 @@ def load_library():
     lib.sfm_group_norm_bwd.argtypes = [vp] * 9 + [i64] * 4 + [ci, ci, vp, i64, vp]
     lib.sfm_group_norm_fwd_ws_size.argtypes = [i64] * 4 + [ci, pi64]
     lib.sfm_group_norm_bwd_ws_size.argtypes = [i64] * 4 + [ci, ci, pi64]
-    for f in ("sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_step", "sfm_group_norm_fwd",
+    lib.sfm_gated_delta_bwd.argtypes = [vp] * 15 + [i64] * 10 + [f32, ci, ci, vp, i64, vp]
+    lib.sfm_gated_delta_bwd_ws_size.argtypes = [i64] * 7 + [ci, ci, pi64]
+    for f in ("sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_step", "sfm_gated_delta_bwd",
+              "sfm_gated_delta_bwd_ws_size", "sfm_group_norm_fwd",
               "sfm_group_norm_bwd", "sfm_group_norm_fwd_ws_size", "sfm_group_norm_bwd_ws_size"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("sfm_selective_scan_fwd", "sfm_selective_scan_fwd_ex", "sfm_selective_scan_fwd_ws",
@@ -522,6 +526,50 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "sfm_gated_delta_fwd")
     return (o, state) if return_state else o
+
+
+def sfm_gated_delta_bwd_ws_size(rows: int, L: int, tokens: int, Hk: int, H: int, dk: int, dv: int,
+                                want_dh0: bool = False, io: str = "bf16") -> int:
+    """Workspace bytes sfm_gated_delta_bwd needs (host only)."""
+    out = ctypes.c_int64(0)
+    _check(load_library().sfm_gated_delta_bwd_ws_size(rows, L, tokens, Hk, H, dk, dv, int(bool(want_dh0)),
+                                                      SFM_BF16 if io == "bf16" else SFM_F32, ctypes.byref(out)),
+           "sfm_gated_delta_bwd_ws_size")
+    return int(out.value)
+
+
+def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None, max_len=None, scale=None,
+                        l2norm=False, grads=None, workspace=None, stream=None):
+    """Gradients of sfm_gated_delta_fwd (same arguments) for do, the gradient of o, and dstate, that of the
+    states after the rows (float32, None: zero).  Returns a dict with dq, dk, dv, dg, dbeta and, with h0,
+    dh0 (float32); `grads` may hold preallocated tensors under those names."""
+    torch = _torch()
+    io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
+    rows, L, tokens = _rows(lead, offsets, max_len)
+    _dev(h0, "h0", torch.float32, (rows, H, dk, dv))
+    _dev(dstate, "dstate", torch.float32, (rows, H, dk, dv))
+    _dev(do, "do", q.dtype, lead + (H, dv))
+    out = dict(grads or {})
+    shapes = dict(dq=lead + (Hk, dk), dk=lead + (Hk, dk), dv=lead + (H, dv), dg=lead + (H,), dbeta=lead + (H,))
+    if h0 is not None:
+        shapes["dh0"] = (rows, H, dk, dv)
+    for name, shape in shapes.items():
+        dt = torch.float32 if name == "dh0" else q.dtype
+        if out.get(name) is None:
+            out[name] = _new(shape, dt, q.device, stream)
+        _dev(out[name], name, dt, shape)
+    need = sfm_gated_delta_bwd_ws_size(rows, L, tokens, Hk, H, dk, dv, h0 is not None, "bf16" if io else "f32")
+    if workspace is None:
+        workspace = _new(need, torch.uint8, q.device, stream)
+    _dev(workspace, "workspace")
+    rc = load_library().sfm_gated_delta_bwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(do), _ptr(dstate), _ptr(out["dq"]),
+        _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out.get("dh0")), _ptr(offsets),
+        rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, dk ** -0.5 if scale is None else scale, io,
+        SFM_DELTA_L2NORM if l2norm else 0, _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    _check(rc, "sfm_gated_delta_bwd")
+    return out
 
 
 def sfm_gated_delta_step(q, k, v, g, beta, state, slots=None, scale=None, l2norm=False, o=None, stream=None):

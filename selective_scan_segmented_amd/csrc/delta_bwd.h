@@ -1,0 +1,612 @@
+// delta_bwd.h -- the backward of the gated delta rule by chunks (kernels; one translation unit per io type).
+//
+// With the forward's names (delta_chunk.h; q' = scale q, both after their norm), dO given and dS' the gradient of
+// the state after the chunk:
+//     dU = A^T dO + e^(G_C - G) K dS',       dR = T^T dU,        dV = beta dR,
+//     dS0 = e^(G_C) dS' + Q'^T (e^G dO) - K^T (beta e^G dR),
+//     dA = lower part of dO U^T,             dM = -strictly lower part of dR U^T,
+//     dq' = e^G dO S0^T + (dA D) K,
+//     dk  = -beta e^G dR S0^T + e^(G_C - G) U dS'^T + (dA D)^T Q' + W K + W^T K,   W_ij = beta_i D_ij dM_ij,
+//     dbeta_i = dR_i.V_i - e^(G_i) k_i.(S0 dR_i) + sum_j dM_ij D_ij k_i.k_j,
+//     dG_i = sum_j (P_ij - P_ji) + e^(G_i) q'_i.(S0 dO_i) - beta_i e^(G_i) k_i.(S0 dR_i) - c_i,
+//         P = dA A + dM M,  c_i = e^(G_C - G_i) k_i.(dS' U_i),
+//     dG_C += sum_i c_i + e^(G_C) <S0, dS'>,    dg = sums of dG from the token to the chunk's end.
+// Four passes: the preparing kernel (T, A), the walk forward (states before the chunks, U), the walk back below
+// (dS', dR, dV, the state's gradient) and, a workgroup to every chunk and head, the rest.
+#pragma once
+
+#include "delta_fwd.h"
+
+namespace sfm {
+
+// The walk back: as delta_walk_kernel, a workgroup to a (row, head) and 64 columns, from the last chunk to the first.
+template <typename T, int DK, int P>
+__global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_reverse_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+    using Sh = ChunkShape<T, DK>;
+    using L = WalkLds<T, DK, P>;
+    using Ops = ChunkOperands<T, P>;
+    constexpr int PW = P < 2 ? P : 2;
+    constexpr int E = (int)sizeof(T);
+    extern __shared__ char lds[];
+    ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
+    T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs),
+      *as = reinterpret_cast<T*>(lds + L::as), *ts = reinterpret_cast<T*>(lds + L::ts);
+
+    const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
+    const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
+    const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
+    const int col = (int)(unit - rh * tiles) * 64 + wave * 16 + l16;
+    int64_t first;
+    int len;
+    delta_row(p, s, first, len);
+    const T* qp = static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk;
+    const T* kp = static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk;
+    const int64_t obase = (first * p.H + h) * p.dv, ldo = (int64_t)p.H * p.dv;
+    const T* gop = static_cast<const T*>(p.dout) + obase;
+    T* dvp = static_cast<T*>(p.dv_) + obase;
+    const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
+    const unsigned soff = col < p.dv ? (unsigned)(g4 * p.dv + col) * 4u : kNowhere;
+    const unsigned ooff = col < p.dv ? (unsigned)(g4 * ldo + col) * E : kNowhere;
+    const int64_t entry0 = (int64_t)chunk_entry(p, s, first) * p.H + h;
+    const int vals = (int)tiles * 64;
+
+    f32x4 dS[DK / 16];
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) dS[d] = f32x4{0, 0, 0, 0};
+    if (p.dhT) {
+        const Buf b = make_buf(p.dhT + sbase, (int64_t)p.dk * p.dv * 4);
+#pragma unroll
+        for (int d = 0; d < DK / 16; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dS[d][r] = buf_load<float>(b, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u);
+    }
+
+    RowShare<T, DK> kr, qr;
+    Linear<Ops::bytes> ops;
+    unsigned v[4][4];
+    auto fetch = [&](int c) {
+        const int64_t t0 = (int64_t)c * kC, n = min((int64_t)kC, len - t0);
+        kr.load(make_buf(kp + t0 * p.ldk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
+        qr.load(make_buf(qp + t0 * p.ldq, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
+        ops.load(p.w_ops + (entry0 + (int64_t)c * p.H) * Ops::bytes);
+        const Buf ob = make_buf(gop + t0 * ldo, n * ldo * E);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(ob, fresh(ooff) + (unsigned)((rt * 16 + r) * ldo) * E);
+    };
+    static_assert(L::as == Ops::a, "T and A lie in LDS as in the workspace");
+    int c = (len + kC - 1) / kC - 1;
+    if (c >= 0) fetch(c);
+
+    for (; c >= 0; --c) {
+        const int64_t t0 = (int64_t)c * kC, n_tok = min((int64_t)kC, len - t0), here = entry0 + (int64_t)c * p.H;
+        lds_barrier();  // the chunk after is done with LDS
+        kr.store(ks, nullptr, 0);
+        qr.store(qs, nullptr, 0);
+        ops.store(lds);
+        lds_barrier();
+        // dO as an operand and, by e^G q', for the state
+        Parts<T, 1> go[2];
+        f32x4 gov[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) gov[rt][r] = Io<T>::of_bits(v[rt][r]);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) split<1>(gov[2 * kb], gov[2 * kb + 1], go[kb]);  // (exact)
+        if (c > 0) fetch(c - 1);
+
+        f32x4 dU[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) dU[rt] = f32x4{0, 0, 0, 0};
+        {
+            Frag<T> fk[2][4];
+            auto load = [&](int kb) {
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) fk[kb & 1][rt] = load_runs<T>(ks + (rt * 16 + l16) * Sh::KS + kb * 32 + g4);
+            };
+            load(0);
+#pragma unroll
+            for (int kb = 0; kb < DK / 32; ++kb) {
+                if (kb + 1 < DK / 32) load(kb + 1);
+                loads_end();
+                Parts<T, P> sp;
+                split<P>(dS[2 * kb], dS[2 * kb + 1], sp);
+                store_planes<PW>(sp, reinterpret_cast<T*>(p.w_ds) + here * PW * vals * DK + (int64_t)col * DK + kb * 32 + g4, (int64_t)vals * DK);
+#pragma unroll
+                for (int q = P - 1; q >= 0; --q)
+#pragma unroll
+                    for (int rt = 0; rt < 4; ++rt) dU[rt] = mma(fk[kb & 1][rt], sp.p[q], dU[rt]);
+            }
+        }
+        {
+            Parts<T, P> at[kLowerFrags];
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+                for (int kb = jt / 2; kb < 2; ++kb) at[upper_frag(jt, kb)] = load_parts_transposed<P>(as, jt, kb);
+            loads_end();
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) dU[rt] *= four(rows->er + rt * 16 + g4) * four(rows->rk + rt * 16 + g4);
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) mma_upper<P, 1>(at, go[kb], kb, dU);
+        }
+        f32x4 dR[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) dR[rt] = f32x4{0, 0, 0, 0};
+        {
+            Parts<T, P> tt[kLowerFrags], up[2];
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+                for (int kb = jt / 2; kb < 2; ++kb) tt[upper_frag(jt, kb)] = load_parts_transposed<P>(ts, jt, kb);
+            loads_end();
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) split<P>(dU[2 * kb], dU[2 * kb + 1], up[kb]);
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) mma_upper<P, P>(tt, up[kb], kb, dR);
+        }
+        const Buf db = make_buf(dvp + t0 * ldo, n_tok * ldo * E);
+        Parts<T, P> wk[2], wq[2];
+        f32x4 wkv[4], wqv[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const f32x4 be = four(rows->beta + rt * 16 + g4), eg = four(rows->eg + rt * 16 + g4);
+            const f32x4 gv = be * dR[rt];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) buf_store<T>(db, fresh(ooff) + (unsigned)((rt * 16 + r) * ldo) * E, from_f32<T>(gv[r]));
+            wkv[rt] = gv * (-eg * four(rows->rk + rt * 16 + g4));
+            wqv[rt] = gov[rt] * (eg * four(rows->rq + rt * 16 + g4) * p.scale);
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            Parts<T, PW> rp;
+            split<PW>(dR[2 * kb], dR[2 * kb + 1], rp);
+            store_planes<PW>(rp, reinterpret_cast<T*>(p.w_dr) + here * PW * vals * kC + (int64_t)col * kC + kb * 32 + g4, (int64_t)vals * kC);
+        }
+        if (c == 0 && !p.dh0) break;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            split<P>(wkv[2 * kb], wkv[2 * kb + 1], wk[kb]);
+            split<P>(wqv[2 * kb], wqv[2 * kb + 1], wq[kb]);
+        }
+        const float ec = rows->eg[kC - 1];
+#pragma unroll
+        for (int d = 0; d < DK / 16; ++d) dS[d] *= ec;
+#pragma unroll
+        for (int d0 = 0; d0 < DK / 16; d0 += 2) {
+            Frag<T> fk[2][2], fq[2][2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    fk[d][kb] = load_transposed<T>(ks + kb * 32 * Sh::KS + (d0 + d) * 16, Sh::KS);
+                    fq[d][kb] = load_transposed<T>(qs + kb * 32 * Sh::KS + (d0 + d) * 16, Sh::KS);
+                }
+            loads_end();
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int q = P - 1; q >= 0; --q)
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        dS[d0 + d] = mma(fk[d][kb], wk[kb].p[q], dS[d0 + d]);
+                        dS[d0 + d] = mma(fq[d][kb], wq[kb].p[q], dS[d0 + d]);
+                    }
+        }
+    }
+    if (!p.dh0) return;
+    const Buf sb = make_buf(p.dh0 + sbase, (int64_t)p.dk * p.dv * 4);
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) buf_store<float>(sb, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u, dS[d][r]);
+}
+
+// ---------------------------------------------------------------- per chunk and head
+constexpr int kVals = 32;  // values to a step of the first phase
+
+template <typename T, int DK, int PW> struct GradLds {
+    using Sh = ChunkShape<T, DK>;
+    static constexpr int E = (int)sizeof(T);
+    static constexpr int VS = ChunkShape<T, kVals>::KS;    // pitch of [token][value]
+    static constexpr int TS = kC + 16 / E;                 // pitch of [value][token]
+    static constexpr int rows = 0;
+    static constexpr int sums = (int)sizeof(ChunkRows);    // float arrays [64]: see Sums
+    static constexpr int work = sums + 11 * kC * 4;
+    // first phase
+    static constexpr int go = work, v = go + kC * VS * E, u = v + kC * VS * E, dr = u + PW * kVals * TS * E,
+                         s0 = dr + PW * kVals * TS * E, ds = s0 + PW * kVals * Sh::KS * E, end1 = ds + PW * kVals * Sh::KS * E;
+    // second phase
+    static constexpr int ks = work, qs = ks + Sh::row_bytes, x = qs + Sh::row_bytes,
+                         w = x + PW * kLowerFrags * kFragSize * E, end2 = w + PW * kLowerFrags * kFragSize * E;
+    static constexpr int bytes = end1 > end2 ? end1 : end2;
+};
+
+// Planes [PW][kVals rows][LEN] of the workspace, `plane` elements apart: through registers into LDS of pitch PITCH.
+template <typename T, int PW, int LEN, int PITCH> struct PlaneBlock {
+    static constexpr int per = 16 / (int)sizeof(T), kRow = LEN / per, kUnits = kVals * kRow / kDeltaThreads;
+    static_assert(kUnits * kDeltaThreads == kVals * kRow, "whole units to a thread");
+    typedef T piece __attribute__((ext_vector_type(per)));
+    piece x[PW][kUnits];
+    __device__ __forceinline__ void load(const T* p, int64_t plane) {
+#pragma unroll
+        for (int q = 0; q < PW; ++q)
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i)
+                x[q][i] = *reinterpret_cast<const piece*>(p + q * plane + (threadIdx.x + i * kDeltaThreads) * per);
+    }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int q = 0; q < PW; ++q)
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int u = threadIdx.x + i * kDeltaThreads;
+                *reinterpret_cast<piece*>(p + (q * kVals + u / kRow) * PITCH + u % kRow * per) = x[q][i];
+            }
+    }
+    __device__ __forceinline__ float value(int i, int e) const {
+        float v = 0.0f;
+#pragma unroll
+        for (int q = PW - 1; q >= 0; --q) v += to_f32((T)x[q][i][e]);
+        return v;
+    }
+};
+
+// parts of rows 16 tile .. + 15 of a [value][row] block, contraction over its 32 values
+template <int PW, typename T> __device__ __forceinline__ Parts<T, PW> load_block(const T* p, int tile, int pitch) {
+    Parts<T, PW> a;
+#pragma unroll
+    for (int q = 0; q < PW; ++q) a.p[q] = load_transposed<T>(p + q * kVals * pitch + tile * 16, pitch);
+    return a;
+}
+
+// c += a b for single accumulators (mma_parts with no waits between like products is the caller's order)
+template <int PA, int PB, int N, typename T>
+__device__ __forceinline__ void mma_all(const Parts<T, PA>& a, const Parts<T, PB> (&b)[N], f32x4* c) {
+    constexpr int top = PA > PB ? PA : PB;
+#pragma unroll
+    for (int p = PA - 1; p >= 0; --p)
+#pragma unroll
+        for (int q = PB - 1; q >= 0; --q)
+            if (p + q < top)
+#pragma unroll
+                for (int n = 0; n < N; ++n) c[n] = mma(a.p[p], b[n].p[q], c[n]);
+}
+
+// A workgroup to every chunk and head, sixteen tokens to a wave.  First phase: the products over values (with S0,
+// dS', U, dR of the workspace), 32 values at a time; second: those over tokens (with K and Q).
+template <typename T, int DK, int PW>
+__global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)) void delta_grads_kernel(const DeltaParams p, unsigned chunks, unsigned units, int ops_bytes) {
+    using Sh = ChunkShape<T, DK>;
+    using L = GradLds<T, DK, PW>;
+    constexpr int E = (int)sizeof(T), ND = DK / 16;
+    extern __shared__ char lds[];
+    ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
+    float* sums = reinterpret_cast<float*>(lds + L::sums);
+    // by token: P's row sums, the other terms of dG, c, dbeta's two halves, dR.V; P's column sums by wave; <S0, dS'>
+    float *row_p = sums, *row_o = sums + kC, *row_c = sums + 2 * kC, *row_b = sums + 3 * kC, *row_e = sums + 4 * kC,
+          *row_v = sums + 5 * kC, *col_p = sums + 6 * kC, *frob = sums + 10 * kC;
+    const unsigned unit = die_local(blockIdx.x, units);
+    const int h = (int)(unit % (unsigned)p.H), hk = (int)((unsigned)h / (unsigned)p.share);
+    const unsigned sc = unit / (unsigned)p.H;
+    const int s = (int)(sc / chunks);
+    int64_t first;
+    int len;
+    delta_row(p, s, first, len);
+    const int chunk = (int)(sc - s * chunks);
+    const int64_t t0 = (int64_t)chunk * kC;
+    if (t0 >= len) return;
+    const int64_t n = min((int64_t)kC, len - t0), tok = first + t0, entry = (int64_t)(chunk_entry(p, s, first) + chunk) * p.H + h;
+    const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
+    const int vals = (p.dv + 63) / 64 * 64;
+
+    RowShare<T, DK> kr, qr;
+    kr.load(make_buf(static_cast<const T*>(p.k) + tok * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
+    qr.load(make_buf(static_cast<const T*>(p.q) + tok * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
+    {
+        Linear<(int)sizeof(ChunkRows)> r;
+        r.load(p.w_ops + entry * ops_bytes);
+        r.store(lds);
+    }
+    col_p[threadIdx.x] = 0.0f;
+
+    f32x4 dq[ND], dkr[ND], dku[ND], da[4], dm[4], rv = {0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < ND; ++d) dq[d] = dkr[d] = dku[d] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) da[j] = dm[j] = f32x4{0, 0, 0, 0};
+    float fr = 0.0f;
+    {
+        T *gs = reinterpret_cast<T*>(lds + L::go), *vs = reinterpret_cast<T*>(lds + L::v), *us = reinterpret_cast<T*>(lds + L::u),
+          *rs = reinterpret_cast<T*>(lds + L::dr), *s0 = reinterpret_cast<T*>(lds + L::s0), *ds = reinterpret_cast<T*>(lds + L::ds);
+        const T* ws = reinterpret_cast<const T*>(p.w_s) + entry * PW * vals * DK;
+        const T* wd = reinterpret_cast<const T*>(p.w_ds) + entry * PW * vals * DK;
+        const T* wu = reinterpret_cast<const T*>(p.w_u) + entry * PW * vals * kC;
+        const T* wr = reinterpret_cast<const T*>(p.w_dr) + entry * PW * vals * kC;
+        const T* gop = static_cast<const T*>(p.dout) + (tok * p.H + h) * p.dv;
+        const T* vp = static_cast<const T*>(p.v) + tok * p.ldv + (int64_t)h * p.dv;
+        RowShare<T, kVals> gr, vr;
+        PlaneBlock<T, PW, DK, Sh::KS> bs, bd;
+        PlaneBlock<T, PW, kC, L::TS> bu, br;
+        auto fetch = [&](int v0) {
+            gr.load(make_buf(gop + v0, n * p.H * p.dv * E - v0 * E), (int64_t)p.H * p.dv, p.dv - v0, p.vec_o);
+            vr.load(make_buf(vp + v0, n * p.ldv * E - v0 * E), p.ldv, p.dv - v0, p.vec_v);
+            bs.load(ws + (int64_t)v0 * DK, (int64_t)vals * DK);
+            bd.load(wd + (int64_t)v0 * DK, (int64_t)vals * DK);
+            bu.load(wu + (int64_t)v0 * kC, (int64_t)vals * kC);
+            br.load(wr + (int64_t)v0 * kC, (int64_t)vals * kC);
+        };
+        fetch(0);
+        for (int v0 = 0; v0 < p.dv; v0 += kVals) {
+            lds_barrier();
+            gr.store(gs, nullptr, 0);
+            vr.store(vs, nullptr, 0);
+            bs.store(s0);
+            bd.store(ds);
+            bu.store(us);
+            br.store(rs);
+#pragma unroll
+            for (int i = 0; i < bs.kUnits; ++i)
+#pragma unroll
+                for (int e = 0; e < bs.per; ++e) fr = __builtin_fmaf(bs.value(i, e), bd.value(i, e), fr);
+            lds_barrier();
+            if (v0 + kVals < p.dv) fetch(v0 + kVals);
+            const Parts<T, 1> fg[1] = {{load_runs<T>(gs + (wave * 16 + l16) * L::VS + g4)}};
+            const Parts<T, 1> fv[1] = {{load_runs<T>(vs + (wave * 16 + l16) * L::VS + g4)}};
+            const Parts<T, PW> fr_[1] = {load_block<PW>(rs, wave, L::TS)}, fu = load_block<PW>(us, wave, L::TS);
+            loads_end();
+            mma_all<PW, 1>(fr_[0], fv, &rv);
+#pragma unroll
+            for (int d0 = 0; d0 < ND; d0 += 2) {
+                Parts<T, PW> fs[2], fd[2];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    fs[d] = load_block<PW>(s0, d0 + d, Sh::KS);
+                    fd[d] = load_block<PW>(ds, d0 + d, Sh::KS);
+                }
+                loads_end();
+                mma_all<1, PW>(fg[0], fs, dq + d0);
+                mma_all<PW, PW>(fr_[0], fs, dkr + d0);
+                mma_all<PW, PW>(fu, fd, dku + d0);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= wave) {
+                    const Parts<T, PW> uj = load_block<PW>(us, j, L::TS);
+                    mma_all<PW, 1>(uj, fg, da + j);
+                    mma_all<PW, PW>(uj, fr_, dm + j);
+                }
+        }
+    }
+    // <S0, dS'> of this wave, and dR.V: the diagonal of the product
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) fr += __shfl_xor(fr, m);
+    if (lane == 0) frob[wave] = fr;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (g4 + r == l16) row_v[wave * 16 + l16] = rv[r];
+
+    T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs), *xs = reinterpret_cast<T*>(lds + L::x),
+      *wsm = reinterpret_cast<T*>(lds + L::w);
+    lds_barrier();  // the first phase's arrays are done with
+    kr.store(ks, nullptr, 0);
+    qr.store(qs, nullptr, 0);
+    lds_barrier();
+
+    // rows 16 wave + g4 .. + 3: the state's shares of dq', dk, dG and dbeta
+    const int i0 = wave * 16 + g4;
+    const f32x4 eg = four(rows->eg + i0), er = four(rows->er + i0), be = four(rows->beta + i0), rk = four(rows->rk + i0),
+                rq = four(rows->rq + i0);
+    {
+        f32x4 sa = {0, 0, 0, 0}, se = sa, sk = sa;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float kv = to_f32(ks[(i0 + r) * Sh::KS + d * 16 + l16]), qv = to_f32(qs[(i0 + r) * Sh::KS + d * 16 + l16]);
+                dq[d][r] *= eg[r];
+                dkr[d][r] *= eg[r];
+                dku[d][r] *= er[r];
+                sa[r] = __builtin_fmaf(qv, dq[d][r], sa[r]);
+                se[r] = __builtin_fmaf(kv, dkr[d][r], se[r]);
+                sk[r] = __builtin_fmaf(kv, dku[d][r], sk[r]);
+                dku[d][r] = __builtin_fmaf(-be[r], dkr[d][r], dku[d][r]);
+            }
+        f32x4 o, e, cc;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            e[r] = lanes_sum<16>(se[r]) * rk[r];
+            cc[r] = lanes_sum<16>(sk[r]) * rk[r];
+            o[r] = lanes_sum<16>(sa[r]) * (rq[r] * p.scale) - be[r] * e[r] - cc[r];
+        }
+        if (l16 == 0) {
+            *reinterpret_cast<f32x4*>(row_o + i0) = o;
+            *reinterpret_cast<f32x4*>(row_e + i0) = e;
+            *reinterpret_cast<f32x4*>(row_c + i0) = cc;
+        }
+    }
+    f32x4(&dk)[ND] = dku;
+
+    // the chunk's own products, tile by tile: column i = 16 wave + l16 of the lane, rows j = 16 tj + g4 .. + 3
+    f32x4 xl[4], wl[4];
+    {
+        const int i = wave * 16 + l16;
+        const float hi = rows->ghi[i], lo = rows->glo[i], qi = rows->rq[i] * p.scale, ki = rows->rk[i], bi = rows->beta[i];
+        float sp = 0.0f, sb = 0.0f;
+#pragma unroll
+        for (int tj = 0; tj < 4; ++tj) {
+            xl[tj] = wl[tj] = f32x4{0, 0, 0, 0};
+            if (tj > wave) continue;
+            const f32x4 qk = rows_product<T, DK>(ks, tj, qs, wave), kk = rows_product<T, DK>(ks, tj, ks, wave);
+            const int j0 = tj * 16 + g4;
+            const f32x4 hj = four(rows->ghi + j0), lj = four(rows->glo + j0), kj = four(rows->rk + j0);
+            f32x4 pc, xi, wi;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float d = exp2_fast((hi - hj[r]) + (lo - lj[r]));
+                const float x = j0 + r <= i ? da[tj][r] * d : 0.0f;
+                const float y = j0 + r < i ? -dm[tj][r] * d : 0.0f;
+                const float yk = y * (ki * kj[r] * kk[r]);
+                pc[r] = __builtin_fmaf(x, qi * kj[r] * qk[r], bi * yk);
+                sp += pc[r];
+                sb += yk;
+                xl[tj][r] = x * kj[r];
+                wl[tj][r] = y * (bi * kj[r]);
+                xi[r] = x * qi;
+                wi[r] = y * (bi * ki);
+            }
+            store_tile<PW>(xi, xs, wave, tj);
+            store_tile<PW>(wi, wsm, wave, tj);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pc[r] = lanes_sum<16>(pc[r]);
+            if (l16 == 0) *reinterpret_cast<f32x4*>(col_p + wave * kC + j0) = pc;
+        }
+        sp += __shfl_xor(sp, 16);
+        sb += __shfl_xor(sb, 16);
+        sp += __shfl_xor(sp, 32);
+        sb += __shfl_xor(sb, 32);
+        if (lane < 16) {
+            row_p[i] = sp;
+            row_b[i] = sb;
+        }
+    }
+    lds_barrier();
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+        const bool low = kb <= wave / 2, up = kb >= wave / 2;
+        Parts<T, PW> xp, wp, xt, wt;
+        split<PW>(xl[2 * kb], xl[2 * kb + 1], xp);
+        split<PW>(wl[2 * kb], wl[2 * kb + 1], wp);
+        if (up) {
+            xt = load_parts_transposed<PW>(xs, wave, kb);
+            wt = load_parts_transposed<PW>(wsm, wave, kb);
+        }
+#pragma unroll
+        for (int d0 = 0; d0 < ND; d0 += 2) {
+            Parts<T, 1> fk[2], fq[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                fk[d].p[0] = load_transposed<T>(ks + kb * 32 * Sh::KS + (d0 + d) * 16, Sh::KS);
+                fq[d].p[0] = load_transposed<T>(qs + kb * 32 * Sh::KS + (d0 + d) * 16, Sh::KS);
+            }
+            loads_end();
+            if (low) {
+                mma_all<PW, 1>(xp, fk, dq + d0);
+                mma_all<PW, 1>(wp, fk, dk + d0);
+            }
+            if (up) {
+                mma_all<PW, 1>(xt, fq, dk + d0);
+                mma_all<PW, 1>(wt, fk, dk + d0);
+            }
+        }
+    }
+    // Through the norms, and out: the unit vector's gradient less its part along the vector.  A head of one key is
+    // all along; what is left of it, eps / (x^2 + eps), is taken as such (the difference would have no digits).
+    f32x4 tq = {0, 0, 0, 0}, tk = tq, fq = rq * p.scale, fk = rk;
+    if (p.l2norm && p.dk == 1) {
+        fq *= rq * rq * kDeltaNormEps;
+        fk *= rk * rk * kDeltaNormEps;
+    } else if (p.l2norm) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                tq[r] = __builtin_fmaf(to_f32(qs[(i0 + r) * Sh::KS + d * 16 + l16]), dq[d][r], tq[r]);
+                tk[r] = __builtin_fmaf(to_f32(ks[(i0 + r) * Sh::KS + d * 16 + l16]), dk[d][r], tk[r]);
+            }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            tq[r] = lanes_sum<16>(tq[r]) * (rq[r] * rq[r]);
+            tk[r] = lanes_sum<16>(tk[r]) * (rk[r] * rk[r]);
+        }
+    }
+    const bool shared = p.share > 1;
+    const int heads = shared ? p.H : p.Hk, head = shared ? h : hk, size = shared ? 4 : E;
+    const int64_t ld = (int64_t)heads * p.dk, base = tok * ld + (int64_t)head * p.dk;
+    const Buf bq = shared ? make_buf(p.w_dq + base, n * ld * 4) : make_buf(static_cast<T*>(p.dq) + base, n * ld * E);
+    const Buf bk = shared ? make_buf(p.w_dk + base, n * ld * 4) : make_buf(static_cast<T*>(p.dk_) + base, n * ld * E);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        const int c = d * 16 + l16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const unsigned at = c < p.dk ? (unsigned)((i0 + r) * ld + c) * (unsigned)size : kNowhere;
+            const float kv = to_f32(ks[(i0 + r) * Sh::KS + c]), qv = to_f32(qs[(i0 + r) * Sh::KS + c]);
+            const float gq = fq[r] * __builtin_fmaf(-qv, tq[r], dq[d][r]);
+            const float gk = fk[r] * __builtin_fmaf(-kv, tk[r], dk[d][r]);
+            if (shared) {
+                buf_store<float>(bq, at, gq);
+                buf_store<float>(bk, at, gk);
+            } else {
+                buf_store<T>(bq, at, from_f32<T>(gq));
+                buf_store<T>(bk, at, from_f32<T>(gk));
+            }
+        }
+    }
+    if (wave != 0) return;
+    // dg: a lane to a token, sums from the chunk's end
+    float x = row_p[lane] + row_o[lane] - ((col_p[lane] + col_p[kC + lane]) + (col_p[2 * kC + lane] + col_p[3 * kC + lane]));
+    float all = row_c[lane];
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m);
+    all += rows->eg[kC - 1] * ((frob[0] + frob[1]) + (frob[2] + frob[3]));
+    if (lane == 63) x += all;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const float o = __shfl_down(x, m);
+        if (lane + m < 64) x += o;
+    }
+    if (lane < n) {
+        const int64_t at = (tok + lane) * p.H + h;
+        static_cast<T*>(p.dg)[at] = from_f32<T>(x);
+        static_cast<T*>(p.dbeta)[at] = from_f32<T>(row_v[lane] - row_e[lane] + row_b[lane]);
+    }
+}
+
+// Shared key heads: the value heads' shares, in order.  A workgroup to every chunk of a row.
+template <typename T>
+__global__ __launch_bounds__(kDeltaThreads) void delta_share_kernel(const DeltaParams p, unsigned chunks) {
+    const int s = (int)(blockIdx.x / chunks);
+    int64_t first;
+    int len;
+    delta_row(p, s, first, len);
+    const int64_t t0 = (int64_t)(blockIdx.x - s * chunks) * kC;
+    if (t0 >= len) return;
+    const int n = (int)min((int64_t)kC, len - t0), width = p.Hk * p.dk;
+    for (int i = threadIdx.x; i < n * width; i += kDeltaThreads) {
+        const int t = i / width, c = i - t * width, hk = c / p.dk;
+        const int64_t tok = first + t0 + t, from = (tok * p.H + (int64_t)hk * p.share) * p.dk + (c - hk * p.dk);
+        float a = 0.0f, b = 0.0f;
+        for (int j = 0; j < p.share; ++j) {
+            a += p.w_dq[from + (int64_t)j * p.dk];
+            b += p.w_dk[from + (int64_t)j * p.dk];
+        }
+        static_cast<T*>(p.dq)[tok * width + c] = from_f32<T>(a);
+        static_cast<T*>(p.dk_)[tok * width + c] = from_f32<T>(b);
+    }
+}
+
+template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParams& p, hipStream_t s) {
+    constexpr int PW = P < 2 ? P : 2;
+    hipError_t e = launch_prepare<T, DK, P>(p, s);
+    if (e != hipSuccess) return e;
+    e = launch_walk<T, DK, P, kStates>(p, s);
+    if (e != hipSuccess) return e;
+    const unsigned tiles = (p.dv + 63) / 64, units = (unsigned)p.rows * p.H * tiles;
+    auto rev = delta_reverse_kernel<T, DK, P>;
+    constexpr int rb = WalkLds<T, DK, P>::bytes, gb = GradLds<T, DK, PW>::bytes;
+    if ((e = allow_lds(rev, rb)) != hipSuccess) return e;
+    hipLaunchKernelGGL(rev, dim3(units), dim3(kDeltaThreads), rb, s, p, tiles, units);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), cu = (unsigned)p.rows * chunks * p.H;
+    auto grads = delta_grads_kernel<T, DK, PW>;
+    if ((e = allow_lds(grads, gb)) != hipSuccess) return e;
+    hipLaunchKernelGGL(grads, dim3(cu), dim3(kDeltaThreads), gb, s, p, chunks, cu, ChunkOperands<T, P>::bytes);
+    if ((e = hipGetLastError()) != hipSuccess || p.share == 1) return e;
+    hipLaunchKernelGGL(delta_share_kernel<T>, dim3((unsigned)p.rows * chunks), dim3(kDeltaThreads), 0, s, p, chunks);
+    return hipGetLastError();
+}
+
+}  // namespace sfm

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
                     Parts<T, P> sp;
                     split<P>(S[2 * kb], S[2 * kb + 1], sp);
                     if constexpr (W == kStates)
-                        store_planes<P>(sp, reinterpret_cast<T*>(p.w_s) + here * P * vals * DK + (int64_t)col * DK + kb * 32 + g4,
+                        store_planes<PY>(sp, reinterpret_cast<T*>(p.w_s) + here * PY * vals * DK + (int64_t)col * DK + kb * 32 + g4,
                                         (int64_t)vals * DK);
 #pragma unroll
                     for (int q = P - 1; q >= 0; --q)
@@ -170,9 +170,9 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
         if constexpr (W == kStates) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                Parts<T, P> up;
-                split<P>(U[2 * kb], U[2 * kb + 1], up);
-                store_planes<P>(up, reinterpret_cast<T*>(p.w_u) + here * P * vals * kC + (int64_t)col * kC + kb * 32 + g4, (int64_t)vals * kC);
+                Parts<T, PY> up;
+                split<PY>(U[2 * kb], U[2 * kb + 1], up);
+                store_planes<PY>(up, reinterpret_cast<T*>(p.w_u) + here * PY * vals * kC + (int64_t)col * kC + kb * 32 + g4, (int64_t)vals * kC);
             }
         } else {
             Parts<T, PY> ap[kLowerFrags], up[2];

@@ -206,6 +206,20 @@ __device__ __forceinline__ void mma_lower(const Parts<T, PA> (&a)[kLowerFrags], 
                 for (int rt = 2 * kb; rt < 4; ++rt) c[rt] = mma(a[lower_frag(rt, kb)].p[p], b.p[q], c[rt]);
 }
 
+// likewise with the transpose of a lower triangular operand (upper_frag's order)
+__device__ __forceinline__ constexpr int upper_frag(int jt, int kb) { return jt < 2 ? 2 * jt + kb : jt + 2; }
+template <int PA, int PB, typename T>
+__device__ __forceinline__ void mma_upper(const Parts<T, PA> (&a)[kLowerFrags], const Parts<T, PB>& b, int kb, f32x4 (&c)[4]) {
+    constexpr int top = PA > PB ? PA : PB;
+#pragma unroll
+    for (int p = PA - 1; p >= 0; --p)
+#pragma unroll
+        for (int q = PB - 1; q >= 0; --q)
+            if (p + q < top)
+#pragma unroll
+                for (int jt = 0; jt < 2 * kb + 2; ++jt) c[jt] = mma(a[upper_frag(jt, kb)].p[p], b.p[q], c[jt]);
+}
+
 // parts of fragment `f` of a computed operand
 template <int P, typename T> __device__ __forceinline__ Parts<T, P> load_parts(const T* base, int f) {
     const int lane = threadIdx.x & 63;
@@ -250,12 +264,12 @@ template <int P, typename T> __device__ __forceinline__ Parts<T, P> load_parts_t
     return a;
 }
 
-// halves of a fragment's parts as P planes of a [row][16-aligned run] array in memory: slots 0..3 go to `at`, 4..7 to
-// `at` + 16 elements (the next tile's rows)
-template <int P, typename T> __device__ __forceinline__ void store_planes(const Parts<T, P>& x, T* at, int64_t plane) {
+// the first PW of a fragment's parts as planes of a [row][16-aligned run] array in memory: slots 0..3 go to `at`,
+// 4..7 to `at` + 16 elements (the next tile's rows)
+template <int PW, int P, typename T> __device__ __forceinline__ void store_planes(const Parts<T, P>& x, T* at, int64_t plane) {
     typedef T quad __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int q = 0; q < P; ++q) {
+    for (int q = 0; q < PW; ++q) {
         if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<quad*>(at + q * plane) = x.p[q].lo;
             *reinterpret_cast<quad*>(at + q * plane + 16) = x.p[q].hi;

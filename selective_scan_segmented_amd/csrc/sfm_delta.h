@@ -29,6 +29,7 @@ struct DeltaParams {
     int l2norm;
     int vec_k, vec_v;    // q and k (v) rows may be loaded 16 bytes at a time
     int vec_s;           // states likewise
+    int vec_o;           // dout likewise
     // backward
     const void* dout;    // [tokens][H][dv]
     const float* dhT;    // [rows][H][dk][dv] or null (zero)
@@ -72,6 +73,8 @@ inline int64_t delta_operand_bytes(int io_dtype, int parts) {
 // chunked forward, one translation unit per io type
 hipError_t launch_delta_fwd_f32(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_fwd_bf16(const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_bwd_f32(const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_bwd_bf16(const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_recurrent(const DeltaParams& p, int io_dtype, hipStream_t s);
 
 }  // namespace sfm

@@ -54,7 +54,7 @@ sfm_status check_inputs(const char* fn, const void* q, const void* k, const void
 constexpr int64_t kRecurrentMax = 4;
 
 struct Ranges {
-    Range ins[8];
+    Range ins[10];
     int n = 0;
     void add(const char* name, const void* p, int64_t bytes) {
         if (p && bytes > 0) ins[n++] = rng(name, p, bytes);
@@ -191,6 +191,100 @@ sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     if (L <= kRecurrentMax) return hip_status(sfm::launch_delta_recurrent(p, io_dtype, hs), fn);
     return hip_status(io_dtype == SFM_F32 ? sfm::launch_delta_fwd_f32(p, hs) : sfm::launch_delta_fwd_bf16(p, hs), fn);
+}
+
+// Workspace regions of the backward, each on 256 bytes.
+struct BwdRegions {
+    int64_t ops, s, ds, u, dr, dq, dk, bytes;
+};
+
+static BwdRegions bwd_regions(int64_t rows, int64_t tokens, int64_t H, bool shared, int64_t dk, int64_t dv, bool want_dh0,
+                              int io_dtype) {
+    const int64_t e = io_bytes(io_dtype), units = sfm::delta_chunk_entries(rows, tokens) * H;
+    const int64_t vals = (dv + 63) / 64 * 64, keys = dk <= 64 ? 64 : 128, planes = io_dtype == SFM_F32 ? 1 : 2;
+    BwdRegions r{};
+    int64_t at = 0;
+    auto take = [&](int64_t n) {
+        const int64_t here = at;
+        at += (n + 255) / 256 * 256;
+        return here;
+    };
+    r.ops = take(units * sfm::delta_operand_bytes(io_dtype, want_dh0 ? 3 : 2));
+    r.s = take(units * planes * vals * keys * e);
+    r.ds = take(units * planes * vals * keys * e);
+    r.u = take(units * planes * vals * sfm::kDeltaChunk * e);
+    r.dr = take(units * planes * vals * sfm::kDeltaChunk * e);
+    r.dq = take(shared ? tokens * H * dk * 4 : 0);
+    r.dk = take(shared ? tokens * H * dk * 4 : 0);
+    r.bytes = at;
+    return r;
+}
+
+sfm_status sfm_gated_delta_bwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t Hk, int64_t H, int64_t dk,
+                                       int64_t dv, int want_dh0, int io_dtype, int64_t* bytes) {
+    static const char* fn = "sfm_gated_delta_bwd_ws_size";
+    if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
+    const sfm_status st = check_sizes(fn, rows, L, tokens, true, Hk, H, dk, dv, io_dtype, 0);
+    if (st != SFM_OK) return st;
+    *bytes = bwd_regions(rows, tokens, H, H != Hk, dk, dv, want_dh0 != 0, io_dtype).bytes;
+    return ok();
+}
+
+sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                               const float* h0, const void* dout, const float* dhT, void* dq, void* dk_out,
+                               void* dv_out, void* dg, void* dbeta, float* dh0, const int32_t* offsets, int64_t rows,
+                               int64_t L, int64_t tokens, int64_t Hk, int64_t H, int64_t dk, int64_t dv, int64_t ldq,
+                               int64_t ldk, int64_t ldv, float scale, int io_dtype, int flags, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+    static const char* fn = "sfm_gated_delta_bwd";
+    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, Hk, H, dk, dv, io_dtype, flags);
+    if (st != SFM_OK) return st;
+    st = check_inputs(fn, q, k, v, g, beta, tokens, Hk, H, dk, dv, ldq, ldk, ldv, io_dtype);
+    if (st != SFM_OK) return st;
+    if (tokens > 0 && (!dout || !dq || !dk_out || !dv_out || !dg || !dbeta))
+        return fail(SFM_ERR_NULL, "%s: dout, dq, dk, dv, dg and dbeta are required", fn);
+    if (rows * H > INT32_MAX / ((L + sfm::kDeltaChunk - 1) / sfm::kDeltaChunk))
+        return fail(SFM_ERR_SHAPE, "%s: too many chunks", fn);
+    const int e = io_bytes(io_dtype);
+    for (const void* x : {(const void*)dout, (const void*)dq, (const void*)dk_out, (const void*)dv_out, (const void*)dg,
+                          (const void*)dbeta})
+        if (!aligned_to(x, e)) return fail(SFM_ERR_ALIGN, "%s: a gradient is not aligned to its element", fn);
+    if (!aligned_to(h0, 4) || !aligned_to(dhT, 4) || !aligned_to(dh0, 4) || !aligned_to(offsets, 4))
+        return fail(SFM_ERR_ALIGN, "%s: h0, dhT, dh0 or offsets not aligned to its element", fn);
+    const BwdRegions w = bwd_regions(rows, tokens, H, H != Hk, dk, dv, dh0 != nullptr, io_dtype);
+    if (!workspace || workspace_bytes < w.bytes)
+        return fail(SFM_ERR_SHAPE, "%s: workspace of %lld bytes needed, %lld given", fn, (long long)w.bytes,
+                    (long long)(workspace ? workspace_bytes : 0));
+    if (!aligned16(workspace)) return fail(SFM_ERR_ALIGN, "%s: workspace not 16-byte aligned", fn);
+    const int64_t sb = rows * H * dk * dv * 4, kb = tokens * Hk * dk * e, vb = tokens * H * dv * e, gb = tokens * H * e;
+    Ranges in, out;
+    in.add_inputs(q, k, v, g, beta, tokens, Hk, H, dk, dv, ldq, ldk, ldv, e);
+    in.add("offsets", offsets, (rows + 1) * 4);
+    in.add("h0", h0, sb);
+    in.add("dout", dout, vb);
+    in.add("dhT", dhT, sb);
+    out.add("dq", dq, kb);
+    out.add("dk", dk_out, kb);
+    out.add("dv", dv_out, vb);
+    out.add("dg", dg, gb);
+    out.add("dbeta", dbeta, gb);
+    out.add("dh0", dh0, sb);
+    out.add("workspace", workspace, w.bytes);
+    for (int i = 0; i < out.n; ++i) {
+        if (const char* n = in.hit(out.ins[i])) return fail(SFM_ERR_ALIAS, "%s: %s overlaps %s", fn, out.ins[i].name, n);
+        for (int j = 0; j < i; ++j)
+            if (overlap(out.ins[i], out.ins[j]))
+                return fail(SFM_ERR_ALIAS, "%s: %s overlaps %s", fn, out.ins[i].name, out.ins[j].name);
+    }
+    sfm::DeltaParams p = params(q, k, v, g, beta, rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
+    char* ws = static_cast<char*>(workspace);
+    p.h0 = h0, p.offsets = offsets, p.dout = dout, p.dhT = dhT;
+    p.dq = dq, p.dk_ = dk_out, p.dv_ = dv_out, p.dg = dg, p.dbeta = dbeta, p.dh0 = dh0;
+    p.w_ops = ws + w.ops, p.w_s = ws + w.s, p.w_ds = ws + w.ds, p.w_u = ws + w.u, p.w_dr = ws + w.dr;
+    p.w_dq = reinterpret_cast<float*>(ws + w.dq), p.w_dk = reinterpret_cast<float*>(ws + w.dk);
+    p.vec_o = aligned16(dout) && dv * e % 16 == 0;
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    return hip_status(io_dtype == SFM_F32 ? sfm::launch_delta_bwd_f32(p, hs) : sfm::launch_delta_bwd_bf16(p, hs), fn);
 }
 
 }  // extern "C"
