@@ -140,14 +140,17 @@ def _dev(t, name, dtype=None, shape=None):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    try:  # the current stream's handle without a Stream object around it (a third of a small call's host time)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 SFM_FUSE_PAD, SFM_FUSE_SWAP, SFM_LAYOUT_BLD = 1, 2, 4
@@ -428,6 +431,12 @@ def sfm_pick_b1(B: int, L: int, D: int, N: int) -> int:
 
 
 # ---------------------------------------------------------------- the gated delta rule
+def _want(t, name, dtype, shape):
+    """_dev for the usual case in one look: a contiguous GPU tensor of this type and shape (or None)."""
+    if t is not None and not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _dev(t, name, dtype, shape)
+
+
 def _new(shape, dtype, device, stream):
     """A tensor for a call on `stream`: memory that the caching allocator hands out again only after it."""
     t = _torch().empty(shape, dtype=dtype, device=device)
@@ -442,12 +451,13 @@ SFM_DELTA_L2NORM = 1
 def _tokens(t, name, heads, width, dtype, lead):
     """Checks a [*lead, heads, width] tensor whose heads are contiguous and whose tokens
     are evenly strided (a slice of a wider projection is fine); returns the token stride."""
-    if t.device.type != "cuda":
+    shape = lead + (heads, width)
+    if not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != lead + (heads, width):
-        raise ValueError(f"{name} must have shape {lead + (heads, width)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return heads * width
     st = t.stride()
@@ -469,8 +479,8 @@ def _delta_args(q, k, v, g, beta, packed):
     ldq = _tokens(q, "q", Hk, dk, q.dtype, lead)
     ldk = _tokens(k, "k", Hk, dk, q.dtype, lead)
     ldv = _tokens(v, "v", H, dv, q.dtype, lead)
-    _dev(g, "g", q.dtype, lead + (H,))
-    _dev(beta, "beta", q.dtype, lead + (H,))
+    _want(g, "g", q.dtype, lead + (H,))
+    _want(beta, "beta", q.dtype, lead + (H,))
     return io, lead, Hk, H, dk, dv, ldq, ldk, ldv
 
 
@@ -506,15 +516,15 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
     torch = _torch()
     io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
     rows, L, tokens = _rows(lead, offsets, max_len)
-    _dev(h0, "h0", torch.float32, (rows, H, dk, dv))
+    _want(h0, "h0", torch.float32, (rows, H, dk, dv))
     if o is None:
         o = _new(lead + (H, dv), q.dtype, q.device, stream)
-    _dev(o, "o", q.dtype, lead + (H, dv))
+    _want(o, "o", q.dtype, lead + (H, dv))
     if return_state and state is None:
         state = _new((rows, H, dk, dv), torch.float32, q.device, stream)
     if not return_state:
         state = None
-    _dev(state, "state", torch.float32, (rows, H, dk, dv))
+    _want(state, "state", torch.float32, (rows, H, dk, dv))
     need = sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, return_state, "bf16" if io else "f32")
     if workspace is None and need:
         workspace = _new(need, torch.uint8, q.device, stream)
@@ -546,9 +556,9 @@ def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None
     torch = _torch()
     io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
     rows, L, tokens = _rows(lead, offsets, max_len)
-    _dev(h0, "h0", torch.float32, (rows, H, dk, dv))
-    _dev(dstate, "dstate", torch.float32, (rows, H, dk, dv))
-    _dev(do, "do", q.dtype, lead + (H, dv))
+    _want(h0, "h0", torch.float32, (rows, H, dk, dv))
+    _want(dstate, "dstate", torch.float32, (rows, H, dk, dv))
+    _want(do, "do", q.dtype, lead + (H, dv))
     out = dict(grads or {})
     shapes = dict(dq=lead + (Hk, dk), dk=lead + (Hk, dk), dv=lead + (H, dv), dg=lead + (H,), dbeta=lead + (H,))
     if h0 is not None:
@@ -557,7 +567,7 @@ def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None
         dt = torch.float32 if name == "dh0" else q.dtype
         if out.get(name) is None:
             out[name] = _new(shape, dt, q.device, stream)
-        _dev(out[name], name, dt, shape)
+        _want(out[name], name, dt, shape)
     need = sfm_gated_delta_bwd_ws_size(rows, L, tokens, Hk, H, dk, dv, h0 is not None, "bf16" if io else "f32")
     if workspace is None:
         workspace = _new(need, torch.uint8, q.device, stream)
@@ -582,10 +592,10 @@ def sfm_gated_delta_step(q, k, v, g, beta, state, slots=None, scale=None, l2norm
     _dev(state, "state", torch.float32)
     if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
         raise ValueError(f"state must have shape (pool, {H}, {dk}, {dv}), got {tuple(state.shape)}")
-    _dev(slots, "slots", torch.int32, (rows,))
+    _want(slots, "slots", torch.int32, (rows,))
     if o is None:
         o = _new((rows, H, dv), q.dtype, q.device, stream)
-    _dev(o, "o", q.dtype, (rows, H, dv))
+    _want(o, "o", q.dtype, (rows, H, dv))
     rc = load_library().sfm_gated_delta_step(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots), _ptr(o), rows, state.shape[0],
         Hk, H, dk, dv, ldq, ldk, ldv, dk ** -0.5 if scale is None else scale, io,
@@ -623,17 +633,17 @@ def sfm_group_norm_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, act=None
     io = _io_code(x)
     N, L, C = _norm_sizes(x)
     _dev(x, "x")
-    _dev(weight, "weight", torch.float32, (C,))
-    _dev(bias, "bias", torch.float32, (C,))
+    _want(weight, "weight", torch.float32, (C,))
+    _want(bias, "bias", torch.float32, (C,))
     if y is None:
         y = _new(x.shape, x.dtype, x.device, stream)
-    _dev(y, "y", x.dtype, x.shape)
+    _want(y, "y", x.dtype, x.shape)
     if mean is None:
         mean = _new((N, num_groups), torch.float32, x.device, stream)
     if rstd is None:
         rstd = _new((N, num_groups), torch.float32, x.device, stream)
-    _dev(mean, "mean", torch.float32, (N, num_groups))
-    _dev(rstd, "rstd", torch.float32, (N, num_groups))
+    _want(mean, "mean", torch.float32, (N, num_groups))
+    _want(rstd, "rstd", torch.float32, (N, num_groups))
     need = sfm_group_norm_ws_size(N, L, C, num_groups, "bf16" if io else "f32")
     if workspace is None and need:
         workspace = _new(need, torch.uint8, x.device, stream)
@@ -652,20 +662,20 @@ def sfm_group_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, act=None, grad
     io = _io_code(x)
     N, L, C = _norm_sizes(x)
     _dev(x, "x")
-    _dev(dy, "dy", x.dtype, x.shape)
+    _want(dy, "dy", x.dtype, x.shape)
     _dev(mean, "mean", torch.float32)
     if mean.dim() != 2 or mean.shape[0] != N:
         raise ValueError(f"mean must be [{N}, groups], got {tuple(mean.shape)}")
     G = mean.shape[1]
-    _dev(rstd, "rstd", torch.float32, (N, G))
-    _dev(weight, "weight", torch.float32, (C,))
-    _dev(bias, "bias", torch.float32, (C,))
+    _want(rstd, "rstd", torch.float32, (N, G))
+    _want(weight, "weight", torch.float32, (C,))
+    _want(bias, "bias", torch.float32, (C,))
     out = dict(grads or {})
     for name, given, shape, dt in (("dx", True, x.shape, x.dtype), ("dw", weight is not None, (C,), torch.float32),
                                    ("db", bias is not None, (C,), torch.float32)):
         if given and out.get(name) is None:
             out[name] = _new(shape, dt, x.device, stream)
-        _dev(out.get(name), name, dt, shape)
+        _want(out.get(name), name, dt, shape)
     need = sfm_group_norm_ws_size(N, L, C, G, "bf16" if io else "f32", True,
                                   out.get("dw") is not None or out.get("db") is not None)
     if workspace is None and need:

@@ -565,26 +565,28 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)
     }
 }
 
-// Shared key heads: the value heads' shares, in order.  A workgroup to every chunk of a row.
+// Shared key heads: the value heads' shares, in order.  A workgroup to every 64 tokens of a row and key head.
 template <typename T>
 __global__ __launch_bounds__(kDeltaThreads) void delta_share_kernel(const DeltaParams p, unsigned chunks) {
-    const int s = (int)(blockIdx.x / chunks);
+    const unsigned sc = blockIdx.x / (unsigned)p.Hk;
+    const int hk = (int)(blockIdx.x - sc * (unsigned)p.Hk), s = (int)(sc / chunks);
     int64_t first;
     int len;
     delta_row(p, s, first, len);
-    const int64_t t0 = (int64_t)(blockIdx.x - s * chunks) * kC;
+    const int64_t t0 = (int64_t)(sc - s * chunks) * kC;
     if (t0 >= len) return;
-    const int n = (int)min((int64_t)kC, len - t0), width = p.Hk * p.dk;
-    for (int i = threadIdx.x; i < n * width; i += kDeltaThreads) {
-        const int t = i / width, c = i - t * width, hk = c / p.dk;
-        const int64_t tok = first + t0 + t, from = (tok * p.H + (int64_t)hk * p.share) * p.dk + (c - hk * p.dk);
-        float a = 0.0f, b = 0.0f;
-        for (int j = 0; j < p.share; ++j) {
-            a += p.w_dq[from + (int64_t)j * p.dk];
-            b += p.w_dk[from + (int64_t)j * p.dk];
+    const int n = (int)min((int64_t)kC, len - t0), ct = threadIdx.x & 31;
+    for (int t = threadIdx.x >> 5; t < n; t += kDeltaThreads / 32) {
+        const int64_t tok = first + t0 + t, from = (tok * p.H + (int64_t)hk * p.share) * p.dk, to = (tok * p.Hk + hk) * p.dk;
+        for (int c = ct; c < p.dk; c += 32) {
+            float a = 0.0f, b = 0.0f;
+            for (int j = 0; j < p.share; ++j) {
+                a += p.w_dq[from + j * p.dk + c];
+                b += p.w_dk[from + j * p.dk + c];
+            }
+            static_cast<T*>(p.dq)[to + c] = from_f32<T>(a);
+            static_cast<T*>(p.dk_)[to + c] = from_f32<T>(b);
         }
-        static_cast<T*>(p.dq)[tok * width + c] = from_f32<T>(a);
-        static_cast<T*>(p.dk_)[tok * width + c] = from_f32<T>(b);
     }
 }
 
@@ -605,7 +607,7 @@ template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParam
     if ((e = allow_lds(grads, gb)) != hipSuccess) return e;
     hipLaunchKernelGGL(grads, dim3(cu), dim3(kDeltaThreads), gb, s, p, chunks, cu, ChunkOperands<T, P>::bytes);
     if ((e = hipGetLastError()) != hipSuccess || p.share == 1) return e;
-    hipLaunchKernelGGL(delta_share_kernel<T>, dim3((unsigned)p.rows * chunks), dim3(kDeltaThreads), 0, s, p, chunks);
+    hipLaunchKernelGGL(delta_share_kernel<T>, dim3((unsigned)p.rows * chunks * p.Hk), dim3(kDeltaThreads), 0, s, p, chunks);
     return hipGetLastError();
 }
 

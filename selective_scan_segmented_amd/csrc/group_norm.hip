@@ -28,8 +28,9 @@ template <typename T, int V> struct alignas(V * sizeof(T)) Unit {
     T e[V];
 };
 
-// sigmoid without overflow: exp2 of a large positive argument is infinity and 1 / infinity is 0
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + exp2_fast(-z * kLog2e)); }
+// sigmoid without overflow: exp2 of a large positive argument is infinity and 1 / infinity is 0 (the reciprocal
+// instruction, one unit in the last place: a full division costs ten times as much, more than all else here)
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-z * kLog2e)); }
 
 __device__ __forceinline__ float act_fwd(float z, int act) { return act ? z * sigmoid(z) : z; }
 
@@ -46,25 +47,49 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// Sum of each group's entries of buf [slots][cw] into out[groups of the run]: a wave to a group.
-__device__ __forceinline__ void group_sums(const float* buf, int slots, int cw, int cg, float* out) {
-    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-    for (int g = threadIdx.x >> 6; g < cw / cg; g += waves) {
-        float v = 0.0f;
-        const int n = slots * cg;
-        for (int i = lane; i < n; i += 64) {
-            const int s = i / cg;
-            v += buf[s * cw + g * cg + (i - s * cg)];
+// Groups of V neighbouring channels from `first` on (relative to where groups are counted from).
+template <int V> struct GroupOf {
+    int g[V];
+    __device__ __forceinline__ GroupOf(int first, int cg) {
+        int q = first / cg, r = first - q * cg;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            g[j] = q;
+            if (++r == cg) r = 0, ++q;
         }
+    }
+};
+
+// Sums of the groups of buf [slots][cw] into out [groups][parts]: `parts` waves share a group (where there are
+// fewer groups than waves), a group's sum is that of its parts (group_sum).
+__device__ __forceinline__ int group_parts(int groups) {
+    const int waves = blockDim.x >> 6;
+    return groups >= waves ? 1 : waves / groups;
+}
+__device__ __forceinline__ void group_sums(const float* buf, int slots, int cw, int cg, int groups, int parts, float* out) {
+    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    const int per = cg < 64 ? 64 / cg : 1;  // slots a wave takes at once
+    const int ls = cg < 64 ? lane / cg : 0, lc = lane - ls * cg;
+    for (int u = threadIdx.x >> 6; u < groups * parts; u += waves) {
+        const int g = u / parts, part = u - g * parts;
+        float v = 0.0f;
+        for (int s = part * per + ls; s < slots && ls < per; s += parts * per)
+            for (int c = lc; c < cg; c += 64) v += buf[s * cw + g * cg + c];
         v = wave_sum(v);
-        if (lane == 0) out[g] = v;
+        if (lane == 0) out[u] = v;
     }
 }
+__device__ __forceinline__ float group_sum(const float* sums, int g, int parts) {
+    float v = sums[g * parts];
+    for (int i = 1; i < parts; ++i) v += sums[g * parts + i];
+    return v;
+}
+constexpr int kMaxWaves = 16;
 
 // ------------------------------------------------------------------------------------------------ slab kernels
 // LDS: [slots][cw] per-thread channel sums (two of them backward), then the groups' sums.
-template <typename T, int V, int U>
-__global__ __launch_bounds__(1024) void norm_slab_fwd_kernel(const NormParams p) {
+template <typename T, int V, int U, int THREADS>
+__global__ __launch_bounds__(THREADS, 4) void norm_slab_fwd_kernel(const NormParams p) {
     extern __shared__ float lds[];
     const int cu = p.cw / V, slots = blockDim.x / cu;
     const int64_t n = blockIdx.x / p.runs;
@@ -72,8 +97,9 @@ __global__ __launch_bounds__(1024) void norm_slab_fwd_kernel(const NormParams p)
     const int slot = threadIdx.x / cu, cl = (threadIdx.x - slot * cu) * V, c = run * p.cw + cl;
     const bool on = slot < slots;
     const int64_t rows = on ? p.L : 0;
-    const int groups = p.cw / p.cg;
-    float* gs = lds + slots * p.cw;
+    const int groups = p.cw / p.cg, parts = group_parts(groups);
+    float *gs = lds + slots * p.cw, *gq = gs + groups * parts;
+    const GroupOf<V> grp(on ? cl : 0, p.cg);
     const T* xp = static_cast<const T*>(p.x) + n * p.L * p.C + c;
     Unit<T, V> x[U];
     float sum[V];
@@ -94,13 +120,14 @@ __global__ __launch_bounds__(1024) void norm_slab_fwd_kernel(const NormParams p)
 #pragma unroll
         for (int j = 0; j < V; ++j) lds[slot * p.cw + cl + j] = sum[j];
     __syncthreads();
-    group_sums(lds, slots, p.cw, p.cg, gs);
+    group_sums(lds, slots, p.cw, p.cg, groups, parts, gs);
     __syncthreads();
     const float total = (float)p.L * (float)p.cg;
     float mean[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        mean[j] = gs[on ? (cl + j) / p.cg : 0] / total;  // (a division: a constant group's mean is exact)
+        // (a division: a constant group's mean is exact)
+        mean[j] = j > 0 && grp.g[j] == grp.g[j > 0 ? j - 1 : 0] ? mean[j > 0 ? j - 1 : 0] : group_sum(gs, grp.g[j], parts) / total;
         sum[j] = 0.0f;
     }
 #pragma unroll
@@ -115,18 +142,21 @@ __global__ __launch_bounds__(1024) void norm_slab_fwd_kernel(const NormParams p)
 #pragma unroll
         for (int j = 0; j < V; ++j) lds[slot * p.cw + cl + j] = sum[j];
     __syncthreads();
-    group_sums(lds, slots, p.cw, p.cg, gs + groups);
+    group_sums(lds, slots, p.cw, p.cg, groups, parts, gq);
     __syncthreads();
-    if ((int)threadIdx.x < groups) {
-        const int64_t at = n * p.G + run * groups + threadIdx.x;
-        p.mean[at] = gs[threadIdx.x] / total;
-        p.rstd[at] = 1.0f / __builtin_sqrtf(gs[groups + threadIdx.x] / total + p.eps);
+    for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+        const int64_t at = n * p.G + run * groups + g;
+        p.mean[at] = group_sum(gs, g, parts) / total;
+        p.rstd[at] = 1.0f / __builtin_sqrtf(group_sum(gq, g, parts) / total + p.eps);
     }
     if (!on) return;
     float a[V], b[V];
 #pragma unroll
+    for (int j = 0; j < V; ++j)
+        a[j] = j > 0 && grp.g[j] == grp.g[j > 0 ? j - 1 : 0] ? a[j > 0 ? j - 1 : 0]
+                                                             : 1.0f / __builtin_sqrtf(group_sum(gq, grp.g[j], parts) / total + p.eps);
+#pragma unroll
     for (int j = 0; j < V; ++j) {
-        a[j] = 1.0f / __builtin_sqrtf(gs[groups + (cl + j) / p.cg] / total + p.eps);
         if (p.w) a[j] *= p.w[c + j];
         b[j] = p.b ? p.b[c + j] : 0.0f;
     }
@@ -144,8 +174,8 @@ __global__ __launch_bounds__(1024) void norm_slab_fwd_kernel(const NormParams p)
     }
 }
 
-template <typename T, int V, int U>
-__global__ __launch_bounds__(512) void norm_slab_bwd_kernel(const NormParams p) {
+template <typename T, int V, int U, int THREADS>
+__global__ __launch_bounds__(THREADS, (U <= 4 ? 3 : 2)) void norm_slab_bwd_kernel(const NormParams p) {
     extern __shared__ float lds[];
     const int cu = p.cw / V, slots = blockDim.x / cu;
     const int64_t n = blockIdx.x / p.runs;
@@ -153,8 +183,9 @@ __global__ __launch_bounds__(512) void norm_slab_bwd_kernel(const NormParams p) 
     const int slot = threadIdx.x / cu, cl = (threadIdx.x - slot * cu) * V, c = run * p.cw + cl;
     const bool on = slot < slots;
     const int64_t rows = on ? p.L : 0;
-    const int groups = p.cw / p.cg;
-    float *l1 = lds, *l2 = lds + slots * p.cw, *gs = l2 + slots * p.cw;
+    const int groups = p.cw / p.cg, parts = group_parts(groups);
+    float *l1 = lds, *l2 = lds + slots * p.cw, *gs = l2 + slots * p.cw, *gq = gs + groups * parts;
+    const GroupOf<V> grp(on ? cl : 0, p.cg);
     const T* xp = static_cast<const T*>(p.x) + n * p.L * p.C + c;
     const T* dp = static_cast<const T*>(p.dy) + n * p.L * p.C + c;
     Unit<T, V> x[U], dy[U];
@@ -169,7 +200,7 @@ __global__ __launch_bounds__(512) void norm_slab_bwd_kernel(const NormParams p) 
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t at = n * p.G + run * groups + (on ? (cl + j) / p.cg : 0);
+        const int64_t at = n * p.G + run * groups + grp.g[j];
         mean[j] = p.mean[at];
         rstd[j] = p.rstd[at];
         w[j] = p.w && on ? p.w[c + j] : 1.0f;
@@ -204,16 +235,16 @@ __global__ __launch_bounds__(512) void norm_slab_bwd_kernel(const NormParams p) 
         l[ch] = p.w ? v * p.w[cc] : v;
     }
     __syncthreads();
-    group_sums(l1, 1, p.cw, p.cg, gs);
-    group_sums(l2, 1, p.cw, p.cg, gs + groups);
+    group_sums(l1, 1, p.cw, p.cg, groups, 1, gs);
+    group_sums(l2, 1, p.cw, p.cg, groups, 1, gq);
     __syncthreads();
     if (!on) return;
     const float inv = 1.0f / ((float)p.L * (float)p.cg);
     float m1[V], m2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        m1[j] = gs[(cl + j) / p.cg] * inv;
-        m2[j] = gs[groups + (cl + j) / p.cg] * inv;
+        m1[j] = gs[grp.g[j]] * inv;
+        m2[j] = gq[grp.g[j]] * inv;
     }
     T* yp = static_cast<T*>(p.y) + n * p.L * p.C + c;
 #pragma unroll
@@ -249,13 +280,14 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormParams p) {
     const int slot = threadIdx.x / cu, cl = (threadIdx.x - slot * cu) * V, c = tile * p.tunits * V + cl;
     const bool on = slot < slots;
     const int64_t r0 = split * p.srows, r1 = min(p.L, r0 + p.srows);
+    const GroupOf<V> grp(on ? c : 0, p.cg);
     float s1[V], s2[V], mean[V], rstd[V], w[V], b[V];
     float count = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         s1[j] = s2[j] = 0.0f;
         if (BWD) {
-            const int64_t at = n * p.G + (on ? (c + j) / p.cg : 0);
+            const int64_t at = n * p.G + grp.g[j];
             mean[j] = p.mean[at];
             rstd[j] = p.rstd[at];
             w[j] = p.w && on ? p.w[c + j] : 1.0f;
@@ -349,31 +381,67 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormParams p) {
     }
 }
 
-// Joins the ranges and the channels of a group (a wave to a group).  Forward: mean and rstd; backward: m1, m2.
+// Joins the ranges of a sample's channels: a workgroup to 16 channels, 16 threads down the ranges of each.  The
+// result takes the place of the first range's sums.
 template <bool BWD>
-__global__ __launch_bounds__(256) void norm_join_kernel(const NormParams p) {
+__global__ __launch_bounds__(256) void norm_join_kernel(const NormParams p, unsigned tiles) {
+    __shared__ float l1[16][17], l2[16][17], lk[16];
+    const unsigned n = blockIdx.x / tiles;
+    const int cl = threadIdx.x & 15, k = threadIdx.x >> 4, c = (int)(blockIdx.x - n * tiles) * 16 + cl;
+    float* part = p.part + (int64_t)n * p.splits * 2 * p.C + c;
+    float a = 0.0f, q = 0.0f, count = 0.0f;
+    if (c < p.C)
+#pragma unroll 4
+        for (int i = k; i < p.splits; i += 16) {
+            const float m = part[(int64_t)i * 2 * p.C], t = part[((int64_t)i * 2 + 1) * p.C];
+            if (BWD) {
+                a += m;
+                q += t;
+            } else {
+                const float rows = (float)min(p.L - i * p.srows, p.srows), d = m - a;
+                a = __builtin_fmaf(d, rows / (count + rows), a);
+                q += t + d * d * (count * rows / (count + rows));
+                count += rows;
+            }
+        }
+    l1[k][cl] = a;
+    l2[k][cl] = q;
+    if (cl == 0) lk[k] = count;
+    __syncthreads();
+    if (k != 0 || c >= p.C) return;
+    for (int i = 1; i < 16; ++i) {
+        const float m = l1[i][cl], t = l2[i][cl], rows = lk[i];
+        if (BWD) {
+            a += m;
+            q += t;
+        } else if (rows > 0.0f) {
+            const float d = m - a;
+            a = __builtin_fmaf(d, rows / (count + rows), a);
+            q += t + d * d * (count * rows / (count + rows));
+            count += rows;
+        }
+    }
+    part[0] = a;
+    part[p.C] = q;
+}
+
+// Joins a group's channels, a wave to a group.  Forward: mean and rstd; backward: m1, m2.
+template <bool BWD>
+__global__ __launch_bounds__(256) void norm_group_kernel(const NormParams p) {
     const int lane = threadIdx.x & 63;
     const int64_t id = blockIdx.x * (int64_t)(blockDim.x >> 6) + (threadIdx.x >> 6);
     if (id >= p.N * p.G) return;
     const int64_t n = id / p.G;
     const int g = (int)(id - n * p.G);
     const float* part = p.part + n * p.splits * 2 * p.C + g * p.cg;
-    const int entries = p.splits * p.cg;
     const float total = (float)p.L * (float)p.cg;
     float s = 0.0f, t = 0.0f;
-    for (int i = lane; i < entries; i += 64) {
-        const int split = i / p.cg, c = i - split * p.cg;
-        const int64_t rows = min(p.L - split * p.srows, p.srows);
-        const float m = part[(int64_t)split * 2 * p.C + c];
-        if (BWD) {
-            const float w = p.w ? p.w[g * p.cg + c] : 1.0f;
-            s = __builtin_fmaf(w, m, s);
-            t = __builtin_fmaf(w, part[((int64_t)split * 2 + 1) * p.C + c], t);
-        } else {
-            s = __builtin_fmaf((float)rows, m, s);
-        }
+    for (int c = lane; c < p.cg; c += 64) {
+        const float w = BWD && p.w ? p.w[g * p.cg + c] : 1.0f;
+        s = __builtin_fmaf(w, part[c], s);
+        if (BWD) t = __builtin_fmaf(w, part[p.C + c], t);
     }
-    s = wave_sum(s) / total;
+    s = wave_sum(s) / (BWD ? total : (float)p.cg);
     if (BWD) {
         t = wave_sum(t) / total;
         if (lane == 0) {
@@ -382,11 +450,9 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const NormParams p) {
         }
         return;
     }
-    for (int i = lane; i < entries; i += 64) {
-        const int split = i / p.cg, c = i - split * p.cg;
-        const int64_t rows = min(p.L - split * p.srows, p.srows);
-        const float d = part[(int64_t)split * 2 * p.C + c] - s;
-        t += __builtin_fmaf(d * d, (float)rows, part[((int64_t)split * 2 + 1) * p.C + c]);
+    for (int c = lane; c < p.cg; c += 64) {
+        const float d = part[c] - s;
+        t += __builtin_fmaf(d * d, (float)p.L, part[p.C + c]);
     }
     t = wave_sum(t) / total;
     if (lane == 0) {
@@ -407,10 +473,11 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormParams p) {
     const int slot = threadIdx.x / cu, c = (tile * p.tunits + (int)threadIdx.x - slot * cu) * V;
     if (slot >= slots) return;
     const int64_t r0 = split * p.srows, r1 = min(p.L, r0 + p.srows);
+    const GroupOf<V> grp(c, p.cg);
     float mean[V], rstd[V], w[V], b[V], m1[V], m2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t at = n * p.G + (c + j) / p.cg;
+        const int64_t at = n * p.G + grp.g[j];
         mean[j] = p.mean[at];
         rstd[j] = p.rstd[at];
         w[j] = p.w ? p.w[c + j] : 1.0f;
@@ -418,6 +485,8 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormParams p) {
         if (BWD) {
             m1[j] = p.gsum[at * 2];
             m2[j] = p.gsum[at * 2 + 1];
+        } else {
+            w[j] *= rstd[j];
         }
     }
     const int64_t base = n * p.L * p.C + c;
@@ -438,13 +507,13 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormParams p) {
                 Unit<T, V> y;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float xh = (to_f32(x[i].e[j]) - mean[j]) * rstd[j];
-                    const float z = __builtin_fmaf(xh, w[j], b[j]);
+                    const float xd = to_f32(x[i].e[j]) - mean[j];
                     if (BWD) {
+                        const float xh = xd * rstd[j], z = __builtin_fmaf(xh, w[j], b[j]);
                         const float dz = act_bwd(to_f32(dy[i].e[j]), z, p.act);
                         y.e[j] = from_f32<T>(rstd[j] * (dz * w[j] - m1[j] - xh * m2[j]));
                     } else {
-                        y.e[j] = from_f32<T>(act_fwd(z, p.act));
+                        y.e[j] = from_f32<T>(act_fwd(__builtin_fmaf(xd, w[j], b[j]), p.act));
                     }
                 }
                 *reinterpret_cast<Unit<T, V>*>(yp + (r + (int64_t)i * slots) * p.C) = y;
@@ -452,37 +521,45 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormParams p) {
     }
 }
 
-// dw, db: the channels' sums over samples and ranges.  A workgroup to 64 channels, 16 threads down each.
-__global__ __launch_bounds__(1024) void norm_weights_kernel(const NormParams p, int64_t parts) {
-    __shared__ float red[2][16][64];
-    const int cl = threadIdx.x & 63, k = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + cl;
+// dw, db: the channels' sums over samples (`stride` floats apart).  A workgroup to 16 channels, 64 threads down each.
+__global__ __launch_bounds__(1024) void norm_weights_kernel(const NormParams p, int64_t stride) {
+    __shared__ float red[2][64][17];
+    const int cl = threadIdx.x & 15, k = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + cl;
     float a = 0.0f, b = 0.0f;
     if (c < p.C)
-        for (int64_t i = k; i < parts; i += 16) {
-            b += p.part[i * 2 * p.C + c];
-            a += p.part[(i * 2 + 1) * p.C + c];
+#pragma unroll 4
+        for (int64_t i = k; i < p.N; i += 64) {
+            b += p.part[i * stride + c];
+            a += p.part[i * stride + p.C + c];
         }
     red[0][k][cl] = a;
     red[1][k][cl] = b;
     __syncthreads();
+    for (int m = 32; m > 0; m >>= 1) {
+        if (k < m) {
+            red[0][k][cl] += red[0][k + m][cl];
+            red[1][k][cl] += red[1][k + m][cl];
+        }
+        __syncthreads();
+    }
     if (k < 2 && c < p.C) {
-        float v = 0.0f;
-        for (int i = 0; i < 16; ++i) v += red[k][i][cl];
         float* out = k == 0 ? p.dw : p.db;
-        if (out) out[c] = v;
+        if (out) out[c] = red[k][0][cl];
     }
 }
 
-template <typename T, int V, int U>
+template <typename T, int V, int U, int THREADS>
 hipError_t launch_slab(const NormParams& p, bool bwd, hipStream_t s) {
     const int slots = p.threads / (p.cw / V);
-    const size_t lds = ((size_t)slots * p.cw * (bwd ? 2 : 1) + 2 * (p.cw / p.cg)) * 4;
+    const size_t lds = ((size_t)slots * p.cw * (bwd ? 2 : 1) + 2 * (p.cw / p.cg + kMaxWaves)) * 4;
     const dim3 grid((unsigned)(p.N * p.runs));
-    if (bwd)
-        hipLaunchKernelGGL((norm_slab_bwd_kernel<T, V, U>), grid, dim3(p.threads), lds, s, p);
-    else
-        hipLaunchKernelGGL((norm_slab_fwd_kernel<T, V, U>), grid, dim3(p.threads), lds, s, p);
+    if constexpr (THREADS <= 512)
+        if (bwd) {
+            hipLaunchKernelGGL((norm_slab_bwd_kernel<T, V, U, THREADS>), grid, dim3(p.threads), lds, s, p);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((norm_slab_fwd_kernel<T, V, U, THREADS>), grid, dim3(p.threads), lds, s, p);
     return hipGetLastError();
 }
 
@@ -490,29 +567,34 @@ template <typename T, int V>
 hipError_t launch_v(const NormParams& p, bool bwd, hipStream_t s) {
     hipError_t e;
     if (p.slab) {
-        e = p.units <= 1 ? launch_slab<T, V, 1>(p, bwd, s)
-            : p.units <= 2 ? launch_slab<T, V, 2>(p, bwd, s)
-            : p.units <= 4 ? launch_slab<T, V, 4>(p, bwd, s)
-                           : launch_slab<T, V, 8>(p, bwd, s);
+        e = p.threads > 512   ? launch_slab<T, V, 8, 1024>(p, bwd, s)
+            : p.threads > 256 ? launch_slab<T, V, 8, 512>(p, bwd, s)
+            : p.units <= 1    ? launch_slab<T, V, 1, 256>(p, bwd, s)
+            : p.units <= 2    ? launch_slab<T, V, 2, 256>(p, bwd, s)
+            : p.units <= 4    ? launch_slab<T, V, 4, 256>(p, bwd, s)
+                              : launch_slab<T, V, 8, 256>(p, bwd, s);
     } else {
         const dim3 grid((unsigned)(p.N * p.splits * p.tiles));
         // the last tile may be narrower and so have more slots; slots x channels never exceeds threads x V
         const size_t lds = ((size_t)2 * p.threads * V + p.threads) * 4;
-        const dim3 jgrid((unsigned)((p.N * p.G + 3) / 4));
+        const unsigned jt = (unsigned)((p.C + 15) / 16);
+        const dim3 jgrid((unsigned)p.N * jt), ggrid((unsigned)((p.N * p.G + 3) / 4));
         if (bwd) {
             hipLaunchKernelGGL((norm_sums_kernel<T, V, true>), grid, dim3(p.threads), lds, s, p);
-            hipLaunchKernelGGL((norm_join_kernel<true>), jgrid, dim3(256), 0, s, p);
+            hipLaunchKernelGGL((norm_join_kernel<true>), jgrid, dim3(256), 0, s, p, jt);
+            hipLaunchKernelGGL((norm_group_kernel<true>), ggrid, dim3(256), 0, s, p);
             hipLaunchKernelGGL((norm_apply_kernel<T, V, true>), grid, dim3(p.threads), 0, s, p);
         } else {
             hipLaunchKernelGGL((norm_sums_kernel<T, V, false>), grid, dim3(p.threads), lds, s, p);
-            hipLaunchKernelGGL((norm_join_kernel<false>), jgrid, dim3(256), 0, s, p);
+            hipLaunchKernelGGL((norm_join_kernel<false>), jgrid, dim3(256), 0, s, p, jt);
+            hipLaunchKernelGGL((norm_group_kernel<false>), ggrid, dim3(256), 0, s, p);
             hipLaunchKernelGGL((norm_apply_kernel<T, V, false>), grid, dim3(p.threads), 0, s, p);
         }
         e = hipGetLastError();
     }
     if (e != hipSuccess || !bwd || !(p.dw || p.db)) return e;
-    hipLaunchKernelGGL(norm_weights_kernel, dim3((unsigned)((p.C + 63) / 64)), dim3(1024), 0, s, p,
-                       p.N * (p.slab ? 1 : (int64_t)p.splits));
+    hipLaunchKernelGGL(norm_weights_kernel, dim3((unsigned)((p.C + 15) / 16)), dim3(1024), 0, s, p,
+                       2 * (int64_t)p.C * (p.slab ? 1 : p.splits));
     return hipGetLastError();
 }
 
@@ -528,7 +610,8 @@ int64_t plan_norm(NormParams& p, int io_bytes, bool aligned, bool backward) {
     const int v = 16 / io_bytes;
     p.vec = aligned && p.C % v == 0 ? v : 1;
     // Slab: the narrowest run of whole groups that is whole units, widened to full 128-byte lines while a thread
-    // still holds at most eight units; the smallest workgroup that does.
+    // still holds at most eight units; the smallest workgroup that does (198 rows of 64 bfloat16 channels: 30 us a
+    // 1280 runs with 256 threads of eight units, 39 us with 512 of four; what a thread does once costs more).
     p.slab = 0;
     // (two tensors backward: half the threads, twice the registers)
     constexpr int kUnits = 8;
@@ -545,7 +628,7 @@ int64_t plan_norm(NormParams& p, int io_bytes, bool aligned, bool backward) {
         const int cu = p.cw / p.vec;
         p.runs = p.C / p.cw;
         for (p.threads = 64; p.threads < kThreads; p.threads *= 2)
-            if (p.threads >= cu && p.L <= (p.threads / cu) * (int64_t)(p.threads < 256 ? 4 : kUnits)) break;
+            if (p.threads >= cu && p.L <= p.threads / cu * (int64_t)(p.threads < 256 ? 4 : kUnits)) break;
         const int slots = p.threads / cu;
         p.units = (int)((p.L + slots - 1) / slots);
         return backward && (p.dw || p.db) ? p.N * 2 * p.C * 4 : 0;
