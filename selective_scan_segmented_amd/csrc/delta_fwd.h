@@ -291,10 +291,4 @@ template <typename T, int DK, int P> hipError_t launch_prepare(const DeltaParams
     return hipGetLastError();
 }
 
-template <typename T, int DK, int P> hipError_t launch_forward(const DeltaParams& p, hipStream_t s) {
-    if (!p.w_ops) return launch_walk<T, DK, P, kWhole>(p, s);
-    const hipError_t e = launch_prepare<T, DK, P>(p, s);
-    return e != hipSuccess ? e : launch_walk<T, DK, P, kPrepared>(p, s);
-}
-
 }  // namespace sfm

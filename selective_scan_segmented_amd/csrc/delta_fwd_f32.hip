@@ -1,5 +1,5 @@
-// delta_fwd_f32.hip -- the chunked forward of the gated delta rule for float32 tensors (delta_fwd.h).
-#include "delta_fwd.h"
+// delta_fwd_f32.hip -- the chunked forward of the gated delta rule for float32 tensors (delta_fwd.h, delta_narrow.h).
+#include "delta_narrow.h"
 
 namespace sfm {
 

@@ -30,6 +30,7 @@ struct DeltaParams {
     int vec_k, vec_v;    // q and k (v) rows may be loaded 16 bytes at a time
     int vec_s;           // states likewise
     int vec_o;           // dout likewise
+    int narrow;          // sixteen columns to a workgroup of the walks (delta_narrow.h)
     // backward
     const void* dout;    // [tokens][H][dv]
     const float* dhT;    // [rows][H][dk][dv] or null (zero)
@@ -63,6 +64,7 @@ constexpr float kDeltaNormEps = 1e-6f;
 constexpr float kDeltaMinGate = -110.0f;
 
 // Workspace of the chunked forward in bytes: 0 where a chunk's T and A are made on the way (delta_fwd.h).
+bool plan_delta_narrow(int64_t rows, int64_t H, int64_t dv);
 int64_t plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dv, bool want_state, int io_dtype);
 // entries of the arrays that hold something for every chunk (chunk_entry): enough for packed and for equal rows
 inline int64_t delta_chunk_entries(int64_t rows, int64_t tokens) { return tokens / kDeltaChunk + rows; }

@@ -104,6 +104,13 @@ int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, 
     return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2) : 0;
 }
 
+// Walks with sixteen columns to a workgroup instead of 64 while the latter would not fill the card.
+// SFM_DELTA_NARROW=0|1 overrides (tuning and tests).
+bool sfm::plan_delta_narrow(int64_t rows, int64_t H, int64_t dv) {
+    if (const char* e = std::getenv("SFM_DELTA_NARROW")) return e[0] == '1';
+    return rows * H * ((dv + 63) / 64) <= 256;
+}
+
 extern "C" {
 
 sfm_status sfm_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -187,6 +194,7 @@ sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
     sfm::DeltaParams p = params(q, k, v, g, beta, rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
     p.h0 = h0, p.hT = hT, p.offsets = offsets, p.o = o;
     p.w_ops = need > 0 ? static_cast<char*>(workspace) : nullptr;
+    p.narrow = sfm::plan_delta_narrow(rows, H, dv);
     p.vec_s = dv % 4 == 0 && aligned16(h0) && aligned16(hT);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     if (L <= kRecurrentMax) return hip_status(sfm::launch_delta_recurrent(p, io_dtype, hs), fn);
