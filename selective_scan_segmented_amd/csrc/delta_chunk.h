@@ -59,6 +59,9 @@ template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_below(double
     return __builtin_bit_cast(double, (long long)(((unsigned long long)(unsigned)hi << 32) | (unsigned)lo));
 }
 
+// this thread's number among the 256 that share a chunk's loads
+__device__ __forceinline__ unsigned share_id() { return threadIdx.x & (kDeltaThreads - 1); }
+
 // One thread's share of a chunk's [64][DK] rows: eight keys of every 2048 / DK-th token.
 template <typename T, int DK> struct RowShare {
     static constexpr int kPer = DK / 8, kUnits = kC * kPer / kDeltaThreads, kStep = kDeltaThreads / kPer;
@@ -69,7 +72,7 @@ template <typename T, int DK> struct RowShare {
     __device__ __forceinline__ void load(const Buf& b, int64_t ld, int dk, bool vec) {
         constexpr int per = 16 / (int)sizeof(T);
         typedef T piece __attribute__((ext_vector_type(per)));
-        const int t0 = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
+        const int t0 = share_id() / kPer, c = share_id() % kPer * 8;
         const unsigned at = fresh((unsigned)(t0 * ld + c) * (unsigned)sizeof(T)), step = (unsigned)(kStep * ld) * (unsigned)sizeof(T);
         if (vec) {
 #pragma unroll
@@ -92,7 +95,7 @@ template <typename T, int DK> struct RowShare {
     // into LDS: the rows and, if wanted, one over their lengths
     __device__ __forceinline__ void store(T* rows, float* factor, int l2norm) const {
         using Sh = ChunkShape<T, DK>;
-        const int t0 = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
+        const int t0 = share_id() / kPer, c = share_id() % kPer * 8;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) *reinterpret_cast<vec8*>(rows + (t0 + i * kStep) * Sh::KS + c) = a[i];
         if (!factor) return;
@@ -308,15 +311,15 @@ template <int N> struct Linear {
     typedef unsigned unit __attribute__((ext_vector_type(4)));
     static constexpr int kUnits = (N / 16 + kDeltaThreads - 1) / kDeltaThreads;
     unit x[kUnits];
-    __device__ __forceinline__ void load(const char* p) {
-        const Buf b = make_buf(p, N);
+    __device__ __forceinline__ void load(const char* p, bool there = true) {
+        const Buf b = make_buf(p, there ? N : 0);
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) x[i] = buf_load<unit>(b, (threadIdx.x + i * kDeltaThreads) * 16u);
+        for (int i = 0; i < kUnits; ++i) x[i] = buf_load<unit>(b, (share_id() + i * kDeltaThreads) * 16u);
     }
     __device__ __forceinline__ void store(char* p) const {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int u = threadIdx.x + i * kDeltaThreads;
+            const int u = share_id() + i * kDeltaThreads;
             if (N % (kDeltaThreads * 16) == 0 || u < N / 16) *reinterpret_cast<unit*>(p + u * 16) = x[i];
         }
     }

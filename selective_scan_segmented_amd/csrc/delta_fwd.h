@@ -112,10 +112,11 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
                         if constexpr (W != kStates) fq[kb & 1][rt] = load_runs<T>(qs + at);
                     }
                 };
-                load(0);
+                constexpr int ahead = W == kWhole && DK == 128 ? 0 : 1;  // (registers for two workgroups to a unit)
+                if (ahead) load(0);
 #pragma unroll
                 for (int kb = 0; kb < DK / 32; ++kb) {
-                    if (kb + 1 < DK / 32) load(kb + 1);
+                    if (kb + ahead < DK / 32) load(kb + ahead);
                     loads_end();
                     Parts<T, P> sp;
                     split<P>(S[2 * kb], S[2 * kb + 1], sp);
@@ -158,14 +159,16 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
         {
             Parts<T, P> tp[kLowerFrags], rp[2];
 #pragma unroll
-            for (int f = 0; f < kLowerFrags; ++f) tp[f] = load_parts<P>(ts, f);
+            for (int rt = 0; rt < 4; ++rt) tp[lower_frag(rt, 0)] = load_parts<P>(ts, lower_frag(rt, 0));
             loads_end();
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) split<P>(X[2 * kb], X[2 * kb + 1], rp[kb]);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) U[rt] = f32x4{0, 0, 0, 0};
+            mma_lower<P, P>(tp, rp[0], 0, U);
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) mma_lower<P, P>(tp, rp[kb], kb, U);
+            for (int rt = 2; rt < 4; ++rt) tp[lower_frag(rt, 1)] = load_parts<P>(ts, lower_frag(rt, 1));
+            mma_lower<P, P>(tp, rp[1], 1, U);
         }
         if constexpr (W == kStates) {
 #pragma unroll

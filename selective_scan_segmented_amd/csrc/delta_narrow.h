@@ -3,8 +3,9 @@
 // A row's chunks follow one another, so where there are few (row, head, 64 column) workgroups the time is that of
 // one chunk in one of them.  Here the four waves share sixteen columns instead of having sixteen each: wave w holds
 // a quarter of the state's keys and computes the tokens 16 w .. + 15 of every product, and what the others need of it
-// (the state's parts, R, U) goes through LDS in operand order.  Three barriers a chunk; the next chunk's operands
-// are stored into the other half of LDS, where that fits, while this one is computed.
+// (the state's parts, R, U) goes through LDS in operand order.  Three barriers a chunk.  Four more waves do nothing
+// but bring the next chunk's operands into the other half of LDS (where two halves fit): a compute unit moves 64
+// bytes a cycle, 1000 cycles for a chunk of 66 KB, and a wave that issues such loads stands still meanwhile.
 #pragma once
 
 #include "delta_fwd.h"
@@ -50,6 +51,23 @@ __device__ __forceinline__ void store_half_both(f32x4 x, T* base, int frag, int 
         }
     }
 }
+// four values of a lane as PW planes of memory
+template <int PW, typename T> __device__ __forceinline__ void store_four(f32x4 x, T* mem, int64_t plane) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<f32x4*>(mem) = x;
+    } else {
+#pragma unroll
+        for (int q = 0; q < PW; ++q) {
+            bf16x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = (__bf16)x[j];
+                x[j] -= (float)v[j];
+            }
+            *reinterpret_cast<bf16x4*>(mem + q * plane) = v;
+        }
+    }
+}
 template <int P, int NF, typename T> __device__ __forceinline__ Parts<T, P> load_exchange(const T* base, int frag) {
     Parts<T, P> a;
 #pragma unroll
@@ -84,12 +102,38 @@ template <typename T, int DK, int P, int PA, int PX> struct NarrowLds {
     static constexpr int state = P * (DK / 32) * kFragSize * E, tokens = PX * 2 * kFragSize * E;
     static constexpr int NB = 2 * half + state + tokens <= 160 * 1024 ? 2 : 1;
     static constexpr int sp = NB * half, xp = sp + state, bytes = xp + tokens;
-    static constexpr int groups = 2 * bytes <= 160 * 1024 ? 2 : 1;
     static constexpr int plane = 2 * kFragSize;  // elements of one plane over tokens
 };
 
-template <typename T, int DK, int P, Walk W>
-__global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+constexpr int kNarrowThreads = 2 * kDeltaThreads;
+
+// What a loading wave does for a row's chunks: chunk number i from memory to registers (load) and on to LDS (store).
+// The compute waves' barriers: the first of chunk c after which the other half is free and before which chunk c's
+// operands are written, and two more; with one half, a fourth at the chunk's end.
+template <int NB, int HALF, typename Load, typename Store>
+__device__ __forceinline__ void narrow_loader(char* lds, int chunks, Load load, Store store) {
+    if (chunks <= 0) return;
+    load(0);
+    store(lds);
+    load(1);
+    for (int c = 0; c < chunks; ++c) {
+        lds_barrier();
+        if (NB == 2) {
+            store(lds + (c & 1 ? 0 : HALF));
+            load(c + 2);
+        }
+        lds_barrier();
+        lds_barrier();
+        if (NB == 1 && c + 1 < chunks) {
+            lds_barrier();
+            store(lds);
+            load(c + 2);
+        }
+    }
+}
+
+template <typename T, int DK, int P, Walk W, bool VEC>
+__global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
     constexpr int PY = P < 2 ? P : 2, E = (int)sizeof(T), DT = DK / 64, NS = DK / 32;
     using Sh = ChunkShape<T, DK>;
     using Ops = ChunkOperands<T, P>;
@@ -99,13 +143,41 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
 
     const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
-    const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4, tok = wave * 16 + g4;
-    const int col = (int)(unit - rh * tiles) * 16 + l16;
     int64_t first;
     int len;
     delta_row(p, s, first, len);
-    const T* qp = static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk;
-    const T* kp = static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk;
+    const int chunks = (len + kC - 1) / kC;
+    int64_t entry = (int64_t)chunk_entry(p, s, first) * p.H + h;
+
+    if (wave_id() >= 4) {
+        const T* qp = static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk;
+        const T* kp = static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk;
+        RowShare<T, DK> kr, qr;
+        Linear<Ops::a> ops;
+        Linear<PY * L::frag_bytes> opa;
+        // Behind the row's end the buffers are empty: with no branch around a load the compiler knows how many are in
+        // flight and waits for no more than it needs.
+        auto load = [&](int c) {
+            const bool in = c < chunks;
+            const int64_t t = in ? (int64_t)c * kC : 0, n = in ? min((int64_t)kC, len - t) : 0;
+            const char* o = p.w_ops + (entry + (in ? (int64_t)c * p.H : 0)) * Ops::bytes;
+            kr.load(make_buf(kp + t * p.ldk, n * p.ldk * E), p.ldk, p.dk, VEC);
+            if (W != kStates) qr.load(make_buf(qp + t * p.ldq, n * p.ldq * E), p.ldq, p.dk, VEC);
+            ops.load(o, in);
+            if (W != kStates) opa.load(o + Ops::a, in);
+        };
+        auto store = [&](char* to) {
+            kr.store(reinterpret_cast<T*>(to + L::ks), nullptr, 0);
+            if (W != kStates) qr.store(reinterpret_cast<T*>(to + L::qs), nullptr, 0);
+            ops.store(to);
+            if (W != kStates) opa.store(to + L::as);
+        };
+        narrow_loader<L::NB, L::half>(lds, chunks, load, store);
+        return;
+    }
+
+    const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4, tok = wave * 16 + g4;
+    const int col = (int)(unit - rh * tiles) * 16 + l16;
     const T* vp = static_cast<const T*>(p.v) + first * p.ldv + (int64_t)h * p.dv;
     T* op = static_cast<T*>(p.o) + (first * p.H + h) * p.dv;
     const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
@@ -114,7 +186,6 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
     const unsigned soff = col < p.dv ? (unsigned)(key * p.dv + col) * 4u : kNowhere;
     const unsigned voff = col < p.dv ? (unsigned)(tok * p.ldv + col) * E : kNowhere;
     const unsigned ooff = col < p.dv ? (unsigned)(tok * p.H * p.dv + col) * E : kNowhere;
-    int64_t entry = (int64_t)chunk_entry(p, s, first) * p.H + h, next = entry;
     const int vals = (p.dv + 63) / 64 * 64;
 
     f32x4 S[DT];
@@ -127,46 +198,20 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[d][r] = buf_load<float>(b, soff + (unsigned)((d * 16 + r) * p.dv) * 4u);
     }
-
-    RowShare<T, DK> kr, qr;
-    Linear<Ops::a> ops;
-    Linear<PY * L::frag_bytes> opa;
-    unsigned vn[4], v[4];
-    auto fetch = [&](int64_t t0) {
-        const int64_t n = min((int64_t)kC, len - t0);
-        kr.load(make_buf(kp + t0 * p.ldk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
-        if (W != kStates) qr.load(make_buf(qp + t0 * p.ldq, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
-        const char* o = p.w_ops + next * Ops::bytes;
-        ops.load(o);
-        if (W != kStates) opa.load(o + Ops::a);
-        next += p.H;
-        const Buf vb = make_buf(vp + t0 * p.ldv, n * p.ldv * E);
+    unsigned v[4];
+    auto fetch = [&](int c) {  // the values of chunk c
+        const bool in = c < chunks;
+        const int64_t t = in ? (int64_t)c * kC : 0, n = in ? min((int64_t)kC, len - t) : 0;
+        const Buf vb = make_buf(vp + t * p.ldv, n * p.ldv * E);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) vn[r] = buf_load_bits<T>(vb, voff + (unsigned)(r * p.ldv) * E);
+        for (int r = 0; r < 4; ++r) v[r] = buf_load_bits<T>(vb, voff + (unsigned)(r * p.ldv) * E);
     };
-    auto stage = [&](char* half) {
-        kr.store(reinterpret_cast<T*>(half + L::ks), nullptr, 0);
-        ops.store(half);
-        if (W != kStates) {
-            qr.store(reinterpret_cast<T*>(half + L::qs), nullptr, 0);
-            opa.store(half + L::as);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = vn[r];
-    };
-    if (len > 0) {
-        fetch(0);
-        stage(lds);
-        if (kC < len) fetch(kC);
-    }
+    fetch(0);
 
-    int side = 0;
-    for (int64_t t0 = 0; t0 < len; t0 += kC) {
-        const int64_t n_tok = min((int64_t)kC, len - t0), here = entry;
-        entry += p.H;
-        const bool more = t0 + kC < len, update = more || (W != kStates && p.hT);
-        char* half = lds + side * L::half;
-        if (L::NB == 2) side ^= 1;
+    for (int c = 0; c < chunks; ++c, entry += p.H) {
+        const int64_t t0 = (int64_t)c * kC, n_tok = min((int64_t)kC, len - t0);
+        const bool update = c + 1 < chunks || (W != kStates && p.hT);
+        const char* half = lds + (L::NB == 2 && (c & 1) ? L::half : 0);
         const ChunkRows* rows = reinterpret_cast<const ChunkRows*>(half);
         const T *ts = reinterpret_cast<const T*>(half + L::ts), *as = reinterpret_cast<const T*>(half + L::as),
                 *ks = reinterpret_cast<const T*>(half + L::ks), *qs = reinterpret_cast<const T*>(half + L::qs);
@@ -176,7 +221,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
             const int td = wave * DT + d;
             if constexpr (W == kStates)
                 store_half_both<PY, P, NS>(S[d], sp, td >> 1, td & 1,
-                                           reinterpret_cast<T*>(p.w_s) + here * PY * vals * DK + (int64_t)col * DK + key + d * 16,
+                                           reinterpret_cast<T*>(p.w_s) + entry * PY * vals * DK + (int64_t)col * DK + key + d * 16,
                                            (int64_t)vals * DK);
             else
                 store_half<P, NS>(S[d], sp, td >> 1, td & 1);
@@ -186,6 +231,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
         f32x4 X[3], Y[3];
         zero3(X);
         zero3(Y);
+        const f32x4 be = four(rows->beta + tok), eg = four(rows->eg + tok), rk = four(rows->rk + tok);
         {
             Parts<T, 1> fk[NS], fq[NS];
             Parts<T, P> fs[NS];
@@ -198,14 +244,13 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
             }
             loads_end();
 #pragma unroll
-            for (int kb = 0; kb < NS; ++kb) {
-                mma_spread<1, P>(fk[kb], fs[kb], X, 0);
-                if constexpr (W != kStates)
+            for (int kb = 0; kb < NS; ++kb) mma_spread<1, P>(fk[kb], fs[kb], X, 0);
+            if constexpr (W != kStates)
+#pragma unroll
+                for (int kb = 0; kb < NS; ++kb)
 #pragma unroll
                     for (int q = PY - 1; q >= 0; --q) Y[(2 * kb + q) % 3] = mma(fq[kb].p[0], fs[kb].p[q], Y[(2 * kb + q) % 3]);
-            }
         }
-        const f32x4 be = four(rows->beta + tok), eg = four(rows->eg + tok), rk = four(rows->rk + tok);
         {
             const f32x4 x = gather3(X);
             f32x4 R;
@@ -213,6 +258,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
             for (int r = 0; r < 4; ++r) R[r] = be[r] * __builtin_fmaf(-(eg[r] * rk[r]), x[r], Io<T>::of_bits(v[r]));
             store_half<P, 2>(R, rp, wave >> 1, wave & 1);
         }
+        fetch(c + 1);
         Parts<T, P> ft[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) ft[kb] = load_parts<P>(ts, lower_frag(wave, wave < 2 ? 0 : kb));
@@ -224,82 +270,57 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) fr[kb] = load_exchange<P, 2>(rp, kb);
             loads_end();
-            f32x4 c[3];
-            zero3(c);
-            mma_spread<P, P>(ft[0], fr[0], c, 0);
-            if (wave >= 2) mma_spread<P, P>(ft[1], fr[1], c, 0);
-            U = gather3(c);
+            f32x4 u[3];
+            zero3(u);
+            mma_spread<P, P>(ft[0], fr[0], u, 0);
+            if (wave >= 2) mma_spread<P, P>(ft[1], fr[1], u, 0);
+            U = gather3(u);
         }
         store_half<P, 2>(U * (four(rows->er + tok) * rk), us, wave >> 1, wave & 1);
-        if constexpr (W == kStates) {
-            f32x4 x = U;
-            T* mem = reinterpret_cast<T*>(p.w_u) + here * PY * vals * kC + (int64_t)col * kC + tok;
-            if constexpr (sizeof(T) == 4) {
-                *reinterpret_cast<f32x4*>(mem) = x;
-            } else {
-#pragma unroll
-                for (int q = 0; q < PY; ++q) {
-                    bf16x4 b;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        b[j] = (__bf16)x[j];
-                        x[j] -= (float)b[j];
-                    }
-                    *reinterpret_cast<bf16x4*>(mem + (int64_t)q * vals * kC) = b;
-                }
-            }
-        } else {
+        if constexpr (W == kStates)
+            store_four<PY>(U, reinterpret_cast<T*>(p.w_u) + entry * PY * vals * kC + (int64_t)col * kC + tok, (int64_t)vals * kC);
+        else
             store_half<PY, 2>(U, up, wave >> 1, wave & 1);
-        }
-        if (L::NB == 2 && more) {
-            stage(lds + side * L::half);
-            if (t0 + 2 * kC < len) fetch(t0 + 2 * kC);
-        }
         lds_barrier();
-        if constexpr (W != kStates) {  // O = e^G Y + A U
-            Parts<T, PY> fa[2], fu[2];
+        // S = e^(G_C) S + (e^(G_C - G) K)^T U, O = e^G Y + A U
+        Parts<T, P> fu[2];
+        Parts<T, PY> fa[2], fo[2];
+        Parts<T, 1> fk[DT][2];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < 2; ++kb) {
+            fu[kb] = load_exchange<P, 2>(us, kb);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) fk[d][kb].p[0] = load_transposed<T>(ks + kb * 32 * Sh::KS + (wave * DT + d) * 16, Sh::KS);
+            if constexpr (W != kStates) {
                 fa[kb] = load_parts<PY>(as, lower_frag(wave, wave < 2 ? 0 : kb));
-                fu[kb] = load_exchange<PY, 2>(up, kb);
+                fo[kb] = load_exchange<PY, 2>(up, kb);
             }
-            loads_end();
+        }
+        loads_end();
+        if (update) {
+            const float ec = rows->eg[kC - 1];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                f32x4 x[3];
+                zero3(x);
+                x[0] = S[d] * ec;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) mma_spread<1, P>(fk[d][kb], fu[kb], x, 0);
+                S[d] = gather3(x);
+            }
+        }
+        if constexpr (W != kStates) {
             const f32x4 f = eg * four(rows->rq + tok) * p.scale;
 #pragma unroll
             for (int i = 0; i < 3; ++i) Y[i] *= f;
-            mma_spread<PY, PY>(fa[0], fu[0], Y, 0);
-            if (wave >= 2) mma_spread<PY, PY>(fa[1], fu[1], Y, 0);
+            mma_spread<PY, PY>(fa[0], fo[0], Y, 0);
+            if (wave >= 2) mma_spread<PY, PY>(fa[1], fo[1], Y, 0);
             const f32x4 o = gather3(Y);
             const Buf ob = make_buf(op + t0 * p.H * p.dv, n_tok * p.H * p.dv * E);
 #pragma unroll
             for (int r = 0; r < 4; ++r) buf_store<T>(ob, ooff + (unsigned)(r * p.H * p.dv) * E, from_f32<T>(o[r]));
         }
-        if (update) {
-            Parts<T, P> fu[2];
-            Parts<T, 1> fk[DT][2];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                fu[kb] = load_exchange<P, 2>(us, kb);
-#pragma unroll
-                for (int d = 0; d < DT; ++d) fk[d][kb].p[0] = load_transposed<T>(ks + kb * 32 * Sh::KS + (wave * DT + d) * 16, Sh::KS);
-            }
-            loads_end();
-            const float ec = rows->eg[kC - 1];
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                f32x4 c[3];
-                zero3(c);
-                c[0] = S[d] * ec;
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) mma_spread<1, P>(fk[d][kb], fu[kb], c, 0);
-                S[d] = gather3(c);
-            }
-        }
-        if (L::NB == 1 && more) {
-            lds_barrier();
-            stage(lds);
-            if (t0 + 2 * kC < len) fetch(t0 + 2 * kC);
-        }
+        if (L::NB == 1 && c + 1 < chunks) lds_barrier();
     }
     if (W == kStates || !p.hT) return;
     const Buf sb = make_buf(p.hT + sbase, (int64_t)p.dk * p.dv * 4);
@@ -311,13 +332,13 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_narrow_kernel(const De
 
 template <typename T, int DK, int P, Walk W> hipError_t launch_narrow(const DeltaParams& p, hipStream_t s) {
     constexpr int PY = P < 2 ? P : 2;
-    auto kern = delta_narrow_kernel<T, DK, P, W>;
+    auto kern = p.vec_k ? delta_narrow_kernel<T, DK, P, W, true> : delta_narrow_kernel<T, DK, P, W, false>;
     constexpr int bytes = NarrowLds<T, DK, P, (W == kStates ? 0 : PY), (W == kStates ? 2 * P : 2 * P + PY)>::bytes;
     const hipError_t e = allow_lds(kern, bytes);
     if (e != hipSuccess) return e;
     // (the backward's arrays have whole tiles of 64 columns)
     const unsigned tiles = W == kStates ? (p.dv + 63) / 64 * 4 : (p.dv + 15) / 16, units = (unsigned)p.rows * p.H * tiles;
-    hipLaunchKernelGGL(kern, dim3(units), dim3(kDeltaThreads), bytes, s, p, tiles, units);
+    hipLaunchKernelGGL(kern, dim3(units), dim3(kNarrowThreads), bytes, s, p, tiles, units);
     return hipGetLastError();
 }
 
