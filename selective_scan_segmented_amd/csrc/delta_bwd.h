@@ -15,7 +15,7 @@
 // (dS', dR, dV, the state's gradient) and, a workgroup to every chunk and head, the rest.
 #pragma once
 
-#include "delta_fwd.h"
+#include "delta_narrow.h"
 
 namespace sfm {
 
@@ -202,6 +202,194 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::group
     for (int d = 0; d < DK / 16; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r) buf_store<float>(sb, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u, dS[d][r]);
+}
+
+// The same with sixteen columns to a workgroup (delta_narrow.h): wave w has a quarter of the state gradient's keys and
+// the tokens 16 w .. + 15.
+template <typename T, int DK, int P, bool VEC>
+__global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_reverse_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+    constexpr int PW = P < 2 ? P : 2, E = (int)sizeof(T), DT = DK / 64, NS = DK / 32;
+    using Sh = ChunkShape<T, DK>;
+    using Ops = ChunkOperands<T, P>;
+    using L = NarrowLds<T, DK, P, P, 3 * P + 1>;  // dU, two factors of the state's update (P planes each), dO (exact)
+    extern __shared__ char lds[];
+    T *sp = reinterpret_cast<T*>(lds + L::sp), *up = reinterpret_cast<T*>(lds + L::xp), *wk = up + P * L::plane,
+      *wq = wk + P * L::plane, *gs = wq + P * L::plane;
+
+    const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
+    const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
+    int64_t first;
+    int len;
+    delta_row(p, s, first, len);
+    const int chunks = (len + kC - 1) / kC;
+    const int64_t entry0 = (int64_t)chunk_entry(p, s, first) * p.H + h;
+
+    if (wave_id() >= 4) {  // step i is chunk chunks - 1 - i
+        const T* qp = static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk;
+        const T* kp = static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk;
+        RowShare<T, DK> kr, qr;
+        Linear<Ops::bytes> ops;
+        static_assert(L::as == Ops::a, "T and A lie in LDS as in the workspace");
+        auto load = [&](int i, int piece) {
+            const bool in = i < chunks;
+            const int c = in ? chunks - 1 - i : 0;
+            const int64_t t = (int64_t)c * kC, n = in ? min((int64_t)kC, len - t) : 0;
+            if (piece == 0) {
+                kr.load(make_buf(kp + t * p.ldk, n * p.ldk * E), p.ldk, p.dk, VEC);
+                return;
+            }
+            qr.load(make_buf(qp + t * p.ldq, n * p.ldq * E), p.ldq, p.dk, VEC);
+            ops.load(p.w_ops + (entry0 + (int64_t)c * p.H) * Ops::bytes, in);
+        };
+        auto store = [&](char* to) {
+            kr.store(reinterpret_cast<T*>(to + L::ks), nullptr, 0);
+            qr.store(reinterpret_cast<T*>(to + L::qs), nullptr, 0);
+            ops.store(to);
+        };
+        narrow_loader<L::NB, L::half>(lds, chunks, load, store);
+        return;
+    }
+
+    __builtin_amdgcn_s_setprio(2);
+    const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4, tok = wave * 16 + g4;
+    const int col = (int)(unit - rh * tiles) * 16 + l16;
+    const int64_t obase = (first * p.H + h) * p.dv, ldo = (int64_t)p.H * p.dv;
+    const T* gop = static_cast<const T*>(p.dout) + obase;
+    T* dvp = static_cast<T*>(p.dv_) + obase;
+    const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
+    const int key = wave * 16 * DT + g4;
+    const unsigned soff = col < p.dv ? (unsigned)(key * p.dv + col) * 4u : kNowhere;
+    const unsigned ooff = col < p.dv ? (unsigned)(tok * ldo + col) * E : kNowhere;
+    const int vals = (p.dv + 63) / 64 * 64;
+
+    f32x4 dS[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) dS[d] = f32x4{0, 0, 0, 0};
+    if (p.dhT) {
+        const Buf b = make_buf(p.dhT + sbase, (int64_t)p.dk * p.dv * 4);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dS[d][r] = buf_load<float>(b, soff + (unsigned)((d * 16 + r) * p.dv) * 4u);
+    }
+    unsigned v[4];
+    auto fetch = [&](int c) {  // dO of chunk c
+        const int64_t t = c >= 0 ? (int64_t)c * kC : 0, n = c >= 0 ? min((int64_t)kC, len - t) : 0;
+        const Buf ob = make_buf(gop + t * ldo, n * ldo * E);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = buf_load_bits<T>(ob, ooff + (unsigned)(r * ldo) * E);
+    };
+    fetch(chunks - 1);
+
+    for (int i = 0; i < chunks; ++i) {
+        const int c = chunks - 1 - i;
+        const int64_t t0 = (int64_t)c * kC, n_tok = min((int64_t)kC, len - t0), entry = entry0 + (int64_t)c * p.H;
+        const char* half = lds + (L::NB == 2 && (i & 1) ? L::half : 0);
+        const ChunkRows* rows = reinterpret_cast<const ChunkRows*>(half);
+        const T *ts = reinterpret_cast<const T*>(half + L::ts), *as = reinterpret_cast<const T*>(half + L::as),
+                *ks = reinterpret_cast<const T*>(half + L::ks), *qs = reinterpret_cast<const T*>(half + L::qs);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            const int td = wave * DT + d;
+            store_half_both<PW, P, NS>(dS[d], sp, td >> 1, td & 1,
+                                       reinterpret_cast<T*>(p.w_ds) + entry * PW * vals * DK + (int64_t)col * DK + key + d * 16,
+                                       (int64_t)vals * DK);
+        }
+        f32x4 gov;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) gov[r] = Io<T>::of_bits(v[r]);
+        store_half<1, 2>(gov, gs, wave >> 1, wave & 1);
+        fetch(c - 1);
+        lds_barrier();
+        const f32x4 be = four(rows->beta + tok), eg = four(rows->eg + tok), rk = four(rows->rk + tok);
+        const f32x4 fq = eg * four(rows->rq + tok) * p.scale, fk = eg * rk;
+        // dU = e^(G_C - G) K dS' + A^T dO
+        {
+            Parts<T, 1> kk[NS], go[2];
+            Parts<T, P> fs[NS], at[2];
+#pragma unroll
+            for (int kb = 0; kb < NS; ++kb) {
+                fs[kb] = load_exchange<P, NS>(sp, kb);
+                kk[kb].p[0] = load_runs<T>(ks + (wave * 16 + l16) * Sh::KS + kb * 32 + g4);
+            }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                at[kb] = load_parts_transposed<P>(as, wave, wave < 2 ? kb : 1);
+                go[kb] = load_exchange<1, 2>(gs, kb);
+            }
+            loads_end();
+            f32x4 x[3];
+            zero3(x);
+#pragma unroll
+            for (int kb = 0; kb < NS; ++kb) mma_spread<1, P>(kk[kb], fs[kb], x, 0);
+            const f32x4 f = four(rows->er + tok) * rk;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) x[j] *= f;
+            if (wave < 2) mma_spread<P, 1>(at[0], go[0], x, 0);
+            mma_spread<P, 1>(at[1], go[1], x, 0);
+            store_half<P, 2>(gather3(x), up, wave >> 1, wave & 1);
+        }
+        store_half<P, 2>(gov * fq, wq, wave >> 1, wave & 1);
+        Parts<T, P> tt[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) tt[kb] = load_parts_transposed<P>(ts, wave, wave < 2 ? kb : 1);
+        lds_barrier();
+        // dR = T^T dU
+        f32x4 dR;
+        {
+            Parts<T, P> fu[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) fu[kb] = load_exchange<P, 2>(up, kb);
+            loads_end();
+            f32x4 x[3];
+            zero3(x);
+            if (wave < 2) mma_spread<P, P>(tt[0], fu[0], x, 0);
+            mma_spread<P, P>(tt[1], fu[1], x, 0);
+            dR = gather3(x);
+        }
+        const f32x4 gv = be * dR;
+        store_half<P, 2>(gv * -fk, wk, wave >> 1, wave & 1);
+        lds_barrier();
+        if (c > 0 || p.dh0) {
+            Parts<T, P> fw[2], fv[2];
+            Parts<T, 1> tk[DT][2], tq[DT][2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                fw[kb] = load_exchange<P, 2>(wk, kb);
+                fv[kb] = load_exchange<P, 2>(wq, kb);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    tk[d][kb].p[0] = load_transposed<T>(ks + kb * 32 * Sh::KS + (wave * DT + d) * 16, Sh::KS);
+                    tq[d][kb].p[0] = load_transposed<T>(qs + kb * 32 * Sh::KS + (wave * DT + d) * 16, Sh::KS);
+                }
+            }
+            loads_end();
+            const float ec = rows->eg[kC - 1];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                f32x4 x[3];
+                zero3(x);
+                x[0] = dS[d] * ec;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    mma_spread<1, P>(tk[d][kb], fw[kb], x, 0);
+                    mma_spread<1, P>(tq[d][kb], fv[kb], x, 1);
+                }
+                dS[d] = gather3(x);
+            }
+        }
+        const Buf db = make_buf(dvp + t0 * ldo, n_tok * ldo * E);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) buf_store<T>(db, ooff + (unsigned)(r * ldo) * E, from_f32<T>(gv[r]));
+        store_four<PW>(dR, reinterpret_cast<T*>(p.w_dr) + entry * PW * vals * kC + (int64_t)col * kC + tok, (int64_t)vals * kC);
+        if (L::NB == 1 && i + 1 < chunks) lds_barrier();
+    }
+    if (!p.dh0) return;
+    const Buf sb = make_buf(p.dh0 + sbase, (int64_t)p.dk * p.dv * 4);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) buf_store<float>(sb, soff + (unsigned)((d * 16 + r) * p.dv) * 4u, dS[d][r]);
 }
 
 // ---------------------------------------------------------------- per chunk and head
@@ -594,13 +782,16 @@ template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParam
     constexpr int PW = P < 2 ? P : 2;
     hipError_t e = launch_prepare<T, DK, P>(p, s);
     if (e != hipSuccess) return e;
-    e = launch_walk<T, DK, P, kStates>(p, s);
+    e = p.narrow ? launch_narrow<T, DK, P, kStates>(p, s) : launch_walk<T, DK, P, kStates>(p, s);
     if (e != hipSuccess) return e;
-    const unsigned tiles = (p.dv + 63) / 64, units = (unsigned)p.rows * p.H * tiles;
-    auto rev = delta_reverse_kernel<T, DK, P>;
-    constexpr int rb = WalkLds<T, DK, P>::bytes, gb = GradLds<T, DK, PW>::bytes;
+    constexpr int gb = GradLds<T, DK, PW>::bytes;
+    const unsigned tiles = (p.dv + 63) / 64 * (p.narrow ? 4 : 1), units = (unsigned)p.rows * p.H * tiles;
+    auto rev = !p.narrow ? delta_reverse_kernel<T, DK, P>
+               : p.vec_k ? delta_narrow_reverse_kernel<T, DK, P, true>
+                         : delta_narrow_reverse_kernel<T, DK, P, false>;
+    const int rb = p.narrow ? NarrowLds<T, DK, P, P, 3 * P + 1>::bytes : WalkLds<T, DK, P>::bytes;
     if ((e = allow_lds(rev, rb)) != hipSuccess) return e;
-    hipLaunchKernelGGL(rev, dim3(units), dim3(kDeltaThreads), rb, s, p, tiles, units);
+    hipLaunchKernelGGL(rev, dim3(units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), rb, s, p, tiles, units);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), cu = (unsigned)p.rows * chunks * p.H;
     auto grads = delta_grads_kernel<T, DK, PW>;

@@ -107,27 +107,33 @@ template <typename T, int DK, int P, int PA, int PX> struct NarrowLds {
 
 constexpr int kNarrowThreads = 2 * kDeltaThreads;
 
-// What a loading wave does for a row's chunks: chunk number i from memory to registers (load) and on to LDS (store).
-// The compute waves' barriers: the first of chunk c after which the other half is free and before which chunk c's
-// operands are written, and two more; with one half, a fourth at the chunk's end.
+// What a loading wave does for a row's chunks: chunk number i from memory to registers (load, in two pieces) and on to
+// LDS (store).  The compute waves' barriers: the first of chunk c after which the other half is free and before which
+// chunk c's operands are written, and two more; with one half, a fourth at the chunk's end.  Everyone waits for the
+// last at a barrier, so the loads are spread over the time between them: little after the second, where the compute
+// waves have the least to do.
 template <int NB, int HALF, typename Load, typename Store>
 __device__ __forceinline__ void narrow_loader(char* lds, int chunks, Load load, Store store) {
     if (chunks <= 0) return;
-    load(0);
+    load(0, 0);
+    load(0, 1);
     store(lds);
-    load(1);
+    load(1, 0);
+    load(1, 1);
     for (int c = 0; c < chunks; ++c) {
         lds_barrier();
         if (NB == 2) {
             store(lds + (c & 1 ? 0 : HALF));
-            load(c + 2);
+            load(c + 2, 0);
         }
         lds_barrier();
         lds_barrier();
+        if (NB == 2) load(c + 2, 1);
         if (NB == 1 && c + 1 < chunks) {
             lds_barrier();
             store(lds);
-            load(c + 2);
+            load(c + 2, 0);
+            load(c + 2, 1);
         }
     }
 }
@@ -157,11 +163,14 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_kernel(const D
         Linear<PY * L::frag_bytes> opa;
         // Behind the row's end the buffers are empty: with no branch around a load the compiler knows how many are in
         // flight and waits for no more than it needs.
-        auto load = [&](int c) {
+        auto load = [&](int c, int piece) {
             const bool in = c < chunks;
             const int64_t t = in ? (int64_t)c * kC : 0, n = in ? min((int64_t)kC, len - t) : 0;
             const char* o = p.w_ops + (entry + (in ? (int64_t)c * p.H : 0)) * Ops::bytes;
-            kr.load(make_buf(kp + t * p.ldk, n * p.ldk * E), p.ldk, p.dk, VEC);
+            if (piece == 0) {
+                kr.load(make_buf(kp + t * p.ldk, n * p.ldk * E), p.ldk, p.dk, VEC);
+                return;
+            }
             if (W != kStates) qr.load(make_buf(qp + t * p.ldq, n * p.ldq * E), p.ldq, p.dk, VEC);
             ops.load(o, in);
             if (W != kStates) opa.load(o + Ops::a, in);
@@ -176,6 +185,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_kernel(const D
         return;
     }
 
+    __builtin_amdgcn_s_setprio(2);  // before the loading waves of the same unit
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4, tok = wave * 16 + g4;
     const int col = (int)(unit - rh * tiles) * 16 + l16;
     const T* vp = static_cast<const T*>(p.v) + first * p.ldv + (int64_t)h * p.dv;

@@ -291,6 +291,7 @@ sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
     p.w_ops = ws + w.ops, p.w_s = ws + w.s, p.w_ds = ws + w.ds, p.w_u = ws + w.u, p.w_dr = ws + w.dr;
     p.w_dq = reinterpret_cast<float*>(ws + w.dq), p.w_dk = reinterpret_cast<float*>(ws + w.dk);
     p.vec_o = aligned16(dout) && dv * e % 16 == 0;
+    p.narrow = sfm::plan_delta_narrow(rows, H, dv);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     return hip_status(io_dtype == SFM_F32 ? sfm::launch_delta_bwd_f32(p, hs) : sfm::launch_delta_bwd_bf16(p, hs), fn);
 }
