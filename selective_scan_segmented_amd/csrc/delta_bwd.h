@@ -19,9 +19,9 @@
 
 namespace sfm {
 
-// The walk back: as delta_walk_kernel, a workgroup to a (row, head) and 64 columns, from the last chunk to the first.
+// The walk back: as the walk forward, a workgroup to a (row, head) and 64 columns, from the last chunk to the first.
 template <typename T, int DK, int P>
-__global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_reverse_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+__device__ __forceinline__ void reverse(const DeltaParams& p, unsigned tiles, unsigned unit) {
     using Sh = ChunkShape<T, DK>;
     using L = WalkLds<T, DK, P>;
     using Ops = ChunkOperands<T, P>;
@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::group
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs),
       *as = reinterpret_cast<T*>(lds + L::as), *ts = reinterpret_cast<T*>(lds + L::ts);
 
-    const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
+    const unsigned rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
     const int col = (int)(unit - rh * tiles) * 64 + wave * 16 + l16;
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::group
 // The same with sixteen columns to a workgroup (delta_narrow.h): wave w has a quarter of the state gradient's keys and
 // the tokens 16 w .. + 15.
 template <typename T, int DK, int P, bool VEC>
-__global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_reverse_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+__device__ __forceinline__ void narrow_reverse(const DeltaParams& p, unsigned tiles, unsigned unit) {
     constexpr int PW = P < 2 ? P : 2, E = (int)sizeof(T), DT = DK / 64, NS = DK / 32;
     using Sh = ChunkShape<T, DK>;
     using Ops = ChunkOperands<T, P>;
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_reverse_kernel
     T *sp = reinterpret_cast<T*>(lds + L::sp), *up = reinterpret_cast<T*>(lds + L::xp), *wk = up + P * L::plane,
       *wq = wk + P * L::plane, *gs = wq + P * L::plane;
 
-    const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
+    const unsigned rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     int64_t first;
     int len;
@@ -390,6 +390,23 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_reverse_kernel
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r) buf_store<float>(sb, soff + (unsigned)((d * 16 + r) * p.dv) * 4u, dS[d][r]);
+}
+
+// Both walks in one launch: they need nothing of each other, and each alone often leaves units idle (2 x 4002 tokens,
+// 8 heads of 128: 92 us and 163 us one after the other).
+template <typename T, int DK, int P>
+__global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_walks_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+    if (blockIdx.x < units)  // (the longer one first)
+        reverse<T, DK, P>(p, tiles, die_local(blockIdx.x, units));
+    else
+        walk<T, DK, P, kStates>(p, tiles, die_local(blockIdx.x - units, units));
+}
+template <typename T, int DK, int P, bool VEC>
+__global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_walks_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+    if (blockIdx.x < units)
+        narrow_reverse<T, DK, P, VEC>(p, tiles, die_local(blockIdx.x, units));
+    else
+        narrow_walk<T, DK, P, kStates, VEC>(p, tiles, die_local(blockIdx.x - units, units));
 }
 
 // ---------------------------------------------------------------- per chunk and head
@@ -753,27 +770,33 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)
     }
 }
 
-// Shared key heads: the value heads' shares, in order.  A workgroup to every 64 tokens of a row and key head.
-template <typename T>
+// Shared key heads: the value heads' shares, in order.  A workgroup to every 16 tokens of a row's 64 and key head; a
+// thread takes V neighbouring keys.
+template <typename T, int V>
 __global__ __launch_bounds__(kDeltaThreads) void delta_share_kernel(const DeltaParams p, unsigned chunks) {
-    const unsigned sc = blockIdx.x / (unsigned)p.Hk;
-    const int hk = (int)(blockIdx.x - sc * (unsigned)p.Hk), s = (int)(sc / chunks);
+    typedef float vec __attribute__((ext_vector_type(V)));
+    const unsigned sq = blockIdx.x / (unsigned)p.Hk, sc = sq / 4;
+    const int hk = (int)(blockIdx.x - sq * (unsigned)p.Hk), s = (int)(sc / chunks);
     int64_t first;
     int len;
     delta_row(p, s, first, len);
-    const int64_t t0 = (int64_t)(sc - s * chunks) * kC;
-    if (t0 >= len) return;
-    const int n = (int)min((int64_t)kC, len - t0), ct = threadIdx.x & 31;
+    const int64_t t0 = (int64_t)(sc - s * chunks) * kC + (sq & 3) * 16;
+    const int n = (int)min((int64_t)16, len - t0), ct = (threadIdx.x & 31) * V;
     for (int t = threadIdx.x >> 5; t < n; t += kDeltaThreads / 32) {
         const int64_t tok = first + t0 + t, from = (tok * p.H + (int64_t)hk * p.share) * p.dk, to = (tok * p.Hk + hk) * p.dk;
-        for (int c = ct; c < p.dk; c += 32) {
-            float a = 0.0f, b = 0.0f;
+        for (int c = ct; c < p.dk; c += 32 * V) {
+            vec a, b;
+#pragma unroll
+            for (int e = 0; e < V; ++e) a[e] = b[e] = 0.0f;
             for (int j = 0; j < p.share; ++j) {
-                a += p.w_dq[from + j * p.dk + c];
-                b += p.w_dk[from + j * p.dk + c];
+                a += *reinterpret_cast<const vec*>(p.w_dq + from + j * p.dk + c);
+                b += *reinterpret_cast<const vec*>(p.w_dk + from + j * p.dk + c);
             }
-            static_cast<T*>(p.dq)[to + c] = from_f32<T>(a);
-            static_cast<T*>(p.dk_)[to + c] = from_f32<T>(b);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                static_cast<T*>(p.dq)[to + c + e] = from_f32<T>(a[e]);
+                static_cast<T*>(p.dk_)[to + c + e] = from_f32<T>(b[e]);
+            }
         }
     }
 }
@@ -782,23 +805,26 @@ template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParam
     constexpr int PW = P < 2 ? P : 2;
     hipError_t e = launch_prepare<T, DK, P>(p, s);
     if (e != hipSuccess) return e;
-    e = p.narrow ? launch_narrow<T, DK, P, kStates>(p, s) : launch_walk<T, DK, P, kStates>(p, s);
-    if (e != hipSuccess) return e;
     constexpr int gb = GradLds<T, DK, PW>::bytes;
     const unsigned tiles = (p.dv + 63) / 64 * (p.narrow ? 4 : 1), units = (unsigned)p.rows * p.H * tiles;
-    auto rev = !p.narrow ? delta_reverse_kernel<T, DK, P>
-               : p.vec_k ? delta_narrow_reverse_kernel<T, DK, P, true>
-                         : delta_narrow_reverse_kernel<T, DK, P, false>;
-    const int rb = p.narrow ? NarrowLds<T, DK, P, P, 3 * P + 1>::bytes : WalkLds<T, DK, P>::bytes;
-    if ((e = allow_lds(rev, rb)) != hipSuccess) return e;
-    hipLaunchKernelGGL(rev, dim3(units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), rb, s, p, tiles, units);
+    auto walks = !p.narrow ? delta_walks_kernel<T, DK, P>
+                 : p.vec_k ? delta_narrow_walks_kernel<T, DK, P, true>
+                           : delta_narrow_walks_kernel<T, DK, P, false>;
+    constexpr int nb = NarrowLds<T, DK, P, P, 3 * P + 1>::bytes, ns = NarrowLds<T, DK, P, 0, 2 * P>::bytes;
+    const int wb = p.narrow ? (nb > ns ? nb : ns) : WalkLds<T, DK, P>::bytes;
+    if ((e = allow_lds(walks, wb)) != hipSuccess) return e;
+    hipLaunchKernelGGL(walks, dim3(2 * units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), wb, s, p, tiles, units);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), cu = (unsigned)p.rows * chunks * p.H;
     auto grads = delta_grads_kernel<T, DK, PW>;
     if ((e = allow_lds(grads, gb)) != hipSuccess) return e;
     hipLaunchKernelGGL(grads, dim3(cu), dim3(kDeltaThreads), gb, s, p, chunks, cu, ChunkOperands<T, P>::bytes);
     if ((e = hipGetLastError()) != hipSuccess || p.share == 1) return e;
-    hipLaunchKernelGGL(delta_share_kernel<T>, dim3((unsigned)p.rows * chunks * p.Hk), dim3(kDeltaThreads), 0, s, p, chunks);
+    const dim3 sg((unsigned)p.rows * chunks * 4 * p.Hk);
+    if (p.dk % 4 == 0)
+        hipLaunchKernelGGL((delta_share_kernel<T, 4>), sg, dim3(kDeltaThreads), 0, s, p, chunks);
+    else
+        hipLaunchKernelGGL((delta_share_kernel<T, 1>), sg, dim3(kDeltaThreads), 0, s, p, chunks);
     return hipGetLastError();
 }
 

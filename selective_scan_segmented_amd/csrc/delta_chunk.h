@@ -165,15 +165,33 @@ template <typename T, int DK> __device__ __forceinline__ f32x4 rows_product(cons
 // registers (a[n - 2]; lane: row i = l % 16, columns 4 (l / 16) .. + 3) until M's place is free.
 template <typename T, int DK>
 __device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const ChunkRows* rows, float scale, float* mt, f32x4 (&a)[3]) {
+    using Sh = ChunkShape<T, DK>;
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
     f32x4 c[5];
 #pragma unroll
-    for (int n = 0; n < 5; ++n) {
-        const int id = wave + 4 * n;
-        const bool m = id < 10;
-        int ti, tj;
-        lower_tile(m ? id : id - 10, ti, tj);
-        c[n] = rows_product<T, DK>(ks, m ? ti : tj, m ? ks : qs, m ? tj : ti);
+    for (int n = 0; n < 5; ++n) c[n] = f32x4{0, 0, 0, 0};
+    constexpr int step = sizeof(T) == 4 ? 32 : 64;  // keys whose fragments are loaded together
+#pragma unroll
+    for (int k0 = 0; k0 < DK; k0 += step) {
+        Frag<T> fa[5][step / 32], fb[5][step / 32];
+#pragma unroll
+        for (int n = 0; n < 5; ++n) {
+            const int id = wave + 4 * n;
+            const bool m = id < 10;
+            int ti, tj;
+            lower_tile(m ? id : id - 10, ti, tj);
+            const int at = l16 * Sh::KS + g4 + k0;
+#pragma unroll
+            for (int i = 0; i < step / 32; ++i) {
+                fa[n][i] = load_runs<T>(ks + (m ? ti : tj) * 16 * Sh::KS + at + i * 32);
+                fb[n][i] = load_runs<T>((m ? ks : qs) + (m ? tj : ti) * 16 * Sh::KS + at + i * 32);
+            }
+        }
+        loads_end();
+#pragma unroll
+        for (int i = 0; i < step / 32; ++i)
+#pragma unroll
+            for (int n = 0; n < 5; ++n) c[n] = mma(fa[n][i], fb[n][i], c[n]);
     }
 #pragma unroll
     for (int n = 0; n < 5; ++n) {
@@ -269,25 +287,33 @@ template <int PT, typename T> __device__ __forceinline__ void store_t(const f32x
         if (j <= (wave | 1)) store_tile<PT>(t[j], ts, wave, j);
 }
 
-// Gates, K and Q (in registers) to LDS, then M, T and A, all by the whole workgroup: T (PT parts) at ts and A (PA
-// parts) at as, where M lies before.  Ends with T and A visible to all.
-template <typename T, int DK, int PT, int PA, typename Between>
-__device__ __forceinline__ void build_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const DeltaParams& p,
-                                            const T* g, const T* beta, int n, ChunkRows* rows, T* ks, T* qs, T* as,
-                                            T* ts, Between between) {
-    float* mt = reinterpret_cast<float*>(as);
+// Gates, K and Q (in registers) to LDS, then M in LDS and, in registers, A's tiles and this wave's rows of T, all by
+// the whole workgroup.  `after` runs between M's making and its use (what needs K, Q or A only).
+template <typename T, int DK, typename After>
+__device__ __forceinline__ void make_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const DeltaParams& p,
+                                           const T* g, const T* beta, int n, ChunkRows* rows, T* ks, T* qs, float* mt,
+                                           f32x4 (&a)[3], f32x4 (&t)[4], After after) {
     kr.store(ks, rows->rk, p.l2norm);
     qr.store(qs, rows->rq, p.l2norm);
     if (wave_id() == 0) chunk_gates<T>(g, beta, p.H, n, rows);
     lds_barrier();
-    f32x4 a[3], t[4];
     chunk_products<T, DK>(ks, qs, rows, p.scale, mt, a);
     lds_barrier();
+    after();
     invert_diagonal(mt);
     lds_barrier();
     inverse_rows(mt, t);
+}
+
+// The same with T (PT parts) at ts and A (PA parts) at as, where M lies before, visible to all at the end.
+template <typename T, int DK, int PT, int PA, typename Between>
+__device__ __forceinline__ void build_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const DeltaParams& p,
+                                            const T* g, const T* beta, int n, ChunkRows* rows, T* ks, T* qs, T* as,
+                                            T* ts, Between between) {
+    f32x4 a[3], t[4];
+    make_chunk<T, DK>(kr, qr, p, g, beta, n, rows, ks, qs, reinterpret_cast<float*>(as), a, t, [] {});
     store_t<PT>(t, ts);
-    between();       // what needs K and Q only
+    between();     // what needs K and Q only
     lds_barrier();  // M is done with
     store_a<PA>(a, as);
     lds_barrier();

@@ -12,10 +12,11 @@ namespace sfm {
 
 // kWhole: T and A of a chunk are made on the way (rows of few chunks, or enough rows to fill the card while some
 // workgroups do that).  kPrepared: they come from the preparing kernel.  kStates: likewise, and instead of outputs
-// the states before the chunks and U are written down, for the backward.
-enum Walk { kWhole, kPrepared, kStates };
+// the states before the chunks and U are written down, for the backward.  kSingle: kWhole for rows of one chunk that
+// begin and end without a state, which leaves R = beta V, U = T R, O = A U.
+enum Walk { kWhole, kPrepared, kStates, kSingle };
 
-template <typename T, int DK, int P> struct WalkLds {
+template <typename T, int DK, int P> struct WalkLds {  // P: parts of T and A
     using Sh = ChunkShape<T, DK>;
     static constexpr int frag_bytes = kLowerFrags * kFragSize * (int)sizeof(T);
     static constexpr int rows = 0;
@@ -28,7 +29,7 @@ template <typename T, int DK, int P> struct WalkLds {
 };
 
 template <typename T, int DK, int P, Walk W>
-__global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+__device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsigned unit) {
     using Sh = ChunkShape<T, DK>;
     using L = WalkLds<T, DK, P>;
     using Ops = ChunkOperands<T, P>;
@@ -39,7 +40,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs),
       *as = reinterpret_cast<T*>(lds + L::as), *ts = reinterpret_cast<T*>(lds + L::ts);
 
-    const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
+    const unsigned rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
     const int col = (int)(unit - rh * tiles) * 64 + wave * 16 + l16;
@@ -63,14 +64,14 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
     f32x4 S[DK / 16];
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d) S[d] = f32x4{0, 0, 0, 0};
-    if (p.h0) {
+    if (W != kSingle && p.h0) {
         const Buf b = make_buf(p.h0 + sbase, (int64_t)p.dk * p.dv * 4);
 #pragma unroll
         for (int d = 0; d < DK / 16; ++d)
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[d][r] = buf_load<float>(b, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u);
     }
-    bool zero = !p.h0;  // the state is zero: its products are left out
+    bool zero = W == kSingle || !p.h0;  // the state is zero: its products are left out
 
     RowShare<T, DK> kr, qr;
     Linear<Ops::a> ops;                // row scalars and T
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
         const int64_t n = min((int64_t)kC, len - t0);
         kr.load(make_buf(kp + t0 * p.ldk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
         if (W != kStates) qr.load(make_buf(qp + t0 * p.ldq, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
-        if (W != kWhole) {
+        if (W == kPrepared || W == kStates) {
             const char* o = p.w_ops + entry * Ops::bytes;
             ops.load(o);
             if (W == kPrepared) opa.load(o + Ops::a);
@@ -91,7 +92,8 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(vb, fresh(voff) + (unsigned)((rt * 16 + r) * p.ldv) * E);
     };
-    if (W != kWhole && len > 0) fetch(0);  // ahead of its use by a chunk
+    constexpr bool kOnTheWay = W == kWhole || W == kSingle;
+    if (!kOnTheWay && len > 0) fetch(0);  // ahead of its use by a chunk
 
     for (int64_t t0 = 0; t0 < len; t0 += kC) {
         const int64_t n_tok = min((int64_t)kC, len - t0);
@@ -102,7 +104,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
         for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = f32x4{0, 0, 0, 0};
         // X = K S, Y = Q S; then R = beta (V - e^G X) in X's place
         auto state_products = [&] {
-            if (!zero || W == kStates) {
+            if (W == kStates || (W != kSingle && !zero)) {
                 Frag<T> fk[2][4], fq[2][4];
                 auto load = [&](int kb) {
 #pragma unroll
@@ -112,7 +114,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
                         if constexpr (W != kStates) fq[kb & 1][rt] = load_runs<T>(qs + at);
                     }
                 };
-                constexpr int ahead = W == kWhole && DK == 128 ? 0 : 1;  // (registers for two workgroups to a unit)
+                constexpr int ahead = kOnTheWay && DK == 128 ? 0 : 1;  // (registers for two workgroups to a unit)
                 if (ahead) load(0);
 #pragma unroll
                 for (int kb = 0; kb < DK / 32; ++kb) {
@@ -137,12 +139,13 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
             for (int rt = 0; rt < 4; ++rt) {
                 const f32x4 be = four(rows->beta + rt * 16 + g4), f = four(rows->eg + rt * 16 + g4) * four(rows->rk + rt * 16 + g4);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) X[rt][r] = be[r] * __builtin_fmaf(-f[r], X[rt][r], Io<T>::of_bits(v[rt][r]));
+                for (int r = 0; r < 4; ++r)
+                    X[rt][r] = be[r] * (W == kSingle ? Io<T>::of_bits(v[rt][r]) : __builtin_fmaf(-f[r], X[rt][r], Io<T>::of_bits(v[rt][r])));
             }
         };
-        if (W == kWhole) fetch(t0);  // (registers that other workgroups on the unit can use better)
+        if (kOnTheWay) fetch(t0);  // (registers that other workgroups on the unit can use better)
         lds_barrier();  // the chunk before is done with LDS
-        if constexpr (W == kWhole) {
+        if constexpr (kOnTheWay) {
             build_chunk<T, DK, P, PY>(kr, qr, p, gp + t0 * p.H, bp + t0 * p.H, (int)n_tok, rows, ks, qs, as, ts, state_products);
         } else {
             kr.store(ks, nullptr, 0);
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
             for (int f = 0; f < kLowerFrags; ++f) ap[f] = load_parts<PY>(as, f);
             loads_end();
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) Y[rt] *= four(rows->eg + rt * 16 + g4) * four(rows->rq + rt * 16 + g4) * p.scale;
+            for (int rt = 0; rt < 4 && W != kSingle; ++rt) Y[rt] *= four(rows->eg + rt * 16 + g4) * four(rows->rq + rt * 16 + g4) * p.scale;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) split<PY>(U[2 * kb], U[2 * kb + 1], up[kb]);
 #pragma unroll
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
                     buf_store<T>(ob, fresh(ooff) + (unsigned)((rt * 16 + r) * p.H * p.dv) * E, from_f32<T>(Y[rt][r]));
         }
         zero = false;
-        if (t0 + kC >= len && (W == kStates || !p.hT)) break;  // nobody asks for the state after the last chunk
+        if (W == kSingle || (t0 + kC >= len && (W == kStates || !p.hT))) break;  // nobody asks for the state after the last chunk
         const float ec = rows->eg[kC - 1];
         Parts<T, P> up[2];
 #pragma unroll
@@ -224,7 +227,7 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
                     for (int d = 0; d < kHalf; ++d) S[half * kHalf + d] = mma(f[d][kb], up[kb].p[q], S[half * kHalf + d]);
         }
     }
-    if (W == kStates || !p.hT) return;
+    if (W == kStates || W == kSingle || !p.hT) return;
     const Buf sb = make_buf(p.hT + sbase, (int64_t)p.dk * p.dv * 4);
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d)
@@ -232,16 +235,25 @@ __global__ __launch_bounds__(kDeltaThreads, (W == kWhole || DK == 64 ? WalkLds<T
         for (int r = 0; r < 4; ++r) buf_store<float>(sb, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u, S[d][r]);
 }
 
-// T, A and the row scalars of every chunk and head, a workgroup to each.
+template <typename T, int DK, int P, Walk W>
+__global__ __launch_bounds__(kDeltaThreads, (W == kSingle && sizeof(T) == 2 ? 3 : W != kPrepared || DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+    walk<T, DK, P, W>(p, tiles, die_local(blockIdx.x, units));
+}
+
+// T, A and the row scalars of every chunk and head, a workgroup to each.  T and A go from registers to memory.
+template <typename T, int DK> struct PrepareLds {
+    static constexpr int rows = 0, mt = (int)sizeof(ChunkRows), ks = mt + kBytesM, qs = ks + ChunkShape<T, DK>::row_bytes,
+                         bytes = qs + ChunkShape<T, DK>::row_bytes;
+    static constexpr int groups = 160 * 1024 / bytes < 3 ? 160 * 1024 / bytes : 3;
+};
 template <typename T, int DK, int P>
-__global__ __launch_bounds__(kDeltaThreads, (WalkLds<T, DK, P>::groups)) void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) {
-    using L = WalkLds<T, DK, P>;
+__global__ __launch_bounds__(kDeltaThreads, (PrepareLds<T, DK>::groups)) void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) {
+    using L = PrepareLds<T, DK>;
     using Ops = ChunkOperands<T, P>;
     constexpr int E = (int)sizeof(T);
     extern __shared__ char lds[];
     ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
-    T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs),
-      *as = reinterpret_cast<T*>(lds + L::as), *ts = reinterpret_cast<T*>(lds + L::ts);
+    T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs);
     const unsigned unit = die_local(blockIdx.x, units);
     const int h = (int)(unit % (unsigned)p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     const unsigned sc = unit / (unsigned)p.H;
@@ -257,12 +269,15 @@ __global__ __launch_bounds__(kDeltaThreads, (WalkLds<T, DK, P>::groups)) void de
     kr.load(make_buf(static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
     qr.load(make_buf(static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
     const int64_t at = first * p.H + h;
-    build_chunk<T, DK, P, P>(kr, qr, p, static_cast<const T*>(p.g) + at, static_cast<const T*>(p.beta) + at, (int)n, rows,
-                             ks, qs, as, ts, [] {});
     char* o = p.w_ops + ((int64_t)(chunk_entry(p, s, first - t0) + (unsigned)(t0 / kC)) * p.H + h) * Ops::bytes;
-    for (int u = threadIdx.x * 16; u < Ops::a; u += kDeltaThreads * 16) *reinterpret_cast<uint4*>(o + u) = *reinterpret_cast<const uint4*>(lds + u);
-    for (int u = threadIdx.x * 16; u < P * L::frag_bytes; u += kDeltaThreads * 16)
-        *reinterpret_cast<uint4*>(o + Ops::a + u) = *reinterpret_cast<const uint4*>(lds + L::as + u);
+    f32x4 a[3], t[4];
+    make_chunk<T, DK>(kr, qr, p, static_cast<const T*>(p.g) + at, static_cast<const T*>(p.beta) + at, (int)n, rows, ks, qs,
+                      reinterpret_cast<float*>(lds + L::mt), a, t, [&] {
+                          store_a<P>(a, reinterpret_cast<T*>(o + Ops::a));
+                          if (threadIdx.x < sizeof(ChunkRows) / 16)
+                              reinterpret_cast<uint4*>(o)[threadIdx.x] = reinterpret_cast<const uint4*>(lds)[threadIdx.x];
+                      });
+    store_t<P>(t, reinterpret_cast<T*>(o + Ops::t));
 }
 
 static_assert(ChunkOperands<float, 1>::bytes == 7 * kC * 4 + 2 * 6 * 64 * 8 * 4 &&
@@ -286,7 +301,7 @@ template <typename T, int DK, int P, Walk W> hipError_t launch_walk(const DeltaP
 
 template <typename T, int DK, int P> hipError_t launch_prepare(const DeltaParams& p, hipStream_t s) {
     auto kern = delta_prepare_kernel<T, DK, P>;
-    constexpr int bytes = WalkLds<T, DK, P>::bytes;
+    constexpr int bytes = PrepareLds<T, DK>::bytes;
     const hipError_t e = allow_lds(kern, bytes);
     if (e != hipSuccess) return e;
     const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), units = (unsigned)p.rows * chunks * p.H;

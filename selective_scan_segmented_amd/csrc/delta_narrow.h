@@ -139,7 +139,7 @@ __device__ __forceinline__ void narrow_loader(char* lds, int chunks, Load load, 
 }
 
 template <typename T, int DK, int P, Walk W, bool VEC>
-__global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+__device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles, unsigned unit) {
     constexpr int PY = P < 2 ? P : 2, E = (int)sizeof(T), DT = DK / 64, NS = DK / 32;
     using Sh = ChunkShape<T, DK>;
     using Ops = ChunkOperands<T, P>;
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_kernel(const D
     extern __shared__ char lds[];
     T *sp = reinterpret_cast<T*>(lds + L::sp), *rp = reinterpret_cast<T*>(lds + L::xp), *us = rp + P * L::plane, *up = us + P * L::plane;
 
-    const unsigned unit = die_local(blockIdx.x, units), rh = unit / tiles;
+    const unsigned rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     int64_t first;
     int len;
@@ -340,23 +340,29 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_kernel(const D
         for (int r = 0; r < 4; ++r) buf_store<float>(sb, soff + (unsigned)((d * 16 + r) * p.dv) * 4u, S[d][r]);
 }
 
-template <typename T, int DK, int P, Walk W> hipError_t launch_narrow(const DeltaParams& p, hipStream_t s) {
+template <typename T, int DK, int P, bool VEC>
+__global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+    narrow_walk<T, DK, P, kPrepared, VEC>(p, tiles, die_local(blockIdx.x, units));
+}
+
+template <typename T, int DK, int P> hipError_t launch_narrow(const DeltaParams& p, hipStream_t s) {
     constexpr int PY = P < 2 ? P : 2;
-    auto kern = p.vec_k ? delta_narrow_kernel<T, DK, P, W, true> : delta_narrow_kernel<T, DK, P, W, false>;
-    constexpr int bytes = NarrowLds<T, DK, P, (W == kStates ? 0 : PY), (W == kStates ? 2 * P : 2 * P + PY)>::bytes;
+    auto kern = p.vec_k ? delta_narrow_kernel<T, DK, P, true> : delta_narrow_kernel<T, DK, P, false>;
+    constexpr int bytes = NarrowLds<T, DK, P, PY, 2 * P + PY>::bytes;
     const hipError_t e = allow_lds(kern, bytes);
     if (e != hipSuccess) return e;
-    // (the backward's arrays have whole tiles of 64 columns)
-    const unsigned tiles = W == kStates ? (p.dv + 63) / 64 * 4 : (p.dv + 15) / 16, units = (unsigned)p.rows * p.H * tiles;
+    const unsigned tiles = (p.dv + 15) / 16, units = (unsigned)p.rows * p.H * tiles;
     hipLaunchKernelGGL(kern, dim3(units), dim3(kNarrowThreads), bytes, s, p, tiles, units);
     return hipGetLastError();
 }
 
 template <typename T, int DK, int P> hipError_t launch_forward(const DeltaParams& p, hipStream_t s) {
+    if (!p.w_ops && p.L <= kC && !p.h0 && !p.hT)
+        if constexpr (P < 3) return launch_walk<T, DK, P, kSingle>(p, s);  // (three parts only with states)
     if (!p.w_ops) return launch_walk<T, DK, P, kWhole>(p, s);
     const hipError_t e = launch_prepare<T, DK, P>(p, s);
     if (e != hipSuccess) return e;
-    return p.narrow ? launch_narrow<T, DK, P, kPrepared>(p, s) : launch_walk<T, DK, P, kPrepared>(p, s);
+    return p.narrow ? launch_narrow<T, DK, P>(p, s) : launch_walk<T, DK, P, kPrepared>(p, s);
 }
 
 }  // namespace sfm

@@ -108,7 +108,7 @@ int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, 
 // SFM_DELTA_NARROW=0|1 overrides (tuning and tests).
 bool sfm::plan_delta_narrow(int64_t rows, int64_t H, int64_t dv) {
     if (const char* e = std::getenv("SFM_DELTA_NARROW")) return e[0] == '1';
-    return rows * H * ((dv + 63) / 64) <= 256;
+    return rows * H * ((dv + 63) / 64) <= 128;
 }
 
 extern "C" {
@@ -251,7 +251,7 @@ sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
     if (st != SFM_OK) return st;
     if (tokens > 0 && (!dout || !dq || !dk_out || !dv_out || !dg || !dbeta))
         return fail(SFM_ERR_NULL, "%s: dout, dq, dk, dv, dg and dbeta are required", fn);
-    if (rows * H > INT32_MAX / ((L + sfm::kDeltaChunk - 1) / sfm::kDeltaChunk))
+    if (rows * H > INT32_MAX / 4 / ((L + sfm::kDeltaChunk - 1) / sfm::kDeltaChunk))
         return fail(SFM_ERR_SHAPE, "%s: too many chunks", fn);
     const int e = io_bytes(io_dtype);
     for (const void* x : {(const void*)dout, (const void*)dq, (const void*)dk_out, (const void*)dv_out, (const void*)dg,
