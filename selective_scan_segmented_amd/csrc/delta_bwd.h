@@ -483,7 +483,7 @@ __device__ __forceinline__ void mma_all(const Parts<T, PA>& a, const Parts<T, PB
 // A workgroup to every chunk and head, sixteen tokens to a wave.  First phase: the products over values (with S0,
 // dS', U, dR of the workspace), 32 values at a time; second: those over tokens (with K and Q).
 template <typename T, int DK, int PW>
-__global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)) void delta_grads_kernel(const DeltaParams p, unsigned chunks, unsigned units, int ops_bytes) {
+__global__ __launch_bounds__(kDeltaThreads, (sizeof(T) == 2 ? 2 : 1)) void delta_grads_kernel(const DeltaParams p, unsigned chunks, unsigned units, int ops_bytes) {
     using Sh = ChunkShape<T, DK>;
     using L = GradLds<T, DK, PW>;
     constexpr int E = (int)sizeof(T), ND = DK / 16;
@@ -507,9 +507,6 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
     const int vals = (p.dv + 63) / 64 * 64;
 
-    RowShare<T, DK> kr, qr;
-    kr.load(make_buf(static_cast<const T*>(p.k) + tok * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
-    qr.load(make_buf(static_cast<const T*>(p.q) + tok * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
     {
         Linear<(int)sizeof(ChunkRows)> r;
         r.load(p.w_ops + entry * ops_bytes);
@@ -543,8 +540,10 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)
             bu.load(wu + (int64_t)v0 * kC, (int64_t)vals * kC);
             br.load(wr + (int64_t)v0 * kC, (int64_t)vals * kC);
         };
-        fetch(0);
+        constexpr bool ahead = DK == 64 || sizeof(T) == 4;  // (else the registers are another workgroup's)
+        if (ahead) fetch(0);
         for (int v0 = 0; v0 < p.dv; v0 += kVals) {
+            if (!ahead) fetch(v0);
             lds_barrier();
             gr.store(gs, nullptr, 0);
             vr.store(vs, nullptr, 0);
@@ -557,7 +556,7 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < bs.per; ++e) fr = __builtin_fmaf(bs.value(i, e), bd.value(i, e), fr);
             lds_barrier();
-            if (v0 + kVals < p.dv) fetch(v0 + kVals);
+            if (ahead && v0 + kVals < p.dv) fetch(v0 + kVals);
             const Parts<T, 1> fg[1] = {{load_runs<T>(gs + (wave * 16 + l16) * L::VS + g4)}};
             const Parts<T, 1> fv[1] = {{load_runs<T>(vs + (wave * 16 + l16) * L::VS + g4)}};
             const Parts<T, PW> fr_[1] = {load_block<PW>(rs, wave, L::TS)}, fu = load_block<PW>(us, wave, L::TS);
@@ -593,6 +592,10 @@ __global__ __launch_bounds__(kDeltaThreads, (DK == 64 && sizeof(T) == 2 ? 2 : 1)
     for (int r = 0; r < 4; ++r)
         if (g4 + r == l16) row_v[wave * 16 + l16] = rv[r];
 
+    // (not before: with its registers another workgroup fits on the unit)
+    RowShare<T, DK> kr, qr;
+    kr.load(make_buf(static_cast<const T*>(p.k) + tok * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
+    qr.load(make_buf(static_cast<const T*>(p.q) + tok * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs), *xs = reinterpret_cast<T*>(lds + L::x),
       *wsm = reinterpret_cast<T*>(lds + L::w);
     lds_barrier();  // the first phase's arrays are done with
