@@ -55,6 +55,23 @@ def test_step_refuses(lib, kw, want):
     assert step(lib, **kw) == want
 
 
+def bwd(lib, **kw):
+    a = dict(q=P, k=2 * P, v=3 * P, g=4 * P, beta=5 * P, h0=None, dout=6 * P, dhT=None, dq=7 * P, dk_=8 * P, dv_=9 * P, dg=10 * P,
+             dbeta=11 * P, dh0=None, off=None, rows=2, L=100, tokens=200, Hk=1, H=2, dk=64, dv=64, ldq=64, ldk=64, ldv=128, scale=0.125,
+             io=1, flags=1, ws=100 * P, wsb=1 << 30)
+    a.update(kw)
+    return lib.sfm_gated_delta_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [c for c in SHARED if "o" not in c[0]] + [
+    (dict(dout=None), NULL), (dict(dg=None), NULL), (dict(ws=None), SHAPE), (dict(wsb=4096), SHAPE), (dict(ws=100 * P + 8), ALIGN),
+    (dict(dq=P), ALIAS), (dict(dk_=7 * P + 64), ALIAS), (dict(dh0=6 * P), ALIAS), (dict(ws=10 * P), ALIAS), (dict(dg=10 * P + 1), ALIGN),
+    (dict(tokens=100), SHAPE), (dict(dhT=12 * P + 2), ALIGN), (dict(rows=1 << 20, L=1 << 20, off=12 * P), SHAPE)])
+def test_backward_refuses(lib, kw, want):
+    assert bwd(lib, **kw) == want
+    assert lib.sfm_last_error().startswith(b"sfm_gated_delta_bwd")
+
+
 def test_workspace_sizes(lib):
     out = ctypes.c_int64(-1)
     f = lib.sfm_gated_delta_fwd_ws_size
@@ -62,6 +79,10 @@ def test_workspace_sizes(lib):
     assert f(2, 100, 200, 2, 64, 64, 0, 1, None) == NULL
     assert f(2, 100, 200, 2, 0, 64, 0, 1, ctypes.byref(out)) == SHAPE
     assert f(2, 100, 200, 2, 64, 64, 0, 9, ctypes.byref(out)) == DTYPE
+    f = lib.sfm_gated_delta_bwd_ws_size
+    assert f(2, 100, 200, 1, 2, 64, 64, 0, 1, None) == NULL
+    assert f(2, 100, 200, 3, 2, 64, 64, 0, 1, ctypes.byref(out)) == SHAPE
+    assert f(2, 100, 200, 1, 2, 64, 64, 0, 1, ctypes.byref(out)) == OK and out.value > 0
     f = lib.sfm_group_norm_fwd_ws_size
     assert f(2, 100, 64, 4, 1, None) == NULL
     assert f(2, 100, 64, 5, 1, ctypes.byref(out)) == SHAPE
@@ -70,6 +91,18 @@ def test_workspace_sizes(lib):
     assert f(1, 100000, 64, 4, 1, ctypes.byref(out)) == OK and out.value > 0
     assert lib.sfm_group_norm_bwd_ws_size(2, 100, 64, 4, 0, 1, ctypes.byref(out)) == OK and out.value == 0
     assert lib.sfm_group_norm_bwd_ws_size(2, 100, 64, 4, 1, 1, ctypes.byref(out)) == OK and out.value > 0
+
+
+def test_launch_plans(lib, monkeypatch):
+    """Few long rows have their triangular inverses made beforehand (workspace); one chunk or many rows do not."""
+    f = sfm.sfm_gated_delta_fwd_ws_size
+    unit = lambda parts: 7 * 64 * 4 + 2 * 6 * 64 * 8 * 2 * parts  # row scalars, two lower triangles of 6 fragments
+    assert f(2, 8192, 16384, 16, 128, 128, True) == (16384 // 64 + 2) * 16 * unit(3)
+    assert f(2, 8192, 16384, 16, 128, 128, False) == (16384 // 64 + 2) * 16 * unit(2)
+    assert f(256, 51, 256 * 51, 10, 64, 64) == 0
+    assert f(512, 198, 512 * 198, 8, 64, 64) == 0
+    monkeypatch.setenv("SFM_DELTA_WALK", "whole")
+    assert f(2, 8192, 16384, 16, 128, 128, True) == 0
 
 
 def norm(lib, **kw):

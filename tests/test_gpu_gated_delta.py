@@ -238,3 +238,19 @@ def test_step_continues_the_rows():
         ref.close(from_dev(o), from_dev(whole[:, i]), "f32", f"token {i}")
     torch.cuda.synchronize()
     ref.close(from_dev(S), from_dev(wT), "f32", "state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("walk,narrow", [("whole", "0"), ("prepared", "0"), ("prepared", "1")])
+@pytest.mark.parametrize("lens,Hk,H,dk,dv", [([200, 0, 64, 1, 130], 1, 2, 64, 64), ([300], 1, 1, 128, 130), ([129, 5], 2, 2, 33, 20)])
+def test_forward_by_every_plan(lens, Hk, H, dk, dv, walk, narrow, io, monkeypatch):
+    """Each way of walking the chunks, whatever the sizes would choose."""
+    monkeypatch.setenv("SFM_DELTA_WALK", walk)
+    monkeypatch.setenv("SFM_DELTA_NARROW", narrow)
+    x = ref.delta_inputs(sum(lens), sum(lens), len(lens), Hk, H, dk, dv, True, io)
+    wo, wT = ref.delta(*x[:6], np.cumsum(lens), dk ** -0.5, True)
+    for state in (True, False):
+        o, hT = call_fwd(x, lens, True, io, True, x[5], state=state)
+        ref.close(o, wo, io, "o")
+        if state:
+            ref.close(hT, wT, "f32", "state")

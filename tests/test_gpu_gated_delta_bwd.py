@@ -150,3 +150,14 @@ def test_strided_projection(io):
     torch.cuda.synchronize()
     for n in a:
         assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("narrow", ["0", "1"])
+@pytest.mark.parametrize("lens,Hk,H,dk,dv", [([200, 0, 64, 1, 130], 1, 2, 64, 64), ([300], 1, 1, 128, 130), ([129, 5], 2, 4, 33, 20)])
+def test_by_every_plan(lens, Hk, H, dk, dv, narrow, io, monkeypatch):
+    """Wide and narrow walks, whatever the sizes would choose."""
+    monkeypatch.setenv("SFM_DELTA_NARROW", narrow)
+    x = ref.delta_inputs(sum(lens), sum(lens), len(lens), Hk, H, dk, dv, True, io)
+    dhT = np.random.default_rng(1).standard_normal(x[5].shape).astype(np.float32).astype(np.float64)
+    check(call_bwd(x, lens, True, io, True, x[5], dhT), ref.delta_bwd(*x[:6], np.cumsum(lens), dk ** -0.5, True, x[6], dhT), io, x[5])
