@@ -17,7 +17,7 @@
 //   cache if it fits there).  Squares are taken about the mean of each batch of eight rows, and batches, channels
 //   and ranges are joined by the exact formula for the squares of a union, again so that a large mean costs nothing.
 // Sums are float32 in a fixed order: repeated calls give the same bits.
-#include "sfm_device.h"
+#include "delta_mma.h"
 #include "sfm_norm.h"
 
 namespace sfm {
@@ -60,117 +60,134 @@ template <int V> struct GroupOf {
     }
 };
 
-// Sums of the groups of buf [slots][cw] into out [groups][parts]: `parts` waves share a group (where there are
-// fewer groups than waves), a group's sum is that of its parts (group_sum).
-__device__ __forceinline__ int group_parts(int groups) {
-    const int waves = blockDim.x >> 6;
-    return groups >= waves ? 1 : waves / groups;
+// A wave's share of a group's entries in [slots][width] arrays, `eg` neighbours to a group: f(slot, column).
+template <typename F> __device__ __forceinline__ void each_entry(int slots, int eg, int g, F f) {
+    const int lane = threadIdx.x & 63;
+    const int per = eg < 64 ? 64 / eg : 1;  // slots a wave takes at once
+    const int ls = eg < 64 ? lane / eg : 0, lc = lane - ls * eg;
+    if (ls >= per) return;
+    for (int s = ls; s < slots; s += per)
+        for (int c = lc; c < eg; c += 64) f(s, g * eg + c);
 }
-__device__ __forceinline__ void group_sums(const float* buf, int slots, int cw, int cg, int groups, int parts, float* out) {
-    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-    const int per = cg < 64 ? 64 / cg : 1;  // slots a wave takes at once
-    const int ls = cg < 64 ? lane / cg : 0, lc = lane - ls * cg;
-    for (int u = threadIdx.x >> 6; u < groups * parts; u += waves) {
-        const int g = u / parts, part = u - g * parts;
-        float v = 0.0f;
-        for (int s = part * per + ls; s < slots && ls < per; s += parts * per)
-            for (int c = lc; c < cg; c += 64) v += buf[s * cw + g * cg + c];
-        v = wave_sum(v);
-        if (lane == 0) out[u] = v;
+
+// Units of a sample's rows as a buffer: zeros past the last row, and stores there are dropped.
+template <typename T, int V> __device__ __forceinline__ Unit<T, V> unit_load(const Buf& b, unsigned at) {
+    if constexpr (V * sizeof(T) == 16) {
+        typedef unsigned word __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(Unit<T, V>, buf_load<word>(b, at));
+    } else {
+        return __builtin_bit_cast(Unit<T, V>, buf_load<T>(b, at));
     }
 }
-__device__ __forceinline__ float group_sum(const float* sums, int g, int parts) {
-    float v = sums[g * parts];
-    for (int i = 1; i < parts; ++i) v += sums[g * parts + i];
-    return v;
+template <typename T, int V> __device__ __forceinline__ void unit_store(const Buf& b, unsigned at, const Unit<T, V>& u) {
+    if constexpr (V * sizeof(T) == 16) {
+        typedef unsigned word __attribute__((ext_vector_type(4)));
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(word, u), b.r, at, 0, 0);
+    } else {
+        buf_store<T>(b, at, u.e[0]);
+    }
 }
-constexpr int kMaxWaves = 16;
 
 // ------------------------------------------------------------------------------------------------ slab kernels
-// LDS: [slots][cw] per-thread channel sums (two of them backward), then the groups' sums.
-template <typename T, int V, int U, int THREADS>
+// LDS, forward: [slots][entries] sums, means and squares about them (an entry is a thread's unit where units do not
+// straddle groups, else a channel), row counts by slot, the groups' mean and 1 / deviation; backward: [slots][cw]
+// sums of dz and of dz xh, then the groups'.
+template <typename T, int V, int U, int THREADS, bool WHOLE>
 __global__ __launch_bounds__(THREADS, 4) void norm_slab_fwd_kernel(const NormParams p) {
+    constexpr int NE = WHOLE ? 1 : V;
     extern __shared__ float lds[];
-    const int cu = p.cw / V, slots = blockDim.x / cu;
+    const int cu = p.cw / V, slots = blockDim.x / cu, ew = cu * NE, eg = p.cg / (V / NE);
     const int64_t n = blockIdx.x / p.runs;
     const int run = (int)(blockIdx.x - n * p.runs);
-    const int slot = threadIdx.x / cu, cl = (threadIdx.x - slot * cu) * V, c = run * p.cw + cl;
+    const int slot = threadIdx.x / cu, u = threadIdx.x - slot * cu, cl = u * V, c = run * p.cw + cl;
     const bool on = slot < slots;
-    const int64_t rows = on ? p.L : 0;
-    const int groups = p.cw / p.cg, parts = group_parts(groups);
-    float *gs = lds + slots * p.cw, *gq = gs + groups * parts;
-    const GroupOf<V> grp(on ? cl : 0, p.cg);
-    const T* xp = static_cast<const T*>(p.x) + n * p.L * p.C + c;
+    const int groups = p.cw / p.cg;
+    float *ls = lds, *lm = ls + slots * ew, *lq = lm + slots * ew, *lr = lq + slots * ew, *gm = lr + slots, *gr = gm + groups;
+    const Buf xb = make_buf(static_cast<const T*>(p.x) + n * p.L * p.C, p.L * p.C * (int)sizeof(T));
+    const unsigned at = on ? (unsigned)(slot * p.C + c) * (unsigned)sizeof(T) : kNowhere, step = (unsigned)(slots * p.C) * (unsigned)sizeof(T);
     Unit<T, V> x[U];
-    float sum[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int64_t r = slot + (int64_t)i * slots;
-        if (r < rows)
-            x[i] = *reinterpret_cast<const Unit<T, V>*>(xp + r * p.C);
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-        if (slot + (int64_t)i * slots < rows)
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum[j] += to_f32(x[i].e[j]);
-    if (on)
-#pragma unroll
-        for (int j = 0; j < V; ++j) lds[slot * p.cw + cl + j] = sum[j];
-    __syncthreads();
-    group_sums(lds, slots, p.cw, p.cg, groups, parts, gs);
-    __syncthreads();
-    const float total = (float)p.L * (float)p.cg;
-    float mean[V];
+    for (int i = 0; i < U; ++i) x[i] = unit_load<T, V>(xb, at + i * step);
+    float w[V], b[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        // (a division: a constant group's mean is exact)
-        mean[j] = j > 0 && grp.g[j] == grp.g[j > 0 ? j - 1 : 0] ? mean[j > 0 ? j - 1 : 0] : group_sum(gs, grp.g[j], parts) / total;
-        sum[j] = 0.0f;
+        w[j] = p.w && on ? p.w[c + j] : 1.0f;
+        b[j] = p.b && on ? p.b[c + j] : 0.0f;
     }
+    // this thread's rows, then the sums over them, their mean and the squares about it
+    const int rows = on && slot < p.L ? ((int)p.L - 1 - slot) / slots + 1 : 0;
+    float s[NE], m[NE], q[NE];
+#pragma unroll
+    for (int j = 0; j < NE; ++j) s[j] = q[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < U; ++i)
-        if (slot + (int64_t)i * slots < rows)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j % NE] += to_f32(x[i].e[j]);
+    const float count = (float)(rows * (V / NE));
+#pragma unroll
+    for (int j = 0; j < NE; ++j) m[j] = rows > 0 ? s[j] / count : 0.0f;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        if (i < rows)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float d = to_f32(x[i].e[j]) - mean[j];
-                sum[j] = __builtin_fmaf(d, d, sum[j]);
+                const float d = to_f32(x[i].e[j]) - m[j % NE];
+                q[j % NE] = __builtin_fmaf(d, d, q[j % NE]);
             }
-    if (on)
+    if (on) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) lds[slot * p.cw + cl + j] = sum[j];
-    __syncthreads();
-    group_sums(lds, slots, p.cw, p.cg, groups, parts, gq);
-    __syncthreads();
-    for (int g = threadIdx.x; g < groups; g += blockDim.x) {
-        const int64_t at = n * p.G + run * groups + g;
-        p.mean[at] = group_sum(gs, g, parts) / total;
-        p.rstd[at] = 1.0f / __builtin_sqrtf(group_sum(gq, g, parts) / total + p.eps);
+        for (int j = 0; j < NE; ++j) {
+            const int e = slot * ew + u * NE + j;
+            ls[e] = s[j];
+            lm[e] = m[j];
+            lq[e] = q[j];
+        }
+        if (u == 0) lr[slot] = count;
     }
-    if (!on) return;
-    float a[V], b[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        a[j] = j > 0 && grp.g[j] == grp.g[j > 0 ? j - 1 : 0] ? a[j > 0 ? j - 1 : 0]
-                                                             : 1.0f / __builtin_sqrtf(group_sum(gq, grp.g[j], parts) / total + p.eps);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (p.w) a[j] *= p.w[c + j];
-        b[j] = p.b ? p.b[c + j] : 0.0f;
+    __syncthreads();
+    const float total = (float)p.L * (float)p.cg;
+    for (int g = threadIdx.x >> 6; g < groups; g += blockDim.x >> 6) {
+        float v = 0.0f;
+        each_entry(slots, eg, g, [&](int k, int e) { v += ls[k * ew + e]; });
+        const float mean = wave_sum(v) / total;  // (a division: a constant group's mean is exact)
+        v = 0.0f;
+        each_entry(slots, eg, g, [&](int k, int e) {
+            const float d = lm[k * ew + e] - mean;
+            v += __builtin_fmaf(d * d, lr[k], lq[k * ew + e]);
+        });
+        const float rstd = 1.0f / __builtin_sqrtf(wave_sum(v) / total + p.eps);
+        if ((threadIdx.x & 63) == 0) {
+            gm[g] = mean;
+            gr[g] = rstd;
+            p.mean[n * p.G + run * groups + g] = mean;
+            p.rstd[n * p.G + run * groups + g] = rstd;
+        }
     }
-    T* yp = static_cast<T*>(p.y) + n * p.L * p.C + c;
+    __syncthreads();
+    float mean[V];
+    if constexpr (WHOLE) {
+        const int g = on ? cl / p.cg : 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            mean[j] = gm[g];
+            w[j] *= gr[g];
+        }
+    } else {
+        const GroupOf<V> grp(on ? cl : 0, p.cg);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            mean[j] = gm[grp.g[j]];
+            w[j] *= gr[grp.g[j]];
+        }
+    }
+    const Buf yb = make_buf(static_cast<T*>(p.y) + n * p.L * p.C, p.L * p.C * (int)sizeof(T));
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int64_t r = slot + (int64_t)i * slots;
-        if (r < rows) {
-            Unit<T, V> y;
+        Unit<T, V> y;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                y.e[j] = from_f32<T>(act_fwd(__builtin_fmaf(to_f32(x[i].e[j]) - mean[j], a[j], b[j]), p.act));
-            *reinterpret_cast<Unit<T, V>*>(yp + r * p.C) = y;
-        }
+        for (int j = 0; j < V; ++j)
+            y.e[j] = from_f32<T>(act_fwd(__builtin_fmaf(to_f32(x[i].e[j]) - mean[j], w[j], b[j]), p.act));
+        unit_store<T, V>(yb, at + i * step, y);
     }
 }
 
@@ -182,41 +199,38 @@ __global__ __launch_bounds__(THREADS, (U <= 4 ? 3 : 2)) void norm_slab_bwd_kerne
     const int run = (int)(blockIdx.x - n * p.runs);
     const int slot = threadIdx.x / cu, cl = (threadIdx.x - slot * cu) * V, c = run * p.cw + cl;
     const bool on = slot < slots;
-    const int64_t rows = on ? p.L : 0;
-    const int groups = p.cw / p.cg, parts = group_parts(groups);
-    float *l1 = lds, *l2 = lds + slots * p.cw, *gs = l2 + slots * p.cw, *gq = gs + groups * parts;
+    const int groups = p.cw / p.cg;
+    float *l1 = lds, *l2 = lds + slots * p.cw, *gs = l2 + slots * p.cw, *gq = gs + groups;
     const GroupOf<V> grp(on ? cl : 0, p.cg);
-    const T* xp = static_cast<const T*>(p.x) + n * p.L * p.C + c;
-    const T* dp = static_cast<const T*>(p.dy) + n * p.L * p.C + c;
+    const Buf xb = make_buf(static_cast<const T*>(p.x) + n * p.L * p.C, p.L * p.C * (int)sizeof(T));
+    const Buf db = make_buf(static_cast<const T*>(p.dy) + n * p.L * p.C, p.L * p.C * (int)sizeof(T));
+    const unsigned at = on ? (unsigned)(slot * p.C + c) * (unsigned)sizeof(T) : kNowhere, step = (unsigned)(slots * p.C) * (unsigned)sizeof(T);
     Unit<T, V> x[U], dy[U];
-    float mean[V], rstd[V], w[V], b[V], s1[V], s2[V];
+    float mean[V], rstd[V], w[V], b[V], s1[V], s2[V], dz[U][V];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int64_t r = slot + (int64_t)i * slots;
-        if (r < rows) {
-            x[i] = *reinterpret_cast<const Unit<T, V>*>(xp + r * p.C);
-            dy[i] = *reinterpret_cast<const Unit<T, V>*>(dp + r * p.C);
-        }
+        x[i] = unit_load<T, V>(xb, at + i * step);
+        dy[i] = unit_load<T, V>(db, at + i * step);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t at = n * p.G + run * groups + grp.g[j];
-        mean[j] = p.mean[at];
-        rstd[j] = p.rstd[at];
+        const int64_t ga = n * p.G + run * groups + grp.g[j];
+        mean[j] = p.mean[ga];
+        rstd[j] = p.rstd[ga];
         w[j] = p.w && on ? p.w[c + j] : 1.0f;
         b[j] = p.b && on ? p.b[c + j] : 0.0f;
         s1[j] = s2[j] = 0.0f;
     }
+    // (rows past the end are zeros: dz = 0)
 #pragma unroll
     for (int i = 0; i < U; ++i)
-        if (slot + (int64_t)i * slots < rows)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float xh = (to_f32(x[i].e[j]) - mean[j]) * rstd[j];
-                const float dz = act_bwd(to_f32(dy[i].e[j]), __builtin_fmaf(xh, w[j], b[j]), p.act);
-                s1[j] += dz;
-                s2[j] = __builtin_fmaf(dz, xh, s2[j]);
-            }
+        for (int j = 0; j < V; ++j) {
+            const float xh = (to_f32(x[i].e[j]) - mean[j]) * rstd[j];
+            dz[i][j] = act_bwd(to_f32(dy[i].e[j]), __builtin_fmaf(xh, w[j], b[j]), p.act);
+            s1[j] += dz[i][j];
+            s2[j] = __builtin_fmaf(dz[i][j], xh, s2[j]);
+        }
     if (on)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -229,37 +243,44 @@ __global__ __launch_bounds__(THREADS, (U <= 4 ? 3 : 2)) void norm_slab_bwd_kerne
         float* l = i < p.cw ? l1 : l2;
         const int ch = i < p.cw ? i : i - p.cw;
         float v = 0.0f;
+#pragma unroll 8
         for (int k = 0; k < slots; ++k) v += l[k * p.cw + ch];
         const int cc = run * p.cw + ch;
         if (p.part) p.part[(n * 2 + (i < p.cw ? 0 : 1)) * p.C + cc] = v;
         l[ch] = p.w ? v * p.w[cc] : v;
     }
     __syncthreads();
-    group_sums(l1, 1, p.cw, p.cg, groups, 1, gs);
-    group_sums(l2, 1, p.cw, p.cg, groups, 1, gq);
+    const float total = (float)p.L * (float)p.cg;
+    for (int g = threadIdx.x >> 6; g < groups; g += blockDim.x >> 6) {
+        float v1 = 0.0f, v2 = 0.0f;
+        each_entry(1, p.cg, g, [&](int, int e) {
+            v1 += l1[e];
+            v2 += l2[e];
+        });
+        v1 = wave_sum(v1);
+        v2 = wave_sum(v2);
+        if ((threadIdx.x & 63) == 0) {
+            gs[g] = v1 / total;
+            gq[g] = v2 / total;
+        }
+    }
     __syncthreads();
-    if (!on) return;
-    const float inv = 1.0f / ((float)p.L * (float)p.cg);
-    float m1[V], m2[V];
+    const Buf yb = make_buf(static_cast<T*>(p.y) + n * p.L * p.C, p.L * p.C * (int)sizeof(T));
+    // dx = rstd (w dz - m1 - xh m2) = (rstd w) dz - (rstd^2 m2) (x - mean) - rstd m1
+    float k2[V], k1[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        m1[j] = gs[grp.g[j]] * inv;
-        m2[j] = gq[grp.g[j]] * inv;
+        w[j] *= rstd[j];
+        k2[j] = rstd[j] * rstd[j] * gq[grp.g[j]];
+        k1[j] = rstd[j] * gs[grp.g[j]];
     }
-    T* yp = static_cast<T*>(p.y) + n * p.L * p.C + c;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int64_t r = slot + (int64_t)i * slots;
-        if (r < rows) {
-            Unit<T, V> y;
+        Unit<T, V> y;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float xh = (to_f32(x[i].e[j]) - mean[j]) * rstd[j];
-                const float dz = act_bwd(to_f32(dy[i].e[j]), __builtin_fmaf(xh, w[j], b[j]), p.act);
-                y.e[j] = from_f32<T>(rstd[j] * (dz * w[j] - m1[j] - xh * m2[j]));
-            }
-            *reinterpret_cast<Unit<T, V>*>(yp + r * p.C) = y;
-        }
+        for (int j = 0; j < V; ++j)
+            y.e[j] = from_f32<T>(__builtin_fmaf(dz[i][j], w[j], -__builtin_fmaf(to_f32(x[i].e[j]) - mean[j], k2[j], k1[j])));
+        unit_store<T, V>(yb, at + i * step, y);
     }
 }
 
@@ -551,15 +572,22 @@ __global__ __launch_bounds__(1024) void norm_weights_kernel(const NormParams p, 
 
 template <typename T, int V, int U, int THREADS>
 hipError_t launch_slab(const NormParams& p, bool bwd, hipStream_t s) {
-    const int slots = p.threads / (p.cw / V);
-    const size_t lds = ((size_t)slots * p.cw * (bwd ? 2 : 1) + 2 * (p.cw / p.cg + kMaxWaves)) * 4;
+    const int cu = p.cw / V, slots = p.threads / cu, groups = p.cw / p.cg;
     const dim3 grid((unsigned)(p.N * p.runs));
     if constexpr (THREADS <= 512)
         if (bwd) {
+            const size_t lds = ((size_t)slots * p.cw * 2 + 2 * groups) * 4;
             hipLaunchKernelGGL((norm_slab_bwd_kernel<T, V, U, THREADS>), grid, dim3(p.threads), lds, s, p);
             return hipGetLastError();
         }
-    hipLaunchKernelGGL((norm_slab_fwd_kernel<T, V, U, THREADS>), grid, dim3(p.threads), lds, s, p);
+    const bool whole = p.cg % V == 0;
+    const size_t lds = ((size_t)slots * (whole ? cu : p.cw) * 3 + slots + 2 * groups) * 4;
+    auto kern = whole ? norm_slab_fwd_kernel<T, V, U, THREADS, true> : norm_slab_fwd_kernel<T, V, U, THREADS, false>;
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kern, grid, dim3(p.threads), lds, s, p);
     return hipGetLastError();
 }
 
@@ -619,7 +647,7 @@ int64_t plan_norm(NormParams& p, int io_bytes, bool aligned, bool backward) {
     for (int k = 1; k <= p.G; ++k) {
         if (p.G % k || (k * p.cg) % p.vec) continue;
         const int64_t cu = (int64_t)k * p.cg / p.vec;
-        if (cu > kThreads || p.L > (kThreads / cu) * (int64_t)kUnits) break;
+        if (cu > kThreads || p.L > (kThreads / cu) * (int64_t)kUnits || p.L * p.C >= 1 << 28) break;
         p.slab = 1;
         p.cw = k * p.cg;
         if ((int64_t)p.cw * io_bytes >= 128) break;
