@@ -287,93 +287,90 @@ __global__ __launch_bounds__(THREADS, (U <= 4 ? 3 : 2)) void norm_slab_bwd_kerne
 // ------------------------------------------------------------------------------------------------ two passes
 constexpr int kBatch = 8;  // rows a thread has in flight
 
+// Rows r0 .. r1 - 1 of sample n as a buffer that starts at row r0 (a range ends below 2^30 bytes: plan_norm).
+template <typename T> __device__ __forceinline__ Buf range_buf(const void* x, const NormParams& p, int64_t n, int64_t r0, int64_t r1) {
+    return make_buf(static_cast<const T*>(x) + (n * p.L + r0) * p.C, (r1 - r0) * p.C * (int)sizeof(T));
+}
+
 // First pass: per-channel sums of one row range.  Forward: the mean and the squares about it; backward: sum dz
-// and sum dz xh.  LDS: [slots][2][units of the tile].
+// and sum dz xh.  LDS: [slots][2][channels of the tile], then row counts by slot.
 template <typename T, int V, bool BWD>
 __global__ __launch_bounds__(256) void norm_sums_kernel(const NormParams p) {
     extern __shared__ float lds[];
-    const int64_t unit = blockIdx.x / p.tiles;
-    const int tile = (int)(blockIdx.x - unit * p.tiles);
-    const int64_t n = unit / p.splits;
-    const int split = (int)(unit - n * p.splits);
-    const int cu = min(p.tunits, p.C / V - tile * p.tunits);
+    const unsigned unit = blockIdx.x / (unsigned)p.tiles, tile = blockIdx.x - unit * p.tiles;
+    const unsigned n = unit / (unsigned)p.splits, split = unit - n * p.splits;
+    const int cu = min(p.tunits, p.C / V - (int)tile * p.tunits);
     const int slots = blockDim.x / cu, cw = cu * V;
     const int slot = threadIdx.x / cu, cl = (threadIdx.x - slot * cu) * V, c = tile * p.tunits * V + cl;
     const bool on = slot < slots;
     const int64_t r0 = split * p.srows, r1 = min(p.L, r0 + p.srows);
-    const GroupOf<V> grp(on ? c : 0, p.cg);
+    const int len = (int)(r1 - r0);
     float s1[V], s2[V], mean[V], rstd[V], w[V], b[V];
     float count = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        s1[j] = s2[j] = 0.0f;
-        if (BWD) {
-            const int64_t at = n * p.G + grp.g[j];
+    for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.0f;
+    if (BWD) {
+        const GroupOf<V> grp(on ? c : 0, p.cg);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t at = (int64_t)n * p.G + grp.g[j];
             mean[j] = p.mean[at];
             rstd[j] = p.rstd[at];
             w[j] = p.w && on ? p.w[c + j] : 1.0f;
             b[j] = p.b && on ? p.b[c + j] : 0.0f;
         }
     }
-    if (on) {
-        const T* xp = static_cast<const T*>(p.x) + n * p.L * p.C + c;
-        const T* dp = BWD ? static_cast<const T*>(p.dy) + n * p.L * p.C + c : nullptr;
-        int64_t r = r0 + slot;
-        for (; r + (int64_t)(kBatch - 1) * slots < r1; r += (int64_t)kBatch * slots) {
-            Unit<T, V> x[kBatch], dy[kBatch];
+    const Buf xb = range_buf<T>(p.x, p, n, r0, r1), db = BWD ? range_buf<T>(p.dy, p, n, r0, r1) : xb;
+    const unsigned step = (unsigned)(slots * p.C) * (unsigned)sizeof(T);
+    unsigned at = on ? (unsigned)(slot * p.C + c) * (unsigned)sizeof(T) : kNowhere;
+    for (int r = slot; r < len && on; r += kBatch * slots, at += kBatch * step) {
+        Unit<T, V> x[kBatch], dy[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                x[i] = *reinterpret_cast<const Unit<T, V>*>(xp + (r + (int64_t)i * slots) * p.C);
-                if (BWD) dy[i] = *reinterpret_cast<const Unit<T, V>*>(dp + (r + (int64_t)i * slots) * p.C);
-            }
-            const float join = count * kBatch / (count + kBatch), step = kBatch / (count + kBatch);
+        for (int i = 0; i < kBatch; ++i) {
+            x[i] = unit_load<T, V>(xb, at + i * step);
+            if (BWD) dy[i] = unit_load<T, V>(db, at + i * step);
+        }
+        if (BWD) {  // (rows past the range are zeros: dz = 0)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float xh = (to_f32(x[i].e[j]) - mean[j]) * rstd[j];
+                    const float dz = act_bwd(to_f32(dy[i].e[j]), __builtin_fmaf(xh, w[j], b[j]), p.act);
+                    s1[j] += dz;
+                    s2[j] = __builtin_fmaf(dz, xh, s2[j]);
+                }
+        } else {
+            // the batch by itself, then the union of it and the `count` values before (s1 their mean, s2 their squares)
+            const int rows = min(kBatch, (len - 1 - r) / slots + 1);
+            const float nb = (float)rows, all = count + nb, join = count * nb / all, part = nb / all, inv = 1.0f / nb;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                if (BWD) {
+                float m = 0.0f, q = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const float xh = (to_f32(x[i].e[j]) - mean[j]) * rstd[j];
-                        const float dz = act_bwd(to_f32(dy[i].e[j]), __builtin_fmaf(xh, w[j], b[j]), p.act);
-                        s1[j] += dz;
-                        s2[j] = __builtin_fmaf(dz, xh, s2[j]);
-                    }
-                } else {
-                    float m = 0.0f, q = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) m += to_f32(x[i].e[j]);
-                    m *= 1.0f / kBatch;
+                for (int i = 0; i < kBatch; ++i) m += to_f32(x[i].e[j]);
+                m *= inv;
+                if (rows == kBatch) {
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) {
                         const float d = to_f32(x[i].e[j]) - m;
                         q = __builtin_fmaf(d, d, q);
                     }
-                    // union of `count` values (s1 their mean, s2 their squares) and the batch
-                    const float d = m - s1[j];
-                    s1[j] = __builtin_fmaf(d, step, s1[j]);
-                    s2[j] += __builtin_fmaf(d * d, join, q);
-                }
-            }
-            count += kBatch;
-        }
-        for (; r < r1; r += slots) {
-            const Unit<T, V> x = *reinterpret_cast<const Unit<T, V>*>(xp + r * p.C);
-            Unit<T, V> dy;
-            if (BWD) dy = *reinterpret_cast<const Unit<T, V>*>(dp + r * p.C);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (BWD) {
-                    const float xh = (to_f32(x.e[j]) - mean[j]) * rstd[j];
-                    const float dz = act_bwd(to_f32(dy.e[j]), __builtin_fmaf(xh, w[j], b[j]), p.act);
-                    s1[j] += dz;
-                    s2[j] = __builtin_fmaf(dz, xh, s2[j]);
                 } else {
-                    const float d = to_f32(x.e[j]) - s1[j];
-                    s1[j] += d / (count + 1.0f);
-                    s2[j] = __builtin_fmaf(d * d, count / (count + 1.0f), s2[j]);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const float d = i < rows ? to_f32(x[i].e[j]) - m : 0.0f;
+                        q = __builtin_fmaf(d, d, q);
+                    }
                 }
+                const float d = m - s1[j];
+                s1[j] = __builtin_fmaf(d, part, s1[j]);
+                s2[j] += __builtin_fmaf(d * d, join, q);
             }
-            count += 1.0f;
+            count = all;
         }
+    }
+    if (on) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             lds[(slot * 2) * cw + cl + j] = s1[j];
@@ -396,7 +393,7 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormParams p) {
                 k += ks;
             }
         }
-        float* out = p.part + ((n * p.splits + split) * 2) * p.C + tile * p.tunits * V + i;
+        float* out = p.part + (((int64_t)n * p.splits + split) * 2) * p.C + tile * p.tunits * V + i;
         out[0] = a;
         out[p.C] = q;
     }
@@ -446,99 +443,121 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const NormParams p, unsi
     part[p.C] = q;
 }
 
-// Joins a group's channels, a wave to a group.  Forward: mean and rstd; backward: m1, m2.
-template <bool BWD>
-__global__ __launch_bounds__(256) void norm_group_kernel(const NormParams p) {
-    const int lane = threadIdx.x & 63;
-    const int64_t id = blockIdx.x * (int64_t)(blockDim.x >> 6) + (threadIdx.x >> 6);
-    if (id >= p.N * p.G) return;
-    const int64_t n = id / p.G;
-    const int g = (int)(id - n * p.G);
-    const float* part = p.part + n * p.splits * 2 * p.C + g * p.cg;
+// Joins the channels of group g (channels `lane`, `lane` + `step`, .. of it, summed by `sum`): forward mean and
+// 1 / deviation, backward m1 and m2.
+template <bool BWD, typename Sum>
+__device__ __forceinline__ void join_group(const NormParams& p, const float* part, int g, int lane, int step, Sum sum, float& r1, float& r2) {
     const float total = (float)p.L * (float)p.cg;
     float s = 0.0f, t = 0.0f;
-    for (int c = lane; c < p.cg; c += 64) {
+#pragma unroll 4
+    for (int c = lane; c < p.cg; c += step) {
         const float w = BWD && p.w ? p.w[g * p.cg + c] : 1.0f;
-        s = __builtin_fmaf(w, part[c], s);
-        if (BWD) t = __builtin_fmaf(w, part[p.C + c], t);
+        s = __builtin_fmaf(w, part[g * p.cg + c], s);
+        if (BWD) t = __builtin_fmaf(w, part[p.C + g * p.cg + c], t);
     }
-    s = wave_sum(s) / (BWD ? total : (float)p.cg);
     if (BWD) {
-        t = wave_sum(t) / total;
-        if (lane == 0) {
-            p.gsum[id * 2] = s;
-            p.gsum[id * 2 + 1] = t;
-        }
+        r1 = sum(s) / total;
+        r2 = sum(t) / total;
         return;
     }
-    for (int c = lane; c < p.cg; c += 64) {
-        const float d = part[c] - s;
-        t += __builtin_fmaf(d * d, (float)p.L, part[p.C + c]);
+    r1 = sum(s) / (float)p.cg;
+#pragma unroll 4
+    for (int c = lane; c < p.cg; c += step) {
+        const float d = part[g * p.cg + c] - r1;
+        t += __builtin_fmaf(d * d, (float)p.L, part[p.C + g * p.cg + c]);
     }
-    t = wave_sum(t) / total;
-    if (lane == 0) {
-        p.mean[id] = s;
-        p.rstd[id] = 1.0f / __builtin_sqrtf(t + p.eps);
-    }
+    r2 = 1.0f / __builtin_sqrtf(sum(t) / total + p.eps);
 }
 
-// Second pass: every value from its group's statistics.
+// Second pass: the tile's groups from their channels' sums (every workgroup for itself: a few loads), then every
+// value from its group's.  LDS: two floats to a group of the tile.
 template <typename T, int V, bool BWD>
 __global__ __launch_bounds__(256) void norm_apply_kernel(const NormParams p) {
-    const int64_t unit = blockIdx.x / p.tiles;
-    const int tile = (int)(blockIdx.x - unit * p.tiles);
-    const int64_t n = unit / p.splits;
-    const int split = (int)(unit - n * p.splits);
-    const int cu = min(p.tunits, p.C / V - tile * p.tunits);
+    extern __shared__ float lds[];
+    const unsigned unit = blockIdx.x / (unsigned)p.tiles, tile = blockIdx.x - unit * p.tiles;
+    const unsigned n = unit / (unsigned)p.splits, split = unit - n * p.splits;
+    const int cu = min(p.tunits, p.C / V - (int)tile * p.tunits);
     const int slots = blockDim.x / cu;
-    const int slot = threadIdx.x / cu, c = (tile * p.tunits + (int)threadIdx.x - slot * cu) * V;
-    if (slot >= slots) return;
+    const int slot = threadIdx.x / cu, c0 = tile * p.tunits * V, c = c0 + ((int)threadIdx.x - slot * cu) * V;
+    const bool on = slot < slots;
     const int64_t r0 = split * p.srows, r1 = min(p.L, r0 + p.srows);
+    const int len = (int)(r1 - r0);
+    const Buf xb = range_buf<T>(p.x, p, n, r0, r1), db = BWD ? range_buf<T>(p.dy, p, n, r0, r1) : xb, yb = range_buf<T>(p.y, p, n, r0, r1);
+    const unsigned step = (unsigned)(slots * p.C) * (unsigned)sizeof(T);
+    unsigned at = on ? (unsigned)(slot * p.C + c) * (unsigned)sizeof(T) : kNowhere;
+    constexpr int B = 4;
+    Unit<T, V> x[B], dy[B];
+    auto fetch = [&] {
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            x[i] = unit_load<T, V>(xb, at + i * step);
+            if (BWD) dy[i] = unit_load<T, V>(db, at + i * step);
+        }
+    };
+    fetch();  // on their way while the groups are joined
+    const int g0 = c0 / p.cg, groups = (c0 + cu * V - 1) / p.cg - g0 + 1;
+    {
+        const float* part = p.part + (int64_t)n * p.splits * 2 * p.C;
+        auto put = [&](int g, float a, float b) {
+            lds[g] = a;
+            lds[groups + g] = b;
+            if (!BWD && split == 0 && (g0 + g) * p.cg >= c0) {
+                p.mean[(int64_t)n * p.G + g0 + g] = a;
+                p.rstd[(int64_t)n * p.G + g0 + g] = b;
+            }
+        };
+        float a, b;
+        if (p.cg <= 32) {
+            for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+                join_group<BWD>(p, part, g0 + g, 0, 1, [](float v) { return v; }, a, b);
+                put(g, a, b);
+            }
+        } else {
+            for (int g = threadIdx.x >> 6; g < groups; g += blockDim.x >> 6) {
+                join_group<BWD>(p, part, g0 + g, threadIdx.x & 63, 64, wave_sum, a, b);
+                if ((threadIdx.x & 63) == 0) put(g, a, b);
+            }
+        }
+    }
+    __syncthreads();
+    if (!on) return;
     const GroupOf<V> grp(c, p.cg);
     float mean[V], rstd[V], w[V], b[V], m1[V], m2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t at = n * p.G + grp.g[j];
-        mean[j] = p.mean[at];
-        rstd[j] = p.rstd[at];
+        const int g = grp.g[j] - g0;
         w[j] = p.w ? p.w[c + j] : 1.0f;
         b[j] = p.b ? p.b[c + j] : 0.0f;
         if (BWD) {
-            m1[j] = p.gsum[at * 2];
-            m2[j] = p.gsum[at * 2 + 1];
+            mean[j] = p.mean[(int64_t)n * p.G + grp.g[j]];
+            rstd[j] = p.rstd[(int64_t)n * p.G + grp.g[j]];
+            m1[j] = lds[g];
+            m2[j] = lds[groups + g];
         } else {
-            w[j] *= rstd[j];
+            mean[j] = lds[g];
+            w[j] *= lds[groups + g];
         }
     }
-    const int64_t base = n * p.L * p.C + c;
-    const T *xp = static_cast<const T*>(p.x) + base, *dp = BWD ? static_cast<const T*>(p.dy) + base : nullptr;
-    T* yp = static_cast<T*>(p.y) + base;
-    constexpr int B = 4;
-    for (int64_t r = r0 + slot; r < r1; r += (int64_t)B * slots) {
-        Unit<T, V> x[B], dy[B];
+    for (int r = slot; r < len; r += B * slots) {
+        Unit<T, V> y[B];
 #pragma unroll
         for (int i = 0; i < B; ++i)
-            if (r + (int64_t)i * slots < r1) {
-                x[i] = *reinterpret_cast<const Unit<T, V>*>(xp + (r + (int64_t)i * slots) * p.C);
-                if (BWD) dy[i] = *reinterpret_cast<const Unit<T, V>*>(dp + (r + (int64_t)i * slots) * p.C);
-            }
 #pragma unroll
-        for (int i = 0; i < B; ++i)
-            if (r + (int64_t)i * slots < r1) {
-                Unit<T, V> y;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xd = to_f32(x[i].e[j]) - mean[j];
-                    if (BWD) {
-                        const float xh = xd * rstd[j], z = __builtin_fmaf(xh, w[j], b[j]);
-                        const float dz = act_bwd(to_f32(dy[i].e[j]), z, p.act);
-                        y.e[j] = from_f32<T>(rstd[j] * (dz * w[j] - m1[j] - xh * m2[j]));
-                    } else {
-                        y.e[j] = from_f32<T>(act_fwd(__builtin_fmaf(xd, w[j], b[j]), p.act));
-                    }
+            for (int j = 0; j < V; ++j) {
+                const float xd = to_f32(x[i].e[j]) - mean[j];
+                if (BWD) {
+                    const float xh = xd * rstd[j];
+                    const float dz = act_bwd(to_f32(dy[i].e[j]), __builtin_fmaf(xh, w[j], b[j]), p.act);
+                    y[i].e[j] = from_f32<T>(rstd[j] * (dz * w[j] - m1[j] - xh * m2[j]));
+                } else {
+                    y[i].e[j] = from_f32<T>(act_fwd(__builtin_fmaf(xd, w[j], b[j]), p.act));
                 }
-                *reinterpret_cast<Unit<T, V>*>(yp + (r + (int64_t)i * slots) * p.C) = y;
             }
+        const unsigned here = at;
+        at += B * step;
+        fetch();
+#pragma unroll
+        for (int i = 0; i < B; ++i) unit_store<T, V>(yb, here + i * step, y[i]);
     }
 }
 
@@ -606,17 +625,16 @@ hipError_t launch_v(const NormParams& p, bool bwd, hipStream_t s) {
         // the last tile may be narrower and so have more slots; slots x channels never exceeds threads x V
         const size_t lds = ((size_t)2 * p.threads * V + p.threads) * 4;
         const unsigned jt = (unsigned)((p.C + 15) / 16);
-        const dim3 jgrid((unsigned)p.N * jt), ggrid((unsigned)((p.N * p.G + 3) / 4));
+        const dim3 jgrid((unsigned)p.N * jt);
+        const size_t glds = ((size_t)2 * (p.tunits * V / p.cg + 2)) * 4;
         if (bwd) {
             hipLaunchKernelGGL((norm_sums_kernel<T, V, true>), grid, dim3(p.threads), lds, s, p);
             hipLaunchKernelGGL((norm_join_kernel<true>), jgrid, dim3(256), 0, s, p, jt);
-            hipLaunchKernelGGL((norm_group_kernel<true>), ggrid, dim3(256), 0, s, p);
-            hipLaunchKernelGGL((norm_apply_kernel<T, V, true>), grid, dim3(p.threads), 0, s, p);
+            hipLaunchKernelGGL((norm_apply_kernel<T, V, true>), grid, dim3(p.threads), glds, s, p);
         } else {
             hipLaunchKernelGGL((norm_sums_kernel<T, V, false>), grid, dim3(p.threads), lds, s, p);
             hipLaunchKernelGGL((norm_join_kernel<false>), jgrid, dim3(256), 0, s, p, jt);
-            hipLaunchKernelGGL((norm_group_kernel<false>), ggrid, dim3(256), 0, s, p);
-            hipLaunchKernelGGL((norm_apply_kernel<T, V, false>), grid, dim3(p.threads), 0, s, p);
+            hipLaunchKernelGGL((norm_apply_kernel<T, V, false>), grid, dim3(p.threads), glds, s, p);
         }
         e = hipGetLastError();
     }
@@ -666,15 +684,16 @@ int64_t plan_norm(NormParams& p, int io_bytes, bool aligned, bool backward) {
     p.tiles = (cu + p.threads - 1) / p.threads;
     p.tunits = (cu + p.tiles - 1) / p.tiles;
     p.tiles = (cu + p.tunits - 1) / p.tunits;
-    // about eight workgroups to a compute unit, ranges of at least 16 rows a slot
+    // about eight workgroups to a compute unit, ranges of at least 16 rows a slot and below 2^30 bytes
     const int64_t want = (2048 + p.N * p.tiles - 1) / (p.N * p.tiles);
     const int64_t slots = p.threads / p.tunits, floor_rows = slots * 16;
     int64_t splits = (p.L + floor_rows - 1) / floor_rows;
     if (splits > want) splits = want;
-    if (splits < 1) splits = 1;
+    const int64_t most = (1 << 28) / p.C, fewest = (p.L + most - 1) / most;
+    if (splits < fewest) splits = fewest;
     p.srows = (p.L + splits - 1) / splits;
     p.splits = (int)((p.L + p.srows - 1) / p.srows);
-    return p.N * p.splits * 2 * (int64_t)p.C * 4 + (backward ? p.N * p.G * 8 : 0);
+    return p.N * p.splits * 2 * (int64_t)p.C * 4;
 }
 
 hipError_t launch_group_norm_fwd(const NormParams& p, int io_dtype, hipStream_t s) {

@@ -29,7 +29,6 @@ struct NormParams {
     int splits;          // two passes: row ranges a sample
     int64_t srows;       // rows to a range
     float* part;         // workspace: per-channel sums [N][splits][2][C]
-    float* gsum;         // workspace, backward, two passes: [N][G][2]
 };
 
 // Fills the plan; returns the workspace bytes of the call.

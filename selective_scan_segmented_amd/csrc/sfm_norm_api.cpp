@@ -138,7 +138,6 @@ sfm_status sfm_group_norm_bwd(const void* dy, const void* x, const float* mean, 
     p.mean = const_cast<float*>(mean), p.rstd = const_cast<float*>(rstd);
     p.part = need > 0 ? static_cast<float*>(workspace) : nullptr;
     sfm::plan_norm(p, e, aligned16(dy) && aligned16(x) && aligned16(dx), true);
-    if (!p.slab) p.gsum = p.part + p.N * p.splits * 2 * (int64_t)p.C;
     return hip_status(sfm::launch_group_norm_bwd(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
 }
 
