@@ -26,6 +26,7 @@ constexpr int kDeltaThreads = 256;
 struct ChunkRows {
     float ghi[kC], glo[kC];  // running sum of g log2(e) in two parts: differences of near values are exact
     float eg[kC];            // e^G
+    float em[kC];            // e^-G where all of the chunk's e^G lie within 2^-64 .. 2^64, else zeros
     float er[kC];            // e^(G_C - G)
     float beta[kC];
     float rk[kC], rq[kC];    // 1 / length of the key and of the query (1 without l2norm)
@@ -118,28 +119,40 @@ template <typename T, int DK> struct RowShare {
 
 // Decays and gates of a chunk (one wave, a lane to a token; tokens past n: no decay, no gate).  The running sum is
 // taken in float64 (its differences, not its values, are what counts).
-template <typename T>
-__device__ __forceinline__ void chunk_gates(const T* g, const T* beta, int64_t ld, int n, ChunkRows* rows) {
-    const int lane = threadIdx.x & 63;
-    const int at = lane < n ? lane : 0;
-    float gv = to_f32(g[at * ld]), bv = to_f32(beta[at * ld]);
-    gv = lane < n ? (gv < kDeltaMinGate ? kDeltaMinGate : gv) : 0.0f;
-    bv = lane < n ? bv : 0.0f;
-    double s = (double)gv * 1.4426950408889634;
-    s += dpp_below<0x111, 0xf>(s);  // lanes 1, 2, 4, 8 below in the row of sixteen
-    s += dpp_below<0x112, 0xf>(s);
-    s += dpp_below<0x114, 0xf>(s);
-    s += dpp_below<0x118, 0xf>(s);
-    s += dpp_below<0x142, 0xa>(s);  // lane 15 of the row before, for rows 1 and 3
-    s += dpp_below<0x143, 0xc>(s);  // lane 31, for rows 2 and 3
-    const double end = __shfl(s, 63);
-    const float hi = (float)s;
-    rows->ghi[lane] = hi;
-    rows->glo[lane] = (float)(s - (double)hi);
-    rows->eg[lane] = exp2_fast((float)s);
-    rows->er[lane] = exp2_fast((float)(end - s));
-    rows->beta[lane] = bv;
-}
+struct ChunkGates {
+    float g, beta;
+    template <typename T> __device__ __forceinline__ void load(const T* gp, const T* bp, int64_t ld, int n) {
+        const int lane = threadIdx.x & 63;
+        const unsigned at = (unsigned)(lane * ld) * (unsigned)sizeof(T);
+        g = Io<T>::of_bits(buf_load_bits<T>(make_buf(gp, n * ld * (int)sizeof(T)), at));
+        beta = Io<T>::of_bits(buf_load_bits<T>(make_buf(bp, n * ld * (int)sizeof(T)), at));
+    }
+    __device__ __forceinline__ void store(ChunkRows* rows) const {
+        const int lane = threadIdx.x & 63;
+        double s = (double)(g < kDeltaMinGate ? kDeltaMinGate : g) * 1.4426950408889634;
+        s += dpp_below<0x111, 0xf>(s);  // lanes 1, 2, 4, 8 below in the row of sixteen
+        s += dpp_below<0x112, 0xf>(s);
+        s += dpp_below<0x114, 0xf>(s);
+        s += dpp_below<0x118, 0xf>(s);
+        s += dpp_below<0x142, 0xa>(s);  // lane 15 of the row before, for rows 1 and 3
+        s += dpp_below<0x143, 0xc>(s);  // lane 31, for rows 2 and 3
+        const double end = __shfl(s, 63);
+        const float hi = (float)s, lo = (float)(s - (double)hi);
+        rows->ghi[lane] = hi;
+        rows->glo[lane] = lo;
+        // the sum's own rounding as a factor: both exponentials good to their last places, and so their products
+        const float fix = lo * kLn2;
+        const float e = exp2_fast(hi), m = exp2_fast(-hi);
+        rows->eg[lane] = __builtin_fmaf(e, fix, e);
+        rows->em[lane] = __ballot(fabsf(hi) <= 64.0f) == ~0ull ? __builtin_fmaf(-m, fix, m) : 0.0f;
+        rows->er[lane] = exp2_fast((float)(end - s));
+        rows->beta[lane] = beta;
+    }
+};
+
+// Whether a decay between two tokens is the product e^(G_i) e^(-G_j): neither factor, nor its product with a row's,
+// leaves float32's range.  Otherwise each pair takes an exponential of its own.
+__device__ __forceinline__ bool mild_decay(const ChunkRows* rows) { return __builtin_amdgcn_readfirstlane(rows->em[0] > 0.0f); }
 
 // tile number 0..9 of the lower triangle of 4 x 4 tiles -> its row and column
 __device__ __forceinline__ void lower_tile(int n, int& ti, int& tj) {
@@ -193,6 +206,7 @@ __device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const C
 #pragma unroll
             for (int n = 0; n < 5; ++n) c[n] = mma(fa[n][i], fb[n][i], c[n]);
     }
+    const bool mild = mild_decay(rows);
 #pragma unroll
     for (int n = 0; n < 5; ++n) {
         const int id = wave + 4 * n;
@@ -200,26 +214,43 @@ __device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const C
         lower_tile(id < 10 ? id : id - 10, ti, tj);
         if (n < 2 || (n == 2 && id < 10)) {
             const int j = tj * 16 + l16, i0 = ti * 16 + g4;
-            const float rj = rows->rk[j], hj = rows->ghi[j], lj = rows->glo[j];
-            const f32x4 hi = four(rows->ghi + i0), lo = four(rows->glo + i0), ri = four(rows->rk + i0), be = four(rows->beta + i0);
+            const f32x4 f = four(rows->rk + i0) * four(rows->beta + i0);
             f32x4 m;
+            if (mild) {
+                const float fj = rows->rk[j] * rows->em[j];
+                m = c[n] * (f * four(rows->eg + i0) * fj);
+            } else {
+                const float fj = rows->rk[j], hj = rows->ghi[j], lj = rows->glo[j];
+                const f32x4 hi = four(rows->ghi + i0), lo = four(rows->glo + i0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                m[r] = i0 + r > j ? c[n][r] * (ri[r] * rj) * (be[r] * exp2_fast((hi[r] - hj) + (lo[r] - lj))) : 0.0f;
+                for (int r = 0; r < 4; ++r) m[r] = i0 + r > j ? c[n][r] * fj * f[r] * exp2_fast((hi[r] - hj) + (lo[r] - lj)) : 0.0f;
+            }
+            if (ti == tj)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) m[r] = g4 + r > l16 ? m[r] : 0.0f;
             *reinterpret_cast<f32x4*>(mt + tile_at(ti, tj) + l16 * 20 + g4) = m;
         } else {
             const int i = ti * 16 + l16, j0 = tj * 16 + g4;
-            const float ri = scale * rows->rq[i], hi = rows->ghi[i], lo = rows->glo[i];
-            const f32x4 hj = four(rows->ghi + j0), lj = four(rows->glo + j0), rj = four(rows->rk + j0);
+            const float fi = scale * rows->rq[i];
+            f32x4& x = a[n < 2 ? 0 : n - 2];
+            if (mild) {
+                x = c[n] * (four(rows->rk + j0) * four(rows->em + j0) * (fi * rows->eg[i]));
+            } else {
+                const float hi = rows->ghi[i], lo = rows->glo[i];
+                const f32x4 hj = four(rows->ghi + j0), lj = four(rows->glo + j0), rj = four(rows->rk + j0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                a[n - 2 < 0 ? 0 : n - 2][r] = j0 + r <= i ? c[n][r] * (ri * rj[r]) * exp2_fast((hi - hj[r]) + (lo - lj[r])) : 0.0f;
+                for (int r = 0; r < 4; ++r) x[r] = j0 + r <= i ? c[n][r] * (fi * rj[r]) * exp2_fast((hi - hj[r]) + (lo - lj[r])) : 0.0f;
+            }
+            if (ti == tj)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = g4 + r <= l16 ? x[r] : 0.0f;
         }
     }
 }
 
-// A's tiles (of chunk_products) as a computed operand; the tile right of a diagonal one in the same step is zeros
-template <int PA, typename T> __device__ __forceinline__ void store_a(const f32x4 (&a)[3], T* as) {
+// A's tiles (of chunk_products) one by one: f(tile, row tile, column tile), and zeros for the tile right of a diagonal
+// one that shares its step of 32
+template <typename F> __device__ __forceinline__ void each_a(const f32x4 (&a)[3], F f) {
     const int wave = wave_id();
 #pragma unroll
     for (int n = 0; n < 3; ++n) {
@@ -227,8 +258,8 @@ template <int PA, typename T> __device__ __forceinline__ void store_a(const f32x
         if (id < 0) continue;
         int ti, tj;
         lower_tile(id, ti, tj);
-        store_tile<PA>(a[n], as, ti, tj);
-        if (ti == tj && !(ti & 1)) store_tile<PA>(f32x4{0, 0, 0, 0}, as, ti, tj + 1);
+        f(a[n], ti, tj);
+        if (ti == tj && !(ti & 1)) f(f32x4{0, 0, 0, 0}, ti, tj + 1);
     }
 }
 
@@ -279,23 +310,23 @@ __device__ __forceinline__ void inverse_rows(const float* mt, f32x4 (&t)[4]) {
     }
 }
 
-// T's rows of this wave as a computed operand
-template <int PT, typename T> __device__ __forceinline__ void store_t(const f32x4 (&t)[4], T* ts) {
+// T's tiles of this wave likewise
+template <typename F> __device__ __forceinline__ void each_t(const f32x4 (&t)[4], F f) {
     const int wave = wave_id();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (j <= (wave | 1)) store_tile<PT>(t[j], ts, wave, j);
+        if (j <= (wave | 1)) f(t[j], wave, j);
 }
 
 // Gates, K and Q (in registers) to LDS, then M in LDS and, in registers, A's tiles and this wave's rows of T, all by
 // the whole workgroup.  `after` runs between M's making and its use (what needs K, Q or A only).
 template <typename T, int DK, typename After>
-__device__ __forceinline__ void make_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const DeltaParams& p,
-                                           const T* g, const T* beta, int n, ChunkRows* rows, T* ks, T* qs, float* mt,
+__device__ __forceinline__ void make_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const ChunkGates& gates,
+                                           const DeltaParams& p, ChunkRows* rows, T* ks, T* qs, float* mt,
                                            f32x4 (&a)[3], f32x4 (&t)[4], After after) {
+    if (wave_id() == 3) gates.store(rows);  // (its loads are the oldest; this wave has least to do below)
     kr.store(ks, rows->rk, p.l2norm);
     qr.store(qs, rows->rq, p.l2norm);
-    if (wave_id() == 0) chunk_gates<T>(g, beta, p.H, n, rows);
     lds_barrier();
     chunk_products<T, DK>(ks, qs, rows, p.scale, mt, a);
     lds_barrier();
@@ -307,15 +338,15 @@ __device__ __forceinline__ void make_chunk(const RowShare<T, DK>& kr, const RowS
 
 // The same with T (PT parts) at ts and A (PA parts) at as, where M lies before, visible to all at the end.
 template <typename T, int DK, int PT, int PA, typename Between>
-__device__ __forceinline__ void build_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const DeltaParams& p,
-                                            const T* g, const T* beta, int n, ChunkRows* rows, T* ks, T* qs, T* as,
-                                            T* ts, Between between) {
+__device__ __forceinline__ void build_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const ChunkGates& gates,
+                                            const DeltaParams& p, ChunkRows* rows, T* ks, T* qs, T* as, T* ts,
+                                            Between between) {
     f32x4 a[3], t[4];
-    make_chunk<T, DK>(kr, qr, p, g, beta, n, rows, ks, qs, reinterpret_cast<float*>(as), a, t, [] {});
-    store_t<PT>(t, ts);
+    make_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, reinterpret_cast<float*>(as), a, t, [] {});
+    each_t(t, [&](f32x4 x, int rt, int tj) { store_tile<PT>(x, ts, rt, tj); });
     between();     // what needs K and Q only
     lds_barrier();  // M is done with
-    store_a<PA>(a, as);
+    each_a(a, [&](f32x4 x, int rt, int tj) { store_tile<PA>(x, as, rt, tj); });
     lds_barrier();
 }
 

@@ -35,6 +35,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     using Ops = ChunkOperands<T, P>;
     constexpr int PY = P < 2 ? P : 2;  // parts that only the outputs see: their type's rounding is far above the third
     constexpr int E = (int)sizeof(T);
+    constexpr bool kOnTheWay = W == kWhole || W == kSingle;
     extern __shared__ char lds[];
     ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs),
@@ -74,11 +75,13 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     bool zero = W == kSingle || !p.h0;  // the state is zero: its products are left out
 
     RowShare<T, DK> kr, qr;
+    ChunkGates gates;
     Linear<Ops::a> ops;                // row scalars and T
     Linear<PY * L::frag_bytes> opa;    // A
     unsigned v[4][4];                  // values' bits
     auto fetch = [&](int64_t t0) {
         const int64_t n = min((int64_t)kC, len - t0);
+        if (kOnTheWay) gates.load(gp + t0 * p.H, bp + t0 * p.H, p.H, (int)n);
         kr.load(make_buf(kp + t0 * p.ldk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
         if (W != kStates) qr.load(make_buf(qp + t0 * p.ldq, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
         if (W == kPrepared || W == kStates) {
@@ -92,7 +95,6 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(vb, fresh(voff) + (unsigned)((rt * 16 + r) * p.ldv) * E);
     };
-    constexpr bool kOnTheWay = W == kWhole || W == kSingle;
     if (!kOnTheWay && len > 0) fetch(0);  // ahead of its use by a chunk
 
     for (int64_t t0 = 0; t0 < len; t0 += kC) {
@@ -146,7 +148,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
         if (kOnTheWay) fetch(t0);  // (registers that other workgroups on the unit can use better)
         lds_barrier();  // the chunk before is done with LDS
         if constexpr (kOnTheWay) {
-            build_chunk<T, DK, P, PY>(kr, qr, p, gp + t0 * p.H, bp + t0 * p.H, (int)n_tok, rows, ks, qs, as, ts, state_products);
+            build_chunk<T, DK, P, PY>(kr, qr, gates, p, rows, ks, qs, as, ts, state_products);
         } else {
             kr.store(ks, nullptr, 0);
             ops.store(lds);
@@ -265,23 +267,25 @@ __global__ __launch_bounds__(kDeltaThreads, (PrepareLds<T, DK>::groups)) void de
     if (t0 >= len) return;
     const int64_t n = min((int64_t)kC, len - t0);
     first += t0;
+    const int64_t at = first * p.H + h;
+    ChunkGates gates;
+    gates.load(static_cast<const T*>(p.g) + at, static_cast<const T*>(p.beta) + at, p.H, (int)n);
     RowShare<T, DK> kr, qr;
     kr.load(make_buf(static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
     qr.load(make_buf(static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
-    const int64_t at = first * p.H + h;
     char* o = p.w_ops + ((int64_t)(chunk_entry(p, s, first - t0) + (unsigned)(t0 / kC)) * p.H + h) * Ops::bytes;
+    const Buf ob = make_buf(o, Ops::bytes);
     f32x4 a[3], t[4];
-    make_chunk<T, DK>(kr, qr, p, static_cast<const T*>(p.g) + at, static_cast<const T*>(p.beta) + at, (int)n, rows, ks, qs,
-                      reinterpret_cast<float*>(lds + L::mt), a, t, [&] {
-                          store_a<P>(a, reinterpret_cast<T*>(o + Ops::a));
-                          if (threadIdx.x < sizeof(ChunkRows) / 16)
-                              reinterpret_cast<uint4*>(o)[threadIdx.x] = reinterpret_cast<const uint4*>(lds)[threadIdx.x];
-                      });
-    store_t<P>(t, reinterpret_cast<T*>(o + Ops::t));
+    make_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, reinterpret_cast<float*>(lds + L::mt), a, t, [&] {
+        each_a(a, [&](f32x4 x, int rt, int tj) { store_tile<P, T>(x, ob, Ops::a, rt, tj); });
+        if (threadIdx.x < sizeof(ChunkRows) / 16)
+            reinterpret_cast<uint4*>(o)[threadIdx.x] = reinterpret_cast<const uint4*>(lds)[threadIdx.x];
+    });
+    each_t(t, [&](f32x4 x, int rt, int tj) { store_tile<P, T>(x, ob, Ops::t, rt, tj); });
 }
 
-static_assert(ChunkOperands<float, 1>::bytes == 7 * kC * 4 + 2 * 6 * 64 * 8 * 4 &&
-              ChunkOperands<__bf16, 3>::bytes == 7 * kC * 4 + 2 * 6 * 64 * 8 * 2 * 3, "delta_operand_bytes");
+static_assert(ChunkOperands<float, 1>::bytes == 8 * kC * 4 + 2 * 6 * 64 * 8 * 4 &&
+              ChunkOperands<__bf16, 3>::bytes == 8 * kC * 4 + 2 * 6 * 64 * 8 * 2 * 3, "delta_operand_bytes");
 
 // dynamic LDS above the default limit has to be asked for
 template <typename K> hipError_t allow_lds(K kern, int bytes) {

@@ -179,6 +179,28 @@ template <int P, typename T> __device__ __forceinline__ void store_tile(f32x4 x,
     }
 }
 
+// the same to memory: byte `at` of a buffer
+template <int P, typename T> __device__ __forceinline__ void store_tile(f32x4 x, const Buf& b, unsigned at, int rt, int tj) {
+    const int lane = threadIdx.x & 63;
+    at += (unsigned)(lower_frag(rt, tj >> 1) * kFragSize + (tj & 1) * 4) * (unsigned)sizeof(T) + (unsigned)lane * 8u * (unsigned)sizeof(T);
+    if constexpr (sizeof(T) == 4) {
+        typedef unsigned word4 __attribute__((ext_vector_type(4)));
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(word4, x), b.r, at, 0, 0);
+    } else {
+        typedef unsigned word2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            bf16x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = (__bf16)x[j];
+                x[j] -= (float)v[j];
+            }
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(word2, v), b.r, at + q * kLowerFrags * kFragSize * 2, 0, 0);
+        }
+    }
+}
+
 // c += a b, a given by its PA parts and b by its PB: the products of parts that are not below the last part of the
 // finer operand, smallest first
 template <int PA, int PB, typename T>

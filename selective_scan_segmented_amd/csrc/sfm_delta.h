@@ -70,7 +70,7 @@ int64_t plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64
 inline int64_t delta_chunk_entries(int64_t rows, int64_t tokens) { return tokens / kDeltaChunk + rows; }
 // bytes of a chunk and head's prepared operands (ChunkOperands), P parts to bfloat16 ones
 inline int64_t delta_operand_bytes(int io_dtype, int parts) {
-    return 7 * kDeltaChunk * 4 + 2 * 6 * 64 * 8 * (io_dtype == 0 ? 4 : 2 * (int64_t)parts);
+    return 8 * kDeltaChunk * 4 + 2 * 6 * 64 * 8 * (io_dtype == 0 ? 4 : 2 * (int64_t)parts);
 }
 // chunked forward, one translation unit per io type
 hipError_t launch_delta_fwd_f32(const DeltaParams& p, hipStream_t s);
