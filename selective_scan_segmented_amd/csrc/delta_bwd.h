@@ -406,7 +406,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_walks_kernel(c
     if (blockIdx.x < units)
         narrow_reverse<T, DK, P, VEC>(p, tiles, die_local(blockIdx.x, units));
     else
-        narrow_walk<T, DK, P, kStates, VEC>(p, tiles, die_local(blockIdx.x - units, units));
+        narrow_walk<T, DK, P, kStates, VEC>(p, tiles / NarrowShape<DK>::CT, die_local(blockIdx.x - units, units / NarrowShape<DK>::CT));
 }
 
 // ---------------------------------------------------------------- per chunk and head
@@ -813,10 +813,10 @@ template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParam
     auto walks = !p.narrow ? delta_walks_kernel<T, DK, P>
                  : p.vec_k ? delta_narrow_walks_kernel<T, DK, P, true>
                            : delta_narrow_walks_kernel<T, DK, P, false>;
-    constexpr int nb = NarrowLds<T, DK, P, P, 3 * P + 1>::bytes, ns = NarrowLds<T, DK, P, 0, 2 * P>::bytes;
+    constexpr int nb = NarrowLds<T, DK, P, P, 3 * P + 1>::bytes, ns = WalkNarrowLds<T, DK, P, 0>::bytes;
     const int wb = p.narrow ? (nb > ns ? nb : ns) : WalkLds<T, DK, P>::bytes;
     if ((e = allow_lds(walks, wb)) != hipSuccess) return e;
-    hipLaunchKernelGGL(walks, dim3(2 * units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), wb, s, p, tiles, units);
+    hipLaunchKernelGGL(walks, dim3(p.narrow ? units + units / NarrowShape<DK>::CT : 2 * units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), wb, s, p, tiles, units);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), cu = (unsigned)p.rows * chunks * p.H;
     auto grads = delta_grads_kernel<T, DK, PW>;

@@ -91,6 +91,24 @@ __device__ __forceinline__ f32x4 mma(const Frag<float>& a, const Frag<float>& b,
     return mma4(a.hi, b.hi, mma4(a.lo, b.lo, c));
 }
 
+// Four values rounded to bfloat16, of which x keeps the rounding errors (exact: a float32's is a float32).  They are
+// taken back from the pairs as packed: two instructions a value and level, where a conversion apiece would be three.
+__device__ __forceinline__ bf16x4 take_part(f32x4& x) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef unsigned word2 __attribute__((ext_vector_type(2)));
+    word2 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        unsigned u = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x[2 * i], x[2 * i + 1]}), bf16x2));
+        asm("" : "+v"(u));
+        w[i] = u;
+        x[2 * i] -= __builtin_bit_cast(float, u << 16);
+        x[2 * i + 1] -= __builtin_bit_cast(float, u & 0xffff0000u);
+    }
+    return __builtin_bit_cast(bf16x4, w);
+}
+
 // A computed operand: P parts whose sum is the float32 values (one part for float32).
 template <typename T, int P> struct Parts {
     Frag<T> p[P];
@@ -100,18 +118,8 @@ template <typename T, int P> struct Parts {
 template <int P> __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Parts<__bf16, P>& out) {
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            out.p[q].v[j] = (__bf16)lo[j];
-            out.p[q].v[4 + j] = (__bf16)hi[j];
-        }
-        if (q + 1 < P) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // exact: the rounding error of a float32 is a float32
-                lo[j] -= (float)out.p[q].v[j];
-                hi[j] -= (float)out.p[q].v[4 + j];
-            }
-        }
+        const bf16x4 a = take_part(lo), b = take_part(hi);
+        out.p[q].v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 }
 template <int P> __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Parts<float, P>& out) {
@@ -168,12 +176,7 @@ template <int P, typename T> __device__ __forceinline__ void store_tile(f32x4 x,
     } else {
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            bf16x4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = (__bf16)x[j];
-                x[j] -= (float)v[j];
-            }
+            const bf16x4 v = take_part(x);
             *reinterpret_cast<bf16x4*>(p + q * kLowerFrags * kFragSize) = v;
         }
     }
@@ -190,12 +193,7 @@ template <int P, typename T> __device__ __forceinline__ void store_tile(f32x4 x,
         typedef unsigned word2 __attribute__((ext_vector_type(2)));
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            bf16x4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = (__bf16)x[j];
-                x[j] -= (float)v[j];
-            }
+            const bf16x4 v = take_part(x);
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(word2, v), b.r, at + q * kLowerFrags * kFragSize * 2, 0, 0);
         }
     }
