@@ -204,17 +204,45 @@ __device__ __forceinline__ void reverse(const DeltaParams& p, unsigned tiles, un
         for (int r = 0; r < 4; ++r) buf_store<float>(sb, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u, dS[d][r]);
 }
 
-// The same with sixteen columns to a workgroup (delta_narrow.h): wave w has a quarter of the state gradient's keys and
-// the tokens 16 w .. + 15.
+// The same with few columns to a workgroup (delta_narrow.h): the waves that carry the state's gradient sum K dS' over
+// their keys, and the others bring the operands and make what does not hang on the state a chunk ahead: A^T dO and
+// Q^T (e^G scale dO).  T lies in LDS for its transposing reads (bfloat16) or is gathered from memory (float32).
+template <typename T, int DK, int P> struct ReverseNarrowLds {
+    using Sh = ChunkShape<T, DK>;
+    using N = NarrowShape<DK>;
+    static constexpr int E = (int)sizeof(T), frag = kFragSize * E, lower = P * kLowerFrags * frag, ex = N::CT * 2 * frag;
+    static constexpr int ks = (int)sizeof(ChunkRows), ts = ks + Sh::row_bytes, half = ts + (E == 2 ? lower : 0);
+    static constexpr int as = 2 * half, qs = as + lower, gs = qs + Sh::row_bytes, wq = gs + ex, up = wq + P * ex, wk = up + P * ex,
+                         xp = wk + P * ex, za = xp + 16 * 1024, zq = za + N::CT * 4 * 1024, bytes = zq + 8 * 1024;
+    static_assert(bytes <= 160 * 1024, "fits a compute unit");
+};
+
+// load_parts_transposed from memory, float32
+__device__ __forceinline__ Frag<float> gather_transposed(const Buf& b, unsigned base, int jt, int kb) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
+    f32x4 x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int it = 2 * kb + i;
+        const int e = lower_frag(it, jt >> 1) * kFragSize + ((l16 >> 2) * 16 + g4) * 8 + (jt & 1) * 4 + (l16 & 3);
+        const unsigned at = fresh(it >= jt ? base + (unsigned)e * 4u : kNowhere);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = buf_load<float>(b, at + (unsigned)j * 32u);
+    }
+    return Frag<float>{x[0], x[1]};
+}
+
 template <typename T, int DK, int P, bool VEC>
 __device__ __forceinline__ void narrow_reverse(const DeltaParams& p, unsigned tiles, unsigned unit) {
-    constexpr int PW = P < 2 ? P : 2, E = (int)sizeof(T), DT = DK / 64, NS = DK / 32;
+    constexpr int PW = P < 2 ? P : 2, E = (int)sizeof(T);
     using Sh = ChunkShape<T, DK>;
     using Ops = ChunkOperands<T, P>;
-    using L = NarrowLds<T, DK, P, P, 3 * P + 1>;  // dU, two factors of the state's update (P planes each), dO (exact)
+    using N = NarrowShape<DK>;
+    using L = ReverseNarrowLds<T, DK, P>;
+    constexpr int CT = N::CT, KW = N::KW, NF = CT * 2;
     extern __shared__ char lds[];
-    T *sp = reinterpret_cast<T*>(lds + L::sp), *up = reinterpret_cast<T*>(lds + L::xp), *wk = up + P * L::plane,
-      *wq = wk + P * L::plane, *gs = wq + P * L::plane;
+    const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
+    const N my(wave & 3);
 
     const unsigned rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
@@ -223,173 +251,286 @@ __device__ __forceinline__ void narrow_reverse(const DeltaParams& p, unsigned ti
     delta_row(p, s, first, len);
     const int chunks = (len + kC - 1) / kC;
     const int64_t entry0 = (int64_t)chunk_entry(p, s, first) * p.H + h;
+    T *up = reinterpret_cast<T*>(lds + L::up), *wk = reinterpret_cast<T*>(lds + L::wk), *wq = reinterpret_cast<T*>(lds + L::wq),
+      *gs = reinterpret_cast<T*>(lds + L::gs);
+    f32x4 *xp = reinterpret_cast<f32x4*>(lds + L::xp) + lane, *za = reinterpret_cast<f32x4*>(lds + L::za) + lane,
+          *zq = reinterpret_cast<f32x4*>(lds + L::zq) + lane;
+    auto half_of = [&](int i) { return lds + (i & 1 ? L::half : 0); };
+    const int col = (int)(unit - rh * tiles) * N::cols + my.cw * 16 + l16;
+    const int64_t obase = (first * p.H + h) * p.dv, ldo = (int64_t)p.H * p.dv;
+    // rows of the transposed triangle: the upper tiles have both steps of 32 columns, the lower ones the second
+    auto both = [&](int i) { return CT == 2 ? i == 0 : my.kw < 2; };
 
-    if (wave_id() >= 4) {  // step i is chunk chunks - 1 - i
+    if (wave >= 4) {  // step i is chunk chunks - 1 - i
+        if (chunks <= 0) return;
         const T* qp = static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk;
         const T* kp = static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk;
+        const T* gop = static_cast<const T*>(p.dout) + obase;
         RowShare<T, DK> kr, qr;
-        Linear<Ops::bytes> ops;
-        static_assert(L::as == Ops::a, "T and A lie in LDS as in the workspace");
-        auto load = [&](int i, int piece) {
+        Linear<(int)sizeof(ChunkRows)> scalars;
+        Linear<L::lower> ta, tt;
+        unsigned v[CT][4];
+        f32x4 eg[CT], rq[CT], Za[CT], Zq[2];
+        auto load_k = [&](int i) {  // (behind the row's end the buffers are empty)
             const bool in = i < chunks;
             const int c = in ? chunks - 1 - i : 0;
             const int64_t t = (int64_t)c * kC, n = in ? min((int64_t)kC, len - t) : 0;
-            if (piece == 0) {
-                kr.load(make_buf(kp + t * p.ldk, n * p.ldk * E), p.ldk, p.dk, VEC);
-                return;
-            }
-            qr.load(make_buf(qp + t * p.ldq, n * p.ldq * E), p.ldq, p.dk, VEC);
-            ops.load(p.w_ops + (entry0 + (int64_t)c * p.H) * Ops::bytes, in);
+            const char* o = p.w_ops + (entry0 + (int64_t)c * p.H) * Ops::bytes;
+            kr.load(make_buf(kp + t * p.ldk, n * p.ldk * E), p.ldk, p.dk, VEC);
+            scalars.load(o, in);
+            if constexpr (E == 2) tt.load(o + Ops::t, in);
         };
-        auto store = [&](char* to) {
+        auto store_k = [&](char* to) {
             kr.store(reinterpret_cast<T*>(to + L::ks), nullptr, 0);
-            qr.store(reinterpret_cast<T*>(to + L::qs), nullptr, 0);
-            ops.store(to);
+            scalars.store(to);
+            if constexpr (E == 2) tt.store(to + L::ts);
         };
-        narrow_loader<L::NB, L::half>(lds, chunks, load, store);
+        auto load_q = [&](int i) {
+            const bool in = i < chunks;
+            const int c = in ? chunks - 1 - i : 0;
+            const int64_t t = (int64_t)c * kC, n = in ? min((int64_t)kC, len - t) : 0;
+            const char* o = p.w_ops + (entry0 + (int64_t)c * p.H) * Ops::bytes;
+            const Buf ob = make_buf(gop + t * ldo, n * ldo * E), rb = make_buf(o, in ? sizeof(ChunkRows) : 0);
+            typedef unsigned word4 __attribute__((ext_vector_type(4)));
+            qr.load(make_buf(qp + t * p.ldq, n * p.ldq * E), p.ldq, p.dk, VEC);
+            ta.load(o + Ops::a, in);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int tok = my.tile(j) * 16 + g4;
+                const unsigned at = fresh(col < p.dv ? (unsigned)(tok * ldo + col) * E : kNowhere);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[j][r] = buf_load_bits<T>(ob, at + (unsigned)(r * ldo) * E);
+                eg[j] = __builtin_bit_cast(f32x4, buf_load<word4>(rb, (unsigned)(offsetof(ChunkRows, eg) + tok * 4)));
+                rq[j] = __builtin_bit_cast(f32x4, buf_load<word4>(rb, (unsigned)(offsetof(ChunkRows, rq) + tok * 4)));
+            }
+        };
+        auto store_q = [&] {  // Q, A and dO, as it is and by e^G scale
+            qr.store(reinterpret_cast<T*>(lds + L::qs), nullptr, 0);
+            ta.store(lds + L::as);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int t = my.tile(j);
+                f32x4 x;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = Io<T>::of_bits(v[j][r]);
+                store_half<1, NF>(x, gs, my.cw * 2 + (t >> 1), t & 1);
+                store_half<P, NF>(x * (eg[j] * rq[j] * p.scale), wq, my.cw * 2 + (t >> 1), t & 1);
+            }
+        };
+        auto products = [&] {
+            const T *as = reinterpret_cast<const T*>(lds + L::as), *qs = reinterpret_cast<const T*>(lds + L::qs) + my.kw * 32;
+            Parts<T, 1> go[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) go[kb] = load_exchange<1, NF>(gs, my.cw * 2 + kb);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                f32x4 x[3];
+                zero3(x);
+                if (both(j)) mma_spread<P, 1>(load_parts_transposed<P>(as, my.tile(j), 0), go[0], x, 0);
+                mma_spread<P, 1>(load_parts_transposed<P>(as, my.tile(j), 1), go[1], x, 0);
+                Za[j] = gather3(x);
+            }
+            Parts<T, P> fv[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) fv[kb] = load_exchange<P, NF>(wq, my.cw * 2 + kb);
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                f32x4 x[3];
+                zero3(x);
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const Parts<T, 1> tq = {{load_eight_transposed<T>(qs + kb * 32 * Sh::KS, Sh::KS, d)}};
+                    mma_spread<1, P>(tq, fv[kb], x, 0);
+                }
+                Zq[d] = gather3(x);
+            }
+        };
+        auto store_za = [&] {
+#pragma unroll
+            for (int j = 0; j < CT; ++j) za[(my.cw * 4 + my.tile(j)) * 64] = Za[j];
+        };
+        load_q(0);
+        load_k(0);
+        store_q();
+        store_k(lds);
+        load_q(1);
+        load_k(1);
+        lds_barrier();
+        products();
+        store_za();
+        for (int i = 0; i < chunks; ++i) {
+            lds_barrier();
+#pragma unroll
+            for (int d = 0; d < 2; ++d) zq[((wave & 3) * 2 + d) * 64] = Zq[d];
+            store_q();
+            load_q(i + 2);
+            lds_barrier();
+            products();
+            store_k(half_of(i + 1));
+            lds_barrier();
+            store_za();
+            load_k(i + 2);
+        }
         return;
     }
 
-    __builtin_amdgcn_s_setprio(2);
-    const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4, tok = wave * 16 + g4;
-    const int col = (int)(unit - rh * tiles) * 16 + l16;
-    const int64_t obase = (first * p.H + h) * p.dv, ldo = (int64_t)p.H * p.dv;
-    const T* gop = static_cast<const T*>(p.dout) + obase;
+    __builtin_amdgcn_s_setprio(3);
     T* dvp = static_cast<T*>(p.dv_) + obase;
     const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
-    const int key = wave * 16 * DT + g4;
+    const int key = my.kw * 32 + 2 * g4;
     const unsigned soff = col < p.dv ? (unsigned)(key * p.dv + col) * 4u : kNowhere;
-    const unsigned ooff = col < p.dv ? (unsigned)(tok * ldo + col) * E : kNowhere;
     const int vals = (p.dv + 63) / 64 * 64;
 
-    f32x4 dS[DT];
+    f32x4 dS[2];
 #pragma unroll
-    for (int d = 0; d < DT; ++d) dS[d] = f32x4{0, 0, 0, 0};
+    for (int d = 0; d < 2; ++d) dS[d] = f32x4{0, 0, 0, 0};
     if (p.dhT) {
         const Buf b = make_buf(p.dhT + sbase, (int64_t)p.dk * p.dv * 4);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < 2; ++d)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dS[d][r] = buf_load<float>(b, soff + (unsigned)((d * 16 + r) * p.dv) * 4u);
+            for (int r = 0; r < 4; ++r) dS[d][r] = buf_load<float>(b, soff + (unsigned)((d * 4 + r) * p.dv) * 4u);
     }
-    unsigned v[4];
-    auto fetch = [&](int c) {  // dO of chunk c
-        const int64_t t = c >= 0 ? (int64_t)c * kC : 0, n = c >= 0 ? min((int64_t)kC, len - t) : 0;
-        const Buf ob = make_buf(gop + t * ldo, n * ldo * E);
+    Parts<T, 1> fk[4];  // K's rows, this wave's keys, of the chunk to come
+    auto load_k = [&](int i) {
+        const T* ks = reinterpret_cast<const T*>(half_of(i) + L::ks) + my.kw * 32 + l16 * Sh::KS + 2 * g4;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = buf_load_bits<T>(ob, ooff + (unsigned)(r * ldo) * E);
+        for (int t = 0; t < 4; ++t) fk[t].p[0] = load_eight<T>(ks + t * 16 * Sh::KS);
     };
-    fetch(chunks - 1);
+    if (chunks > 0) {
+        lds_barrier();
+        load_k(0);
+    }
 
     for (int i = 0; i < chunks; ++i) {
         const int c = chunks - 1 - i;
         const int64_t t0 = (int64_t)c * kC, n_tok = min((int64_t)kC, len - t0), entry = entry0 + (int64_t)c * p.H;
-        const char* half = lds + (L::NB == 2 && (i & 1) ? L::half : 0);
+        const char* half = half_of(i);
         const ChunkRows* rows = reinterpret_cast<const ChunkRows*>(half);
-        const T *ts = reinterpret_cast<const T*>(half + L::ts), *as = reinterpret_cast<const T*>(half + L::as),
-                *ks = reinterpret_cast<const T*>(half + L::ks), *qs = reinterpret_cast<const T*>(half + L::qs);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            const int td = wave * DT + d;
-            store_half_both<PW, P, NS>(dS[d], sp, td >> 1, td & 1,
-                                       reinterpret_cast<T*>(p.w_ds) + entry * PW * vals * DK + (int64_t)col * DK + key + d * 16,
-                                       (int64_t)vals * DK);
-        }
-        f32x4 gov;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) gov[r] = Io<T>::of_bits(v[r]);
-        store_half<1, 2>(gov, gs, wave >> 1, wave & 1);
-        fetch(c - 1);
-        lds_barrier();
-        const f32x4 be = four(rows->beta + tok), eg = four(rows->eg + tok), rk = four(rows->rk + tok);
-        const f32x4 fq = eg * four(rows->rq + tok) * p.scale, fk = eg * rk;
-        // dU = e^(G_C - G) K dS' + A^T dO
+        const T* ks = reinterpret_cast<const T*>(half + L::ks);
+        // K dS' over this wave's keys
         {
-            Parts<T, 1> kk[NS], go[2];
-            Parts<T, P> fs[NS], at[2];
+            Parts<T, P> fs;
+            split<P>(dS[0], dS[1], fs);
+            f32x4 x[4];
 #pragma unroll
-            for (int kb = 0; kb < NS; ++kb) {
-                fs[kb] = load_exchange<P, NS>(sp, kb);
-                kk[kb].p[0] = load_runs<T>(ks + (wave * 16 + l16) * Sh::KS + kb * 32 + g4);
-            }
+            for (int t = 0; t < 4; ++t) x[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                at[kb] = load_parts_transposed<P>(as, wave, wave < 2 ? kb : 1);
-                go[kb] = load_exchange<1, 2>(gs, kb);
-            }
-            loads_end();
-            f32x4 x[3];
-            zero3(x);
+            for (int q = 0; q < P; ++q)
 #pragma unroll
-            for (int kb = 0; kb < NS; ++kb) mma_spread<1, P>(kk[kb], fs[kb], x, 0);
-            const f32x4 f = four(rows->er + tok) * rk;
+                for (int t = 0; t < 4; ++t) x[t] = mma(fk[t].p[0], fs.p[q], x[t]);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) x[j] *= f;
-            if (wave < 2) mma_spread<P, 1>(at[0], go[0], x, 0);
-            mma_spread<P, 1>(at[1], go[1], x, 0);
-            store_half<P, 2>(gather3(x), up, wave >> 1, wave & 1);
+            for (int t = 0; t < 4; ++t) xp[((my.cw * 4 + t) * KW + my.kw) * 64] = x[t];
+            store_eight<PW>(fs, reinterpret_cast<T*>(p.w_ds) + entry * PW * vals * DK + (int64_t)col * DK + key, (int64_t)vals * DK);
         }
-        store_half<P, 2>(gov * fq, wq, wave >> 1, wave & 1);
-        Parts<T, P> tt[2];
+        f32x4 er[CT], be[CT], fw[CT];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) tt[kb] = load_parts_transposed<P>(ts, wave, wave < 2 ? kb : 1);
+        for (int j = 0; j < CT; ++j) {
+            const int tok = my.tile(j) * 16 + g4;
+            er[j] = four(rows->er + tok) * four(rows->rk + tok);
+        }
+        lds_barrier();
+        // dU = e^(G_C - G) K dS' + A^T dO
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int t = my.tile(j);
+            f32x4 x[KW];
+#pragma unroll
+            for (int k = 0; k < KW; ++k) x[k] = xp[((my.cw * 4 + t) * KW + k) * 64];
+            const f32x4 z = za[(my.cw * 4 + t) * 64];
+            f32x4 sum = x[0] + x[1];
+            if constexpr (KW == 4) sum += x[2] + x[3];
+            store_half<P, NF>(sum * er[j] + z, up, my.cw * 2 + (t >> 1), t & 1);
+        }
+        Parts<T, P> tt[CT][2];
+        if constexpr (E == 2) {
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+                    if (CT == 1 || kb == 1 || j == 0)
+                        tt[j][kb] = load_parts_transposed<P>(reinterpret_cast<const T*>(half + L::ts), my.tile(j), both(j) ? kb : 1);
+        } else {
+            const Buf tb = make_buf(p.w_ops + entry * Ops::bytes, Ops::bytes);
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+                    if (CT == 1 || kb == 1 || j == 0) tt[j][kb].p[0] = gather_transposed(tb, Ops::t, my.tile(j), both(j) ? kb : 1);
+        }
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int tok = my.tile(j) * 16 + g4;
+            be[j] = four(rows->beta + tok);
+            fw[j] = -four(rows->eg + tok) * four(rows->rk + tok);
+        }
         lds_barrier();
         // dR = T^T dU
-        f32x4 dR;
+        f32x4 dR[CT];
         {
             Parts<T, P> fu[2];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) fu[kb] = load_exchange<P, 2>(up, kb);
+            for (int kb = 0; kb < 2; ++kb) fu[kb] = load_exchange<P, NF>(up, my.cw * 2 + kb);
             loads_end();
-            f32x4 x[3];
-            zero3(x);
-            if (wave < 2) mma_spread<P, P>(tt[0], fu[0], x, 0);
-            mma_spread<P, P>(tt[1], fu[1], x, 0);
-            dR = gather3(x);
-        }
-        const f32x4 gv = be * dR;
-        store_half<P, 2>(gv * -fk, wk, wave >> 1, wave & 1);
-        lds_barrier();
-        if (c > 0 || p.dh0) {
-            Parts<T, P> fw[2], fv[2];
-            Parts<T, 1> tk[DT][2], tq[DT][2];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                fw[kb] = load_exchange<P, 2>(wk, kb);
-                fv[kb] = load_exchange<P, 2>(wq, kb);
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    tk[d][kb].p[0] = load_transposed<T>(ks + kb * 32 * Sh::KS + (wave * DT + d) * 16, Sh::KS);
-                    tq[d][kb].p[0] = load_transposed<T>(qs + kb * 32 * Sh::KS + (wave * DT + d) * 16, Sh::KS);
-                }
-            }
-            loads_end();
-            const float ec = rows->eg[kC - 1];
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
+            for (int j = 0; j < CT; ++j) {
                 f32x4 x[3];
                 zero3(x);
-                x[0] = dS[d] * ec;
+                if (both(j)) mma_spread<P, P>(tt[j][0], fu[0], x, 0);
+                mma_spread<P, P>(tt[j][1], fu[1], x, 0);
+                dR[j] = gather3(x);
+            }
+        }
+        Parts<T, 1> kt[2][2];
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    mma_spread<1, P>(tk[d][kb], fw[kb], x, 0);
-                    mma_spread<1, P>(tq[d][kb], fv[kb], x, 1);
-                }
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) kt[d][kb].p[0] = load_eight_transposed<T>(ks + kb * 32 * Sh::KS + my.kw * 32, Sh::KS, d);
+        loads_end();
+        const Buf db = make_buf(dvp + t0 * ldo, n_tok * ldo * E);
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int t = my.tile(j);
+            const f32x4 gv = be[j] * dR[j];
+            store_half<P, NF>(gv * fw[j], wk, my.cw * 2 + (t >> 1), t & 1);
+            const unsigned at = fresh(col < p.dv ? (unsigned)((t * 16 + g4) * ldo + col) * E : kNowhere);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) buf_store<T>(db, at + (unsigned)(r * ldo) * E, from_f32<T>(gv[r]));
+            store_four<PW>(dR[j], reinterpret_cast<T*>(p.w_dr) + entry * PW * vals * kC + (int64_t)col * kC + t * 16 + g4, (int64_t)vals * kC);
+        }
+        const float ec = rows->eg[kC - 1];
+        lds_barrier();
+        // dS = e^(G_C) dS' + K^T (-beta e^G dR) + Q^T (e^G scale dO)
+        Parts<T, P> fv[2];
+        f32x4 z[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) fv[kb] = load_exchange<P, NF>(wk, my.cw * 2 + kb);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) z[d] = zq[(wave * 2 + d) * 64];
+        if (CT == 1) load_k(i + 1);
+        loads_end();
+        if (c > 0 || p.dh0) {
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                f32x4 x[3];
+                zero3(x);
+                x[0] = dS[d] * ec + z[d];
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) mma_spread<1, P>(kt[d][kb], fv[kb], x, 0);
                 dS[d] = gather3(x);
             }
         }
-        const Buf db = make_buf(dvp + t0 * ldo, n_tok * ldo * E);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) buf_store<T>(db, ooff + (unsigned)(r * ldo) * E, from_f32<T>(gv[r]));
-        store_four<PW>(dR, reinterpret_cast<T*>(p.w_dr) + entry * PW * vals * kC + (int64_t)col * kC + tok, (int64_t)vals * kC);
-        if (L::NB == 1 && i + 1 < chunks) lds_barrier();
+        if (CT > 1) {
+            loads_end();
+            load_k(i + 1);
+        }
     }
     if (!p.dh0) return;
     const Buf sb = make_buf(p.dh0 + sbase, (int64_t)p.dk * p.dv * 4);
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < 2; ++d)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) buf_store<float>(sb, soff + (unsigned)((d * 16 + r) * p.dv) * 4u, dS[d][r]);
+        for (int r = 0; r < 4; ++r) buf_store<float>(sb, soff + (unsigned)((d * 4 + r) * p.dv) * 4u, dS[d][r]);
 }
 
 // Both walks in one launch: they need nothing of each other, and each alone often leaves units idle (2 x 4002 tokens,
@@ -406,7 +547,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_walks_kernel(c
     if (blockIdx.x < units)
         narrow_reverse<T, DK, P, VEC>(p, tiles, die_local(blockIdx.x, units));
     else
-        narrow_walk<T, DK, P, kStates, VEC>(p, tiles / NarrowShape<DK>::CT, die_local(blockIdx.x - units, units / NarrowShape<DK>::CT));
+        narrow_walk<T, DK, P, kStates, VEC>(p, tiles, die_local(blockIdx.x - units, units));
 }
 
 // ---------------------------------------------------------------- per chunk and head
@@ -809,14 +950,14 @@ template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParam
     hipError_t e = launch_prepare<T, DK, P>(p, s);
     if (e != hipSuccess) return e;
     constexpr int gb = GradLds<T, DK, PW>::bytes;
-    const unsigned tiles = (p.dv + 63) / 64 * (p.narrow ? 4 : 1), units = (unsigned)p.rows * p.H * tiles;
+    const unsigned tiles = (p.dv + 63) / 64 * (p.narrow ? 64 / NarrowShape<DK>::cols : 1), units = (unsigned)p.rows * p.H * tiles;
     auto walks = !p.narrow ? delta_walks_kernel<T, DK, P>
                  : p.vec_k ? delta_narrow_walks_kernel<T, DK, P, true>
                            : delta_narrow_walks_kernel<T, DK, P, false>;
-    constexpr int nb = NarrowLds<T, DK, P, P, 3 * P + 1>::bytes, ns = WalkNarrowLds<T, DK, P, 0>::bytes;
+    constexpr int nb = ReverseNarrowLds<T, DK, P>::bytes, ns = WalkNarrowLds<T, DK, P, 0>::bytes;
     const int wb = p.narrow ? (nb > ns ? nb : ns) : WalkLds<T, DK, P>::bytes;
     if ((e = allow_lds(walks, wb)) != hipSuccess) return e;
-    hipLaunchKernelGGL(walks, dim3(p.narrow ? units + units / NarrowShape<DK>::CT : 2 * units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), wb, s, p, tiles, units);
+    hipLaunchKernelGGL(walks, dim3(2 * units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), wb, s, p, tiles, units);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), cu = (unsigned)p.rows * chunks * p.H;
     auto grads = delta_grads_kernel<T, DK, PW>;

@@ -333,9 +333,9 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
                     for (int j = 0; j < 3; ++j) y[i][j] *= f;
                 }
                 load_q(c + 1);
-                load_a(c);
             }
             lds_barrier();
+            if constexpr (kOut) load_a(c);
             store_k(half_of(c + 1));
             lds_barrier();
             load_k(c + 2);
