@@ -300,7 +300,8 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
             }
         };
         auto load_a = [&](int c) {
-            const Buf ob = make_buf(p.w_ops + (entry + (int64_t)c * p.H) * Ops::bytes, Ops::bytes);
+            const bool in = c < chunks;
+            const Buf ob = make_buf(p.w_ops + (entry + (in ? (int64_t)c * p.H : 0)) * Ops::bytes, in ? Ops::bytes : 0);
 #pragma unroll
             for (int i = 0; i < CT; ++i)
 #pragma unroll
@@ -310,7 +311,10 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
         load_k(0);
         store_k(lds);
         load_k(1);
-        if constexpr (kOut) load_q(0);
+        if constexpr (kOut) {
+            load_q(0);
+            load_a(0);
+        }
         lds_barrier();
         for (int c = 0; c < chunks; ++c) {
             lds_barrier();
@@ -335,10 +339,9 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
                 load_q(c + 1);
             }
             lds_barrier();
-            if constexpr (kOut) load_a(c);
             store_k(half_of(c + 1));
-            lds_barrier();
             load_k(c + 2);
+            lds_barrier();
             if constexpr (kOut) {
                 const int64_t t0 = (int64_t)c * kC, n_tok = min((int64_t)kC, len - t0);
                 const Buf ob = make_buf(op + t0 * p.H * p.dv, n_tok * p.H * p.dv * E);
@@ -354,6 +357,7 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
 #pragma unroll
                     for (int r = 0; r < 4; ++r) buf_store<T>(ob, ooff + (unsigned)(r * p.H * p.dv) * E, from_f32<T>(o[r]));
                 }
+                load_a(c + 1);
             }
         }
         return;
@@ -396,17 +400,15 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
     };
     const int64_t entry0 = entry;
     Parts<T, P> ft[CT][2];  // T's rows of this wave's tokens
-    auto load_t = [&](int c) {
+    auto load_t = [&](int c, int kb) {
         const bool in = c < chunks;
         const Buf b = make_buf(p.w_ops + (entry0 + (in ? (int64_t)c * p.H : 0)) * Ops::bytes, in ? Ops::bytes : 0);
 #pragma unroll
         for (int i = 0; i < CT; ++i)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-                if (CT == 1 || kb == 0 || i == 1) ft[i][kb] = load_parts<P, P, T>(b, Ops::t, lower_frag(my.tile(i), kb), kb == 0 || my.two(i));
+            if (CT == 1 || kb == 0 || i == 1) ft[i][kb] = load_parts<P, P, T>(b, Ops::t, lower_frag(my.tile(i), kb), kb == 0 || my.two(i));
     };
     if (chunks > 0) {
-        load_t(0);
+        load_t(0, 0);
         fetch(0);
         lds_barrier();
         load_k(0);
@@ -431,6 +433,7 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
                 for (int t = 0; t < 4; ++t) x[t] = mma(fk[t].p[0], fs.p[q], x[t]);
 #pragma unroll
             for (int t = 0; t < 4; ++t) xp[((my.cw * 4 + t) * KW + my.kw) * 64] = x[t];
+            load_t(c, 1);
             if constexpr (W == kStates)
                 store_eight<PY>(fs, reinterpret_cast<T*>(p.w_s) + entry * PY * vals * DK + (int64_t)col * DK + key, (int64_t)vals * DK);
         }
@@ -495,7 +498,6 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
                 uf[(my.cw * 4 + t) * 64] = U[i];
         }
         const float ec = rows->eg[kC - 1];
-        load_t(c + 1);
         lds_barrier();
         // S = e^(G_C) S + (e^(G_C - G) K)^T U
         Parts<T, P> fu[2];
@@ -511,6 +513,11 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
                 x[0] = S[d] * ec;
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) mma_spread<1, P>(kt[d][kb], fu[kb], x, 0);
+                if (d == 0) {  // (spread over this beat: a wave stands still while a load finds no room)
+                    loads_end();
+                    load_t(c + 1, 0);
+                    loads_end();
+                }
                 S[d] = gather3(x);
             }
         }
