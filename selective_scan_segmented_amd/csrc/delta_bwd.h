@@ -947,7 +947,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_share_kernel(const DeltaP
 
 template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParams& p, hipStream_t s) {
     constexpr int PW = P < 2 ? P : 2;
-    hipError_t e = launch_prepare<T, DK, P>(p, s);
+    hipError_t e = launch_prepare<T, DK, P, P>(p, s);
     if (e != hipSuccess) return e;
     constexpr int gb = GradLds<T, DK, PW>::bytes;
     const unsigned tiles = (p.dv + 63) / 64 * (p.narrow ? 64 / NarrowShape<DK>::cols : 1), units = (unsigned)p.rows * p.H * tiles;

@@ -174,13 +174,10 @@ template <typename T, int DK> __device__ __forceinline__ f32x4 rows_product(cons
     return c;
 }
 
-// The twenty lower tiles of M and A, five to a wave: task w + 4 n, M's ten first.  M goes to LDS; A's stay in
-// registers (a[n - 2]; lane: row i = l % 16, columns 4 (l / 16) .. + 3) until M's place is free.
-template <typename T, int DK>
-__device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const ChunkRows* rows, float scale, float* mt, f32x4 (&a)[3]) {
+// The twenty lower tiles of K K^T (for M) and Q K^T (for A), five to a wave: task w + 4 n, M's ten first.
+template <typename T, int DK> __device__ __forceinline__ void chunk_products(const T* ks, const T* qs, f32x4 (&c)[5]) {
     using Sh = ChunkShape<T, DK>;
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
-    f32x4 c[5];
 #pragma unroll
     for (int n = 0; n < 5; ++n) c[n] = f32x4{0, 0, 0, 0};
     constexpr int step = sizeof(T) == 4 ? 32 : 64;  // keys whose fragments are loaded together
@@ -206,6 +203,12 @@ __device__ __forceinline__ void chunk_products(const T* ks, const T* qs, const C
 #pragma unroll
             for (int n = 0; n < 5; ++n) c[n] = mma(fa[n][i], fb[n][i], c[n]);
     }
+}
+
+// M and A from them and a head's gates.  M goes to LDS; A's tiles stay in registers (a[n - 2]; lane: row i = l % 16,
+// columns 4 (l / 16) .. + 3) until M's place is free.
+__device__ __forceinline__ void chunk_triangles(const f32x4 (&c)[5], const ChunkRows* rows, float scale, float* mt, f32x4 (&a)[3]) {
+    const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
     const bool mild = mild_decay(rows);
 #pragma unroll
     for (int n = 0; n < 5; ++n) {
@@ -318,17 +321,22 @@ template <typename F> __device__ __forceinline__ void each_t(const f32x4 (&t)[4]
         if (j <= (wave | 1)) f(t[j], wave, j);
 }
 
-// Gates, K and Q (in registers) to LDS, then M in LDS and, in registers, A's tiles and this wave's rows of T, all by
-// the whole workgroup.  `after` runs between M's making and its use (what needs K, Q or A only).
-template <typename T, int DK, typename After>
-__device__ __forceinline__ void make_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const ChunkGates& gates,
-                                           const DeltaParams& p, ChunkRows* rows, T* ks, T* qs, float* mt,
-                                           f32x4 (&a)[3], f32x4 (&t)[4], After after) {
+// Gates, K and Q (in registers) to LDS, and their products.
+template <typename T, int DK>
+__device__ __forceinline__ void start_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const ChunkGates& gates,
+                                            const DeltaParams& p, ChunkRows* rows, T* ks, T* qs, f32x4 (&c)[5]) {
     if (wave_id() == 3) gates.store(rows);  // (its loads are the oldest; this wave has least to do below)
     kr.store(ks, rows->rk, p.l2norm);
     qr.store(qs, rows->rq, p.l2norm);
     lds_barrier();
-    chunk_products<T, DK>(ks, qs, rows, p.scale, mt, a);
+    chunk_products<T, DK>(ks, qs, c);
+}
+// From them M in LDS and, in registers, A's tiles and this wave's rows of T, all by the whole workgroup.  `after` runs
+// between M's making and its use (what needs K, Q or A only).
+template <typename After>
+__device__ __forceinline__ void finish_chunk(const f32x4 (&c)[5], const DeltaParams& p, const ChunkRows* rows, float* mt,
+                                             f32x4 (&a)[3], f32x4 (&t)[4], After after) {
+    chunk_triangles(c, rows, p.scale, mt, a);
     lds_barrier();
     after();
     invert_diagonal(mt);
@@ -336,13 +344,14 @@ __device__ __forceinline__ void make_chunk(const RowShare<T, DK>& kr, const RowS
     inverse_rows(mt, t);
 }
 
-// The same with T (PT parts) at ts and A (PA parts) at as, where M lies before, visible to all at the end.
+// Both, with T (PT parts) at ts and A (PA parts) at as, where M lies before, visible to all at the end.
 template <typename T, int DK, int PT, int PA, typename Between>
 __device__ __forceinline__ void build_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const ChunkGates& gates,
                                             const DeltaParams& p, ChunkRows* rows, T* ks, T* qs, T* as, T* ts,
                                             Between between) {
-    f32x4 a[3], t[4];
-    make_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, reinterpret_cast<float*>(as), a, t, [] {});
+    f32x4 c[5], a[3], t[4];
+    start_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, c);
+    finish_chunk(c, p, rows, reinterpret_cast<float*>(as), a, t, [] {});
     each_t(t, [&](f32x4 x, int rt, int tj) { store_tile<PT>(x, ts, rt, tj); });
     between();     // what needs K and Q only
     lds_barrier();  // M is done with
@@ -357,9 +366,9 @@ __device__ __forceinline__ unsigned chunk_entry(const DeltaParams& p, int s, int
 }
 
 // What the preparing kernel leaves of a chunk and head: the row scalars, T and A (P parts each).
-template <typename T, int P> struct ChunkOperands {
+template <typename T, int P, int PA = P> struct ChunkOperands {
     static constexpr int frag_bytes = kLowerFrags * kFragSize * (int)sizeof(T);
-    static constexpr int t = (int)sizeof(ChunkRows), a = t + P * frag_bytes, bytes = a + P * frag_bytes;
+    static constexpr int t = (int)sizeof(ChunkRows), a = t + P * frag_bytes, bytes = a + PA * frag_bytes;
     static_assert(sizeof(ChunkRows) % 16 == 0 && frag_bytes % 16 == 0, "whole 16-byte units");
 };
 

@@ -32,8 +32,8 @@ template <typename T, int DK, int P, Walk W>
 __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsigned unit) {
     using Sh = ChunkShape<T, DK>;
     using L = WalkLds<T, DK, P>;
-    using Ops = ChunkOperands<T, P>;
     constexpr int PY = P < 2 ? P : 2;  // parts that only the outputs see: their type's rounding is far above the third
+    using Ops = ChunkOperands<T, P, W == kStates ? P : PY>;
     constexpr int E = (int)sizeof(T);
     constexpr bool kOnTheWay = W == kWhole || W == kSingle;
     extern __shared__ char lds[];
@@ -248,17 +248,18 @@ template <typename T, int DK> struct PrepareLds {
                          bytes = qs + ChunkShape<T, DK>::row_bytes;
     static constexpr int groups = 160 * 1024 / bytes < 3 ? 160 * 1024 / bytes : 3;
 };
-template <typename T, int DK, int P>
-__global__ __launch_bounds__(kDeltaThreads, (PrepareLds<T, DK>::groups)) void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) {
+// ALL: every head of a key head by one workgroup, K K^T and Q K^T made once.
+template <typename T, int DK, int P, int PA, bool ALL>
+__global__ __launch_bounds__(kDeltaThreads, (PrepareLds<T, DK>::groups))
+void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) {
     using L = PrepareLds<T, DK>;
-    using Ops = ChunkOperands<T, P>;
+    using Ops = ChunkOperands<T, P, PA>;
     constexpr int E = (int)sizeof(T);
     extern __shared__ char lds[];
     ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs);
-    const unsigned unit = die_local(blockIdx.x, units);
-    const int h = (int)(unit % (unsigned)p.H), hk = (int)((unsigned)h / (unsigned)p.share);
-    const unsigned sc = unit / (unsigned)p.H;
+    const unsigned heads = ALL ? p.share : 1, unit = die_local(blockIdx.x, units), groups = (unsigned)p.H / heads, sc = unit / groups;
+    const int h = (int)((unit - sc * groups) * heads), hk = (int)((unsigned)h / (unsigned)p.share);
     const int s = (int)(sc / chunks);
     int64_t first;
     int len;
@@ -267,25 +268,34 @@ __global__ __launch_bounds__(kDeltaThreads, (PrepareLds<T, DK>::groups)) void de
     if (t0 >= len) return;
     const int64_t n = min((int64_t)kC, len - t0);
     first += t0;
-    const int64_t at = first * p.H + h;
+    const T *gp = static_cast<const T*>(p.g) + first * p.H + h, *bp = static_cast<const T*>(p.beta) + first * p.H + h;
     ChunkGates gates;
-    gates.load(static_cast<const T*>(p.g) + at, static_cast<const T*>(p.beta) + at, p.H, (int)n);
+    gates.load(gp, bp, p.H, (int)n);
     RowShare<T, DK> kr, qr;
     kr.load(make_buf(static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
     qr.load(make_buf(static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
     char* o = p.w_ops + ((int64_t)(chunk_entry(p, s, first - t0) + (unsigned)(t0 / kC)) * p.H + h) * Ops::bytes;
-    const Buf ob = make_buf(o, Ops::bytes);
-    f32x4 a[3], t[4];
-    make_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, reinterpret_cast<float*>(lds + L::mt), a, t, [&] {
-        each_a(a, [&](f32x4 x, int rt, int tj) { store_tile<P, T>(x, ob, Ops::a, rt, tj); });
-        if (threadIdx.x < sizeof(ChunkRows) / 16)
-            reinterpret_cast<uint4*>(o)[threadIdx.x] = reinterpret_cast<const uint4*>(lds)[threadIdx.x];
-    });
-    each_t(t, [&](f32x4 x, int rt, int tj) { store_tile<P, T>(x, ob, Ops::t, rt, tj); });
+    float* mt = reinterpret_cast<float*>(lds + L::mt);
+    f32x4 c[5], a[3], t[4];
+    start_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, c);
+    for (unsigned j = 0;; o += Ops::bytes) {
+        const Buf ob = make_buf(o, Ops::bytes);
+        const bool more = ++j < heads;
+        if (more) gates.load(gp + j, bp + j, p.H, (int)n);
+        finish_chunk(c, p, rows, mt, a, t, [&] {
+            each_a(a, [&](f32x4 x, int rt, int tj) { store_tile<PA, T>(x, ob, Ops::a, rt, tj); });
+            if (threadIdx.x < sizeof(ChunkRows) / 16)
+                reinterpret_cast<uint4*>(o)[threadIdx.x] = reinterpret_cast<const uint4*>(lds)[threadIdx.x];
+        });
+        if (more && wave_id() == 0) gates.store(rows);  // (done with the head's; the first rows of T are the shortest)
+        each_t(t, [&](f32x4 x, int rt, int tj) { store_tile<P, T>(x, ob, Ops::t, rt, tj); });
+        if (!more) return;
+        lds_barrier();
+    }
 }
 
 static_assert(ChunkOperands<float, 1>::bytes == 8 * kC * 4 + 2 * 6 * 64 * 8 * 4 &&
-              ChunkOperands<__bf16, 3>::bytes == 8 * kC * 4 + 2 * 6 * 64 * 8 * 2 * 3, "delta_operand_bytes");
+              ChunkOperands<__bf16, 3, 2>::bytes == 8 * kC * 4 + 6 * 64 * 8 * 2 * 5, "delta_operand_bytes");
 
 // dynamic LDS above the default limit has to be asked for
 template <typename K> hipError_t allow_lds(K kern, int bytes) {
@@ -303,12 +313,14 @@ template <typename T, int DK, int P, Walk W> hipError_t launch_walk(const DeltaP
     return hipGetLastError();
 }
 
-template <typename T, int DK, int P> hipError_t launch_prepare(const DeltaParams& p, hipStream_t s) {
-    auto kern = delta_prepare_kernel<T, DK, P>;
+template <typename T, int DK, int P, int PA> hipError_t launch_prepare(const DeltaParams& p, hipStream_t s) {
+    const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), groups = (unsigned)p.rows * chunks * p.Hk;
+    const bool all = p.share > 1 && groups >= 256;  // (where that leaves every compute unit one)
+    auto kern = all ? delta_prepare_kernel<T, DK, P, PA, true> : delta_prepare_kernel<T, DK, P, PA, false>;
     constexpr int bytes = PrepareLds<T, DK>::bytes;
     const hipError_t e = allow_lds(kern, bytes);
     if (e != hipSuccess) return e;
-    const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), units = (unsigned)p.rows * chunks * p.H;
+    const unsigned units = all ? groups : groups * p.share;
     hipLaunchKernelGGL(kern, dim3(units), dim3(kDeltaThreads), bytes, s, p, chunks, units);
     return hipGetLastError();
 }

@@ -243,7 +243,7 @@ template <typename T, int DK, int P, Walk W, bool VEC>
 __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles, unsigned unit) {
     constexpr int PY = P < 2 ? P : 2, E = (int)sizeof(T), NS = DK / 32;
     using Sh = ChunkShape<T, DK>;
-    using Ops = ChunkOperands<T, P>;
+    using Ops = ChunkOperands<T, P, W == kStates ? P : PY>;
     using N = NarrowShape<DK>;
     using L = WalkNarrowLds<T, DK, P, (W == kStates ? 0 : PY)>;
     constexpr int CT = N::CT, KW = N::KW;
@@ -306,7 +306,7 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
             for (int i = 0; i < CT; ++i)
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
-                    if (CT == 1 || kb == 0 || i == 1) fa[i][kb] = load_parts<PY, P, T>(ob, Ops::a, lower_frag(my.tile(i), kb), kb == 0 || my.two(i));
+                    if (CT == 1 || kb == 0 || i == 1) fa[i][kb] = load_parts<PY, PY, T>(ob, Ops::a, lower_frag(my.tile(i), kb), kb == 0 || my.two(i));
         };
         load_k(0);
         store_k(lds);
@@ -555,7 +555,7 @@ template <typename T, int DK, int P> hipError_t launch_forward(const DeltaParams
     if (!p.w_ops && p.L <= kC && !p.h0 && !p.hT)
         if constexpr (P < 3) return launch_walk<T, DK, P, kSingle>(p, s);  // (three parts only with states)
     if (!p.w_ops) return launch_walk<T, DK, P, kWhole>(p, s);
-    const hipError_t e = launch_prepare<T, DK, P>(p, s);
+    const hipError_t e = launch_prepare<T, DK, P, (P < 2 ? P : 2)>(p, s);  // (A makes the output only)
     if (e != hipSuccess) return e;
     return p.narrow ? launch_narrow<T, DK, P>(p, s) : launch_walk<T, DK, P, kPrepared>(p, s);
 }

@@ -68,9 +68,9 @@ bool plan_delta_narrow(int64_t rows, int64_t H, int64_t dv);
 int64_t plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dv, bool want_state, int io_dtype);
 // entries of the arrays that hold something for every chunk (chunk_entry): enough for packed and for equal rows
 inline int64_t delta_chunk_entries(int64_t rows, int64_t tokens) { return tokens / kDeltaChunk + rows; }
-// bytes of a chunk and head's prepared operands (ChunkOperands), P parts to bfloat16 ones
-inline int64_t delta_operand_bytes(int io_dtype, int parts) {
-    return 8 * kDeltaChunk * 4 + 2 * 6 * 64 * 8 * (io_dtype == 0 ? 4 : 2 * (int64_t)parts);
+// bytes of a chunk and head's prepared operands (ChunkOperands), with the parts of bfloat16 ones
+inline int64_t delta_operand_bytes(int io_dtype, int parts_t, int parts_a) {
+    return 8 * kDeltaChunk * 4 + 6 * 64 * 8 * (io_dtype == 0 ? 8 : 2 * (int64_t)(parts_t + parts_a));
 }
 // chunked forward, one translation unit per io type
 hipError_t launch_delta_fwd_f32(const DeltaParams& p, hipStream_t s);

@@ -101,7 +101,7 @@ int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, 
     if (rows * H > INT32_MAX / chunks) return 0;
     bool prepared = chunks > 1 && rows * H * ((dv + 63) / 64) <= 1024;
     if (const char* e = std::getenv("SFM_DELTA_WALK")) prepared = e[0] == 'p' || (e[0] != 'w' && prepared);
-    return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2) : 0;
+    return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2, 2) : 0;
 }
 
 // Walks with sixteen columns to a workgroup instead of 64 while the latter would not fill the card.
@@ -217,7 +217,7 @@ static BwdRegions bwd_regions(int64_t rows, int64_t tokens, int64_t H, bool shar
         at += (n + 255) / 256 * 256;
         return here;
     };
-    r.ops = take(units * sfm::delta_operand_bytes(io_dtype, want_dh0 ? 3 : 2));
+    r.ops = take(units * sfm::delta_operand_bytes(io_dtype, want_dh0 ? 3 : 2, want_dh0 ? 3 : 2));
     r.s = take(units * planes * vals * keys * e);
     r.ds = take(units * planes * vals * keys * e);
     r.u = take(units * planes * vals * sfm::kDeltaChunk * e);

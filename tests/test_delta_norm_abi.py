@@ -96,7 +96,7 @@ def test_workspace_sizes(lib):
 def test_launch_plans(lib, monkeypatch):
     """Few long rows have their triangular inverses made beforehand (workspace); one chunk or many rows do not."""
     f = sfm.sfm_gated_delta_fwd_ws_size
-    unit = lambda parts: 8 * 64 * 4 + 2 * 6 * 64 * 8 * 2 * parts  # row scalars, two lower triangles of 6 fragments
+    unit = lambda parts: 8 * 64 * 4 + 6 * 64 * 8 * 2 * (parts + 2)  # row scalars, two lower triangles of 6 fragments
     assert f(2, 8192, 16384, 16, 128, 128, True) == (16384 // 64 + 2) * 16 * unit(3)
     assert f(2, 8192, 16384, 16, 128, 128, False) == (16384 // 64 + 2) * 16 * unit(2)
     assert f(256, 51, 256 * 51, 10, 64, 64) == 0
