@@ -254,3 +254,32 @@ def test_forward_by_every_plan(lens, Hk, H, dk, dv, walk, narrow, io, monkeypatc
         ref.close(o, wo, io, "o")
         if state:
             ref.close(hT, wT, "f32", "state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("narrow", ["0", "1"])
+def test_forward_many_chunks_of_shared_heads(io, narrow, monkeypatch):
+    """Rows times chunks past the card's compute units: one workgroup prepares all value heads of a key head."""
+    monkeypatch.setenv("SFM_DELTA_WALK", "prepared")
+    monkeypatch.setenv("SFM_DELTA_NARROW", narrow)
+    lens, Hk, H, dk, dv = [130] * 44, 2, 6, 24, 16
+    x = ref.delta_inputs(31, sum(lens), len(lens), Hk, H, dk, dv, True, io)
+    o, hT = call_fwd(x, lens, False, io, True, x[5])
+    wo, wT = ref.delta(*x[:6], np.cumsum(lens), dk ** -0.5, True)
+    ref.close(o, wo, io, "o")
+    ref.close(hT, wT, "f32", "state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("walk", ["whole", "prepared"])
+def test_forward_mild_and_steep_chunks(io, walk, monkeypatch):
+    """Chunks whose decays are products of two exponentials next to one whose are not, and one that grows."""
+    monkeypatch.setenv("SFM_DELTA_WALK", walk)
+    T, H, d = 256, 2, 64
+    x = ref.delta_inputs(13, T, 1, 1, H, d, d, True, io)
+    x[3][:] = np.repeat([-0.01, -3.0, -0.7, 0.0625], 64)[:, None]
+    x[3][:] = ref.cast(x[3], io)
+    o, hT = call_fwd(x, [T], False, io, True, x[5])
+    wo, wT = ref.delta(*x[:6], [T], d ** -0.5, True)
+    ref.close(o, wo, io, "o")
+    ref.close(hT, wT, "f32", "state")

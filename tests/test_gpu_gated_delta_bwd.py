@@ -161,3 +161,15 @@ def test_by_every_plan(lens, Hk, H, dk, dv, narrow, io, monkeypatch):
     x = ref.delta_inputs(sum(lens), sum(lens), len(lens), Hk, H, dk, dv, True, io)
     dhT = np.random.default_rng(1).standard_normal(x[5].shape).astype(np.float32).astype(np.float64)
     check(call_bwd(x, lens, True, io, True, x[5], dhT), ref.delta_bwd(*x[:6], np.cumsum(lens), dk ** -0.5, True, x[6], dhT), io, x[5])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("narrow", ["0", "1"])
+def test_many_chunks_of_shared_heads(io, narrow, monkeypatch):
+    """Rows times chunks past the card's compute units: one workgroup prepares all value heads of a key head."""
+    monkeypatch.setenv("SFM_DELTA_NARROW", narrow)
+    lens, Hk, H, dk, dv = [130] * 44, 2, 6, 24, 16
+    x = ref.delta_inputs(31, sum(lens), len(lens), Hk, H, dk, dv, True, io)
+    got = call_bwd(x, lens, False, io, True, x[5], None)
+    want = ref.delta_bwd(*x[:6], np.cumsum(lens), dk ** -0.5, True, x[6], np.zeros(x[5].shape))
+    check(got, want, io, x[5])
