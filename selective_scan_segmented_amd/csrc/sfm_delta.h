@@ -64,8 +64,8 @@ constexpr float kDeltaNormEps = 1e-6f;
 constexpr float kDeltaMinGate = -110.0f;
 
 // Workspace of the chunked forward in bytes: 0 where a chunk's T and A are made on the way (delta_fwd.h).
-bool plan_delta_narrow(int64_t rows, int64_t H, int64_t dv);
-int64_t plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dv, bool want_state, int io_dtype);
+bool plan_delta_narrow(int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back);
+int64_t plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype);
 // entries of the arrays that hold something for every chunk (chunk_entry): enough for packed and for equal rows
 inline int64_t delta_chunk_entries(int64_t rows, int64_t tokens) { return tokens / kDeltaChunk + rows; }
 // bytes of a chunk and head's prepared operands (ChunkOperands), with the parts of bfloat16 ones

@@ -50,8 +50,10 @@ sfm_status check_inputs(const char* fn, const void* q, const void* k, const void
     return SFM_OK;
 }
 
-// Rows up to this long go token by token.
-constexpr int64_t kRecurrentMax = 4;
+// Rows up to this long go token by token: a chunk costs its 64 tokens whatever is in it, a token its own reads of the
+// values and, the first, the state's.  At 256 rows x 16 heads of 64 x 64: 10 us a token against 49 us a chunk in
+// bfloat16 (87 us with states, 48 us for four tokens), against 89 us in float32 (39 us for four).
+int64_t recurrent_most(int io_dtype, bool state) { return io_dtype == SFM_F32 ? 10 : state ? 7 : 4; }
 
 struct Ranges {
     Range ins[10];
@@ -93,22 +95,37 @@ sfm::DeltaParams params(const void* q, const void* k, const void* v, const void*
 
 }  // namespace
 
-// Few (row, head, column tile) workgroups walk long rows: the chunks' triangular inverses, which need no state, are
-// then made beforehand by the whole card (two launches) instead of inside the walk.
+// Workgroups of 64 value columns that rows of the longest one's length would make of all the tokens: what a launch
+// has to fill the card with, and keeps filling it with, also where packed rows differ.
+static int64_t delta_units(int64_t L, int64_t tokens, int64_t H, int64_t dv) { return tokens * H * ((dv + 63) / 64) / L; }
+
+// Few such workgroups walk long rows: the chunks' triangular inverses, which need no state, are then made beforehand
+// by the whole card (two launches) instead of inside the walk.  Past 256 the other workgroups of a unit hide their
+// making and the operands' way through memory costs more than it saves, unless several column tiles share them
+// (values wider than keys).  bfloat16, inside / beforehand:
+//     1024 tokens, 64 x 64: 114 / 57 us for 128 workgroups, 114 / 89 us for 256, 146 / 169 us for 384;
+//     1024 tokens, 128 x 128: 140 / 66 us for 128, 143 / 109 us for 256, 186 / 217 us for 512;
+//     packed rows to 2048, 64 x 128: 264 / 237 us for 321, 432 / 378 us for 620;
+//     two chunks, 64 x 64: 18 / 19 us for 128, 17 / 21 us for 256 (float32: 23 / 22 us, 24 / 28 us).
 // SFM_DELTA_WALK=whole|prepared overrides (tuning and tests).
-int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dv, bool want_state, int io_dtype) {
+int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype) {
     const int64_t chunks = (L + kDeltaChunk - 1) / kDeltaChunk;
     if (rows * H > INT32_MAX / chunks) return 0;
-    bool prepared = chunks > 1 && rows * H * ((dv + 63) / 64) <= 1024;
+    const int64_t most = chunks < 3 ? 128 : ((dv + 63) / 64 > (dk + 63) / 64 ? 1024 : 256);
+    bool prepared = chunks > 1 && delta_units(L, tokens, H, dv) <= most;
     if (const char* e = std::getenv("SFM_DELTA_WALK")) prepared = e[0] == 'p' || (e[0] != 'w' && prepared);
     return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2, 2) : 0;
 }
 
-// Walks with sixteen columns to a workgroup instead of 64 while the latter would not fill the card.
+// Walks with few columns to a workgroup (delta_narrow.h) while those of 64 leave units idle.  A unit holds one of them,
+// two of bfloat16 with 64 keys; the backward has two walks at once.  64 columns / few, 2048 tokens, bfloat16:
+//     64 x 64: 142 / 97 us for 128 workgroups of 64 columns, 215 / 210 us for 256, 338 / 337 us for 384;
+//     128 x 128: 172 / 114 us for 128, 194 / 178 us for 192, 214 / 241 us for 256;
+//     backward, 64 x 64: 211 / 180 us for 64, 281 / 285 us for 96; 128 x 128: 274 / 216 us for 64, 414 / 472 us for 128.
 // SFM_DELTA_NARROW=0|1 overrides (tuning and tests).
-bool sfm::plan_delta_narrow(int64_t rows, int64_t H, int64_t dv) {
+bool sfm::plan_delta_narrow(int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back) {
     if (const char* e = std::getenv("SFM_DELTA_NARROW")) return e[0] == '1';
-    return rows * H * ((dv + 63) / 64) <= 128;
+    return delta_units(L, tokens, H, dv) <= (back ? 64 : (dk <= 64 && io_dtype != 0 ? 256 : 128));
 }
 
 extern "C" {
@@ -149,7 +166,7 @@ sfm_status sfm_gated_delta_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, 
     if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
     const sfm_status st = check_sizes(fn, rows, L, tokens, true, 1, H, dk, dv, io_dtype, 0);
     if (st != SFM_OK) return st;
-    *bytes = L <= kRecurrentMax ? 0 : sfm::plan_delta_fwd(rows, L, tokens, H, dv, want_state != 0, io_dtype);
+    *bytes = sfm::plan_delta_fwd(rows, L, tokens, H, dk, dv, want_state != 0, io_dtype);
     return ok();
 }
 
@@ -194,10 +211,10 @@ sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
     sfm::DeltaParams p = params(q, k, v, g, beta, rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
     p.h0 = h0, p.hT = hT, p.offsets = offsets, p.o = o;
     p.w_ops = need > 0 ? static_cast<char*>(workspace) : nullptr;
-    p.narrow = sfm::plan_delta_narrow(rows, H, dv);
+    p.narrow = sfm::plan_delta_narrow(L, tokens, H, dk, dv, io_dtype, false);
     p.vec_s = dv % 4 == 0 && aligned16(h0) && aligned16(hT);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (L <= kRecurrentMax) return hip_status(sfm::launch_delta_recurrent(p, io_dtype, hs), fn);
+    if (L <= recurrent_most(io_dtype, h0 || hT)) return hip_status(sfm::launch_delta_recurrent(p, io_dtype, hs), fn);
     return hip_status(io_dtype == SFM_F32 ? sfm::launch_delta_fwd_f32(p, hs) : sfm::launch_delta_fwd_bf16(p, hs), fn);
 }
 
@@ -291,7 +308,7 @@ sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
     p.w_ops = ws + w.ops, p.w_s = ws + w.s, p.w_ds = ws + w.ds, p.w_u = ws + w.u, p.w_dr = ws + w.dr;
     p.w_dq = reinterpret_cast<float*>(ws + w.dq), p.w_dk = reinterpret_cast<float*>(ws + w.dk);
     p.vec_o = aligned16(dout) && dv * e % 16 == 0;
-    p.narrow = sfm::plan_delta_narrow(rows, H, dv);
+    p.narrow = sfm::plan_delta_narrow(L, tokens, H, dk, dv, io_dtype, true);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     return hip_status(io_dtype == SFM_F32 ? sfm::launch_delta_bwd_f32(p, hs) : sfm::launch_delta_bwd_bf16(p, hs), fn);
 }
