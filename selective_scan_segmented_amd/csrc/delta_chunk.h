@@ -5,7 +5,8 @@
 //     M = strictly lower part of beta_i D_ij k_i.k_j,     T = (I + M)^-1,
 //     R = beta (V - e^G K S0),   U = T R,   A = scale x lower part of D_ij q_i.k_j,
 // the recurrence gives    O = scale e^G Q S0 + A U,     S' = e^(G_C) S0 + (e^(G_C - G) K)^T U.
-// Every exponent is at most zero (g <= 0), so nothing overflows.  Query and key lengths (l2norm), decays and gates
+// Every D_ij is at most one (g <= 0): it is e^(G_i) e^(-G_j) where a chunk's factors are within 2^-64 .. 2^64, and
+// otherwise an exponential of its own, so nothing overflows.  Query and key lengths (l2norm), decays and gates
 // are factors of whole rows or columns: they are applied to float32 accumulators, and the input operands of the
 // matrix instructions stay the tensors' own values.
 //

@@ -4,6 +4,11 @@
 // A workgroup takes one (row, head) and 64 columns of its values, 16 to a wave, and walks the row's chunks; the
 // state's columns stay in the wave's accumulators (float32) all the way.  S0, R and U pass from product to product
 // inside a lane (delta_mma.h), so waves meet only over K, Q, T and A in LDS.
+//
+// What bounds it: one chunk takes a workgroup some 7 us with its triangles made on the way (18000 cycles, half of them
+// waiting: float32 substitutions, LDS, barriers) and 3.8 us without; the matrix unit is busy 1900 cycles of them with 64
+// keys.  Other workgroups of the unit fill the gaps, three of them for rows of one chunk: 256 x 51 tokens x 10 heads
+// of 64 x 64 in 36 us (64 MB, 1.8 TB/s; 148 us before loads were bounded, and operands kept in fragment order).
 #pragma once
 
 #include "delta_chunk.h"
@@ -248,7 +253,9 @@ template <typename T, int DK> struct PrepareLds {
                          bytes = qs + ChunkShape<T, DK>::row_bytes;
     static constexpr int groups = 160 * 1024 / bytes < 3 ? 160 * 1024 / bytes : 3;
 };
-// ALL: every head of a key head by one workgroup, K K^T and Q K^T made once.
+// Bound by that latency too (the chunk's 18000 cycles, three to a unit), and by the write: 26 to 32 KB to a chunk and
+// head.  ALL: every value head of a key head by one workgroup, K K^T and Q K^T made once (2 x 8192 tokens, 16 heads of
+// 128 over 8: 53 us, 60 with a workgroup to each).
 template <typename T, int DK, int P, int PA, bool ALL>
 __global__ __launch_bounds__(kDeltaThreads, (PrepareLds<T, DK>::groups))
 void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) {

@@ -1,11 +1,18 @@
-// delta_narrow.h -- the walks of delta_fwd.h and delta_bwd.h for few long rows: sixteen columns to a workgroup.
+// delta_narrow.h -- the walks of delta_fwd.h and delta_bwd.h for few long rows: 16 columns to a workgroup (128 keys)
+// or 32 (64 keys).
 //
 // A row's chunks follow one another, so where there are few (row, head, 64 column) workgroups the time is that of
-// one chunk in one of them.  Here the four waves share sixteen columns instead of having sixteen each: wave w holds
-// a quarter of the state's keys and computes the tokens 16 w .. + 15 of every product, and what the others need of it
-// (the state's parts, R, U) goes through LDS in operand order.  Three barriers a chunk.  Four more waves do nothing
-// but bring the next chunk's operands into the other half of LDS (where two halves fit): a compute unit moves 64
-// bytes a cycle, 1000 cycles for a chunk of 66 KB, and a wave that issues such loads stands still meanwhile.
+// one chunk in one of them, and that is a chain: the state's parts, K S, R, U, the state.  Here four waves share the
+// columns, each with 32 keys x 16 columns of the state: K S is then summed over keys through LDS (32 KB a chunk,
+// against 60 KB were every wave to read the state's parts for tokens of its own), and the state's parts need not pass
+// through LDS before it.  Three barriers a chunk.  Four more waves bring K and Q a chunk ahead, and make the output a
+// beat behind; their waits are not the chain's.  Issuing a load stops a wave while the unit takes 64 bytes a cycle,
+// so the chain's own loads (T's fragments, straight to registers) are spread over the beat with most else to do.
+//
+// 2 rows x 8192 tokens x 16 heads of 128 x 128: 205 us for 128 chunks, 3500 cycles each, of which the vector units
+// are busy 1300 and LDS 1530; 64 columns to a workgroup: 690 us.  What is left is the chain's own latency (2900
+// cycles a chunk where 64 workgroups run) and, with all units busy, 76 KB a chunk and unit from the L2 caches: 11.8
+// TB/s over the card.
 #pragma once
 
 #include "delta_fwd.h"
@@ -22,22 +29,6 @@ template <int P, int NF, typename T> __device__ __forceinline__ void store_half(
         for (int q = 0; q < P; ++q) {
             const bf16x4 v = take_part(x);
             *reinterpret_cast<bf16x4*>(p + q * NF * kFragSize) = v;
-        }
-    }
-}
-// likewise to memory: PW planes `plane` apart, and LDS, from one splitting
-template <int PW, int P, int NF, typename T>
-__device__ __forceinline__ void store_half_both(f32x4 x, T* base, int frag, int half, T* mem, int64_t plane) {
-    T* p = base + frag * kFragSize + (threadIdx.x & 63) * 8 + half * 4;
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<f32x4*>(p) = x;
-        *reinterpret_cast<f32x4*>(mem) = x;
-    } else {
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-            const bf16x4 v = take_part(x);
-            *reinterpret_cast<bf16x4*>(p + q * NF * kFragSize) = v;
-            if (q < PW) *reinterpret_cast<bf16x4*>(mem + q * plane) = v;
         }
     }
 }
@@ -76,52 +67,7 @@ __device__ __forceinline__ void mma_spread(const Parts<T, PA>& a, const Parts<T,
 __device__ __forceinline__ f32x4 gather3(const f32x4 (&c)[3]) { return (c[0] + c[1]) + c[2]; }
 __device__ __forceinline__ void zero3(f32x4 (&c)[3]) { c[0] = c[1] = c[2] = f32x4{0, 0, 0, 0}; }
 
-// LDS: NB halves of a chunk's operands, then the exchange.  PA: parts of A kept; PX: planes of the exchange's arrays
-// over tokens, all together.
-template <typename T, int DK, int P, int PA, int PX> struct NarrowLds {
-    using Sh = ChunkShape<T, DK>;
-    static constexpr int E = (int)sizeof(T);
-    static constexpr int frag_bytes = kLowerFrags * kFragSize * E;
-    static constexpr int ts = (int)sizeof(ChunkRows), as = ts + P * frag_bytes, ks = as + PA * frag_bytes,
-                         qs = ks + Sh::row_bytes, half = qs + Sh::row_bytes;
-    static constexpr int state = P * (DK / 32) * kFragSize * E, tokens = PX * 2 * kFragSize * E;
-    static constexpr int NB = 2 * half + state + tokens <= 160 * 1024 ? 2 : 1;
-    static constexpr int sp = NB * half, xp = sp + state, bytes = xp + tokens;
-    static constexpr int plane = 2 * kFragSize;  // elements of one plane over tokens
-};
-
 constexpr int kNarrowThreads = 2 * kDeltaThreads;
-
-// What a loading wave does for a row's chunks: chunk number i from memory to registers (load, in two pieces) and on to
-// LDS (store).  The compute waves' barriers: the first of chunk c after which the other half is free and before which
-// chunk c's operands are written, and two more; with one half, a fourth at the chunk's end.  Everyone waits for the
-// last at a barrier, so the loads are spread over the time between them: little after the second, where the compute
-// waves have the least to do.
-template <int NB, int HALF, typename Load, typename Store>
-__device__ __forceinline__ void narrow_loader(char* lds, int chunks, Load load, Store store) {
-    if (chunks <= 0) return;
-    load(0, 0);
-    load(0, 1);
-    store(lds);
-    load(1, 0);
-    load(1, 1);
-    for (int c = 0; c < chunks; ++c) {
-        lds_barrier();
-        if (NB == 2) {
-            store(lds + (c & 1 ? 0 : HALF));
-            load(c + 2, 0);
-        }
-        lds_barrier();
-        lds_barrier();
-        if (NB == 2) load(c + 2, 1);
-        if (NB == 1 && c + 1 < chunks) {
-            lds_barrier();
-            store(lds);
-            load(c + 2, 0);
-            load(c + 2, 1);
-        }
-    }
-}
 
 // ---------------------------------------------------------------- the walk
 // Wave w of the four that carry the state has keys 32 kw .. + 31 and columns 16 cw .. + 15 of it.
@@ -135,8 +81,8 @@ template <int DK> struct NarrowShape {
     __device__ __forceinline__ bool two(int i) const { return CT == 2 ? i == 1 : kw >= 2; }
 };
 
-// LDS of the walk: two halves for a chunk's row scalars, T and K, then what the waves hand one another: the state's
-// first PS parts, K S's four tiles in KW sums each, R and U (PX parts), and U for the output.
+// LDS of the walk: two halves for a chunk's row scalars and K, then what the waves hand one another: the state's first
+// PS parts, K S's four tiles in KW sums each, R and U, and U for the output.
 template <typename T, int DK, int P, int PS> struct WalkNarrowLds {
     using Sh = ChunkShape<T, DK>;
     using N = NarrowShape<DK>;
