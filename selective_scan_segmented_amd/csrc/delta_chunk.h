@@ -346,13 +346,13 @@ __device__ __forceinline__ void finish_chunk(const f32x4 (&c)[5], const DeltaPar
 }
 
 // Both, with T (PT parts) at ts and A (PA parts) at as, where M lies before, visible to all at the end.
-template <typename T, int DK, int PT, int PA, typename Between>
+template <typename T, int DK, int PT, int PA, typename After, typename Between>
 __device__ __forceinline__ void build_chunk(const RowShare<T, DK>& kr, const RowShare<T, DK>& qr, const ChunkGates& gates,
                                             const DeltaParams& p, ChunkRows* rows, T* ks, T* qs, T* as, T* ts,
-                                            Between between) {
+                                            After after, Between between) {
     f32x4 c[5], a[3], t[4];
     start_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, c);
-    finish_chunk(c, p, rows, reinterpret_cast<float*>(as), a, t, [] {});
+    finish_chunk(c, p, rows, reinterpret_cast<float*>(as), a, t, after);
     each_t(t, [&](f32x4 x, int rt, int tj) { store_tile<PT>(x, ts, rt, tj); });
     between();     // what needs K and Q only
     lds_barrier();  // M is done with

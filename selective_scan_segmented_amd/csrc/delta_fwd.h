@@ -21,22 +21,25 @@ namespace sfm {
 // begin and end without a state, which leaves R = beta V, U = T R, O = A U.
 enum Walk { kWhole, kPrepared, kStates, kSingle };
 
-template <typename T, int DK, int P> struct WalkLds {  // P: parts of T and A
+// P: parts of T and A.  SINGLE: T takes the place of K and Q, which a chunk without states needs no more by then.
+template <typename T, int DK, int P, bool SINGLE = false> struct WalkLds {
     using Sh = ChunkShape<T, DK>;
     static constexpr int frag_bytes = kLowerFrags * kFragSize * (int)sizeof(T);
     static constexpr int rows = 0;
-    static constexpr int ts = (int)sizeof(ChunkRows);              // T, A: as ChunkOperands has them
-    static constexpr int as = ts + P * frag_bytes;                 // (M before A)
+    static constexpr int as = (int)sizeof(ChunkRows) + (SINGLE ? 0 : P * frag_bytes);  // (M before A)
     static constexpr int ks = as + (P * frag_bytes > kBytesM ? P * frag_bytes : kBytesM);
     static constexpr int qs = ks + Sh::row_bytes;
     static constexpr int bytes = qs + Sh::row_bytes;
-    static constexpr int groups = 160 * 1024 / bytes < 2 ? 1 : 2;  // workgroups to a compute unit
+    static constexpr int ts = SINGLE ? ks : (int)sizeof(ChunkRows);  // (T, A: as ChunkOperands has them)
+    static_assert(!SINGLE || P * frag_bytes <= 2 * Sh::row_bytes, "T's place");
+    static constexpr int fit = 160 * 1024 / bytes, most = SINGLE && sizeof(T) == 2 ? 4 : SINGLE ? 3 : 2;
+    static constexpr int groups = fit < 1 ? 1 : fit < most ? fit : most;  // workgroups to a compute unit
 };
 
 template <typename T, int DK, int P, Walk W>
 __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsigned unit) {
     using Sh = ChunkShape<T, DK>;
-    using L = WalkLds<T, DK, P>;
+    using L = WalkLds<T, DK, P, W == kSingle>;
     constexpr int PY = P < 2 ? P : 2;  // parts that only the outputs see: their type's rounding is far above the third
     using Ops = ChunkOperands<T, P, W == kStates ? P : PY>;
     constexpr int E = (int)sizeof(T);
@@ -84,6 +87,14 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     Linear<Ops::a> ops;                // row scalars and T
     Linear<PY * L::frag_bytes> opa;    // A
     unsigned v[4][4];                  // values' bits
+    auto fetch_v = [&](int64_t t0) {
+        const int64_t n = min((int64_t)kC, len - t0);
+        const Buf vb = make_buf(vp + t0 * p.ldv, n * p.ldv * E);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(vb, fresh(voff) + (unsigned)((rt * 16 + r) * p.ldv) * E);
+    };
     auto fetch = [&](int64_t t0) {
         const int64_t n = min((int64_t)kC, len - t0);
         if (kOnTheWay) gates.load(gp + t0 * p.H, bp + t0 * p.H, p.H, (int)n);
@@ -94,11 +105,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
             ops.load(o);
             if (W == kPrepared) opa.load(o + Ops::a);
         }
-        const Buf vb = make_buf(vp + t0 * p.ldv, n * p.ldv * E);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(vb, fresh(voff) + (unsigned)((rt * 16 + r) * p.ldv) * E);
+        if (!kOnTheWay) fetch_v(t0);
     };
     if (!kOnTheWay && len > 0) fetch(0);  // ahead of its use by a chunk
 
@@ -153,7 +160,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
         if (kOnTheWay) fetch(t0);  // (registers that other workgroups on the unit can use better)
         lds_barrier();  // the chunk before is done with LDS
         if constexpr (kOnTheWay) {
-            build_chunk<T, DK, P, PY>(kr, qr, gates, p, rows, ks, qs, as, ts, state_products);
+            build_chunk<T, DK, P, PY>(kr, qr, gates, p, rows, ks, qs, as, ts, [&] { fetch_v(t0); }, state_products);
         } else {
             kr.store(ks, nullptr, 0);
             ops.store(lds);
@@ -243,7 +250,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
 }
 
 template <typename T, int DK, int P, Walk W>
-__global__ __launch_bounds__(kDeltaThreads, (W == kSingle && sizeof(T) == 2 ? 3 : W != kPrepared || DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+__global__ __launch_bounds__(kDeltaThreads, (W != kPrepared || DK == 64 ? WalkLds<T, DK, P, W == kSingle>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
     walk<T, DK, P, W>(p, tiles, die_local(blockIdx.x, units));
 }
 
@@ -312,7 +319,7 @@ template <typename K> hipError_t allow_lds(K kern, int bytes) {
 
 template <typename T, int DK, int P, Walk W> hipError_t launch_walk(const DeltaParams& p, hipStream_t s) {
     auto kern = delta_walk_kernel<T, DK, P, W>;
-    constexpr int bytes = WalkLds<T, DK, P>::bytes;
+    constexpr int bytes = WalkLds<T, DK, P, W == kSingle>::bytes;
     const hipError_t e = allow_lds(kern, bytes);
     if (e != hipSuccess) return e;
     const unsigned tiles = (p.dv + 63) / 64, units = (unsigned)p.rows * p.H * tiles;
