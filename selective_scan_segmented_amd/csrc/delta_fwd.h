@@ -7,8 +7,9 @@
 //
 // What bounds it: one chunk takes a workgroup some 7 us with its triangles made on the way (18000 cycles, half of them
 // waiting: float32 substitutions, LDS, barriers) and 3.8 us without; the matrix unit is busy 1900 cycles of them with 64
-// keys.  Other workgroups of the unit fill the gaps, three of them for rows of one chunk: 256 x 51 tokens x 10 heads
-// of 64 x 64 in 36 us (64 MB, 1.8 TB/s; 148 us before loads were bounded, and operands kept in fragment order).
+// keys.  Other workgroups of the unit fill the gaps, three of them (four for rows of one chunk, where T
+// takes the place of K and Q): 256 x 51 tokens x 10 heads of 64 x 64 in 33 us (67 MB, 2.0 TB/s), 1024 workgroups of 1024
+// tokens in 273 us (294 with two).
 #pragma once
 
 #include "delta_chunk.h"
@@ -52,7 +53,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     const unsigned rh = unit / tiles;
     const int s = (int)(rh / (unsigned)p.H), h = (int)(rh - (unsigned)s * p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
-    const int col = (int)(unit - rh * tiles) * 64 + wave * 16 + l16;
+    const int col0 = (int)(unit - rh * tiles) * 64 + wave * 16, col = col0 + l16;
     int64_t first;
     int len;
     delta_row(p, s, first, len);
@@ -64,9 +65,12 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     T* op = static_cast<T*>(p.o) + (first * p.H + h) * p.dv;
     const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
     // this lane's column in a state, in the values and in the output
-    const unsigned soff = col < p.dv ? (unsigned)(g4 * p.dv + col) * 4u : kNowhere;
-    const unsigned voff = col < p.dv ? (unsigned)(g4 * p.ldv + col) * E : kNowhere;
-    const unsigned ooff = col < p.dv ? (unsigned)(g4 * p.H * p.dv + col) * E : kNowhere;
+    // this lane's place in rows of `ld` elements: its column, rows 4 (l / 16) on (taken afresh: see fresh)
+    auto place = [&](int64_t ld, unsigned size) {
+        const unsigned l = fresh(threadIdx.x);
+        const int c = col0 + (int)(l & 15);
+        return c < p.dv ? (unsigned)((int)(l >> 4 & 3) * 4 * (int)ld + c) * size : kNowhere;
+    };
     int64_t entry = (int64_t)chunk_entry(p, s, first) * p.H + h;
     const int vals = (int)tiles * 64;  // values in the workspace: whole tiles
 
@@ -75,10 +79,11 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     for (int d = 0; d < DK / 16; ++d) S[d] = f32x4{0, 0, 0, 0};
     if (W != kSingle && p.h0) {
         const Buf b = make_buf(p.h0 + sbase, (int64_t)p.dk * p.dv * 4);
+        const unsigned at = place(p.dv, 4);
 #pragma unroll
         for (int d = 0; d < DK / 16; ++d)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[d][r] = buf_load<float>(b, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u);
+            for (int r = 0; r < 4; ++r) S[d][r] = buf_load<float>(b, at + (unsigned)((d * 16 + r) * p.dv) * 4u);
     }
     bool zero = W == kSingle || !p.h0;  // the state is zero: its products are left out
 
@@ -90,10 +95,11 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     auto fetch_v = [&](int64_t t0) {
         const int64_t n = min((int64_t)kC, len - t0);
         const Buf vb = make_buf(vp + t0 * p.ldv, n * p.ldv * E);
+        const unsigned at = place(p.ldv, E);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(vb, fresh(voff) + (unsigned)((rt * 16 + r) * p.ldv) * E);
+            for (int r = 0; r < 4; ++r) v[rt][r] = buf_load_bits<T>(vb, at + (unsigned)((rt * 16 + r) * p.ldv) * E);
     };
     auto fetch = [&](int64_t t0) {
         const int64_t n = min((int64_t)kC, len - t0);
@@ -121,14 +127,15 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
             if (W == kStates || (W != kSingle && !zero)) {
                 Frag<T> fk[2][4], fq[2][4];
                 auto load = [&](int kb) {
+                    const int base = (int)fresh((unsigned)(l16 * Sh::KS + g4));
 #pragma unroll
                     for (int rt = 0; rt < 4; ++rt) {
-                        const int at = (rt * 16 + l16) * Sh::KS + kb * 32 + g4;
+                        const int at = base + rt * 16 * Sh::KS + kb * 32;
                         fk[kb & 1][rt] = load_runs<T>(ks + at);
                         if constexpr (W != kStates) fq[kb & 1][rt] = load_runs<T>(qs + at);
                     }
                 };
-                constexpr int ahead = kOnTheWay && DK == 128 ? 0 : 1;  // (registers for two workgroups to a unit)
+                constexpr int ahead = kOnTheWay && (DK == 128 || (P == 2 && sizeof(T) == 2)) ? 0 : 1;  // (registers for two workgroups to a unit)
                 if (ahead) load(0);
 #pragma unroll
                 for (int kb = 0; kb < DK / 32; ++kb) {
@@ -196,6 +203,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
             }
         } else {
             Parts<T, PY> ap[kLowerFrags], up[2];
+            if (W == kWhole) loads_end();  // (T's registers first)
 #pragma unroll
             for (int f = 0; f < kLowerFrags; ++f) ap[f] = load_parts<PY>(as, f);
             loads_end();
@@ -206,11 +214,12 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) mma_lower<PY, PY>(ap, up[kb], kb, Y);
             const Buf ob = make_buf(op + t0 * p.H * p.dv, n_tok * p.H * p.dv * E);
+            const unsigned at = place((int64_t)p.H * p.dv, E);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    buf_store<T>(ob, fresh(ooff) + (unsigned)((rt * 16 + r) * p.H * p.dv) * E, from_f32<T>(Y[rt][r]));
+                    buf_store<T>(ob, at + (unsigned)((rt * 16 + r) * p.H * p.dv) * E, from_f32<T>(Y[rt][r]));
         }
         zero = false;
         if (W == kSingle || (t0 + kC >= len && (W == kStates || !p.hT))) break;  // nobody asks for the state after the last chunk
@@ -243,14 +252,15 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
     }
     if (W == kStates || W == kSingle || !p.hT) return;
     const Buf sb = make_buf(p.hT + sbase, (int64_t)p.dk * p.dv * 4);
+    const unsigned at = place(p.dv, 4);
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) buf_store<float>(sb, fresh(soff) + (unsigned)((d * 16 + r) * p.dv) * 4u, S[d][r]);
+        for (int r = 0; r < 4; ++r) buf_store<float>(sb, at + (unsigned)((d * 16 + r) * p.dv) * 4u, S[d][r]);
 }
 
 template <typename T, int DK, int P, Walk W>
-__global__ __launch_bounds__(kDeltaThreads, (W != kPrepared || DK == 64 ? WalkLds<T, DK, P, W == kSingle>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
+__global__ __launch_bounds__(kDeltaThreads, (W == kWhole && DK == 64 && P == 2 && sizeof(T) == 2 ? 3 : W != kPrepared || DK == 64 ? WalkLds<T, DK, P, W == kSingle>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
     walk<T, DK, P, W>(p, tiles, die_local(blockIdx.x, units));
 }
 

@@ -103,15 +103,15 @@ static int64_t delta_units(int64_t L, int64_t tokens, int64_t H, int64_t dv) { r
 // by the whole card (two launches) instead of inside the walk.  Past 256 the other workgroups of a unit hide their
 // making and the operands' way through memory costs more than it saves, unless several column tiles share them
 // (values wider than keys).  bfloat16, inside / beforehand:
-//     1024 tokens, 64 x 64: 114 / 57 us for 128 workgroups, 114 / 89 us for 256, 146 / 169 us for 384;
+//     1024 tokens, 64 x 64: 114 / 57 us for 128 workgroups, 115 / 90 us for 256, 143 / 167 us for 384;
 //     1024 tokens, 128 x 128: 140 / 66 us for 128, 143 / 109 us for 256, 186 / 217 us for 512;
-//     packed rows to 2048, 64 x 128: 264 / 237 us for 321, 432 / 378 us for 620;
+//     1024 tokens, 64 x 128: 142 / 133 us for 512, 182 / 202 us for 768;
 //     two chunks, 64 x 64: 18 / 19 us for 128, 17 / 21 us for 256 (float32: 23 / 22 us, 24 / 28 us).
 // SFM_DELTA_WALK=whole|prepared overrides (tuning and tests).
 int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype) {
     const int64_t chunks = (L + kDeltaChunk - 1) / kDeltaChunk;
     if (rows * H > INT32_MAX / chunks) return 0;
-    const int64_t most = chunks < 3 ? 128 : ((dv + 63) / 64 > (dk + 63) / 64 ? 1024 : 256);
+    const int64_t most = chunks < 3 ? 128 : ((dv + 63) / 64 > (dk + 63) / 64 ? 512 : 256);
     bool prepared = chunks > 1 && delta_units(L, tokens, H, dv) <= most;
     if (const char* e = std::getenv("SFM_DELTA_WALK")) prepared = e[0] == 'p' || (e[0] != 'w' && prepared);
     return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2, 2) : 0;
