@@ -110,9 +110,15 @@ def sfm_version() -> int:
     return load_library().sfm_version()
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:  # (an import statement costs a call of its own time: 0.2 us)
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _io_code(t) -> int:
@@ -445,6 +451,14 @@ def _new(shape, dtype, device, stream):
     return t
 
 
+def _new_like(t, stream):
+    """_new of a contiguous tensor's shape and type, in less host time."""
+    t = _torch().empty_like(t)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 SFM_DELTA_L2NORM = 1
 
 
@@ -452,14 +466,14 @@ def _tokens(t, name, heads, width, dtype, lead):
     """Checks a [*lead, heads, width] tensor whose heads are contiguous and whose tokens
     are evenly strided (a slice of a wider projection is fine); returns the token stride."""
     shape = lead + (heads, width)
+    if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return heads * width
     if not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return heads * width
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
     ld = st[-3]
     if (width > 1 and st[-1] != 1) or (heads > 1 and st[-2] != width) or \
@@ -471,16 +485,17 @@ def _tokens(t, name, heads, width, dtype, lead):
 def _delta_args(q, k, v, g, beta, packed):
     """Checks shared by the gated delta rule's functions; returns the sizes and strides."""
     io = _io_code(q)
-    lead = tuple(q.shape[:-2])
-    Hk, dk = q.shape[-2:]
-    H, dv = v.shape[-2:]
+    shape, wide = q.shape, v.shape
+    lead, Hk, dk, H, dv = shape[:-2], shape[-2], shape[-1], wide[-2], wide[-1]
     if packed and lead[0] != 1:
         raise ValueError("packed rows (offsets) are one batch entry: [1, tokens, heads, size]")
-    ldq = _tokens(q, "q", Hk, dk, q.dtype, lead)
-    ldk = _tokens(k, "k", Hk, dk, q.dtype, lead)
-    ldv = _tokens(v, "v", H, dv, q.dtype, lead)
-    _want(g, "g", q.dtype, lead + (H,))
-    _want(beta, "beta", q.dtype, lead + (H,))
+    dtype = q.dtype
+    ldq = _tokens(q, "q", Hk, dk, dtype, lead)
+    ldk = _tokens(k, "k", Hk, dk, dtype, lead)
+    ldv = _tokens(v, "v", H, dv, dtype, lead)
+    heads = lead + (H,)
+    _want(g, "g", dtype, heads)
+    _want(beta, "beta", dtype, heads)
     return io, lead, Hk, H, dk, dv, ldq, ldk, ldv
 
 
@@ -517,15 +532,17 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
     io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
     rows, L, tokens = _rows(lead, offsets, max_len)
     _want(h0, "h0", torch.float32, (rows, H, dk, dv))
-    if o is None:
-        o = _new(lead + (H, dv), q.dtype, q.device, stream)
-    _want(o, "o", q.dtype, lead + (H, dv))
-    if return_state and state is None:
-        state = _new((rows, H, dk, dv), torch.float32, q.device, stream)
+    if o is not None:
+        _want(o, "o", q.dtype, lead + (H, dv))
+    else:
+        o = _new_like(v, stream) if v.is_contiguous() else _new(lead + (H, dv), q.dtype, q.device, stream)
     if not return_state:
         state = None
-    _want(state, "state", torch.float32, (rows, H, dk, dv))
-    need = sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, return_state, "bf16" if io else "f32")
+    elif state is not None:
+        _want(state, "state", torch.float32, (rows, H, dk, dv))
+    else:
+        state = _new((rows, H, dk, dv), torch.float32, q.device, stream)
+    need = 0 if L <= 64 else sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, return_state, "bf16" if io else "f32")
     if workspace is None and need:
         workspace = _new(need, torch.uint8, q.device, stream)
     _dev(workspace, "workspace")
@@ -590,12 +607,13 @@ def sfm_gated_delta_step(q, k, v, g, beta, state, slots=None, scale=None, l2norm
     io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, False)
     rows = lead[0]
     _dev(state, "state", torch.float32)
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+    if state.dim() != 4 or state.shape[1:] != (H, dk, dv):
         raise ValueError(f"state must have shape (pool, {H}, {dk}, {dv}), got {tuple(state.shape)}")
     _want(slots, "slots", torch.int32, (rows,))
-    if o is None:
-        o = _new((rows, H, dv), q.dtype, q.device, stream)
-    _want(o, "o", q.dtype, (rows, H, dv))
+    if o is not None:
+        _want(o, "o", q.dtype, (rows, H, dv))
+    else:
+        o = _new_like(v, stream) if v.is_contiguous() else _new((rows, H, dv), q.dtype, q.device, stream)
     rc = load_library().sfm_gated_delta_step(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots), _ptr(o), rows, state.shape[0],
         Hk, H, dk, dv, ldq, ldk, ldv, dk ** -0.5 if scale is None else scale, io,
@@ -636,14 +654,17 @@ def sfm_group_norm_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, act=None
     _want(weight, "weight", torch.float32, (C,))
     _want(bias, "bias", torch.float32, (C,))
     if y is None:
-        y = _new(x.shape, x.dtype, x.device, stream)
-    _want(y, "y", x.dtype, x.shape)
+        y = _new_like(x, stream)
+    else:
+        _want(y, "y", x.dtype, x.shape)
     if mean is None:
         mean = _new((N, num_groups), torch.float32, x.device, stream)
+    else:
+        _want(mean, "mean", torch.float32, (N, num_groups))
     if rstd is None:
-        rstd = _new((N, num_groups), torch.float32, x.device, stream)
-    _want(mean, "mean", torch.float32, (N, num_groups))
-    _want(rstd, "rstd", torch.float32, (N, num_groups))
+        rstd = _new_like(mean, stream)
+    else:
+        _want(rstd, "rstd", torch.float32, (N, num_groups))
     need = sfm_group_norm_ws_size(N, L, C, num_groups, "bf16" if io else "f32")
     if workspace is None and need:
         workspace = _new(need, torch.uint8, x.device, stream)
