@@ -954,7 +954,9 @@ template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParam
     hipError_t e = launch_prepare<T, DK, P, P>(p, s);
     if (e != hipSuccess) return e;
     constexpr int gb = GradLds<T, DK, PW>::bytes;
-    const unsigned tiles = (p.dv + 63) / 64 * (p.narrow ? 64 / NarrowShape<DK>::cols : 1), units = (unsigned)p.rows * p.H * tiles;
+    // (few columns: those that the last pass reads, kVals at a time)
+    const unsigned tiles = p.narrow ? (p.dv + kVals - 1) / kVals * (kVals / NarrowShape<DK>::cols) : (p.dv + 63) / 64;
+    const unsigned units = (unsigned)p.rows * p.H * tiles;
     auto walks = !p.narrow ? delta_walks_kernel<T, DK, P>
                  : p.vec_k ? delta_narrow_walks_kernel<T, DK, P, true>
                            : delta_narrow_walks_kernel<T, DK, P, false>;

@@ -102,30 +102,38 @@ static int64_t delta_units(int64_t L, int64_t tokens, int64_t H, int64_t dv) { r
 // Few such workgroups walk long rows: the chunks' triangular inverses, which need no state, are then made beforehand
 // by the whole card (two launches) instead of inside the walk.  Past 256 the other workgroups of a unit hide their
 // making and the operands' way through memory costs more than it saves, unless several column tiles share them
-// (values wider than keys).  bfloat16, inside / beforehand:
+// (values wider than keys); with few values the walk with few columns is the faster one for longer.  bfloat16, inside /
+// beforehand:
 //     1024 tokens, 64 x 64: 114 / 57 us for 128 workgroups, 115 / 90 us for 256, 143 / 167 us for 384;
 //     1024 tokens, 128 x 128: 140 / 66 us for 128, 143 / 109 us for 256, 186 / 217 us for 512;
 //     1024 tokens, 64 x 128: 142 / 133 us for 512, 182 / 202 us for 768;
+//     1024 tokens, 64 x 32: 142 / 131 us for 384, 144 / 182 us for 512 (float32: 273 / 212 us, 276 / 259 us);
 //     two chunks, 64 x 64: 18 / 19 us for 128, 17 / 21 us for 256 (float32: 23 / 22 us, 24 / 28 us).
 // SFM_DELTA_WALK=whole|prepared overrides (tuning and tests).
 int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype) {
     const int64_t chunks = (L + kDeltaChunk - 1) / kDeltaChunk;
     if (rows * H > INT32_MAX / chunks) return 0;
-    const int64_t most = chunks < 3 ? 128 : ((dv + 63) / 64 > (dk + 63) / 64 ? 512 : 256);
+    const int64_t most = chunks < 3 ? 128 : (dv + 63) / 64 > (dk + 63) / 64 ? 512 : dv <= 32 ? 384 : 256;
     bool prepared = chunks > 1 && delta_units(L, tokens, H, dv) <= most;
     if (const char* e = std::getenv("SFM_DELTA_WALK")) prepared = e[0] == 'p' || (e[0] != 'w' && prepared);
     return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2, 2) : 0;
 }
 
-// Walks with few columns to a workgroup (delta_narrow.h) while those of 64 leave units idle.  A unit holds one of them,
-// two of bfloat16 with 64 keys; the backward has two walks at once.  64 columns / few, 2048 tokens, bfloat16:
-//     64 x 64: 142 / 97 us for 128 workgroups of 64 columns, 215 / 210 us for 256, 338 / 337 us for 384;
-//     128 x 128: 172 / 114 us for 128, 194 / 178 us for 192, 214 / 241 us for 256;
-//     backward, 64 x 64: 211 / 180 us for 64, 281 / 285 us for 96; 128 x 128: 274 / 216 us for 64, 414 / 472 us for 128.
+// Walks with few columns to a workgroup (delta_narrow.h: 32 with up to 64 keys, else 16) while there are no more of
+// them than run at once, two to a unit of bfloat16 with 64 keys; with 128 keys also twice that, two after one another
+// being no slower.  The backward has two walks at once.  64 columns / few, 2048 tokens, bfloat16:
+//     64 x 64: 142 / 97 us for 256 of them, 215 / 210 us for 512, 338 / 337 us for 768;
+//     128 x 128: 172 / 114 us for 512, 194 / 178 us for 768, 214 / 241 us for 1024;
+//     backward, 64 x 64: 211 / 180 us for 128, 281 / 285 us for 192; 128 x 128: 274 / 216 us for 256, 414 / 472 us for 512.
+// With up to 32 values half of the 64 columns are nobody's, and few are faster at any number: 64 x 32, 1024 tokens, 92 /
+// 69 us for 240 rows and heads, 190 / 182 us for 512; backward 281 / 239 us, 545 / 492 us.
 // SFM_DELTA_NARROW=0|1 overrides (tuning and tests).
 bool sfm::plan_delta_narrow(int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back) {
     if (const char* e = std::getenv("SFM_DELTA_NARROW")) return e[0] == '1';
-    return delta_units(L, tokens, H, dv) <= (back ? 64 : (dk <= 64 && io_dtype != 0 ? 256 : 128));
+    if (dv <= 32) return true;
+    const bool few = dk <= 64;
+    const int64_t cols = few ? 32 : 16, groups = tokens * H * ((dv + cols - 1) / cols) / L;
+    return groups <= (back ? (few ? 128 : 256) : few && io_dtype == 0 ? 256 : 512);
 }
 
 extern "C" {
