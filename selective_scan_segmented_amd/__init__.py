@@ -577,14 +577,13 @@ def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None
     _want(dstate, "dstate", torch.float32, (rows, H, dk, dv))
     _want(do, "do", q.dtype, lead + (H, dv))
     out = dict(grads or {})
-    shapes = dict(dq=lead + (Hk, dk), dk=lead + (Hk, dk), dv=lead + (H, dv), dg=lead + (H,), dbeta=lead + (H,))
-    if h0 is not None:
-        shapes["dh0"] = (rows, H, dk, dv)
-    for name, shape in shapes.items():
-        dt = torch.float32 if name == "dh0" else q.dtype
-        if out.get(name) is None:
-            out[name] = _new(shape, dt, q.device, stream)
-        _want(out[name], name, dt, shape)
+    for name, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta), ("dh0", h0)):
+        if like is None:
+            continue
+        if out.get(name) is not None:
+            _want(out[name], name, like.dtype, like.shape)
+        else:
+            out[name] = _new_like(like, stream) if like.is_contiguous() else _new(like.shape, like.dtype, q.device, stream)
     need = sfm_gated_delta_bwd_ws_size(rows, L, tokens, Hk, H, dk, dv, h0 is not None, "bf16" if io else "f32")
     if workspace is None:
         workspace = _new(need, torch.uint8, q.device, stream)
@@ -692,11 +691,11 @@ def sfm_group_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, act=None, grad
     _want(weight, "weight", torch.float32, (C,))
     _want(bias, "bias", torch.float32, (C,))
     out = dict(grads or {})
-    for name, given, shape, dt in (("dx", True, x.shape, x.dtype), ("dw", weight is not None, (C,), torch.float32),
-                                   ("db", bias is not None, (C,), torch.float32)):
-        if given and out.get(name) is None:
-            out[name] = _new(shape, dt, x.device, stream)
-        _want(out.get(name), name, dt, shape)
+    for name, like in (("dx", x), ("dw", weight), ("db", bias)):
+        if out.get(name) is not None:
+            _want(out[name], name, *((x.dtype, x.shape) if name == "dx" else (torch.float32, (C,))))
+        elif like is not None:
+            out[name] = _new_like(like, stream)
     need = sfm_group_norm_ws_size(N, L, C, G, "bf16" if io else "f32", True,
                                   out.get("dw") is not None or out.get("db") is not None)
     if workspace is None and need:

@@ -677,8 +677,10 @@ int64_t plan_norm(NormParams& p, int io_bytes, bool aligned, bool backward) {
     if (p.slab) {
         const int cu = p.cw / p.vec;
         p.runs = p.C / p.cw;
+        // (a wave joins its groups one after the other: four of them at most; 32 groups of 3 channels, 3 rows: 14 us a call, 32 with one wave)
+        const int joiners = std::min(kThreads, (p.cw / p.cg + 3) / 4 * 64);
         for (p.threads = 64; p.threads < kThreads; p.threads *= 2)
-            if (p.threads >= cu && p.L <= p.threads / cu * (int64_t)(p.threads < 256 ? 4 : kUnits)) break;
+            if (p.threads >= cu && p.threads >= joiners && p.L <= p.threads / cu * (int64_t)(p.threads < 256 ? 4 : kUnits)) break;
         const int slots = p.threads / cu;
         p.units = (int)((p.L + slots - 1) / slots);
         return backward && (p.dw || p.db) ? p.N * 2 * p.C * 4 : 0;
