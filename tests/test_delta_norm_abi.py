@@ -105,6 +105,21 @@ def test_launch_plans(lib, monkeypatch):
     assert f(2, 8192, 16384, 16, 128, 128, True) == 0
 
 
+
+@pytest.mark.parametrize("rows,L,H,dk,dv,beforehand", [
+    (16, 1024, 16, 64, 64, True), (24, 1024, 16, 64, 64, False), (16, 1024, 16, 64, 128, True),
+    (24, 1024, 16, 64, 128, False), (24, 1024, 16, 64, 32, True), (32, 1024, 16, 64, 32, False),
+    (8, 128, 16, 64, 64, True), (16, 128, 16, 64, 64, False), (1, 64, 1, 64, 64, False)])
+def test_inverses_beforehand_by_filled_workgroups(lib, rows, L, H, dk, dv, beforehand):
+    """A workspace is asked for exactly where the chunks' triangular inverses are made beforehand."""
+    assert (sfm.sfm_gated_delta_fwd_ws_size(rows, L, rows * L, H, dk, dv) > 0) == beforehand
+
+
+def test_ragged_rows_count_by_their_tokens(lib):
+    """Packed rows fill the card by their tokens, not by the longest row's."""
+    assert sfm.sfm_gated_delta_fwd_ws_size(32, 2048, 32 * 2048, 16, 64, 64) == 0
+    assert sfm.sfm_gated_delta_fwd_ws_size(32, 2048, 32 * 700, 16, 64, 64) > 0
+
 def norm(lib, **kw):
     a = dict(x=P, w=2 * P, b=3 * P, y=4 * P, mean=5 * P, rstd=6 * P, N=2, L=100, C=64, G=4, eps=1e-5, act=1, io=1, ws=None, wsb=0)
     a.update(kw)

@@ -130,3 +130,24 @@ def test_gradient_against_differences():
         up[i], down[i] = a[i] + h * d, a[i] - h * d
         num = (f(*up) - f(*down)) / (2 * h)
         assert abs(num - np.sum(got * d)) <= 2e-3 * abs(num), name
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("N,L,C,G", [(4, 3, 96, 32), (2, 40, 120, 40), (3, 6, 64, 64)])
+def test_many_groups_to_a_slab(N, L, C, G, io):
+    """More narrow groups to a workgroup than its rows need waves: they are joined by waves added for it."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    x, dy, w, b = inputs(N + L + C, N, L, C, io)
+    xd, dyd, wd, bd = dev(x, io), dev(dy, io), dev(w, "f32"), dev(b, "f32")
+    y, mean, rstd = sfm.sfm_group_norm_fwd(xd, G, wd, bd, act="silu")
+    g = sfm.sfm_group_norm_bwd(dyd, xd, mean, rstd, wd, bd, act="silu")
+    torch.cuda.synchronize()
+    wy, wm, wr = ref.group_norm(x, G, w, b, 1e-5, "silu")
+    ref.close(from_dev(y), wy, io, "y")
+    ref.close(from_dev(mean), wm, "f32", "mean")
+    ref.close(from_dev(rstd), wr, "f32", "rstd")
+    dx, dw, db = ref.group_norm_bwd(dy, x, from_dev(mean), from_dev(rstd), w, b, "silu")
+    ref.close(from_dev(g["dx"]), dx, io, "dx")
+    ref.close(from_dev(g["dw"]), dw, "f32", "dw", (2e-5, 1e-4))
+    ref.close(from_dev(g["db"]), db, "f32", "db", (2e-5, 1e-4))
