@@ -378,7 +378,6 @@ __device__ __forceinline__ void narrow_reverse(const DeltaParams& p, unsigned ti
         return;
     }
 
-    __builtin_amdgcn_s_setprio(3);
     T* dvp = static_cast<T*>(p.dv_) + obase;
     const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
     const int key = my.kw * 32 + 2 * g4;

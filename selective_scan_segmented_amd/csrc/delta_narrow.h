@@ -309,7 +309,6 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
         return;
     }
 
-    __builtin_amdgcn_s_setprio(3);  // before the other waves of the same unit: the chunks wait for these
     const T* vp = static_cast<const T*>(p.v) + first * p.ldv + (int64_t)h * p.dv;
     const int64_t sbase = (int64_t)rh * (p.dk * p.dv);
     const int key = my.kw * 32 + 2 * g4;
