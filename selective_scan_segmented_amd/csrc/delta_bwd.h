@@ -541,16 +541,16 @@ __device__ __forceinline__ void narrow_reverse(const DeltaParams& p, unsigned ti
 template <typename T, int DK, int P>
 __global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_walks_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
     if (blockIdx.x < units)  // (the longer one first)
-        reverse<T, DK, P>(p, tiles, die_local(blockIdx.x, units));
+        reverse<T, DK, P>(p, tiles, row_unit(p, blockIdx.x, units, tiles * p.H, tiles * p.share));
     else
-        walk<T, DK, P, kStates>(p, tiles, die_local(blockIdx.x - units, units));
+        walk<T, DK, P, kStates>(p, tiles, row_unit(p, blockIdx.x - units, units, tiles * p.H, tiles * p.share));
 }
 template <typename T, int DK, int P, bool VEC>
 __global__ __launch_bounds__(kNarrowThreads, 2) void delta_narrow_walks_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
     if (blockIdx.x < units)
-        narrow_reverse<T, DK, P, VEC>(p, tiles, die_local(blockIdx.x, units));
+        narrow_reverse<T, DK, P, VEC>(p, tiles, row_unit(p, blockIdx.x, units, tiles * p.H, tiles * p.share));
     else
-        narrow_walk<T, DK, P, kStates, VEC>(p, tiles, die_local(blockIdx.x - units, units));
+        narrow_walk<T, DK, P, kStates, VEC>(p, tiles, row_unit(p, blockIdx.x - units, units, tiles * p.H, tiles * p.share));
 }
 
 // ---------------------------------------------------------------- per chunk and head
@@ -637,7 +637,7 @@ __global__ __launch_bounds__(kDeltaThreads, (sizeof(T) == 2 ? 2 : 1)) void delta
     // by token: P's row sums, the other terms of dG, c, dbeta's two halves, dR.V; P's column sums by wave; <S0, dS'>
     float *row_p = sums, *row_o = sums + kC, *row_c = sums + 2 * kC, *row_b = sums + 3 * kC, *row_e = sums + 4 * kC,
           *row_v = sums + 5 * kC, *col_p = sums + 6 * kC, *frob = sums + 10 * kC;
-    const unsigned unit = die_local(blockIdx.x, units);
+    const unsigned unit = row_unit(p, blockIdx.x, units, chunks * p.H, p.share);
     const int h = (int)(unit % (unsigned)p.H), hk = (int)((unsigned)h / (unsigned)p.share);
     const unsigned sc = unit / (unsigned)p.H;
     const int s = (int)(sc / chunks);

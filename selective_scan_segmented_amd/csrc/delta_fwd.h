@@ -261,7 +261,7 @@ __device__ __forceinline__ void walk(const DeltaParams& p, unsigned tiles, unsig
 
 template <typename T, int DK, int P, Walk W>
 __global__ __launch_bounds__(kDeltaThreads, (W == kWhole && DK == 64 && P == 2 && sizeof(T) == 2 ? 3 : W != kPrepared || DK == 64 ? WalkLds<T, DK, P, W == kSingle>::groups : 1)) void delta_walk_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
-    walk<T, DK, P, W>(p, tiles, die_local(blockIdx.x, units));
+    walk<T, DK, P, W>(p, tiles, row_unit(p, blockIdx.x, units, tiles * p.H, tiles * p.share));
 }
 
 // T, A and the row scalars of every chunk and head, a workgroup to each.  T and A go from registers to memory.
@@ -282,7 +282,8 @@ void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) 
     extern __shared__ char lds[];
     ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs);
-    const unsigned heads = ALL ? p.share : 1, unit = die_local(blockIdx.x, units), groups = (unsigned)p.H / heads, sc = unit / groups;
+    const unsigned heads = ALL ? p.share : 1, groups = (unsigned)p.H / heads, unit = row_unit(p, blockIdx.x, units, chunks * groups, p.share / heads),
+                   sc = unit / groups;
     const int h = (int)((unit - sc * groups) * heads), hk = (int)((unsigned)h / (unsigned)p.share);
     const int s = (int)(sc / chunks);
     int64_t first;

@@ -481,7 +481,7 @@ __device__ __forceinline__ void narrow_walk(const DeltaParams& p, unsigned tiles
 
 template <typename T, int DK, int P, bool VEC>
 __global__ __launch_bounds__(kNarrowThreads, (DK == 64 && sizeof(T) == 2 && VEC ? 4 : 2)) void delta_narrow_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
-    narrow_walk<T, DK, P, kPrepared, VEC>(p, tiles, die_local(blockIdx.x, units));
+    narrow_walk<T, DK, P, kPrepared, VEC>(p, tiles, row_unit(p, blockIdx.x, units, tiles * p.H, tiles * p.share));
 }
 
 template <typename T, int DK, int P> hipError_t launch_narrow(const DeltaParams& p, hipStream_t s) {
