@@ -14,8 +14,8 @@
 // Four passes: the preparing kernel (T, A), the walk forward (states before the chunks, U), the walk back below
 // (dS', dR, dV, the state's gradient) and, a workgroup to every chunk and head, the rest.  The walks are bound as the
 // forward's (a chunk's latency); the last pass reads 4 bytes of every state and gradient value (260 KB to a chunk and
-// head of 128 x 128) with two workgroups to a unit, 3.4 TB/s.  64 rows x 198 tokens x 5 heads of 64: 100 us = 17
-// preparing + 40 walks + 43; 2 x 4002 x 8 heads of 128 over 4 key heads: 251 us = 19 + 135 + 76 + 20 for the sums over
+// head of 128 x 128) with two workgroups to a unit, 3.5 TB/s.  64 rows x 198 tokens x 5 heads of 64: 101 us = 17
+// preparing + 40 walks + 43; 2 x 4002 x 8 heads of 128 over 4 key heads: 246 us = 19 + 135 + 74 + 18 for the sums over
 // shared heads.
 #pragma once
 
