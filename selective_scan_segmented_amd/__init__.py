@@ -7,6 +7,10 @@ stream, and turns non-zero status codes into exceptions.  Every step runs in
 the library's kernels; there is no fallback -- if ``libsfm.so`` is missing the
 first call raises.
 
+`stream` (a torch.cuda.Stream; None: the current one) is where a call's kernels run.  What the call allocates comes
+from that stream's memory pool.  What the caller passes has to be ready there, and to live until the call's kernels
+are through; what it returns has to be waited for as any work of that stream.
+
 Functions keep the C names:
   sfm_selective_scan_fwd, sfm_dwconv1d_fold, sfm_aux_pad_swap, sfm_pick_b1,
   sfm_gated_delta_fwd, sfm_gated_delta_step, sfm_group_norm_fwd, sfm_group_norm_bwd
@@ -159,6 +163,26 @@ def _stream(stream):
         return torch.cuda.current_stream().cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one).
+
+    It comes from that stream's own pool: a block of another pool may still be read or written there by kernels that
+    `stream` does not wait for, such as an earlier call's whose workspace it was.  The caller has it on the current
+    stream, so its memory is not handed out again before that stream is past its free either."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _new_like(t, stream):
+    """_new of a contiguous tensor's shape and type, in less host time."""
+    return _torch().empty_like(t) if stream is None else _new(t.shape, t.dtype, t.device, stream)
+
+
 SFM_FUSE_PAD, SFM_FUSE_SWAP, SFM_LAYOUT_BLD = 1, 2, 4
 SFM_NOALLOC_SCRATCH_BYTES = 32 << 20  # static scratch of sfm_selective_scan_fwd_noalloc (include/sfm.h)
 
@@ -219,7 +243,7 @@ def _fwd_ex(u, delta, A, Bm, Cm, Dskip, delta_bias, delta_softplus, conv_w, conv
         K = conv_w.shape[1]
         _dev(conv_b, "conv_b", torch.float32, (D,))
     if y is None:
-        y = torch.empty(tl(D, L), dtype=u.dtype, device=u.device)
+        y = _new(tl(D, L), u.dtype, u.device, stream)
     _dev(y, "y", u.dtype, tl(D, L))
     args = (_ptr(u), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(delta_bias),
             int(bool(delta_softplus)), _ptr(conv_w), _ptr(conv_b), K, int(conv_pad_left), _ACT[conv_act], _ptr(y),
@@ -232,7 +256,7 @@ def _fwd_ex(u, delta, A, Bm, Cm, Dskip, delta_bias, delta_softplus, conv_w, conv
         need = sfm_selective_scan_fwd_ws_size(B // B2, B2, D, N, L, K, "bf16" if io == SFM_BF16 else "f32",
                                               int(flags))
         if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=u.device)
+            workspace = _new(max(need, 16), torch.uint8, u.device, stream)
         _dev(workspace, "workspace")
         rc = load_library().sfm_selective_scan_fwd_ws(*args, _ptr(workspace),
                                                       workspace.numel() * workspace.element_size(),
@@ -333,12 +357,12 @@ def sfm_selective_scan_bwd(u, delta, A, Bm, Cm, dy, Dskip=None, delta_bias=None,
             shapes["dconv_b"] = ((D,), torch.float32)
     for k, (shape, dt) in shapes.items():
         if g.get(k) is None:
-            g[k] = torch.empty(shape, dtype=dt, device=u.device)
+            g[k] = _new(shape, dt, u.device, stream)
         _dev(g[k], k, dt, shape)
     need = sfm_selective_scan_bwd_workspace_size(B // B2, B2, D, N, L, K, "bf16" if io == SFM_BF16 else "f32",
                                                  flags)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=u.device)
+        workspace = _new(max(need, 16), torch.uint8, u.device, stream)
     _dev(workspace, "workspace")
     rc = load_library().sfm_selective_scan_bwd(
         _ptr(u), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(delta_bias), int(bool(delta_softplus)),
@@ -368,7 +392,7 @@ def sfm_aux_pad_bwd_ex(gpad, gx=None, flags=0, stream=None):
         shape = (B, D, L - 2)
     _dev(gpad, "gpad")
     if gx is None:
-        gx = _torch().empty(shape, dtype=gpad.dtype, device=gpad.device)
+        gx = _new(shape, gpad.dtype, gpad.device, stream)
     _dev(gx, "gx", gpad.dtype, shape)
     _check(load_library().sfm_aux_pad_bwd_ex(_ptr(gpad), _ptr(gx), B, D, L - 2, io, int(flags), _stream(stream)),
            "sfm_aux_pad_bwd")
@@ -388,7 +412,7 @@ def sfm_dwconv1d_fold(x, w, bias=None, pad_left=1, act=None, out=None, B2=1, str
         raise ValueError("w must be [D, K]")
     _dev(bias, "bias", torch.float32, (D,))
     if out is None:
-        out = torch.empty_like(x)
+        out = _new_like(x, stream)
     _dev(out, "out", x.dtype, (B, D, L))
     rc = load_library().sfm_dwconv1d_fold(_ptr(x), _ptr(w), _ptr(bias), _ptr(out), B // B2, B2, D, L, w.shape[1],
                                           int(pad_left), _ACT[act], io, _stream(stream))
@@ -399,19 +423,18 @@ def sfm_dwconv1d_fold(x, w, bias=None, pad_left=1, act=None, out=None, B2=1, str
 def sfm_aux_pad_swap(inp, out=None, mode="pad", stream=None):
     """mode 'pad': [B, D, T] -> [B, D, T+2] with mean-initialised ends;
     mode 'swap': [B, D, L] -> ends exchanged (in place when ``out is inp``)."""
-    torch = _torch()
     io = _io_code(inp)
     B, D, n = inp.shape
     _dev(inp, "in")
     if mode == "pad":
         T, code = n, SFM_AUX_PAD
         if out is None:
-            out = torch.empty((B, D, T + 2), dtype=inp.dtype, device=inp.device)
+            out = _new((B, D, T + 2), inp.dtype, inp.device, stream)
         _dev(out, "out", inp.dtype, (B, D, T + 2))
     elif mode == "swap":
         T, code = n - 2, SFM_AUX_SWAP
         if out is None:
-            out = torch.empty_like(inp)
+            out = _new_like(inp, stream)
         _dev(out, "out", inp.dtype, (B, D, n))
     else:
         raise ValueError(f"mode must be 'pad' or 'swap', got {mode!r}")
@@ -441,22 +464,6 @@ def _want(t, name, dtype, shape):
     """_dev for the usual case in one look: a contiguous GPU tensor of this type and shape (or None)."""
     if t is not None and not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         _dev(t, name, dtype, shape)
-
-
-def _new(shape, dtype, device, stream):
-    """A tensor for a call on `stream`: memory that the caching allocator hands out again only after it."""
-    t = _torch().empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
-def _new_like(t, stream):
-    """_new of a contiguous tensor's shape and type, in less host time."""
-    t = _torch().empty_like(t)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 SFM_DELTA_L2NORM = 1
