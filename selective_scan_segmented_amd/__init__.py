@@ -576,7 +576,7 @@ def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None
                         l2norm=False, grads=None, workspace=None, stream=None):
     """Gradients of sfm_gated_delta_fwd (same arguments) for do, the gradient of o, and dstate, that of the
     states after the rows (float32, None: zero).  Returns a dict with dq, dk, dv, dg, dbeta and, with h0,
-    dh0 (float32); `grads` may hold preallocated tensors under those names."""
+    dh0 (float32); `grads` may hold preallocated tensors under those names, dh0 also without h0."""
     torch = _torch()
     io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
     rows, L, tokens = _rows(lead, offsets, max_len)
@@ -585,13 +585,13 @@ def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None
     _want(do, "do", q.dtype, lead + (H, dv))
     out = dict(grads or {})
     for name, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta), ("dh0", h0)):
-        if like is None:
-            continue
-        if out.get(name) is not None:
+        if like is None:  # (dh0 of states that were zero: only where the caller gives a tensor for it)
+            _want(out.get(name), name, torch.float32, (rows, H, dk, dv))
+        elif out.get(name) is not None:
             _want(out[name], name, like.dtype, like.shape)
         else:
             out[name] = _new_like(like, stream) if like.is_contiguous() else _new(like.shape, like.dtype, q.device, stream)
-    need = sfm_gated_delta_bwd_ws_size(rows, L, tokens, Hk, H, dk, dv, h0 is not None, "bf16" if io else "f32")
+    need = sfm_gated_delta_bwd_ws_size(rows, L, tokens, Hk, H, dk, dv, out.get("dh0") is not None, "bf16" if io else "f32")
     if workspace is None:
         workspace = _new(need, torch.uint8, q.device, stream)
     _dev(workspace, "workspace")

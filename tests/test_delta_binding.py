@@ -1,0 +1,107 @@
+"""What the gated delta rule's binding checks before it calls the library (host only, stand-ins for GPU tensors)."""
+import types
+
+import pytest
+import torch
+
+import selective_scan_segmented_amd as sfm
+
+SIDE = types.SimpleNamespace(cuda_stream=0)
+
+
+class Stub:
+    """A GPU tensor as the binding sees one: sizes, strides, type and an address that nothing reads."""
+    is_cuda = True
+    count = 0
+
+    def __init__(self, *shape, dtype=torch.bfloat16, stride=None):
+        self.shape, self.dtype = torch.Size(shape), dtype
+        Stub.count += 1
+        self.at = Stub.count << 32
+        dense, n = [], 1
+        for size in reversed(shape):
+            dense.insert(0, n)
+            n *= size
+        self.dense, self.steps = tuple(dense), tuple(stride or dense)
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return self.steps
+
+    def is_contiguous(self):
+        return self.steps == self.dense
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's calls in place of the calls: (name, arguments)."""
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("_ws_size"):
+                def size(*a):
+                    seen.append((name, a))
+                    return 0
+                return size
+            return lambda *a: seen.append((name, a)) or 0
+
+    monkeypatch.setattr(sfm, "load_library", Library)
+    monkeypatch.setattr(sfm, "_dev", check)
+    return seen
+
+
+def check(t, name, dtype=None, shape=None):
+    """_dev for stand-ins."""
+    if t is None:
+        return
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {shape}")
+
+
+B, L, HK, H, DK, DV = 2, 100, 1, 2, 64, 32
+
+
+def args(lead=(B, L)):
+    return [Stub(*lead, HK, DK), Stub(*lead, HK, DK), Stub(*lead, H, DV), Stub(*lead, H), Stub(*lead, H)]
+
+
+def grads(lead=(B, L), **more):
+    g = {"dq": Stub(*lead, HK, DK), "dk": Stub(*lead, HK, DK), "dv": Stub(*lead, H, DV), "dg": Stub(*lead, H), "dbeta": Stub(*lead, H)}
+    return dict(g, **more)
+
+
+def backward(g, **kw):
+    return sfm.sfm_gated_delta_bwd(*args(), Stub(B, L, H, DV), grads=g, workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE, **kw)
+
+
+@pytest.mark.parametrize("dh0", [Stub(B, H, DK, 16, dtype=torch.float32), Stub(1, H, DK, DV, dtype=torch.float32),
+                                 Stub(B, H, DK, DV), Stub(B, H, DK, DV, dtype=torch.float32, stride=(1, 1, 1, 1))])
+@pytest.mark.parametrize("h0", [None, Stub(B, H, DK, DV, dtype=torch.float32)])
+def test_a_wrong_dh0_is_refused_with_and_without_h0(calls, dh0, h0):
+    with pytest.raises((TypeError, ValueError), match="dh0"):
+        backward(grads(dh0=dh0), h0=h0)
+    assert not any(n == "sfm_gated_delta_bwd" for n, _ in calls)
+
+
+def test_dh0_without_h0_counts_in_the_workspace(calls):
+    dh0 = Stub(B, H, DK, DV, dtype=torch.float32)
+    assert backward(grads(dh0=dh0))["dh0"] is dh0
+    size, call = calls
+    assert size[0] == "sfm_gated_delta_bwd_ws_size" and size[1][7] == 1
+    assert call[0] == "sfm_gated_delta_bwd" and call[1][13] == dh0.at

@@ -1,0 +1,31 @@
+"""The gated delta rule's calls in the forms that a user's program gives them, against the float64 definition."""
+import numpy as np
+import pytest
+
+import delta_reference as ref
+from helpers import from_dev
+from test_gpu_gated_delta import dev, f32
+from test_gpu_gated_delta_bwd import GRADE_H0
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gradient_of_states_that_were_zero(io):
+    """dh0 into a tensor of the caller's without h0: that of states of zeros; one that does not fit is refused."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    lens, H, dk, dv = [70, 70], 2, 64, 48
+    x = ref.delta_inputs(17, sum(lens), 2, 1, H, dk, dv, True, io)
+    t = [dev(a.reshape((2, 70) + a.shape[1:]), io) for a in x[:5] + [x[6]]]
+    dh0 = torch.full((2, H, dk, dv), float("nan"), device="cuda")
+    got = sfm.sfm_gated_delta_bwd(*t, l2norm=True, grads={"dh0": dh0})
+    torch.cuda.synchronize()
+    assert got["dh0"] is dh0
+    zero = np.zeros(x[5].shape)
+    want = ref.delta_bwd(*x[:5], zero, np.cumsum(lens), dk ** -0.5, True, x[6], zero)
+    ref.close(from_dev(dh0), want["dh0"], "f32", "dh0", GRADE_H0)
+    with pytest.raises(ValueError, match="dh0"):
+        sfm.sfm_gated_delta_bwd(*t, l2norm=True, grads={"dh0": dh0[:1].contiguous()})
+    with pytest.raises(TypeError, match="dh0"):
+        sfm.sfm_gated_delta_bwd(*t, l2norm=True, grads={"dh0": dh0.bfloat16()})
