@@ -489,10 +489,13 @@ def _tokens(t, name, heads, width, dtype, lead):
     return max(ld, heads * width)
 
 
-def _delta_args(q, k, v, g, beta, packed):
+def _delta_args(q, k, v, g, beta, packed, form="[B, L, heads, size]"):
     """Checks shared by the gated delta rule's functions; returns the sizes and strides."""
     io = _io_code(q)
     shape, wide = q.shape, v.shape
+    dims = form.count(",") + 1
+    if len(shape) != dims or len(wide) != dims:
+        raise ValueError(f"q, k and v must be {form}, got q {tuple(shape)} and v {tuple(wide)}")
     lead, Hk, dk, H, dv = shape[:-2], shape[-2], shape[-1], wide[-2], wide[-1]
     if packed and lead[0] != 1:
         raise ValueError("packed rows (offsets) are one batch entry: [1, tokens, heads, size]")
@@ -610,7 +613,7 @@ def sfm_gated_delta_step(q, k, v, g, beta, state, slots=None, scale=None, l2norm
     float32, updated in place; slots int32 [R] (row r's state; outside the pool: padding) or None
     (state r).  Returns o [R, H, dv]."""
     torch = _torch()
-    io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, False)
+    io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, False, "[R, heads, size]")
     rows = lead[0]
     _dev(state, "state", torch.float32)
     if state.dim() != 4 or state.shape[1:] != (H, dk, dv):

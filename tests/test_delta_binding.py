@@ -105,3 +105,30 @@ def test_dh0_without_h0_counts_in_the_workspace(calls):
     size, call = calls
     assert size[0] == "sfm_gated_delta_bwd_ws_size" and size[1][7] == 1
     assert call[0] == "sfm_gated_delta_bwd" and call[1][13] == dh0.at
+
+
+@pytest.mark.parametrize("lead", [(), (B,), (B, L, 3)])
+@pytest.mark.parametrize("back", [False, True])
+def test_rows_take_four_dimensions(calls, lead, back):
+    """Tensors of another rank were read as far as two of their dimensions, and the rest of the output left as it was."""
+    o = Stub(*lead, H, DV)
+    with pytest.raises(ValueError, match=r"\[B, L, heads, size\]"):
+        if back:
+            sfm.sfm_gated_delta_bwd(*args(lead), o, grads=grads(lead), workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE)
+        else:
+            sfm.sfm_gated_delta_fwd(*args(lead), o=o, workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE)
+    assert not calls
+
+
+@pytest.mark.parametrize("lead", [(), (3, 2), (3, 1)])
+def test_a_step_takes_three_dimensions(calls, lead):
+    with pytest.raises(ValueError, match=r"\[R, heads, size\]"):
+        sfm.sfm_gated_delta_step(*args(lead), Stub(4, H, DK, DV, dtype=torch.float32), o=Stub(3, H, DV), stream=SIDE)
+    assert not calls
+
+
+def test_values_of_another_rank_are_refused(calls):
+    t = args()
+    t[2] = Stub(B, L, 1, H, DV)
+    with pytest.raises(ValueError, match=r"\[B, L, heads, size\]"):
+        sfm.sfm_gated_delta_fwd(*t, o=Stub(B, L, H, DV), workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE)
