@@ -482,9 +482,11 @@ def _tokens(t, name, heads, width, dtype, lead):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
-    ld = st[-3]
+    single = len(lead) == 2 and lead[1] == 1  # rows of one token: the tokens are the rows'
+    ld = st[0] if single else st[-3]
     if (width > 1 and st[-1] != 1) or (heads > 1 and st[-2] != width) or \
-            (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * ld) or (ld < heads * width and lead[-1] > 1):
+            (len(lead) == 2 and not single and lead[0] > 1 and st[0] != lead[1] * ld) or \
+            (ld < heads * width and lead.numel() > 1):
         raise ValueError(f"{name}: heads must be contiguous and tokens evenly strided, got strides {st}")
     return max(ld, heads * width)
 

@@ -132,3 +132,27 @@ def test_values_of_another_rank_are_refused(calls):
     t[2] = Stub(B, L, 1, H, DV)
     with pytest.raises(ValueError, match=r"\[B, L, heads, size\]"):
         sfm.sfm_gated_delta_fwd(*t, o=Stub(B, L, H, DV), workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE)
+
+
+@pytest.mark.parametrize("rows,steps", [(3, (5000, 7, DK, 1)), (3, (5000, 5000, DK, 1)), (1, (7, 7, DK, 1))])
+def test_one_token_of_each_row_of_a_projection(calls, rows, steps):
+    """X[:, i:i + 1]: tokens are as far apart as the rows, whatever the stride of the dimension of one token says."""
+    t = args((rows, 1))
+    t[0] = Stub(rows, 1, HK, DK, stride=steps)
+    t[2] = Stub(rows, 1, H, DV, stride=(9000, 11, DV, 1))
+    sfm.sfm_gated_delta_fwd(*t, o=Stub(rows, 1, H, DV), stream=SIDE)
+    (name, a), = calls
+    assert name == "sfm_gated_delta_fwd"
+    if rows > 1:
+        assert a[16:19] == (5000, HK * DK, 9000)
+    else:  # one token: any stride that holds its heads
+        assert a[16] >= HK * DK and a[18] >= H * DV
+
+
+@pytest.mark.parametrize("lead,steps", [((3, 1), (0, 7, DK, 1)), ((3, 1), (HK * DK - 1, 1, DK, 1)), ((2, 5), (7 * DK, DK, DK, 1)),
+                                        ((2, 5), (0, DK, DK, 1)), ((2, 5), (5 * DK, DK, DK, 2))])
+def test_tokens_on_top_of_one_another_or_unevenly_apart_are_refused(calls, lead, steps):
+    t = args(lead)
+    t[0] = Stub(*lead, HK, DK, stride=steps)
+    with pytest.raises(ValueError, match="q: heads must be contiguous"):
+        sfm.sfm_gated_delta_fwd(*t, o=Stub(*lead, H, DV), workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE)

@@ -29,3 +29,25 @@ def test_gradient_of_states_that_were_zero(io):
         sfm.sfm_gated_delta_bwd(*t, l2norm=True, grads={"dh0": dh0[:1].contiguous()})
     with pytest.raises(TypeError, match="dh0"):
         sfm.sfm_gated_delta_bwd(*t, l2norm=True, grads={"dh0": dh0.bfloat16()})
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_one_token_of_each_row_of_a_projection(io):
+    """q, k and v as one token of every row of a longer projection: the bits of contiguous copies."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    R, T, H, d = 3, 5, 2, 64
+    x = ref.delta_inputs(23, R * T, R, H, H, d, d, True, io)
+    wide = dev(np.concatenate([a.reshape(R, T, -1) for a in x[:3]], -1), io)
+    q, k, v = (wide[:, 2:3, i * H * d:(i + 1) * H * d].unflatten(-1, (H, d)) for i in range(3))
+    g, beta, do = (dev(a.reshape((R, T) + a.shape[1:])[:, 2:3], io) for a in (x[3], x[4], x[6]))
+    h0 = f32(x[5])
+    o, s = sfm.sfm_gated_delta_fwd(q, k, v, g, beta, h0=h0, l2norm=True, return_state=True)
+    got = sfm.sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=h0, l2norm=True)
+    own = [a.contiguous() for a in (q, k, v)]
+    o2, s2 = sfm.sfm_gated_delta_fwd(*own, g, beta, h0=h0, l2norm=True, return_state=True)
+    want = sfm.sfm_gated_delta_bwd(*own, g, beta, do, h0=h0, l2norm=True)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(s, s2)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
