@@ -156,3 +156,14 @@ def test_tokens_on_top_of_one_another_or_unevenly_apart_are_refused(calls, lead,
     t[0] = Stub(*lead, HK, DK, stride=steps)
     with pytest.raises(ValueError, match="q: heads must be contiguous"):
         sfm.sfm_gated_delta_fwd(*t, o=Stub(*lead, H, DV), workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE)
+
+
+@pytest.mark.parametrize("max_len", [None, 0])
+def test_packed_rows_that_are_all_empty(calls, max_len):
+    off = Stub(4, dtype=torch.int32)
+    h0 = Stub(3, H, DK, DV, dtype=torch.float32)
+    state = Stub(3, H, DK, DV, dtype=torch.float32)
+    sfm.sfm_gated_delta_fwd(*args((1, 0)), offsets=off, max_len=max_len, h0=h0, state=state, return_state=True,
+                            o=Stub(1, 0, H, DV), stream=SIDE)
+    (name, a), = calls
+    assert name == "sfm_gated_delta_fwd" and a[9:12] == (3, 1, 0)

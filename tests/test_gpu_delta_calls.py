@@ -51,3 +51,21 @@ def test_one_token_of_each_row_of_a_projection(io):
     assert torch.equal(o, o2) and torch.equal(s, s2)
     for n in want:
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("max_len", [None, 0, 5])
+def test_packed_rows_that_are_all_empty(io, max_len):
+    """A batch without a token: the states pass through, forward and back."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    R, H, dk, dv = 3, 2, 64, 48
+    x = ref.delta_inputs(29, 1, R, 1, H, dk, dv, True, io)
+    t = [dev(a[None, :0], io) for a in x[:5] + [x[6]]]
+    h0, off = f32(x[5]), torch.zeros(R + 1, dtype=torch.int32, device="cuda")
+    o, s = sfm.sfm_gated_delta_fwd(*t[:5], h0=h0, offsets=off, max_len=max_len, return_state=True)
+    _, z = sfm.sfm_gated_delta_fwd(*t[:5], offsets=off, max_len=max_len, return_state=True)
+    got = sfm.sfm_gated_delta_bwd(*t, h0=h0, dstate=h0 + 1, offsets=off, max_len=max_len)
+    torch.cuda.synchronize()
+    assert o.shape == t[2].shape and torch.equal(s, h0) and torch.equal(z, torch.zeros_like(h0))
+    assert torch.equal(got["dh0"], h0 + 1) and got["dq"].numel() == 0
