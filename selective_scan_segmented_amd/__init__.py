@@ -540,7 +540,8 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
     h0: [B, H, dk, dv] float32 states before the rows, or None.  offsets (int32 [rows + 1] on the
     GPU): packed rows, tensors [1, tokens, ...]; max_len bounds the longest row.  scale defaults to
     dk ** -0.5; l2norm divides q and k by their length.  Returns o [B, L, H, dv], and with
-    return_state the states after the rows (written to `state` if given; h0 itself is allowed)."""
+    return_state the states after the rows.  `state`, if given, takes those in either case (h0
+    itself is allowed)."""
     torch = _torch()
     io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
     rows, L, tokens = _rows(lead, offsets, max_len)
@@ -549,13 +550,11 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
         _want(o, "o", q.dtype, lead + (H, dv))
     else:
         o = _new_like(v, stream) if v.is_contiguous() else _new(lead + (H, dv), q.dtype, q.device, stream)
-    if not return_state:
-        state = None
-    elif state is not None:
+    if state is not None:
         _want(state, "state", torch.float32, (rows, H, dk, dv))
-    else:
+    elif return_state:
         state = _new((rows, H, dk, dv), torch.float32, q.device, stream)
-    need = 0 if L <= 64 else sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, return_state, "bf16" if io else "f32")
+    need = 0 if L <= 64 else sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, state is not None, "bf16" if io else "f32")
     if workspace is None and need:
         workspace = _new(need, torch.uint8, q.device, stream)
     _dev(workspace, "workspace")

@@ -167,3 +167,19 @@ def test_packed_rows_that_are_all_empty(calls, max_len):
                             o=Stub(1, 0, H, DV), stream=SIDE)
     (name, a), = calls
     assert name == "sfm_gated_delta_fwd" and a[9:12] == (3, 1, 0)
+
+
+@pytest.mark.parametrize("given,asked", [(True, False), (True, True), (False, False)])
+def test_a_state_given_is_written(calls, given, asked):
+    """Also where it is not asked for as a result."""
+    state = Stub(B, H, DK, DV, dtype=torch.float32) if given else None
+    o = Stub(B, L, H, DV)
+    got = sfm.sfm_gated_delta_fwd(*args(), o=o, state=state, return_state=asked, workspace=Stub(1 << 20, dtype=torch.uint8), stream=SIDE)
+    size, call = calls
+    assert size[1][6] == given and call[1][7] == (state.at if given else None)
+    assert got == (o, state) if asked else got is o
+
+
+def test_a_wrong_state_is_refused(calls):
+    with pytest.raises(ValueError, match="state"):
+        sfm.sfm_gated_delta_fwd(*args(), o=Stub(B, L, H, DV), state=Stub(1, H, DK, DV, dtype=torch.float32), stream=SIDE)

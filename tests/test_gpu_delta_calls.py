@@ -69,3 +69,17 @@ def test_packed_rows_that_are_all_empty(io, max_len):
     torch.cuda.synchronize()
     assert o.shape == t[2].shape and torch.equal(s, h0) and torch.equal(z, torch.zeros_like(h0))
     assert torch.equal(got["dh0"], h0 + 1) and got["dq"].numel() == 0
+
+
+@pytest.mark.parametrize("L", [3, 40, 150])
+def test_a_state_given_is_written(L):
+    """The states go to the caller's tensor whether or not they are asked for as a result."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    x = ref.delta_inputs(37, 2 * L, 2, 1, 2, 64, 64, True, "bf16")
+    t = [dev(a.reshape((2, L) + a.shape[1:]), "bf16") for a in x[:5]]
+    h0 = f32(x[5])
+    o, want = sfm.sfm_gated_delta_fwd(*t, h0=h0, l2norm=True, return_state=True)
+    o2 = sfm.sfm_gated_delta_fwd(*t, h0=h0, l2norm=True, state=h0)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(h0, want)
