@@ -375,8 +375,8 @@ sfm_status sfm_scan_plan_string(int64_t B1, int64_t B2, int64_t D, int64_t N, in
  * workspace: device memory of at least sfm_gated_delta_fwd_ws_size() bytes
  *   (may be NULL when that is 0), 16-byte aligned, owned by the caller.
  * How the chunks of a row are walked follows from the sizes; for tuning and tests the
- * environment overrides it: SFM_DELTA_WALK=whole|prepared (the chunks' triangular
- * inverses made on the way or beforehand), SFM_DELTA_NARROW=0|1 (64 value columns or
+ * environment overrides it: SFM_DELTA_WALK=whole|prepared (the triangular inverses of
+ * rows of several chunks made on the way or beforehand), SFM_DELTA_NARROW=0|1 (64 value columns or
  * few to a workgroup).  The size query and the call must see the same setting.
  * Returns SFM_OK, or NULL/SHAPE/DTYPE/ALIAS/ALIGN (nothing launched), HIP.
  */

@@ -113,8 +113,9 @@ static int64_t delta_units(int64_t L, int64_t tokens, int64_t H, int64_t dv) { r
 int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype) {
     const int64_t chunks = (L + kDeltaChunk - 1) / kDeltaChunk;
     if (rows * H > INT32_MAX / chunks) return 0;
+    if (chunks < 2) return 0;  // (nothing to walk, whatever the override says)
     const int64_t most = chunks < 3 ? 128 : (dv + 63) / 64 > (dk + 63) / 64 ? 512 : dv <= 32 ? 384 : 256;
-    bool prepared = chunks > 1 && delta_units(L, tokens, H, dv) <= most;
+    bool prepared = delta_units(L, tokens, H, dv) <= most;
     if (const char* e = std::getenv("SFM_DELTA_WALK")) prepared = e[0] == 'p' || (e[0] != 'w' && prepared);
     return prepared ? delta_chunk_entries(rows, tokens) * H * delta_operand_bytes(io_dtype, want_state ? 3 : 2, 2) : 0;
 }

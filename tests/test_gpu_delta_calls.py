@@ -83,3 +83,21 @@ def test_a_state_given_is_written(L):
     o2 = sfm.sfm_gated_delta_fwd(*t, h0=h0, l2norm=True, state=h0)
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and torch.equal(h0, want)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("walk,narrow", [("whole", "0"), ("prepared", "0"), ("prepared", "1")])
+@pytest.mark.parametrize("L", [1, 3, 12, 51, 64])
+def test_rows_of_one_chunk_by_every_plan(L, walk, narrow, io, monkeypatch):
+    """The overrides, with rows that no plan prepares."""
+    from test_gpu_gated_delta import call_fwd
+    monkeypatch.setenv("SFM_DELTA_WALK", walk)
+    monkeypatch.setenv("SFM_DELTA_NARROW", narrow)
+    lens = [L, L]
+    x = ref.delta_inputs(L, sum(lens), 2, 1, 2, 64, 48, True, io)
+    wo, wT = ref.delta(*x[:6], np.cumsum(lens), 64 ** -0.5, True)
+    for state in (True, False):
+        o, hT = call_fwd(x, lens, False, io, True, x[5], state=state)
+        ref.close(o, wo, io, "o")
+        if state:
+            ref.close(hT, wT, "f32", "state")
