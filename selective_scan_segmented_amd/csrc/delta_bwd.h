@@ -627,7 +627,7 @@ __device__ __forceinline__ void mma_all(const Parts<T, PA>& a, const Parts<T, PB
 // A workgroup to every chunk and head, sixteen tokens to a wave.  First phase: the products over values (with S0,
 // dS', U, dR of the workspace), 32 values at a time; second: those over tokens (with K and Q).
 template <typename T, int DK, int PW>
-__global__ __launch_bounds__(kDeltaThreads, (sizeof(T) == 2 ? 2 : 1)) void delta_grads_kernel(const DeltaParams p, unsigned chunks, unsigned units, int ops_bytes) {
+__global__ __launch_bounds__(kDeltaThreads, (sizeof(T) == 2 ? 2 : 1)) void delta_grads_kernel(const DeltaParams p, unsigned entries, unsigned units, int ops_bytes) {
     using Sh = ChunkShape<T, DK>;
     using L = GradLds<T, DK, PW>;
     constexpr int E = (int)sizeof(T), ND = DK / 16;
@@ -637,17 +637,11 @@ __global__ __launch_bounds__(kDeltaThreads, (sizeof(T) == 2 ? 2 : 1)) void delta
     // by token: P's row sums, the other terms of dG, c, dbeta's two halves, dR.V; P's column sums by wave; <S0, dS'>
     float *row_p = sums, *row_o = sums + kC, *row_c = sums + 2 * kC, *row_b = sums + 3 * kC, *row_e = sums + 4 * kC,
           *row_v = sums + 5 * kC, *col_p = sums + 6 * kC, *frob = sums + 10 * kC;
-    const unsigned unit = row_unit(p, blockIdx.x, units, chunks * p.H, p.share);
+    const unsigned unit = row_unit(p, blockIdx.x, units, entries / (unsigned)p.rows * p.H, p.share);
     const int h = (int)(unit % (unsigned)p.H), hk = (int)((unsigned)h / (unsigned)p.share);
-    const unsigned sc = unit / (unsigned)p.H;
-    const int s = (int)(sc / chunks);
-    int64_t first;
-    int len;
-    delta_row(p, s, first, len);
-    const int chunk = (int)(sc - s * chunks);
-    const int64_t t0 = (int64_t)chunk * kC;
-    if (t0 >= len) return;
-    const int64_t n = min((int64_t)kC, len - t0), tok = first + t0, entry = (int64_t)(chunk_entry(p, s, first) + chunk) * p.H + h;
+    ChunkAt at;
+    if (!chunk_at(p, unit / (unsigned)p.H, at)) return;
+    const int64_t n = min((int64_t)kC, at.len - at.t0), tok = at.first + at.t0, entry = unit;  // (entry and head)
     const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g4 = (lane >> 4) * 4;
     const int vals = (p.dv + 63) / 64 * 64;
 
@@ -920,17 +914,16 @@ __global__ __launch_bounds__(kDeltaThreads, (sizeof(T) == 2 ? 2 : 1)) void delta
 // Shared key heads: the value heads' shares, in order.  A workgroup to every 16 tokens of a row's 64 and key head; a
 // thread takes V neighbouring keys.
 template <typename T, int V>
-__global__ __launch_bounds__(kDeltaThreads) void delta_share_kernel(const DeltaParams p, unsigned chunks) {
+__global__ __launch_bounds__(kDeltaThreads) void delta_share_kernel(const DeltaParams p) {
     typedef float vec __attribute__((ext_vector_type(V)));
-    const unsigned sq = blockIdx.x / (unsigned)p.Hk, sc = sq / 4;
-    const int hk = (int)(blockIdx.x - sq * (unsigned)p.Hk), s = (int)(sc / chunks);
-    int64_t first;
-    int len;
-    delta_row(p, s, first, len);
-    const int64_t t0 = (int64_t)(sc - s * chunks) * kC + (sq & 3) * 16;
-    const int n = (int)min((int64_t)16, len - t0), ct = (threadIdx.x & 31) * V;
+    const unsigned sq = blockIdx.x / (unsigned)p.Hk;
+    const int hk = (int)(blockIdx.x - sq * (unsigned)p.Hk);
+    ChunkAt at;
+    if (!chunk_at(p, sq / 4, at)) return;
+    const int64_t t0 = at.t0 + (sq & 3) * 16;
+    const int n = (int)min((int64_t)16, at.len - t0), ct = (threadIdx.x & 31) * V;
     for (int t = threadIdx.x >> 5; t < n; t += kDeltaThreads / 32) {
-        const int64_t tok = first + t0 + t, from = (tok * p.H + (int64_t)hk * p.share) * p.dk, to = (tok * p.Hk + hk) * p.dk;
+        const int64_t tok = at.first + t0 + t, from = (tok * p.H + (int64_t)hk * p.share) * p.dk, to = (tok * p.Hk + hk) * p.dk;
         for (int c = ct; c < p.dk; c += 32 * V) {
             vec a, b;
 #pragma unroll
@@ -964,16 +957,16 @@ template <typename T, int DK, int P> hipError_t launch_backward(const DeltaParam
     if ((e = allow_lds(walks, wb)) != hipSuccess) return e;
     hipLaunchKernelGGL(walks, dim3(2 * units), dim3(p.narrow ? kNarrowThreads : kDeltaThreads), wb, s, p, tiles, units);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), cu = (unsigned)p.rows * chunks * p.H;
+    const unsigned entries = launch_entries(p), cu = entries * p.H;
     auto grads = delta_grads_kernel<T, DK, PW>;
     if ((e = allow_lds(grads, gb)) != hipSuccess) return e;
-    hipLaunchKernelGGL(grads, dim3(cu), dim3(kDeltaThreads), gb, s, p, chunks, cu, ChunkOperands<T, P>::bytes);
+    hipLaunchKernelGGL(grads, dim3(cu), dim3(kDeltaThreads), gb, s, p, entries, cu, ChunkOperands<T, P>::bytes);
     if ((e = hipGetLastError()) != hipSuccess || p.share == 1) return e;
-    const dim3 sg((unsigned)p.rows * chunks * 4 * p.Hk);
+    const dim3 sg(entries * 4 * p.Hk);
     if (p.dk % 4 == 0)
-        hipLaunchKernelGGL((delta_share_kernel<T, 4>), sg, dim3(kDeltaThreads), 0, s, p, chunks);
+        hipLaunchKernelGGL((delta_share_kernel<T, 4>), sg, dim3(kDeltaThreads), 0, s, p);
     else
-        hipLaunchKernelGGL((delta_share_kernel<T, 1>), sg, dim3(kDeltaThreads), 0, s, p, chunks);
+        hipLaunchKernelGGL((delta_share_kernel<T, 1>), sg, dim3(kDeltaThreads), 0, s, p);
     return hipGetLastError();
 }
 

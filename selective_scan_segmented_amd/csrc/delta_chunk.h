@@ -366,6 +366,42 @@ __device__ __forceinline__ unsigned chunk_entry(const DeltaParams& p, int s, int
     return p.offsets ? (unsigned)(first / kC) + s : (unsigned)s * ((p.L + kC - 1) / kC);
 }
 
+// The chunk that an entry holds, for the kernels that take the entries one by one: its row, that row's first token and
+// length, and where in the row it starts.  Packed rows: the last row whose first entry is not past this one, found by
+// the wave 64 rows at a time (one step to 64 rows, two to 4096).
+struct ChunkAt {
+    int s, len;
+    int64_t first, t0;
+};
+__device__ __forceinline__ bool chunk_at(const DeltaParams& p, unsigned entry, ChunkAt& at) {
+    if (!p.offsets) {
+        const unsigned chunks = (unsigned)(p.L + kC - 1) / kC;
+        at.s = (int)(entry / chunks);
+        delta_row(p, at.s, at.first, at.len);
+        at.t0 = (int64_t)(entry - (unsigned)at.s * chunks) * kC;
+        return at.t0 < at.len;
+    }
+    int lo = 0, n = p.rows;
+    for (;;) {
+        const int step = (n + 63) / 64, i = (threadIdx.x & 63) * step;
+        bool before = false;
+        if (i < n) {
+            const int64_t o = p.offsets[lo + i], first = o < 0 ? 0 : o > p.tokens ? p.tokens : o;
+            before = (unsigned)(first / kC) + (unsigned)(lo + i) <= entry;
+        }
+        const int there = __builtin_popcountll(__ballot(before));
+        if (there == 0) return false;  // (tokens before the first row)
+        const int at_lane = (there - 1) * step;
+        lo += at_lane;
+        n = min(step, n - at_lane);
+        if (step == 1) break;
+    }
+    at.s = lo;
+    delta_row(p, at.s, at.first, at.len);
+    at.t0 = ((int64_t)entry - (int64_t)chunk_entry(p, at.s, at.first)) * kC;
+    return at.t0 >= 0 && at.t0 < at.len;  // (a row leaves up to one entry free)
+}
+
 // What the preparing kernel leaves of a chunk and head: the row scalars, T and A (P parts each).
 template <typename T, int P, int PA = P> struct ChunkOperands {
     static constexpr int frag_bytes = kLowerFrags * kFragSize * (int)sizeof(T);

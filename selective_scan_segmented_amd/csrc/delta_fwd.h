@@ -275,31 +275,26 @@ template <typename T, int DK> struct PrepareLds {
 // 128 over 8: 53 us, 60 with a workgroup to each).
 template <typename T, int DK, int P, int PA, bool ALL>
 __global__ __launch_bounds__(kDeltaThreads, (PrepareLds<T, DK>::groups))
-void delta_prepare_kernel(const DeltaParams p, unsigned chunks, unsigned units) {
+void delta_prepare_kernel(const DeltaParams p, unsigned entries, unsigned units) {
     using L = PrepareLds<T, DK>;
     using Ops = ChunkOperands<T, P, PA>;
     constexpr int E = (int)sizeof(T);
     extern __shared__ char lds[];
     ChunkRows* rows = reinterpret_cast<ChunkRows*>(lds + L::rows);
     T *ks = reinterpret_cast<T*>(lds + L::ks), *qs = reinterpret_cast<T*>(lds + L::qs);
-    const unsigned heads = ALL ? p.share : 1, groups = (unsigned)p.H / heads, unit = row_unit(p, blockIdx.x, units, chunks * groups, p.share / heads),
-                   sc = unit / groups;
-    const int h = (int)((unit - sc * groups) * heads), hk = (int)((unsigned)h / (unsigned)p.share);
-    const int s = (int)(sc / chunks);
-    int64_t first;
-    int len;
-    delta_row(p, s, first, len);
-    const int64_t t0 = (int64_t)(sc - s * chunks) * kC;
-    if (t0 >= len) return;
-    const int64_t n = min((int64_t)kC, len - t0);
-    first += t0;
+    const unsigned heads = ALL ? p.share : 1, groups = (unsigned)p.H / heads,
+                   unit = row_unit(p, blockIdx.x, units, entries / (unsigned)p.rows * groups, p.share / heads), entry = unit / groups;
+    const int h = (int)((unit - entry * groups) * heads), hk = (int)((unsigned)h / (unsigned)p.share);
+    ChunkAt at;
+    if (!chunk_at(p, entry, at)) return;
+    const int64_t n = min((int64_t)kC, at.len - at.t0), first = at.first + at.t0;
     const T *gp = static_cast<const T*>(p.g) + first * p.H + h, *bp = static_cast<const T*>(p.beta) + first * p.H + h;
     ChunkGates gates;
     gates.load(gp, bp, p.H, (int)n);
     RowShare<T, DK> kr, qr;
     kr.load(make_buf(static_cast<const T*>(p.k) + first * p.ldk + (int64_t)hk * p.dk, n * p.ldk * E), p.ldk, p.dk, p.vec_k);
     qr.load(make_buf(static_cast<const T*>(p.q) + first * p.ldq + (int64_t)hk * p.dk, n * p.ldq * E), p.ldq, p.dk, p.vec_k);
-    char* o = p.w_ops + ((int64_t)(chunk_entry(p, s, first - t0) + (unsigned)(t0 / kC)) * p.H + h) * Ops::bytes;
+    char* o = p.w_ops + ((int64_t)entry * p.H + h) * Ops::bytes;
     float* mt = reinterpret_cast<float*>(lds + L::mt);
     f32x4 c[5], a[3], t[4];
     start_chunk<T, DK>(kr, qr, gates, p, rows, ks, qs, c);
@@ -338,15 +333,22 @@ template <typename T, int DK, int P, Walk W> hipError_t launch_walk(const DeltaP
     return hipGetLastError();
 }
 
+// The entries that hold a chunk, or may: launches of a workgroup to each are of this size.  Packed rows: by their
+// tokens, since L only bounds the longest (256 rows of 200 tokens or fewer, 8 heads of 64, L all their tokens: 113 us
+// forward, 790 with a workgroup to every row and chunk of L; the backward 460, 2093).
+inline unsigned launch_entries(const DeltaParams& p) {
+    return p.offsets ? (unsigned)delta_chunk_entries(p.rows, p.tokens) : (unsigned)p.rows * (unsigned)((p.L + kC - 1) / kC);
+}
+
 template <typename T, int DK, int P, int PA> hipError_t launch_prepare(const DeltaParams& p, hipStream_t s) {
-    const unsigned chunks = (unsigned)((p.L + kC - 1) / kC), groups = (unsigned)p.rows * chunks * p.Hk;
+    const unsigned entries = launch_entries(p), groups = entries * p.Hk;
     const bool all = p.share > 1 && groups >= 256;  // (where that leaves every compute unit one)
     auto kern = all ? delta_prepare_kernel<T, DK, P, PA, true> : delta_prepare_kernel<T, DK, P, PA, false>;
     constexpr int bytes = PrepareLds<T, DK>::bytes;
     const hipError_t e = allow_lds(kern, bytes);
     if (e != hipSuccess) return e;
     const unsigned units = all ? groups : groups * p.share;
-    hipLaunchKernelGGL(kern, dim3(units), dim3(kDeltaThreads), bytes, s, p, chunks, units);
+    hipLaunchKernelGGL(kern, dim3(units), dim3(kDeltaThreads), bytes, s, p, entries, units);
     return hipGetLastError();
 }
 
