@@ -366,7 +366,8 @@ sfm_status sfm_scan_plan_string(int64_t B1, int64_t B2, int64_t D, int64_t N, in
  *            L of them (L bounds the longest row; offsets outside the tokens are
  *            cut to them, tokens of no row and those past L keep their old o)
  *   H must be a multiple of Hk: value head h uses key head h / (H / Hk).
- *   dk 1..128, dv 1..256.  Tensors need their element's alignment only; rows on
+ *   dk 1..128, dv 1..256; rows * H * ceil(dv / 64) below 2^24 (a launch holds fewer
+ *   than 2^32 work items).  Tensors need their element's alignment only; rows on
  *   16 bytes are loaded 16 bytes at a time.
  *   flags & SFM_DELTA_L2NORM: q and k are divided by sqrt(sum of squares + 1e-6)
  *            of their head first.
@@ -401,8 +402,10 @@ sfm_status sfm_gated_delta_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, 
  *   dh0 [rows, H, dk, dv] f32 or NULL (not wanted).  Tokens of no row keep their old
  *   gradients.  workspace: at least sfm_gated_delta_bwd_ws_size() bytes (want_dh0:
  *   dh0 != NULL), 16-byte aligned: for every 64 tokens of a row and head the states
- *   before them, their gradients after them and what passes between them.  No
- *   atomics: repeated calls give the same bits.
+ *   before them, their gradients after them and what passes between them.  Twice the
+ *   workgroups above, and (tokens / 64 + rows) * H (with shared heads the larger of
+ *   that and 4 Hk a chunk), have to stay below 2^24.  No atomics: repeated calls give
+ *   the same bits.
  */
 sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                                const float* h0, const void* dout, const float* dhT, void* dq, void* dk_out,

@@ -9,7 +9,7 @@ namespace sfm {
 constexpr int kDeltaChunk = 64;        // tokens to a chunk of the chunked kernels
 constexpr int kDeltaMaxK = 128;        // largest key head
 constexpr int kDeltaMaxV = 256;        // largest value head
-constexpr int64_t kDeltaMaxUnits = 1LL << 28;  // rows x heads (each is at most four workgroups wide)
+constexpr int64_t kDeltaMaxGroups = (1LL << 24) - 1;  // workgroups of 256 to a launch, which holds fewer than 2^32 work items
 
 // One call's rows, heads and strides (forward, backward and the token-by-token form).
 struct DeltaParams {
@@ -64,7 +64,7 @@ constexpr float kDeltaNormEps = 1e-6f;
 constexpr float kDeltaMinGate = -110.0f;
 
 // Workspace of the chunked forward in bytes: 0 where a chunk's T and A are made on the way (delta_fwd.h).
-bool plan_delta_narrow(int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back);
+bool plan_delta_narrow(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back);
 int64_t plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype);
 // entries of the arrays that hold something for every chunk (chunk_entry): enough for packed and for equal rows
 inline int64_t delta_chunk_entries(int64_t rows, int64_t tokens) { return tokens / kDeltaChunk + rows; }

@@ -16,7 +16,7 @@ bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t
 
 // Sizes, strides and types every entry point of the rule shares.
 sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, bool packed, int64_t Hk, int64_t H,
-                       int64_t dk, int64_t dv, int io_dtype, int flags) {
+                       int64_t dk, int64_t dv, int io_dtype, int flags, bool back) {
     if (io_dtype != SFM_F32 && io_dtype != SFM_BF16) return fail(SFM_ERR_DTYPE, "%s: io_dtype %d", fn, io_dtype);
     if (flags & ~SFM_DELTA_L2NORM) return fail(SFM_ERR_SHAPE, "%s: unknown flags 0x%x", fn, flags);
     if (!sane(rows, 1 << 24) || !sane(L, 1 << 24) || tokens < 0 || tokens > (1LL << 31) - 1)
@@ -31,8 +31,12 @@ sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, 
         return fail(SFM_ERR_SHAPE, "%s: head sizes dk=%lld (1 to %d), dv=%lld (1 to %d)", fn, (long long)dk,
                     sfm::kDeltaMaxK, (long long)dv, sfm::kDeltaMaxV);
     const int64_t widest = dk > dv ? dk : dv;
-    if (tokens * H > (1LL << 40) / widest || rows * H > sfm::kDeltaMaxUnits)
-        return fail(SFM_ERR_SHAPE, "%s: tensor too large", fn);
+    if (tokens * H > (1LL << 40) / widest) return fail(SFM_ERR_SHAPE, "%s: tensor too large", fn);
+    // the largest launches that no plan avoids: the walks, and the backward's by chunk and head (shared heads: four to one)
+    const int64_t walks = rows * H * ((dv + 63) / 64) * (back ? 2 : 1), heads = H != Hk && 4 * Hk > H ? 4 * Hk : H;
+    if (walks > sfm::kDeltaMaxGroups || (back && sfm::delta_chunk_entries(rows, tokens) * heads > sfm::kDeltaMaxGroups))
+        return fail(SFM_ERR_SHAPE, "%s: rows=%lld tokens=%lld with %lld heads are more workgroups than a launch holds", fn,
+                    (long long)rows, (long long)tokens, (long long)H);
     return SFM_OK;
 }
 
@@ -112,8 +116,8 @@ static int64_t delta_units(int64_t L, int64_t tokens, int64_t H, int64_t dv) { r
 // SFM_DELTA_WALK=whole|prepared overrides (tuning and tests).
 int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype) {
     const int64_t chunks = (L + kDeltaChunk - 1) / kDeltaChunk;
-    if (rows * H > INT32_MAX / chunks) return 0;
     if (chunks < 2) return 0;  // (nothing to walk, whatever the override says)
+    if (delta_chunk_entries(rows, tokens) * H > kDeltaMaxGroups) return 0;  // (more than one launch can prepare)
     const int64_t most = chunks < 3 ? 128 : (dv + 63) / 64 > (dk + 63) / 64 ? 512 : dv <= 32 ? 384 : 256;
     bool prepared = delta_units(L, tokens, H, dv) <= most;
     if (const char* e = std::getenv("SFM_DELTA_WALK")) prepared = e[0] == 'p' || (e[0] != 'w' && prepared);
@@ -129,11 +133,13 @@ int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, 
 // With up to 32 values half of the 64 columns are nobody's, and few are faster at any number: 64 x 32, 1024 tokens, 92 /
 // 69 us for 240 rows and heads, 190 / 182 us for 512; backward 281 / 239 us, 545 / 492 us.
 // SFM_DELTA_NARROW=0|1 overrides (tuning and tests).
-bool sfm::plan_delta_narrow(int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back) {
+bool sfm::plan_delta_narrow(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back) {
+    const bool few = dk <= 64;
+    const int64_t cols = few ? 32 : 16;
+    if (rows * H * ((dv + 31) / 32 * (32 / cols)) * (back ? 4 : 2) > kDeltaMaxGroups) return false;  // (workgroups of 512)
     if (const char* e = std::getenv("SFM_DELTA_NARROW")) return e[0] == '1';
     if (dv <= 32) return true;
-    const bool few = dk <= 64;
-    const int64_t cols = few ? 32 : 16, groups = tokens * H * ((dv + cols - 1) / cols) / L;
+    const int64_t groups = tokens * H * ((dv + cols - 1) / cols) / L;
     return groups <= (back ? (few ? 128 : 256) : few && io_dtype == 0 ? 256 : 512);
 }
 
@@ -144,7 +150,7 @@ sfm_status sfm_gated_delta_step(const void* q, const void* k, const void* v, con
                                 int64_t H, int64_t dk, int64_t dv, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
                                 int io_dtype, int flags, void* stream) {
     static const char* fn = "sfm_gated_delta_step";
-    sfm_status st = check_sizes(fn, rows, 1, rows, false, Hk, H, dk, dv, io_dtype, flags);
+    sfm_status st = check_sizes(fn, rows, 1, rows, false, Hk, H, dk, dv, io_dtype, flags, false);
     if (st != SFM_OK) return st;
     st = check_inputs(fn, q, k, v, g, beta, rows, Hk, H, dk, dv, ldq, ldk, ldv, io_dtype);
     if (st != SFM_OK) return st;
@@ -173,7 +179,7 @@ sfm_status sfm_gated_delta_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, 
                                        int want_state, int io_dtype, int64_t* bytes) {
     static const char* fn = "sfm_gated_delta_fwd_ws_size";
     if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
-    const sfm_status st = check_sizes(fn, rows, L, tokens, true, 1, H, dk, dv, io_dtype, 0);
+    const sfm_status st = check_sizes(fn, rows, L, tokens, true, 1, H, dk, dv, io_dtype, 0, false);
     if (st != SFM_OK) return st;
     *bytes = sfm::plan_delta_fwd(rows, L, tokens, H, dk, dv, want_state != 0, io_dtype);
     return ok();
@@ -185,7 +191,7 @@ sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
                                int64_t ldk, int64_t ldv, float scale, int io_dtype, int flags, void* workspace,
                                int64_t workspace_bytes, void* stream) {
     static const char* fn = "sfm_gated_delta_fwd";
-    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, Hk, H, dk, dv, io_dtype, flags);
+    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, Hk, H, dk, dv, io_dtype, flags, false);
     if (st != SFM_OK) return st;
     st = check_inputs(fn, q, k, v, g, beta, tokens, Hk, H, dk, dv, ldq, ldk, ldv, io_dtype);
     if (st != SFM_OK) return st;
@@ -220,7 +226,7 @@ sfm_status sfm_gated_delta_fwd(const void* q, const void* k, const void* v, cons
     sfm::DeltaParams p = params(q, k, v, g, beta, rows, L, tokens, Hk, H, dk, dv, ldq, ldk, ldv, scale, flags, io_dtype);
     p.h0 = h0, p.hT = hT, p.offsets = offsets, p.o = o;
     p.w_ops = need > 0 ? static_cast<char*>(workspace) : nullptr;
-    p.narrow = sfm::plan_delta_narrow(L, tokens, H, dk, dv, io_dtype, false);
+    p.narrow = sfm::plan_delta_narrow(rows, L, tokens, H, dk, dv, io_dtype, false);
     p.vec_s = dv % 4 == 0 && aligned16(h0) && aligned16(hT);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     if (L <= recurrent_most(io_dtype, h0 || hT)) return hip_status(sfm::launch_delta_recurrent(p, io_dtype, hs), fn);
@@ -258,7 +264,7 @@ sfm_status sfm_gated_delta_bwd_ws_size(int64_t rows, int64_t L, int64_t tokens, 
                                        int64_t dv, int want_dh0, int io_dtype, int64_t* bytes) {
     static const char* fn = "sfm_gated_delta_bwd_ws_size";
     if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
-    const sfm_status st = check_sizes(fn, rows, L, tokens, true, Hk, H, dk, dv, io_dtype, 0);
+    const sfm_status st = check_sizes(fn, rows, L, tokens, true, Hk, H, dk, dv, io_dtype, 0, true);
     if (st != SFM_OK) return st;
     *bytes = bwd_regions(rows, tokens, H, H != Hk, dk, dv, want_dh0 != 0, io_dtype).bytes;
     return ok();
@@ -271,14 +277,12 @@ sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
                                int64_t ldk, int64_t ldv, float scale, int io_dtype, int flags, void* workspace,
                                int64_t workspace_bytes, void* stream) {
     static const char* fn = "sfm_gated_delta_bwd";
-    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, Hk, H, dk, dv, io_dtype, flags);
+    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, Hk, H, dk, dv, io_dtype, flags, true);
     if (st != SFM_OK) return st;
     st = check_inputs(fn, q, k, v, g, beta, tokens, Hk, H, dk, dv, ldq, ldk, ldv, io_dtype);
     if (st != SFM_OK) return st;
     if (tokens > 0 && (!dout || !dq || !dk_out || !dv_out || !dg || !dbeta))
         return fail(SFM_ERR_NULL, "%s: dout, dq, dk, dv, dg and dbeta are required", fn);
-    if (rows * H > INT32_MAX / 4 / ((L + sfm::kDeltaChunk - 1) / sfm::kDeltaChunk))
-        return fail(SFM_ERR_SHAPE, "%s: too many chunks", fn);
     const int e = io_bytes(io_dtype);
     for (const void* x : {(const void*)dout, (const void*)dq, (const void*)dk_out, (const void*)dv_out, (const void*)dg,
                           (const void*)dbeta})
@@ -317,7 +321,7 @@ sfm_status sfm_gated_delta_bwd(const void* q, const void* k, const void* v, cons
     p.w_ops = ws + w.ops, p.w_s = ws + w.s, p.w_ds = ws + w.ds, p.w_u = ws + w.u, p.w_dr = ws + w.dr;
     p.w_dq = reinterpret_cast<float*>(ws + w.dq), p.w_dk = reinterpret_cast<float*>(ws + w.dk);
     p.vec_o = aligned16(dout) && dv * e % 16 == 0;
-    p.narrow = sfm::plan_delta_narrow(L, tokens, H, dk, dv, io_dtype, true);
+    p.narrow = sfm::plan_delta_narrow(rows, L, tokens, H, dk, dv, io_dtype, true);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     return hip_status(io_dtype == SFM_F32 ? sfm::launch_delta_bwd_f32(p, hs) : sfm::launch_delta_bwd_bf16(p, hs), fn);
 }
