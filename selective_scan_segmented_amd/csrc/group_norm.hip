@@ -21,6 +21,8 @@
 //   16 x 12544 x 160 bfloat16, 32 groups: 49 us for 192 MB (16 sums, 4 join, 28 apply); backward at 4 x 12544 x 320
 //   float32: 72 us for 321 MB (30, 5, 34, 4 the weights').
 // Sums are float32 in a fixed order: repeated calls give the same bits.
+#include <algorithm>
+
 #include "delta_mma.h"
 #include "sfm_norm.h"
 
@@ -614,37 +616,54 @@ hipError_t launch_slab(const NormParams& p, bool bwd, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The launches of one part of a call's samples.
+template <typename T, int V>
+hipError_t launch_samples(const NormParams& p, bool bwd, hipStream_t s) {
+    if (p.slab)
+        return p.threads > 512   ? launch_slab<T, V, 8, 1024>(p, bwd, s)
+               : p.threads > 256 ? launch_slab<T, V, 8, 512>(p, bwd, s)
+               : p.units <= 1    ? launch_slab<T, V, 1, 256>(p, bwd, s)
+               : p.units <= 2    ? launch_slab<T, V, 2, 256>(p, bwd, s)
+               : p.units <= 4    ? launch_slab<T, V, 4, 256>(p, bwd, s)
+                                 : launch_slab<T, V, 8, 256>(p, bwd, s);
+    const dim3 grid((unsigned)(p.N * p.splits * p.tiles));
+    // the last tile may be narrower and so have more slots; slots x channels never exceeds threads x V
+    const size_t lds = ((size_t)2 * p.threads * V + p.threads) * 4;
+    const unsigned jt = (unsigned)((p.C + 15) / 16);
+    const size_t glds = ((size_t)2 * (p.tunits * V / p.cg + 2)) * 4;
+    hipLaunchKernelGGL((bwd ? norm_sums_kernel<T, V, true> : norm_sums_kernel<T, V, false>), grid, dim3(p.threads), lds, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (p.splits > 1) {  // (one range's sums are the sample's)
+        hipLaunchKernelGGL((bwd ? norm_join_kernel<true> : norm_join_kernel<false>), dim3((unsigned)p.N * jt), dim3(256), 0, s, p, jt);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((bwd ? norm_apply_kernel<T, V, true> : norm_apply_kernel<T, V, false>), grid, dim3(p.threads), glds, s, p);
+    return hipGetLastError();
+}
+
 template <typename T, int V>
 hipError_t launch_v(const NormParams& p, bool bwd, hipStream_t s) {
-    hipError_t e;
-    if (p.slab) {
-        e = p.threads > 512   ? launch_slab<T, V, 8, 1024>(p, bwd, s)
-            : p.threads > 256 ? launch_slab<T, V, 8, 512>(p, bwd, s)
-            : p.units <= 1    ? launch_slab<T, V, 1, 256>(p, bwd, s)
-            : p.units <= 2    ? launch_slab<T, V, 2, 256>(p, bwd, s)
-            : p.units <= 4    ? launch_slab<T, V, 4, 256>(p, bwd, s)
-                              : launch_slab<T, V, 8, 256>(p, bwd, s);
-    } else {
-        const dim3 grid((unsigned)(p.N * p.splits * p.tiles));
-        // the last tile may be narrower and so have more slots; slots x channels never exceeds threads x V
-        const size_t lds = ((size_t)2 * p.threads * V + p.threads) * 4;
-        const unsigned jt = (unsigned)((p.C + 15) / 16);
-        const dim3 jgrid((unsigned)p.N * jt);
-        const size_t glds = ((size_t)2 * (p.tunits * V / p.cg + 2)) * 4;
-        if (bwd) {
-            hipLaunchKernelGGL((norm_sums_kernel<T, V, true>), grid, dim3(p.threads), lds, s, p);
-            hipLaunchKernelGGL((norm_join_kernel<true>), jgrid, dim3(256), 0, s, p, jt);
-            hipLaunchKernelGGL((norm_apply_kernel<T, V, true>), grid, dim3(p.threads), glds, s, p);
-        } else {
-            hipLaunchKernelGGL((norm_sums_kernel<T, V, false>), grid, dim3(p.threads), lds, s, p);
-            hipLaunchKernelGGL((norm_join_kernel<false>), jgrid, dim3(256), 0, s, p, jt);
-            hipLaunchKernelGGL((norm_apply_kernel<T, V, false>), grid, dim3(p.threads), glds, s, p);
-        }
-        e = hipGetLastError();
+    // A launch holds fewer than 2^32 work items: so many samples to one (2^20 tokens of 4096 channels in 64 groups, each
+    // normed by itself, are 2^26 workgroups of 64).
+    const int64_t wide = p.slab ? p.runs : std::max((int64_t)p.splits * p.tiles, (int64_t)(p.C + 15) / 16);
+    const int64_t most = ((1LL << 32) - 1) / (p.slab ? p.threads : 256) / wide;
+    const int64_t sums = 2 * (int64_t)p.C * (p.slab ? 1 : p.splits);  // floats a sample leaves in the workspace
+    hipError_t e = hipSuccess;
+    for (int64_t n = 0; n < p.N && e == hipSuccess; n += most) {
+        NormParams q = p;
+        const int64_t at = n * p.L * p.C * (int64_t)sizeof(T);
+        q.x = static_cast<const char*>(p.x) + at;
+        if (p.dy) q.dy = static_cast<const char*>(p.dy) + at;
+        q.y = static_cast<char*>(p.y) + at;
+        q.mean += n * p.G;
+        q.rstd += n * p.G;
+        if (p.part) q.part += n * sums;
+        q.N = std::min(p.N - n, most);
+        e = launch_samples<T, V>(q, bwd, s);
     }
     if (e != hipSuccess || !bwd || !(p.dw || p.db)) return e;
-    hipLaunchKernelGGL(norm_weights_kernel, dim3((unsigned)((p.C + 15) / 16)), dim3(1024), 0, s, p,
-                       2 * (int64_t)p.C * (p.slab ? 1 : p.splits));
+    hipLaunchKernelGGL(norm_weights_kernel, dim3((unsigned)((p.C + 15) / 16)), dim3(1024), 0, s, p, sums);
     return hipGetLastError();
 }
 
