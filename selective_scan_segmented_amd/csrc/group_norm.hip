@@ -158,8 +158,8 @@ __global__ __launch_bounds__(THREADS, 4) void norm_slab_fwd_kernel(const NormPar
         const float mean = wave_sum(v) / total;  // (a division: a constant group's mean is exact)
         v = 0.0f;
         each_entry(slots, eg, g, [&](int k, int e) {
-            const float d = lm[k * ew + e] - mean;
-            v += __builtin_fmaf(d * d, lr[k], lq[k * ew + e]);
+            const float n = lr[k], d = lm[k * ew + e] - mean;
+            v += __builtin_fmaf(d * n, d, lq[k * ew + e]);  // (in this order: a slot without rows adds 0 whatever the mean)
         });
         const float rstd = 1.0f / __builtin_sqrtf(wave_sum(v) / total + p.eps);
         if ((threadIdx.x & 63) == 0) {
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormParams p) {
                 }
                 const float d = m - s1[j];
                 s1[j] = __builtin_fmaf(d, part, s1[j]);
-                s2[j] += __builtin_fmaf(d * d, join, q);
+                s2[j] += __builtin_fmaf(d * join, d, q);  // (in this order: 0 for the first batch, also where d * d overflows)
             }
             count = all;
         }
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const NormParams p, unsi
             } else {
                 const float rows = (float)min(p.L - i * p.srows, p.srows), d = m - a;
                 a = __builtin_fmaf(d, rows / (count + rows), a);
-                q += t + d * d * (count * rows / (count + rows));
+                q += t + d * (count * rows / (count + rows)) * d;  // (0 for the first range)
                 count += rows;
             }
         }
