@@ -611,7 +611,7 @@ template <int PW, typename T> __device__ __forceinline__ Parts<T, PW> load_block
     return a;
 }
 
-// c += a b for single accumulators (mma_parts with no waits between like products is the caller's order)
+// c[n] += a b[n], the products of parts as in mma_lower
 template <int PA, int PB, int N, typename T>
 __device__ __forceinline__ void mma_all(const Parts<T, PA>& a, const Parts<T, PB> (&b)[N], f32x4* c) {
     constexpr int top = PA > PB ? PA : PB;

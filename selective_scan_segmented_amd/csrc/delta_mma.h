@@ -199,21 +199,9 @@ template <int P, typename T> __device__ __forceinline__ void store_tile(f32x4 x,
     }
 }
 
-// c += a b, a given by its PA parts and b by its PB: the products of parts that are not below the last part of the
-// finer operand, smallest first
-template <int PA, int PB, typename T>
-__device__ __forceinline__ f32x4 mma_parts(const Parts<T, PA>& a, const Parts<T, PB>& b, f32x4 c) {
-    constexpr int top = PA > PB ? PA : PB;
-#pragma unroll
-    for (int p = PA - 1; p >= 0; --p)
-#pragma unroll
-        for (int q = PB - 1; q >= 0; --q)
-            if (p + q < top) c = mma(a.p[p], b.p[q], c);
-    return c;
-}
-
-// c[rt] += the step kb of 32 columns of a lower triangular operand (its fragments' parts) times b; products of like
-// size follow one another, so that no accumulator waits for itself
+// c[rt] += the step kb of 32 columns of a lower triangular operand (its fragments' parts) times b: the products of parts
+// that are not below the last part of the finer operand, smallest first; those of like size follow one another, so that
+// no accumulator waits for itself
 template <int PA, int PB, typename T>
 __device__ __forceinline__ void mma_lower(const Parts<T, PA> (&a)[kLowerFrags], const Parts<T, PB>& b, int kb, f32x4 (&c)[4]) {
     constexpr int top = PA > PB ? PA : PB;
