@@ -364,7 +364,9 @@ sfm_status sfm_scan_plan_string(int64_t B1, int64_t B2, int64_t D, int64_t N, in
  *            else int32 [rows + 1] on the device, rising from 0 to tokens: row r
  *            is tokens offsets[r] .. offsets[r + 1] - 1 (possibly none), at most
  *            L of them (L bounds the longest row; offsets outside the tokens are
- *            cut to them, tokens of no row and those past L keep their old o)
+ *            cut to them, tokens of no row and those past L keep their old o).  An L
+ *            of all the tokens is taken as no bound, and how the rows are walked then
+ *            goes by four times their average length
  *   H must be a multiple of Hk: value head h uses key head h / (H / Hk).
  *   dk 1..128, dv 1..256; rows * H * ceil(dv / 64) below 2^24 (a launch holds fewer
  *   than 2^32 work items).  Tensors need their element's alignment only; rows on

@@ -538,7 +538,8 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
 
     q, k: [B, L, Hk, dk]; v: [B, L, H, dv]; g (log decay), beta: [B, L, H]; float32 or bfloat16.
     h0: [B, H, dk, dv] float32 states before the rows, or None.  offsets (int32 [rows + 1] on the
-    GPU): packed rows, tensors [1, tokens, ...]; max_len bounds the longest row.  scale defaults to
+    GPU): packed rows, tensors [1, tokens, ...]; max_len bounds the longest row (None: unknown, and planned as
+    no more than four times the average: give it where one row is far longer).  scale defaults to
     dk ** -0.5; l2norm divides q and k by their length.  Returns o [B, L, H, dv], and with
     return_state the states after the rows.  `state`, if given, takes those in either case (h0
     itself is allowed)."""

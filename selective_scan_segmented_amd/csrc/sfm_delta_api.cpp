@@ -99,6 +99,16 @@ sfm::DeltaParams params(const void* q, const void* k, const void* v, const void*
 
 }  // namespace
 
+// The longest row as the plans see it: L, or where L says nothing of it (packed rows, all the tokens or more) at most
+// four times their average.  With L all the tokens, planned by this / by L: 1000 rows to 400 tokens, 16 heads of 128:
+// 2440 us, no workspace / 3290 us, 1.8 GB; 256 rows to 200 tokens, 8 heads of 64: 77 / 113 us; their backwards 10.9 /
+// 15.5 ms, 357 / 460 us.  Against that, one row of 16384 among 200 of 100 (16 heads of 64) or of 50000 among 1000 of 50
+// (128) takes 3 times what it does with its length in L: 1960 / 630 us, 7.6 / 2.6 ms.
+static int64_t delta_longest(int64_t rows, int64_t L, int64_t tokens) {
+    const int64_t four = (4 * tokens + rows - 1) / rows;
+    return L < tokens || four >= L ? L : four < 1 ? 1 : four;
+}
+
 // Workgroups of 64 value columns that rows of the longest one's length would make of all the tokens: what a launch
 // has to fill the card with, and keeps filling it with, also where packed rows differ.
 static int64_t delta_units(int64_t L, int64_t tokens, int64_t H, int64_t dv) { return tokens * H * ((dv + 63) / 64) / L; }
@@ -115,6 +125,7 @@ static int64_t delta_units(int64_t L, int64_t tokens, int64_t H, int64_t dv) { r
 //     two chunks, 64 x 64: 18 / 19 us for 128, 17 / 21 us for 256 (float32: 23 / 22 us, 24 / 28 us).
 // SFM_DELTA_WALK=whole|prepared overrides (tuning and tests).
 int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, bool want_state, int io_dtype) {
+    L = delta_longest(rows, L, tokens);
     const int64_t chunks = (L + kDeltaChunk - 1) / kDeltaChunk;
     if (chunks < 2) return 0;  // (nothing to walk, whatever the override says)
     if (delta_chunk_entries(rows, tokens) * H > kDeltaMaxGroups) return 0;  // (more than one launch can prepare)
@@ -134,6 +145,7 @@ int64_t sfm::plan_delta_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t H, 
 // 69 us for 240 rows and heads, 190 / 182 us for 512; backward 281 / 239 us, 545 / 492 us.
 // SFM_DELTA_NARROW=0|1 overrides (tuning and tests).
 bool sfm::plan_delta_narrow(int64_t rows, int64_t L, int64_t tokens, int64_t H, int64_t dk, int64_t dv, int io_dtype, bool back) {
+    L = delta_longest(rows, L, tokens);
     const bool few = dk <= 64;
     const int64_t cols = few ? 32 : 16;
     if (rows * H * ((dv + 31) / 32 * (32 / cols)) * (back ? 4 : 2) > kDeltaMaxGroups) return false;  // (workgroups of 512)

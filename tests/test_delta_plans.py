@@ -53,3 +53,15 @@ def test_the_calls_refuse_what_the_queries_refuse():
     assert b"more workgroups than a launch holds" in lib.sfm_last_error()
     assert lib.sfm_gated_delta_step(*args, 6 * P, None, 9 * P, rows, rows, 1, 16, 64, 64, 64, 64, 1024, *tail, None) == 2
     assert b"more workgroups than a launch holds" in lib.sfm_last_error()
+
+
+def test_rows_without_a_bound_are_planned_by_their_average():
+    """L of all the tokens says nothing of the longest row: many short rows need no workspace then either."""
+    f = sfm.sfm_gated_delta_fwd_ws_size
+    assert f(1000, 400, 200000, 16, 128, 128) == 0
+    assert f(1000, 200000, 200000, 16, 128, 128) == 0
+    assert f(1000, 1 << 20, 200000, 16, 128, 128) == 0
+    # few rows, or one among a few that may hold all the tokens: as by the bound
+    for rows in (1, 2, 4, 8):
+        assert f(rows, 20000, 20000, 16, 128, 128) > 0
+    assert f(64, 64, 0, 16, 128, 128) == f(64, 1, 0, 16, 128, 128) == 0
