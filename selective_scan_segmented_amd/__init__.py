@@ -518,8 +518,10 @@ def _rows(lead, offsets, max_len):
     _dev(offsets, "offsets", torch.int32)
     if offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets must be int32 [rows + 1]")
-    # (rows that are all empty: their longest, a bound, is taken as 1)
-    return offsets.numel() - 1, max(1, lead[1] if max_len is None else int(max_len)), lead[1]
+    L = lead[1] if max_len is None else int(max_len)
+    if L == 0 and lead[1] == 0:
+        L = 1  # (rows that are all empty: the longest's bound, which has to be positive)
+    return offsets.numel() - 1, L, lead[1]
 
 
 def sfm_gated_delta_fwd_ws_size(rows: int, L: int, tokens: int, H: int, dk: int, dv: int, want_state: bool = False,

@@ -183,3 +183,11 @@ def test_a_state_given_is_written(calls, given, asked):
 def test_a_wrong_state_is_refused(calls):
     with pytest.raises(ValueError, match="state"):
         sfm.sfm_gated_delta_fwd(*args(), o=Stub(B, L, H, DV), state=Stub(1, H, DK, DV, dtype=torch.float32), stream=SIDE)
+
+
+@pytest.mark.parametrize("tokens,max_len", [(0, -1), (0, -5), (7, 0), (7, -1)])
+def test_a_bound_that_is_none_goes_to_the_library(calls, tokens, max_len):
+    """Only rows without a token are taken as rows of one at most: other bounds below 1 are the library's to refuse."""
+    sfm.sfm_gated_delta_fwd(*args((1, tokens)), offsets=Stub(4, dtype=torch.int32), max_len=max_len, o=Stub(1, tokens, H, DV), stream=SIDE)
+    (name, a), = calls
+    assert name == "sfm_gated_delta_fwd" and a[9:12] == (3, max_len, tokens)
