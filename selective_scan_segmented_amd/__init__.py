@@ -178,6 +178,15 @@ def _new(shape, dtype, device, stream):
     return t
 
 
+def _scratch(size, device, stream):
+    """A workspace for a call on `stream`: from its pool, and nothing that the caller has on another one."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
 def _new_like(t, stream):
     """_new of a contiguous tensor's shape and type, in less host time."""
     return _torch().empty_like(t) if stream is None else _new(t.shape, t.dtype, t.device, stream)
@@ -256,7 +265,7 @@ def _fwd_ex(u, delta, A, Bm, Cm, Dskip, delta_bias, delta_softplus, conv_w, conv
         need = sfm_selective_scan_fwd_ws_size(B // B2, B2, D, N, L, K, "bf16" if io == SFM_BF16 else "f32",
                                               int(flags))
         if workspace is None:
-            workspace = _new(max(need, 16), torch.uint8, u.device, stream)
+            workspace = _scratch(max(need, 16), u.device, stream)
         _dev(workspace, "workspace")
         rc = load_library().sfm_selective_scan_fwd_ws(*args, _ptr(workspace),
                                                       workspace.numel() * workspace.element_size(),
@@ -362,7 +371,7 @@ def sfm_selective_scan_bwd(u, delta, A, Bm, Cm, dy, Dskip=None, delta_bias=None,
     need = sfm_selective_scan_bwd_workspace_size(B // B2, B2, D, N, L, K, "bf16" if io == SFM_BF16 else "f32",
                                                  flags)
     if workspace is None:
-        workspace = _new(max(need, 16), torch.uint8, u.device, stream)
+        workspace = _scratch(max(need, 16), u.device, stream)
     _dev(workspace, "workspace")
     rc = load_library().sfm_selective_scan_bwd(
         _ptr(u), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(delta_bias), int(bool(delta_softplus)),
@@ -559,7 +568,7 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
         state = _new((rows, H, dk, dv), torch.float32, q.device, stream)
     need = 0 if L <= 64 else sfm_gated_delta_fwd_ws_size(rows, L, tokens, H, dk, dv, state is not None, "bf16" if io else "f32")
     if workspace is None and need:
-        workspace = _new(need, torch.uint8, q.device, stream)
+        workspace = _scratch(need, q.device, stream)
     _dev(workspace, "workspace")
     rc = load_library().sfm_gated_delta_fwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(o), _ptr(state), _ptr(offsets), rows, L,
@@ -601,7 +610,7 @@ def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None
             out[name] = _new_like(like, stream) if like.is_contiguous() else _new(like.shape, like.dtype, q.device, stream)
     need = sfm_gated_delta_bwd_ws_size(rows, L, tokens, Hk, H, dk, dv, out.get("dh0") is not None, "bf16" if io else "f32")
     if workspace is None:
-        workspace = _new(need, torch.uint8, q.device, stream)
+        workspace = _scratch(need, q.device, stream)
     _dev(workspace, "workspace")
     rc = load_library().sfm_gated_delta_bwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(do), _ptr(dstate), _ptr(out["dq"]),
@@ -681,7 +690,7 @@ def sfm_group_norm_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, act=None
         _want(rstd, "rstd", torch.float32, (N, num_groups))
     need = sfm_group_norm_ws_size(N, L, C, num_groups, "bf16" if io else "f32")
     if workspace is None and need:
-        workspace = _new(need, torch.uint8, x.device, stream)
+        workspace = _scratch(need, x.device, stream)
     _dev(workspace, "workspace")
     rc = load_library().sfm_group_norm_fwd(
         _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), N, L, C, num_groups, eps, _ACT[act], io,
@@ -714,7 +723,7 @@ def sfm_group_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, act=None, grad
     need = sfm_group_norm_ws_size(N, L, C, G, "bf16" if io else "f32", True,
                                   out.get("dw") is not None or out.get("db") is not None)
     if workspace is None and need:
-        workspace = _new(need, torch.uint8, x.device, stream)
+        workspace = _scratch(need, x.device, stream)
     _dev(workspace, "workspace")
     rc = load_library().sfm_group_norm_bwd(
         _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(out["dx"]), _ptr(out.get("dw")),

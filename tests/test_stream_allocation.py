@@ -53,3 +53,11 @@ def test_the_current_stream(fake, like):
     src = fake.empty((2, 3), "f32", "gpu")
     t = sfm._new_like(src, None) if like else sfm._new((2, 3), "f32", "gpu", None)
     assert t.pool == "current" and not t.held
+
+
+def test_a_workspace_is_its_streams_alone(fake):
+    """Nobody has it on the current stream, so its memory is there for the next call as soon as the call returns."""
+    fake.uint8 = "uint8"
+    t = sfm._scratch(64, "gpu", "side")
+    assert t.pool == "side" and not t.held and (t.shape, t.dtype, t.device) == (64, "uint8", "gpu")
+    assert sfm._scratch(64, "gpu", None).pool == "current"
