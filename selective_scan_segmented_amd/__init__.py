@@ -13,7 +13,7 @@ are through; what it returns has to be waited for as any work of that stream.
 
 Functions keep the C names:
   sfm_selective_scan_fwd, sfm_dwconv1d_fold, sfm_aux_pad_swap, sfm_pick_b1,
-  sfm_gated_delta_fwd, sfm_gated_delta_step, sfm_group_norm_fwd, sfm_group_norm_bwd
+  sfm_gated_delta_fwd, sfm_gated_delta_bwd, sfm_gated_delta_step, sfm_group_norm_fwd, sfm_group_norm_bwd
 """
 from __future__ import annotations
 
@@ -551,7 +551,8 @@ def sfm_gated_delta_fwd(q, k, v, g, beta, h0=None, offsets=None, max_len=None, s
     h0: [B, H, dk, dv] float32 states before the rows, or None.  offsets (int32 [rows + 1] on the
     GPU): packed rows, tensors [1, tokens, ...]; max_len bounds the longest row (None: unknown, and planned as
     no more than four times the average: give it where one row is far longer).  scale defaults to
-    dk ** -0.5; l2norm divides q and k by their length.  Returns o [B, L, H, dv], and with
+    dk ** -0.5; l2norm divides q and k by their length.  Tokens of no row, and those past max_len in
+    one, are not written: a new output holds anything there.  Returns o [B, L, H, dv], and with
     return_state the states after the rows.  `state`, if given, takes those in either case (h0
     itself is allowed)."""
     torch = _torch()
@@ -593,7 +594,8 @@ def sfm_gated_delta_bwd(q, k, v, g, beta, do, h0=None, dstate=None, offsets=None
                         l2norm=False, grads=None, workspace=None, stream=None):
     """Gradients of sfm_gated_delta_fwd (same arguments) for do, the gradient of o, and dstate, that of the
     states after the rows (float32, None: zero).  Returns a dict with dq, dk, dv, dg, dbeta and, with h0,
-    dh0 (float32); `grads` may hold preallocated tensors under those names, dh0 also without h0."""
+    dh0 (float32); `grads` may hold preallocated tensors under those names, dh0 also without h0.
+    Tokens that the forward does not write get no gradients: a new tensor holds anything there."""
     torch = _torch()
     io, lead, Hk, H, dk, dv, ldq, ldk, ldv = _delta_args(q, k, v, g, beta, offsets is not None)
     rows, L, tokens = _rows(lead, offsets, max_len)

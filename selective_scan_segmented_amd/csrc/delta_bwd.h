@@ -14,9 +14,9 @@
 // Four passes: the preparing kernel (T, A), the walk forward (states before the chunks, U), the walk back below
 // (dS', dR, dV, the state's gradient) and, a workgroup to every chunk and head, the rest.  The walks are bound as the
 // forward's (a chunk's latency); the last pass reads 4 bytes of every state and gradient value (260 KB to a chunk and
-// head of 128 x 128) with two workgroups to a unit, 3.5 TB/s.  64 rows x 198 tokens x 5 heads of 64: 101 us = 17
-// preparing + 40 walks + 43; 2 x 4002 x 8 heads of 128 over 4 key heads: 246 us = 19 + 135 + 74 + 18 for the sums over
-// shared heads.
+// head of 128 x 128) with two workgroups to a unit, 3.6 TB/s.  64 rows x 198 tokens x 5 heads of 64: 101 us = 17
+// preparing + 42 walks + 42 (float32, 16 rows: 84 = 11 + 33 + 40); 2 x 4002 x 8 heads of 128 over 4 key heads: 246 us =
+// 19 + 137 + 72 + 18 for the sums over shared heads.
 #pragma once
 
 #include "delta_narrow.h"
@@ -537,7 +537,7 @@ __device__ __forceinline__ void narrow_reverse(const DeltaParams& p, unsigned ti
 }
 
 // Both walks in one launch: they need nothing of each other, and each alone often leaves units idle (2 x 4002 tokens,
-// 8 heads of 128: 88 us and 125 us one after the other, 135 us together).
+// 8 heads of 128: 88 us and 125 us one after the other, 137 us together).
 template <typename T, int DK, int P>
 __global__ __launch_bounds__(kDeltaThreads, (DK == 64 ? WalkLds<T, DK, P>::groups : 1)) void delta_walks_kernel(const DeltaParams p, unsigned tiles, unsigned units) {
     if (blockIdx.x < units)  // (the longer one first)

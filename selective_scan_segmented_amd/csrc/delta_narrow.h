@@ -9,9 +9,9 @@
 // beat behind; their waits are not the chain's.  Issuing a load stops a wave while the unit takes 64 bytes a cycle,
 // so the chain's own loads (T's fragments, straight to registers) are spread over the beat with most else to do.
 //
-// 2 rows x 8192 tokens x 16 heads of 128 x 128: 205 us for 128 chunks, 3500 cycles each, of which the vector units
-// are busy 1300 and LDS 1530; 64 columns to a workgroup: 690 us.  What is left is the chain's own latency (2900
-// cycles a chunk where 64 workgroups run) and, with all units busy, 76 KB a chunk and unit from the L2 caches: 11.8
+// 2 rows x 8192 tokens x 16 heads of 128 x 128: 204 us for 128 chunks, 3500 cycles each, of which the vector units
+// are busy 1300 and LDS 1530; 64 columns to a workgroup: 630 us.  What is left is the chain's own latency (2900
+// cycles a chunk where 64 workgroups run) and, with all units busy, 76 KB a chunk and unit from the L2 caches: 12
 // TB/s over the card.
 #pragma once
 

@@ -8,7 +8,7 @@
 // of 4 columns, so a state row is read as whole 256-byte runs and every load is in flight at once.  With
 // o = scale (S^T q + (k.q) u) taken on the decayed state before its update, S^T k and S^T q share one reduction
 // over the row groups (two lane exchanges, one pass through LDS, one barrier a token).  256 requests x 16 heads of
-// 128 x 128: 108 us for 540 MB, 5.0 TB/s; one request of 5 heads of 64 x 64: 5 us on the card, 12 us with the call.
+// 128 x 128: 106 us for 540 MB, 5.1 TB/s; one request of 5 heads of 64 x 64: 5 us on the card, 9.6 us with the call.
 #include "sfm_delta.h"
 #include "sfm_device.h"
 

@@ -11,15 +11,17 @@
 //
 // * Slab kernels: a sample's rows of some whole groups stay in the registers of one workgroup from the load to the
 //   store (one read, one write, one launch).  Threads take the means of their own values and the squares about them,
-//   which are joined exactly, so a mean far from zero costs no digits.  256 x 198 x 320 bfloat16, 5 groups: 20 us,
-//   3.2 TB/s; backward at 256 x 51 x 640, 10 groups: 23 us, 2.2 TB/s (load, sums, store in turn: what one
-//   workgroup waits for, the others of the unit hide in part).
+//   which are joined exactly, so a mean far from zero costs no digits.  256 x 198 x 320 bfloat16, 5 groups: 18 us,
+//   3.6 TB/s; backward at 256 x 51 x 640, 10 groups: 18 us, 2.8 TB/s, and 4 for the weights (load, sums, store in
+//   turn: what one workgroup waits for, the others of the unit hide in part).  Samples of a token fill few of a
+//   workgroup's lanes (a run of 64 channels 8 of 64), and each leaves its channels' sums for the weights: 50688 tokens
+//   of 320 channels, 5 groups, 231 us forward; backward 278, and 144 for the weights from 130 MB of sums.
 // * Two passes, where a group does not fit: row ranges of a sample to separate workgroups, which leave per-channel
 //   sums; a small kernel joins them in a fixed order; the second pass reads the input again (from the last-level
 //   cache if it fits there).  Squares are taken about the mean of each batch of eight rows, and batches, channels
 //   and ranges are joined by the exact formula for the squares of a union, again so that a large mean costs nothing.
-//   16 x 12544 x 160 bfloat16, 32 groups: 49 us for 192 MB (16 sums, 4 join, 28 apply); backward at 4 x 12544 x 320
-//   float32: 72 us for 321 MB (30, 5, 34, 4 the weights').
+//   16 x 12544 x 160 bfloat16, 32 groups: 48 us for 192 MB (16 sums, 5 join, 27 apply); backward at 4 x 12544 x 320
+//   float32: 73 us for 321 MB (29, 5, 34, 5 the weights').
 // Sums are float32 in a fixed order: repeated calls give the same bits.
 #include <algorithm>
 
