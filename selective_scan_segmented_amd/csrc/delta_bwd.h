@@ -892,8 +892,9 @@ __global__ __launch_bounds__(kDeltaThreads, (sizeof(T) == 2 ? 2 : 1)) void delta
         }
     }
     if (wave != 0) return;
-    // dg: a lane to a token, sums from the chunk's end
-    float x = row_p[lane] + row_o[lane] - ((col_p[lane] + col_p[kC + lane]) + (col_p[2 * kC + lane] + col_p[3 * kC + lane]));
+    // dg: a lane to a token, sums from the chunk's end.  (P's sums first: a row of one token that begins without a state
+    // has nothing else, and its gradient is zero to the last bit.)
+    float x = row_p[lane] - ((col_p[lane] + col_p[kC + lane]) + (col_p[2 * kC + lane] + col_p[3 * kC + lane])) + row_o[lane];
     float all = row_c[lane];
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m);

@@ -101,3 +101,20 @@ def test_rows_of_one_chunk_by_every_plan(L, walk, narrow, io, monkeypatch):
         ref.close(o, wo, io, "o")
         if state:
             ref.close(hT, wT, "f32", "state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (8, 192), (128, 33)])
+@pytest.mark.parametrize("dhT", [False, True])
+def test_decay_of_rows_of_one_token(dhT, dk, dv, io):
+    """A token that begins its row without a state has nothing to decay: its dg is zero, not the rounding of sums that
+    cancel."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    R, H = 40, 3
+    x = ref.delta_inputs(dk + dv, R, R, 1, H, dk, dv, True, io)
+    t = [dev(a[:, None], io) for a in x[:5] + [x[6]]]
+    got = sfm.sfm_gated_delta_bwd(*t, dstate=f32(x[5]) if dhT else None, l2norm=True)
+    torch.cuda.synchronize()
+    assert (got["dg"] == 0).all()
+    assert (got["dbeta"] != 0).any()
