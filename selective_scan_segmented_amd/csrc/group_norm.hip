@@ -274,13 +274,15 @@ __global__ __launch_bounds__(THREADS, (U <= 4 ? 3 : 2)) void norm_slab_bwd_kerne
     }
     __syncthreads();
     const Buf yb = make_buf(static_cast<T*>(p.y) + n * p.L * p.C, p.L * p.C * (int)sizeof(T));
-    // dx = rstd (w dz - m1 - xh m2) = (rstd w) dz - (rstd^2 m2) (x - mean) - rstd m1
+    // dx = rstd (w dz - m1 - xh m2) = (rstd w) dz - (rstd^2 m2) (x - mean) - rstd m1.  In a group of one value nothing
+    // varies: its dx is zero, where the rounding of w dz - m1 by rstd, 1 / sqrt(eps) there, would be left.
+    const float vary = p.L * p.cg > 1 ? 1.0f : 0.0f;
     float k2[V], k1[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        w[j] *= rstd[j];
+        w[j] *= rstd[j] * vary;
         k2[j] = rstd[j] * rstd[j] * gq[grp.g[j]];
-        k1[j] = rstd[j] * gs[grp.g[j]];
+        k1[j] = rstd[j] * gs[grp.g[j]] * vary;
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {

@@ -43,3 +43,22 @@ def test_large_constant_groups(L, io):
     assert (from_dev(mean) == 2.0 ** 100).all()
     ref.close(from_dev(rstd), np.full((2, 4), 1e-5 ** -0.5), "f32", "rstd")
     assert np.array_equal(from_dev(y), np.broadcast_to(b, x.shape))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("N,C", [(1, 1), (21, 64), (7, 135), (3, 2560)])
+def test_groups_of_one_value(N, C, act, io):
+    """y is the bias's, and nothing of dy reaches x or the weight: exact zeros, not their rounding by 1 / sqrt(eps)."""
+    import selective_scan_segmented_amd as sfm
+    rng = np.random.default_rng(C)
+    x, dy = (ref.cast(rng.standard_normal((N, 1, C)), io) for _ in range(2))
+    w, b = (rng.uniform(0.5, 1.5, C).astype(np.float32).astype(np.float64) for _ in range(2))
+    y, mean, rstd = sfm.sfm_group_norm_fwd(dev(x, io), C, dev(w, "f32"), dev(b, "f32"), act=act)
+    g = sfm.sfm_group_norm_bwd(dev(dy, io), dev(x, io), mean, rstd, dev(w, "f32"), dev(b, "f32"), act=act)
+    assert np.array_equal(from_dev(mean)[:, None], x)
+    wy, _, _ = ref.group_norm(x, C, w, b, 1e-5, act)
+    _, _, db = ref.group_norm_bwd(dy, x, x[:, 0], from_dev(rstd), w, b, act)
+    ref.close(from_dev(y), wy, io, "y")
+    ref.close(from_dev(g["db"]), db, "f32", "db", (2e-5, 1e-4))
+    assert (from_dev(g["dx"]) == 0).all() and (from_dev(g["dw"]) == 0).all()
