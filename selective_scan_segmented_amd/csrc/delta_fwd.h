@@ -7,10 +7,9 @@
 //
 // What bounds it: one chunk takes a workgroup some 7 us with its triangles made on the way (18000 cycles, half of them
 // waiting: float32 substitutions, LDS, barriers) and 3.8 us without; the matrix unit is busy 1900 cycles of them with 64
-// keys.  Other workgroups of the unit fill the gaps, three of them (four for rows of one chunk, where T
-// takes the place of K and Q): 256 x 51 tokens x 10 heads of 64 x 64 in 32 us (67 MB, 2.1 TB/s; 2560 workgroups in
-// 1024 places, so the third round is half empty), 1024 workgroups of 1024
-// tokens in 273 us (294 with two).
+// keys.  Other workgroups of the unit fill the gaps, three of them (four for rows of one chunk, where T takes the place
+// of K and Q): 256 x 51 tokens x 10 heads of 64 x 64 in 32 us (67 MB, 2.1 TB/s; 2560 workgroups in 1024 places, so the
+// third round is half empty), 1024 workgroups of 1024 tokens in 273 us (294 with two).
 #pragma once
 
 #include "delta_chunk.h"
