@@ -460,6 +460,100 @@ sfm_status sfm_group_norm_bwd(const void* dy, const void* x, const float* mean, 
 sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G, int want_weights, int io_dtype,
                                       int64_t* bytes);
 
+/*
+ * The gated linear recurrence: one state a channel, both of its gates from the data.
+ * For a token of a row and a channel of rate lam,
+ *   log a = -c softplus(lam) sigmoid(r);  h <- a h + sqrt(1 - a^2) sigmoid(i) x;  y = h,
+ * h float32, zero (or h0) before the row's first token.
+ *
+ * sfm_gated_recurrence_fwd -- whole rows.
+ *   x, r, i  [tokens, D] io        token strides ldx, ldr, ldi (elements, D to 2^22)
+ *   lam      [D] f32;  c > 0 (8 is usual)
+ *   h0       [rows, D] f32 or NULL (zero)
+ *   y        [tokens, D] io, contiguous
+ *   hT       [rows, D] f32 or NULL: the states after each row (a row without tokens:
+ *            its h0); hT == h0 is allowed
+ *   offsets  as for sfm_gated_delta_fwd: NULL for equal rows (tokens == rows * L), or
+ *            int32 [rows + 1] on the device; L bounds the longest row, offsets outside
+ *            the tokens are cut to them, tokens of no row and those past L keep their old y
+ *   D 1..65536.  Tensors need their element's alignment only; rows on 16 bytes with D a
+ *   multiple of 16 bytes are loaded in wider pieces.
+ * A non-finite value of a token stays in its row and channel.  Repeated calls give the same bits.
+ * workspace: at least sfm_gated_recurrence_fwd_ws_size() bytes (may be NULL when that is
+ *   0), 16-byte aligned, owned by the caller.
+ */
+sfm_status sfm_gated_recurrence_fwd(const void* x, const void* r, const void* i, const float* lam, const float* h0,
+                                    void* y, float* hT, const int32_t* offsets, int64_t rows, int64_t L,
+                                    int64_t tokens, int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, float c,
+                                    int io_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+sfm_status sfm_gated_recurrence_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t D, int io_dtype,
+                                            int64_t* bytes);
+
+/*
+ * sfm_gated_recurrence_bwd -- gradients of sfm_gated_recurrence_fwd (same inputs and
+ * sizes) for the gradients dy [tokens, D] io of y and dhT [rows, D] f32 (or NULL: zero)
+ * of the states after the rows.  y [tokens, D] io is the forward's output: the states as
+ * the forward stored them are the ones that the gradients of the decays see.
+ *   dx, dr, di [tokens, D] io, contiguous;  dlam [D] f32;  dh0 [rows, D] f32 or NULL
+ *   (not wanted).  Tokens of no row keep their old gradients.  No atomics on sums:
+ *   repeated calls give the same bits.
+ */
+sfm_status sfm_gated_recurrence_bwd(const void* x, const void* r, const void* i, const float* lam, const float* h0,
+                                    const void* y, const void* dy, const float* dhT, void* dx, void* dr, void* di,
+                                    float* dlam, float* dh0, const int32_t* offsets, int64_t rows, int64_t L,
+                                    int64_t tokens, int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, float c,
+                                    int io_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+sfm_status sfm_gated_recurrence_bwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t D, int io_dtype,
+                                            int64_t* bytes);
+
+/*
+ * sfm_gated_recurrence_step -- one token of each of `rows` requests (serving) on a pool
+ * of states, updated in place: x, r, i [rows, D] io with strides as above; state
+ * [pool, D] f32; slots and y as for sfm_gated_delta_step.
+ */
+sfm_status sfm_gated_recurrence_step(const void* x, const void* r, const void* i, const float* lam, float* state,
+                                     const int32_t* slots, void* y, int64_t rows, int64_t pool, int64_t D,
+                                     int64_t ldx, int64_t ldr, int64_t ldi, float c, int io_dtype, void* stream);
+
+/*
+ * Norm of every head's query and key, and the rotation of its pairs by the token's
+ * position, in one pass.  For a head x of d values:
+ *   z = w x / sqrt(mean(x^2) + eps)   with SFM_QK_NORM (w: wq or wk, [d] f32 or NULL: 1), else z = x;
+ *   the first rot values are rot / 2 pairs, (j, j + rot / 2) or with SFM_QK_NEIGHBOURS
+ *   (2j, 2j + 1), and pair j becomes (z1 cos - z2 sin, z2 cos + z1 sin) of the angle
+ *   position * freqs[j] (taken in 64 bits); values from rot on stay z.
+ *
+ * sfm_qk_norm_rope_fwd:
+ *   q [tokens, Hq, d], k [tokens, Hk, d] io   token strides ldq, ldk (heads' width to 2^22)
+ *   positions  int32 [period, axes] on the device: token t has row t mod period (period
+ *              divides tokens: rows that share their positions give them once)
+ *   freqs      [rot / 2] f32 on the device
+ *   sections   [axes] on the host: pairs that go by each of the 1 to 4 position axes, in
+ *              order, rot / 2 in all (may be NULL with one axis)
+ *   qo, ko     like q, k, contiguous, over no input
+ *   d 1..256; rot even, 0..d (0: no rotation, positions and freqs may be NULL); eps at
+ *   least 2^-126.
+ * sfm_qk_norm_rope_bwd: gradients dq, dk (contiguous) of q and k for dqo and dko
+ *   (contiguous), and with the norm dwq, dwk [d] f32 or NULL (not wanted); workspace: at
+ *   least sfm_qk_norm_rope_bwd_ws_size() bytes (want_weights: dwq or dwk given), may be
+ *   NULL when that is 0; 16-byte aligned.  Repeated calls give the same bits.
+ */
+#define SFM_QK_NORM 1
+#define SFM_QK_NEIGHBOURS 2
+sfm_status sfm_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, const float* wk,
+                                const int32_t* positions, const float* freqs, void* qo, void* ko, int64_t tokens,
+                                int64_t period, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, int64_t axes,
+                                const int64_t* sections, int64_t ldq, int64_t ldk, float eps, int io_dtype, int flags,
+                                void* stream);
+sfm_status sfm_qk_norm_rope_bwd(const void* dqo, const void* dko, const void* q, const void* k, const float* wq,
+                                const float* wk, const int32_t* positions, const float* freqs, void* dq, void* dk,
+                                float* dwq, float* dwk, int64_t tokens, int64_t period, int64_t Hq, int64_t Hk,
+                                int64_t d, int64_t rot, int64_t axes, const int64_t* sections, int64_t ldq,
+                                int64_t ldk, float eps, int io_dtype, int flags, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+sfm_status sfm_qk_norm_rope_bwd_ws_size(int64_t tokens, int64_t Hq, int64_t Hk, int64_t d, int want_weights,
+                                        int io_dtype, int64_t* bytes);
+
 /* Static text for a status code. */
 const char* sfm_status_string(sfm_status s);
 

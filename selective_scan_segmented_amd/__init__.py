@@ -13,7 +13,8 @@ are through; what it returns has to be waited for as any work of that stream.
 
 Functions keep the C names:
   sfm_selective_scan_fwd, sfm_dwconv1d_fold, sfm_aux_pad_swap, sfm_pick_b1,
-  sfm_gated_delta_fwd, sfm_gated_delta_bwd, sfm_gated_delta_step, sfm_group_norm_fwd, sfm_group_norm_bwd
+  sfm_gated_delta_fwd, sfm_gated_delta_bwd, sfm_gated_delta_step, sfm_group_norm_fwd, sfm_group_norm_bwd,
+  sfm_gated_recurrence_fwd, sfm_gated_recurrence_bwd, sfm_gated_recurrence_step, sfm_qk_norm_rope_fwd, sfm_qk_norm_rope_bwd
 """
 from __future__ import annotations
 
@@ -27,6 +28,9 @@ __all__ = ["sfm_selective_scan_fwd", "sfm_selective_scan_fwd_ex", "sfm_selective
            "sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_bwd",
            "sfm_gated_delta_bwd_ws_size", "sfm_gated_delta_step", "sfm_group_norm_fwd",
            "sfm_group_norm_bwd", "sfm_group_norm_ws_size",
+           "sfm_gated_recurrence_fwd", "sfm_gated_recurrence_fwd_ws_size", "sfm_gated_recurrence_bwd",
+           "sfm_gated_recurrence_bwd_ws_size", "sfm_gated_recurrence_step", "sfm_qk_norm_rope_fwd",
+           "sfm_qk_norm_rope_bwd", "sfm_qk_norm_rope_bwd_ws_size",
            "sfm_pick_b1", "sfm_scan_plan_string", "sfm_version", "library_path", "load_library", "SFMError"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -88,6 +92,18 @@ def load_library():
     lib.sfm_group_norm_bwd_ws_size.argtypes = [i64] * 4 + [ci, ci, pi64]
     lib.sfm_gated_delta_bwd.argtypes = [vp] * 15 + [i64] * 10 + [f32, ci, ci, vp, i64, vp]
     lib.sfm_gated_delta_bwd_ws_size.argtypes = [i64] * 7 + [ci, ci, pi64]
+    lib.sfm_gated_recurrence_fwd.argtypes = [vp] * 8 + [i64] * 7 + [f32, ci, vp, i64, vp]
+    lib.sfm_gated_recurrence_fwd_ws_size.argtypes = [i64] * 4 + [ci, pi64]
+    lib.sfm_gated_recurrence_bwd.argtypes = [vp] * 14 + [i64] * 7 + [f32, ci, vp, i64, vp]
+    lib.sfm_gated_recurrence_bwd_ws_size.argtypes = [i64] * 4 + [ci, pi64]
+    lib.sfm_gated_recurrence_step.argtypes = [vp] * 7 + [i64] * 6 + [f32, ci, vp]
+    lib.sfm_qk_norm_rope_fwd.argtypes = [vp] * 8 + [i64] * 7 + [vp, i64, i64, f32, ci, ci, vp]
+    lib.sfm_qk_norm_rope_bwd.argtypes = [vp] * 12 + [i64] * 7 + [vp, i64, i64, f32, ci, ci, vp, i64, vp]
+    lib.sfm_qk_norm_rope_bwd_ws_size.argtypes = [i64] * 4 + [ci, ci, pi64]
+    for f in ("sfm_gated_recurrence_fwd", "sfm_gated_recurrence_fwd_ws_size", "sfm_gated_recurrence_bwd",
+              "sfm_gated_recurrence_bwd_ws_size", "sfm_gated_recurrence_step", "sfm_qk_norm_rope_fwd",
+              "sfm_qk_norm_rope_bwd", "sfm_qk_norm_rope_bwd_ws_size"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("sfm_gated_delta_fwd", "sfm_gated_delta_fwd_ws_size", "sfm_gated_delta_step", "sfm_gated_delta_bwd",
               "sfm_gated_delta_bwd_ws_size", "sfm_group_norm_fwd",
               "sfm_group_norm_bwd", "sfm_group_norm_fwd_ws_size", "sfm_group_norm_bwd_ws_size"):
@@ -732,4 +748,270 @@ def sfm_group_norm_bwd(dy, x, mean, rstd, weight=None, bias=None, act=None, grad
         _ptr(out.get("db")), N, L, C, G, _ACT[act], io, _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "sfm_group_norm_bwd")
+    return out
+
+
+# ---------------------------------------------------------------- the gated linear recurrence
+def _channels(t, name, dtype, shape):
+    """Checks a [..., D] tensor whose channels are contiguous and whose tokens are evenly strided (a slice of a
+    wider projection is fine); returns the token stride."""
+    D = shape[-1]
+    if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return D
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    single = len(shape) == 3 and shape[1] == 1  # rows of one token: the tokens are the rows'
+    ld = st[0] if single else st[-2]
+    if (D > 1 and st[-1] != 1) or (len(shape) == 3 and not single and shape[0] > 1 and st[0] != shape[1] * ld) or \
+            (ld < D and shape.numel() > D):
+        raise ValueError(f"{name}: channels must be contiguous and tokens evenly strided, got strides {st}")
+    return max(ld, D)
+
+
+def _recurrence_args(x, r, i, lam, packed, dims, form):
+    """Checks shared by the recurrence's functions; returns the io code and the strides."""
+    io = _io_code(x)
+    shape = x.shape
+    if len(shape) != dims:
+        raise ValueError(f"x, r and i must be {form}, got {tuple(shape)}")
+    if packed and shape[0] != 1:
+        raise ValueError("packed rows (offsets) are one batch entry: [1, tokens, D]")
+    dtype = x.dtype
+    lds = _channels(x, "x", dtype, shape), _channels(r, "r", dtype, shape), _channels(i, "i", dtype, shape)
+    _want(lam, "lam", _torch().float32, shape[-1:])
+    return io, lds
+
+
+def _same_device(stream, *tensors):
+    """The call's tensors and its stream are the current device's: kernels are launched there."""
+    here = _torch()._C._cuda_getDevice()
+    if stream is not None and stream.device_index != here:
+        raise ValueError(f"stream is of GPU {stream.device_index}, the current one is {here}")
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor is on GPU {t.get_device()}, the current one is {here}: call under torch.cuda.device")
+
+
+def _size(name, *sizes):
+    """A host-only size query of the library."""
+    out = ctypes.c_int64(0)
+    _check(getattr(load_library(), name)(*sizes, ctypes.byref(out)), name)
+    return int(out.value)
+
+
+def sfm_gated_recurrence_fwd_ws_size(rows: int, L: int, tokens: int, D: int, io: str = "bf16") -> int:
+    """Workspace bytes sfm_gated_recurrence_fwd needs (host only)."""
+    return _size("sfm_gated_recurrence_fwd_ws_size", rows, L, tokens, D, SFM_BF16 if io == "bf16" else SFM_F32)
+
+
+def sfm_gated_recurrence_bwd_ws_size(rows: int, L: int, tokens: int, D: int, io: str = "bf16") -> int:
+    """Workspace bytes sfm_gated_recurrence_bwd needs (host only)."""
+    return _size("sfm_gated_recurrence_bwd_ws_size", rows, L, tokens, D, SFM_BF16 if io == "bf16" else SFM_F32)
+
+
+def sfm_gated_recurrence_fwd(x, r, i, lam, c=8.0, h0=None, offsets=None, max_len=None, y=None, return_state=False,
+                             state=None, workspace=None, stream=None):
+    """The gated linear recurrence over whole rows (see include/sfm.h):
+
+        log a = -c softplus(lam) sigmoid(r);  h <- a h + sqrt(1 - a^2) sigmoid(i) x;  y = h
+
+    x, r, i: [B, L, D] float32 or bfloat16 (r and i before their sigmoids; slices of one projection are taken in
+    place); lam: [D] float32; h0: [B, D] float32 states before the rows, or None.  offsets, max_len: packed rows as
+    for sfm_gated_delta_fwd, tensors [1, tokens, D].  Tokens of no row, and those past max_len in one, are not
+    written: a new output holds anything there.  Returns y [B, L, D], and with return_state the float32 states after
+    the rows.  `state`, if given, takes those in either case (h0 itself is allowed)."""
+    torch = _torch()
+    io, (ldx, ldr, ldi) = _recurrence_args(x, r, i, lam, offsets is not None, 3, "[B, L, D]")
+    rows, L, tokens = _rows(x.shape, offsets, max_len)
+    D = x.shape[2]
+    _want(h0, "h0", torch.float32, (rows, D))
+    if y is not None:
+        _want(y, "y", x.dtype, x.shape)
+    else:
+        y = _new_like(x, stream) if x.is_contiguous() else _new(x.shape, x.dtype, x.device, stream)
+    if state is not None:
+        _want(state, "state", torch.float32, (rows, D))
+    elif return_state:
+        state = _new((rows, D), torch.float32, x.device, stream)
+    need = _size("sfm_gated_recurrence_fwd_ws_size", rows, L, tokens, D, io)
+    if workspace is None and need:
+        workspace = _scratch(need, x.device, stream)
+    _dev(workspace, "workspace")
+    _same_device(stream, x, r, i, lam, h0, y, state, offsets, workspace)
+    rc = load_library().sfm_gated_recurrence_fwd(
+        _ptr(x), _ptr(r), _ptr(i), _ptr(lam), _ptr(h0), _ptr(y), _ptr(state), _ptr(offsets), rows, L, tokens, D, ldx,
+        ldr, ldi, c, io, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    _check(rc, "sfm_gated_recurrence_fwd")
+    return (y, state) if return_state else y
+
+
+def sfm_gated_recurrence_bwd(x, r, i, lam, y, dy, c=8.0, h0=None, dstate=None, offsets=None, max_len=None, grads=None,
+                             workspace=None, stream=None):
+    """Gradients of sfm_gated_recurrence_fwd (same arguments; y is what it returned) for dy, the gradient of y, and
+    dstate, that of the states after the rows (float32, None: zero).  Returns a dict with dx, dr, di, dlam (float32)
+    and, with h0, dh0 (float32); `grads` may hold preallocated tensors under those names, dh0 also without h0.
+    Tokens that the forward does not write get no gradients: a new tensor holds anything there."""
+    torch = _torch()
+    io, (ldx, ldr, ldi) = _recurrence_args(x, r, i, lam, offsets is not None, 3, "[B, L, D]")
+    rows, L, tokens = _rows(x.shape, offsets, max_len)
+    D = x.shape[2]
+    states = (rows, D)
+    _want(h0, "h0", torch.float32, states)
+    _want(dstate, "dstate", torch.float32, states)
+    _want(y, "y", x.dtype, x.shape)
+    _want(dy, "dy", x.dtype, x.shape)
+    out = dict(grads or {})
+    for name, like in (("dx", x), ("dr", r), ("di", i), ("dlam", lam), ("dh0", h0)):
+        if like is None:  # (dh0 of states that were zero: only where the caller gives a tensor for it)
+            _want(out.get(name), name, torch.float32, states)
+        elif out.get(name) is not None:
+            _want(out[name], name, like.dtype, like.shape)
+        else:
+            out[name] = _new_like(like, stream) if like.is_contiguous() else _new(like.shape, like.dtype, x.device, stream)
+    need = _size("sfm_gated_recurrence_bwd_ws_size", rows, L, tokens, D, io)
+    if workspace is None and need:
+        workspace = _scratch(need, x.device, stream)
+    _dev(workspace, "workspace")
+    _same_device(stream, x, r, i, lam, h0, y, dy, dstate, offsets, workspace, *out.values())
+    rc = load_library().sfm_gated_recurrence_bwd(
+        _ptr(x), _ptr(r), _ptr(i), _ptr(lam), _ptr(h0), _ptr(y), _ptr(dy), _ptr(dstate), _ptr(out["dx"]),
+        _ptr(out["dr"]), _ptr(out["di"]), _ptr(out["dlam"]), _ptr(out.get("dh0")), _ptr(offsets), rows, L, tokens, D,
+        ldx, ldr, ldi, c, io, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "sfm_gated_recurrence_bwd")
+    return out
+
+
+def sfm_gated_recurrence_step(x, r, i, lam, state, slots=None, c=8.0, y=None, stream=None):
+    """One token of each request: x, r, i [R, D]; state [pool, D] float32, updated in place; slots int32 [R] (row r's
+    state; outside the pool: padding, a zero y) or None (state r).  Returns y [R, D]."""
+    torch = _torch()
+    io, (ldx, ldr, ldi) = _recurrence_args(x, r, i, lam, False, 2, "[R, D]")
+    rows, D = x.shape
+    _dev(state, "state", torch.float32)
+    if state.dim() != 2 or state.shape[1] != D:
+        raise ValueError(f"state must have shape (pool, {D}), got {tuple(state.shape)}")
+    _want(slots, "slots", torch.int32, (rows,))
+    if y is not None:
+        _want(y, "y", x.dtype, x.shape)
+    else:
+        y = _new_like(x, stream) if x.is_contiguous() else _new(x.shape, x.dtype, x.device, stream)
+    _same_device(stream, x, r, i, lam, state, slots, y)
+    rc = load_library().sfm_gated_recurrence_step(
+        _ptr(x), _ptr(r), _ptr(i), _ptr(lam), _ptr(state), _ptr(slots), _ptr(y), rows, state.shape[0], D, ldx, ldr,
+        ldi, c, io, _stream(stream))
+    _check(rc, "sfm_gated_recurrence_step")
+    return y
+
+
+# ---------------------------------------------------------------- norm and rotation of queries and keys
+SFM_QK_NORM, SFM_QK_NEIGHBOURS = 1, 2
+
+
+def _rope_args(q, k, wq, wk, positions, freqs, sections, interleaved, norm):
+    """Checks shared by the norm and rotation's functions; returns what both calls pass on."""
+    torch = _torch()
+    io = _io_code(q)
+    if q.dim() not in (3, 4) or k.dim() != q.dim():
+        raise ValueError(f"q and k must be [tokens, heads, size] or [B, L, heads, size], got {tuple(q.shape)} and {tuple(k.shape)}")
+    lead, Hq, d, Hk = q.shape[:-2], q.shape[-2], q.shape[-1], k.shape[-2]
+    ldq = _tokens(q, "q", Hq, d, q.dtype, lead)
+    ldk = _tokens(k, "k", Hk, d, q.dtype, lead)
+    _want(wq, "wq", torch.float32, (d,))
+    _want(wk, "wk", torch.float32, (d,))
+    tokens = lead.numel()
+    rot, axes, period, parts = 0, 1, 1, None
+    if freqs is not None:
+        _dev(freqs, "freqs", torch.float32)
+        _dev(positions, "positions", torch.int32)
+        if positions is None or freqs.dim() != 1 or not freqs.numel():
+            raise ValueError("a rotation takes positions and freqs [rot / 2]")
+        rot = 2 * freqs.numel()
+        sections = (freqs.numel(),) if sections is None else tuple(int(n) for n in sections)
+        axes = len(sections)
+        parts = (ctypes.c_int64 * max(1, axes))(*sections)
+        shape, last = tuple(positions.shape), (axes,)
+        if axes == 1 and shape in (tuple(lead), tuple(lead[-1:])):  # one axis: without a dimension of its own
+            last = ()
+        if shape == tuple(lead) + last:
+            period = tokens
+        elif len(lead) == 2 and shape == tuple(lead[-1:]) + last:  # rows that share their positions
+            period = lead[-1]
+        else:
+            raise ValueError(f"positions must be {tuple(lead)} or {tuple(lead[-1:])} with {axes} axes, got {shape}")
+    elif positions is not None or sections is not None:
+        raise ValueError("positions and sections without freqs")
+    flags = (SFM_QK_NORM if norm else 0) | (SFM_QK_NEIGHBOURS if interleaved else 0)
+    return io, lead, Hq, Hk, d, ldq, ldk, tokens, period, rot, axes, parts, flags
+
+
+def sfm_qk_norm_rope_fwd(q, k, wq=None, wk=None, positions=None, freqs=None, sections=None, interleaved=False, norm=True,
+                         eps=1e-6, qo=None, ko=None, stream=None):
+    """Norm of every head's query and key by its root mean square, and the rotation of its pairs by the token's
+    position, in one pass (see include/sfm.h).
+
+    q: [B, L, Hq, d], k: [B, L, Hk, d], or [tokens, heads, d] (one token of each request); float32 or bfloat16, slices
+    of one projection are taken in place.  wq, wk: [d] float32 or None (norm=False: no norm, no weights).
+    freqs: [rot / 2] float32, the angle of pair j a position (None: no rotation); the first rot values of a head are
+    pairs (j, j + rot / 2), or neighbours with `interleaved`.  positions: int32 [B, L], or [L] for rows that share
+    them, or [tokens]; with sections, the pairs that go by each axis, their last dimension is the axes.
+    Returns the normed and rotated q and k, contiguous."""
+    io, lead, Hq, Hk, d, ldq, ldk, tokens, period, rot, axes, parts, flags = _rope_args(
+        q, k, wq, wk, positions, freqs, sections, interleaved, norm)
+    if qo is not None:
+        _want(qo, "qo", q.dtype, q.shape)
+    else:
+        qo = _new_like(q, stream) if q.is_contiguous() else _new(q.shape, q.dtype, q.device, stream)
+    if ko is not None:
+        _want(ko, "ko", q.dtype, k.shape)
+    else:
+        ko = _new_like(k, stream) if k.is_contiguous() else _new(k.shape, q.dtype, q.device, stream)
+    _same_device(stream, q, k, wq, wk, positions, freqs, qo, ko)
+    rc = load_library().sfm_qk_norm_rope_fwd(
+        _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(freqs), _ptr(qo), _ptr(ko), tokens, period, Hq, Hk,
+        d, rot, axes, parts, ldq, ldk, eps, io, flags, _stream(stream))
+    _check(rc, "sfm_qk_norm_rope_fwd")
+    return qo, ko
+
+
+def sfm_qk_norm_rope_bwd_ws_size(tokens: int, Hq: int, Hk: int, d: int, want_weights: bool = True, io: str = "bf16") -> int:
+    """Workspace bytes sfm_qk_norm_rope_bwd needs (host only)."""
+    return _size("sfm_qk_norm_rope_bwd_ws_size", tokens, Hq, Hk, d, int(bool(want_weights)),
+                 SFM_BF16 if io == "bf16" else SFM_F32)
+
+
+def sfm_qk_norm_rope_bwd(dqo, dko, q, k, wq=None, wk=None, positions=None, freqs=None, sections=None, interleaved=False,
+                         norm=True, eps=1e-6, grads=None, workspace=None, stream=None):
+    """Gradients of sfm_qk_norm_rope_fwd (same arguments) for dqo and dko, the gradients of its outputs: a dict with
+    dq, dk and, for the weights given, dwq and dwk (float32).  `grads` may hold preallocated tensors under those
+    names, with the norm dwq and dwk also without weights."""
+    torch = _torch()
+    io, lead, Hq, Hk, d, ldq, ldk, tokens, period, rot, axes, parts, flags = _rope_args(
+        q, k, wq, wk, positions, freqs, sections, interleaved, norm)
+    _want(dqo, "dqo", q.dtype, q.shape)
+    _want(dko, "dko", q.dtype, k.shape)
+    out = dict(grads or {})
+    for name, like in (("dq", q), ("dk", k), ("dwq", wq), ("dwk", wk)):
+        if out.get(name) is not None:
+            _want(out[name], name, *((torch.float32, (d,)) if like is None else (like.dtype, like.shape)))
+        elif like is not None:
+            out[name] = _new_like(like, stream) if like.is_contiguous() else _new(like.shape, like.dtype, q.device, stream)
+    need = _size("sfm_qk_norm_rope_bwd_ws_size", tokens, Hq, Hk, d,
+                 int(out.get("dwq") is not None or out.get("dwk") is not None), io)
+    if workspace is None and need:
+        workspace = _scratch(need, q.device, stream)
+    _dev(workspace, "workspace")
+    _same_device(stream, q, k, wq, wk, positions, freqs, dqo, dko, workspace, *out.values())
+    rc = load_library().sfm_qk_norm_rope_bwd(
+        _ptr(dqo), _ptr(dko), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(freqs), _ptr(out["dq"]),
+        _ptr(out["dk"]), _ptr(out.get("dwq")), _ptr(out.get("dwk")), tokens, period, Hq, Hk, d, rot, axes, parts, ldq,
+        ldk, eps, io, flags, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    _check(rc, "sfm_qk_norm_rope_bwd")
     return out

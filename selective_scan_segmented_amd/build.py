@@ -24,7 +24,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsfm.so")
 SOURCES = ["scan.hip", "scan_cl.hip", "conv.hip", "aux.hip", "bwd.hip", "layout.hip", "sfm_api.cpp", "delta_step.hip", "delta_fwd_f32.hip", "delta_fwd_bf16.hip",
            "delta_bwd_f32.hip", "delta_bwd_bf16.hip",
-           "sfm_delta_api.cpp", "group_norm.hip", "sfm_norm_api.cpp"] + [
+           "sfm_delta_api.cpp", "group_norm.hip", "sfm_norm_api.cpp",
+           "recurrence.hip", "sfm_rec_api.cpp", "qk_rope.hip", "sfm_rope_api.cpp"] + [
     f"scan_{io}_n{n}.hip" for io in ("f32", "bf16") for n in (4, 8, 16)] + [
     f"split_{io}_n{n}.hip" for io in ("f32", "bf16") for n in (4, 8, 16)]
 ARCH = os.environ.get("SFM_OFFLOAD_ARCH", "gfx950")

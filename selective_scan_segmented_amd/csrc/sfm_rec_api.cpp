@@ -1,0 +1,215 @@
+// sfm_rec_api.cpp -- the C ABI of the gated linear recurrence (declared in include/sfm.h): argument checks and dispatch.
+#include "sfm.h"
+
+#include <hip/hip_runtime.h>
+
+#include "sfm_api_util.h"
+#include "sfm_rec.h"
+
+using namespace sfm::api;
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, bool packed, int64_t D, int io_dtype) {
+    if (io_dtype != SFM_F32 && io_dtype != SFM_BF16) return fail(SFM_ERR_DTYPE, "%s: io_dtype %d", fn, io_dtype);
+    if (!sane(rows, 1 << 24) || !sane(L, 1 << 24) || tokens < 0 || tokens > (1LL << 31) - 1 || !sane(D, 1 << 16))
+        return fail(SFM_ERR_SHAPE, "%s: rows=%lld L=%lld tokens=%lld D=%lld out of range", fn, (long long)rows,
+                    (long long)L, (long long)tokens, (long long)D);
+    if (!packed && tokens != rows * L)
+        return fail(SFM_ERR_SHAPE, "%s: %lld tokens are not rows=%lld of L=%lld", fn, (long long)tokens,
+                    (long long)rows, (long long)L);
+    // a launch holds fewer than 2^32 work items
+    if (rows * ((D + 255) / 256) >= 1 << 24)
+        return fail(SFM_ERR_SHAPE, "%s: rows=%lld of %lld channels are more workgroups than a launch holds", fn,
+                    (long long)rows, (long long)D);
+    return SFM_OK;
+}
+
+sfm_status check_inputs(const char* fn, const void* x, const void* r, const void* i, const float* lam, int64_t tokens,
+                        int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, float c, int io_dtype) {
+    if (!lam || (tokens > 0 && (!x || !r || !i))) return fail(SFM_ERR_NULL, "%s: x, r, i and lam are required", fn);
+    for (int64_t ld : {ldx, ldr, ldi})
+        if (ld < D || ld > 1 << 22)
+            return fail(SFM_ERR_SHAPE, "%s: token strides %lld, %lld, %lld below D=%lld (or too large)", fn,
+                        (long long)ldx, (long long)ldr, (long long)ldi, (long long)D);
+    if (!(c > 0.0f && c <= 1e6f)) return fail(SFM_ERR_SHAPE, "%s: c=%g", fn, (double)c);
+    const uintptr_t e = io_bytes(io_dtype);
+    if (!aligned_to(x, e) || !aligned_to(r, e) || !aligned_to(i, e) || !aligned_to(lam, 4))
+        return fail(SFM_ERR_ALIGN, "%s: an input is not aligned to its element", fn);
+    return SFM_OK;
+}
+
+struct Ranges {
+    Range of[10];
+    int n = 0;
+    void add(const char* name, const void* p, int64_t bytes) {
+        if (p && bytes > 0) of[n++] = rng(name, p, bytes);
+    }
+    void add_inputs(const void* x, const void* r, const void* i, const float* lam, int64_t tokens, int64_t D, int64_t ldx,
+                    int64_t ldr, int64_t ldi, int e) {
+        add("lam", lam, D * 4);
+        if (tokens <= 0) return;
+        add("x", x, ((tokens - 1) * ldx + D) * e);
+        add("r", r, ((tokens - 1) * ldr + D) * e);
+        add("i", i, ((tokens - 1) * ldi + D) * e);
+    }
+};
+
+// No output on an input (but `same`, which may be the input of exactly that place) or on another output.
+sfm_status check_ranges(const char* fn, const Ranges& in, const Ranges& out, const void* same = nullptr) {
+    for (int j = 0; j < out.n; ++j) {
+        const Range& o = out.of[j];
+        for (int k = 0; k < in.n; ++k)
+            if (overlap(o, in.of[k]) && !(same && o.lo == reinterpret_cast<uintptr_t>(same) && in.of[k].lo == o.lo && in.of[k].hi == o.hi))
+                return fail(SFM_ERR_ALIAS, "%s: %s overlaps %s", fn, o.name, in.of[k].name);
+        for (int k = 0; k < j; ++k)
+            if (overlap(o, out.of[k])) return fail(SFM_ERR_ALIAS, "%s: %s overlaps %s", fn, o.name, out.of[k].name);
+    }
+    return SFM_OK;
+}
+
+sfm_status check_workspace(const char* fn, const void* ws, int64_t have, int64_t need) {
+    if (need <= 0) return SFM_OK;
+    if (!ws || have < need)
+        return fail(SFM_ERR_SHAPE, "%s: workspace of %lld bytes needed, %lld given", fn, (long long)need,
+                    (long long)(ws ? have : 0));
+    if (!aligned16(ws)) return fail(SFM_ERR_ALIGN, "%s: workspace not 16-byte aligned", fn);
+    return SFM_OK;
+}
+
+sfm::RecParams params(const void* x, const void* r, const void* i, const float* lam, int64_t rows, int64_t L, int64_t tokens,
+                      int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, float c) {
+    sfm::RecParams p{};
+    p.x = x, p.r = r, p.i = i, p.lam = lam;
+    p.ldx = ldx, p.ldr = ldr, p.ldi = ldi, p.tokens = tokens;
+    p.rows = (int)rows, p.L = (int)L, p.D = (int)D, p.c = c;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+sfm_status sfm_gated_recurrence_fwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t D, int io_dtype,
+                                            int64_t* bytes) {
+    static const char* fn = "sfm_gated_recurrence_fwd_ws_size";
+    if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
+    const sfm_status st = check_sizes(fn, rows, L, tokens, true, D, io_dtype);
+    if (st != SFM_OK) return st;
+    *bytes = sfm::plan_rec_fwd(rows, L, tokens, D, io_dtype);
+    return ok();
+}
+
+sfm_status sfm_gated_recurrence_bwd_ws_size(int64_t rows, int64_t L, int64_t tokens, int64_t D, int io_dtype,
+                                            int64_t* bytes) {
+    static const char* fn = "sfm_gated_recurrence_bwd_ws_size";
+    if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
+    const sfm_status st = check_sizes(fn, rows, L, tokens, true, D, io_dtype);
+    if (st != SFM_OK) return st;
+    *bytes = sfm::plan_rec_bwd(rows, L, tokens, D, io_dtype);
+    return ok();
+}
+
+sfm_status sfm_gated_recurrence_fwd(const void* x, const void* r, const void* i, const float* lam, const float* h0, void* y,
+                                    float* hT, const int32_t* offsets, int64_t rows, int64_t L, int64_t tokens, int64_t D,
+                                    int64_t ldx, int64_t ldr, int64_t ldi, float c, int io_dtype, void* workspace,
+                                    int64_t workspace_bytes, void* stream) {
+    static const char* fn = "sfm_gated_recurrence_fwd";
+    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, D, io_dtype);
+    if (st != SFM_OK) return st;
+    st = check_inputs(fn, x, r, i, lam, tokens, D, ldx, ldr, ldi, c, io_dtype);
+    if (st != SFM_OK) return st;
+    if (tokens > 0 && !y) return fail(SFM_ERR_NULL, "%s: y is required", fn);
+    const int e = io_bytes(io_dtype);
+    if (!aligned_to(h0, 4) || !aligned_to(hT, 4) || !aligned_to(offsets, 4) || !aligned_to(y, e))
+        return fail(SFM_ERR_ALIGN, "%s: h0, hT, offsets or y not aligned to its element", fn);
+    const int64_t need = sfm::plan_rec_fwd(rows, L, tokens, D, io_dtype);
+    st = check_workspace(fn, workspace, workspace_bytes, need);
+    if (st != SFM_OK) return st;
+    Ranges in, out;
+    in.add_inputs(x, r, i, lam, tokens, D, ldx, ldr, ldi, e);
+    in.add("offsets", offsets, (rows + 1) * 4);
+    in.add("h0", h0, rows * D * 4);
+    out.add("y", y, tokens * D * e);
+    out.add("hT", hT, rows * D * 4);
+    out.add("workspace", workspace, need);
+    st = check_ranges(fn, in, out, hT);
+    if (st != SFM_OK) return st;
+    sfm::RecParams p = params(x, r, i, lam, rows, L, tokens, D, ldx, ldr, ldi, c);
+    p.h0 = h0, p.y = y, p.hT = hT, p.offsets = offsets;
+    return hip_status(sfm::launch_rec_fwd(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
+}
+
+sfm_status sfm_gated_recurrence_bwd(const void* x, const void* r, const void* i, const float* lam, const float* h0,
+                                    const void* y, const void* dy, const float* dhT, void* dx, void* dr, void* di,
+                                    float* dlam, float* dh0, const int32_t* offsets, int64_t rows, int64_t L,
+                                    int64_t tokens, int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, float c, int io_dtype,
+                                    void* workspace, int64_t workspace_bytes, void* stream) {
+    static const char* fn = "sfm_gated_recurrence_bwd";
+    sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, D, io_dtype);
+    if (st != SFM_OK) return st;
+    st = check_inputs(fn, x, r, i, lam, tokens, D, ldx, ldr, ldi, c, io_dtype);
+    if (st != SFM_OK) return st;
+    if (!dlam || (tokens > 0 && (!y || !dy || !dx || !dr || !di)))
+        return fail(SFM_ERR_NULL, "%s: y, dy, dx, dr, di and dlam are required", fn);
+    const int e = io_bytes(io_dtype);
+    for (const void* t : {y, dy, (const void*)dx, (const void*)dr, (const void*)di})
+        if (!aligned_to(t, e)) return fail(SFM_ERR_ALIGN, "%s: y, dy or a gradient not aligned to its element", fn);
+    for (const void* t : {(const void*)h0, (const void*)dhT, (const void*)dh0, (const void*)dlam, (const void*)offsets})
+        if (!aligned_to(t, 4)) return fail(SFM_ERR_ALIGN, "%s: h0, dhT, dh0, dlam or offsets not aligned to its element", fn);
+    const int64_t need = sfm::plan_rec_bwd(rows, L, tokens, D, io_dtype);
+    st = check_workspace(fn, workspace, workspace_bytes, need);
+    if (st != SFM_OK) return st;
+    const int64_t nb = tokens * D * e, sb = rows * D * 4;
+    Ranges in, out;
+    in.add_inputs(x, r, i, lam, tokens, D, ldx, ldr, ldi, e);
+    in.add("offsets", offsets, (rows + 1) * 4);
+    in.add("h0", h0, sb);
+    in.add("y", y, nb);
+    in.add("dy", dy, nb);
+    in.add("dhT", dhT, sb);
+    out.add("dx", dx, nb);
+    out.add("dr", dr, nb);
+    out.add("di", di, nb);
+    out.add("dlam", dlam, D * 4);
+    out.add("dh0", dh0, sb);
+    out.add("workspace", workspace, need);
+    st = check_ranges(fn, in, out);
+    if (st != SFM_OK) return st;
+    sfm::RecParams p = params(x, r, i, lam, rows, L, tokens, D, ldx, ldr, ldi, c);
+    p.h0 = h0, p.offsets = offsets, p.y = const_cast<void*>(y), p.dy = dy, p.dhT = dhT;
+    p.dx = dx, p.dr = dr, p.di = di, p.dlam = dlam, p.dh0 = dh0;
+    p.w_lam = static_cast<float*>(workspace);
+    return hip_status(sfm::launch_rec_bwd(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
+}
+
+sfm_status sfm_gated_recurrence_step(const void* x, const void* r, const void* i, const float* lam, float* state,
+                                     const int32_t* slots, void* y, int64_t rows, int64_t pool, int64_t D, int64_t ldx,
+                                     int64_t ldr, int64_t ldi, float c, int io_dtype, void* stream) {
+    static const char* fn = "sfm_gated_recurrence_step";
+    sfm_status st = check_sizes(fn, rows, 1, rows, false, D, io_dtype);
+    if (st != SFM_OK) return st;
+    st = check_inputs(fn, x, r, i, lam, rows, D, ldx, ldr, ldi, c, io_dtype);
+    if (st != SFM_OK) return st;
+    if (!state || !y) return fail(SFM_ERR_NULL, "%s: state and y are required", fn);
+    if (!sane(pool, 1 << 24)) return fail(SFM_ERR_SHAPE, "%s: a pool of %lld states", fn, (long long)pool);
+    if (!slots && pool < rows)
+        return fail(SFM_ERR_SHAPE, "%s: %lld states for %lld rows (no slots)", fn, (long long)pool, (long long)rows);
+    const int e = io_bytes(io_dtype);
+    if (!aligned_to(state, 4) || !aligned_to(slots, 4) || !aligned_to(y, e))
+        return fail(SFM_ERR_ALIGN, "%s: state, slots or y not aligned to its element", fn);
+    Ranges in, out;
+    in.add_inputs(x, r, i, lam, rows, D, ldx, ldr, ldi, e);
+    in.add("slots", slots, rows * 4);
+    out.add("state", state, pool * D * 4);
+    out.add("y", y, rows * D * e);
+    st = check_ranges(fn, in, out);
+    if (st != SFM_OK) return st;
+    sfm::RecParams p = params(x, r, i, lam, rows, 1, rows, D, ldx, ldr, ldi, c);
+    p.hT = state, p.slots = slots, p.pool = pool, p.y = y;
+    return hip_status(sfm::launch_rec_step(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
+}
+
+}  // extern "C"
