@@ -1,0 +1,163 @@
+// rec_block.h -- what the forward and the backward of the gated linear recurrence share (gfx950): the place of a
+// workgroup among the rows, loads of a chunk, and the states handed from block to block.
+#pragma once
+
+#include "rec_gates.h"
+#include "sfm_rec.h"
+
+namespace sfm {
+
+// `lane` neighbouring channels of a token as they lie in memory: 4 bytes, or one bfloat16 where two are not aligned.
+template <typename T, int C> struct RecPack;
+template <> struct RecPack<__bf16, 2> {
+    uint32_t v;
+    static constexpr uint32_t kMinusInf = 0xff80ff80u;
+    __device__ __forceinline__ void load(const __bf16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ float get(int j) const { return __uint_as_float(j ? v & 0xffff0000u : v << 16); }
+    static __device__ __forceinline__ void store(__bf16* p, const float (&f)[2]) {
+        typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<bf2*>(p) = bf2{(__bf16)f[0], (__bf16)f[1]};
+    }
+};
+template <> struct RecPack<__bf16, 1> {
+    uint32_t v;
+    static constexpr uint32_t kMinusInf = 0xff80u;
+    __device__ __forceinline__ void load(const __bf16* p) { v = *reinterpret_cast<const uint16_t*>(p); }
+    __device__ __forceinline__ float get(int) const { return __uint_as_float(v << 16); }
+    static __device__ __forceinline__ void store(__bf16* p, const float (&f)[1]) { *p = (__bf16)f[0]; }
+};
+template <> struct RecPack<float, 1> {
+    uint32_t v;
+    static constexpr uint32_t kMinusInf = 0xff800000u;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ float get(int) const { return __uint_as_float(v); }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[1]) { *p = f[0]; }
+};
+
+// first token and length of row s; offsets outside the tokens (a caller's mistake) are cut to them
+__device__ __forceinline__ void rec_row(const RecParams& p, int s, int64_t& first, int& len) {
+    if (!p.offsets) {
+        first = (int64_t)s * p.L;
+        len = p.L;
+        return;
+    }
+    int64_t lo = p.offsets[s], hi = p.offsets[s + 1];
+    lo = lo < 0 ? 0 : (lo > p.tokens ? p.tokens : lo);
+    hi = hi < lo ? lo : (hi > p.tokens ? p.tokens : hi);
+    first = lo;
+    len = hi - lo > p.L ? p.L : (int)(hi - lo);
+}
+
+// Packed rows of several blocks: row s has the entries from first / block + s on, as many as it has blocks and one if it
+// has no token, so that entries of rows never meet and tokens / block + rows of them suffice.  The row of an entry is
+// the last one that starts at it or before, found by 64 lanes at a time.
+__device__ __forceinline__ int64_t rec_entry(const RecParams& p, int s, int block) {
+    int64_t lo = p.offsets[s];
+    lo = lo < 0 ? 0 : (lo > p.tokens ? p.tokens : lo);
+    return lo / block + s;
+}
+__device__ __forceinline__ int rec_row_of(const RecParams& p, int64_t entry, int block, int lane) {
+    int lo = 0, hi = p.rows;  // the row is in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64, s = lo + lane * step;
+        const uint64_t m = __ballot(s < hi && rec_entry(p, s, block) <= entry);
+        const int k = m ? 63 - __builtin_clzll(m) : 0;  // (entry 0 of row 0 or later: lane 0 is always in)
+        lo += k * step;
+        hi = hi < lo + step ? hi : lo + step;
+    }
+    return lo;
+}
+
+// A block takes a state h to A h + H.  Its word says so: A's bits (0 <= A <= 1, or NaN) and H's; kRecWhole in A's
+// place: H is the state after the block; all ones: nothing yet.  A word is written and read in one piece, so that no
+// other order of memory matters.
+constexpr uint32_t kRecEmpty = 0xffffffffu, kRecWhole = 0xbf800000u;  // (the latter -1: no A has its sign)
+template <bool BACK> constexpr int kRecWindow = BACK ? 4 : 8;  // (what the backward holds leaves it fewer registers)
+
+__device__ __forceinline__ void rec_publish(uint64_t* at, uint32_t tag, float h) {
+    __hip_atomic_store(at, (uint64_t)__float_as_uint(h) << 32 | tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t rec_factor(float a) { return a == a ? __float_as_uint(a) & 0x7fffffffu : 0x7fc00000u; }
+
+// The state before a block from the words of those before it in the walk (`before` of them, `step` apart, the first
+// the nearest; the farthest is always whole in the end).  From the nearest whole one on the words are applied in the
+// order of the walk, one after the other as their owners do: the same bits wherever the whole one is found.
+// Every wait ends: tickets are drawn in the order of the walk, so the blocks waited for run already or are through, the
+// first waits for none, and every workgroup of packed rows says in the end that its word is whole, whatever a caller's
+// offsets make of its place.  The limit is far beyond any wait; past it the state is NaN.
+template <bool BACK>
+__device__ __forceinline__ float rec_look_back(const uint64_t* near, int64_t step, int before) {
+    const int n = before < kRecWindow<BACK> ? before : kRecWindow<BACK>;
+    for (int polls = 0; polls < 1 << 24; ++polls) {
+        uint64_t w[kRecWindow<BACK>];
+#pragma unroll
+        for (int k = 0; k < kRecWindow<BACK>; ++k)
+            w[k] = k < n ? __hip_atomic_load(near + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : ~0ull;
+        int whole = -1;
+        bool open = true;
+#pragma unroll
+        for (int k = 0; k < kRecWindow<BACK>; ++k) {
+            const uint32_t tag = (uint32_t)w[k];
+            if (open && tag == kRecWhole) whole = k;
+            open = open && tag != kRecWhole && tag != kRecEmpty;
+        }
+        if (whole >= 0) {
+            float h = 0.0f;
+#pragma unroll
+            for (int k = kRecWindow<BACK> - 1; k >= 0; --k) {
+                const float H = __uint_as_float((uint32_t)(w[k] >> 32));
+                if (k == whole) h = H;
+                if (k < whole) h = __builtin_fmaf(__uint_as_float((uint32_t)w[k]), h, H);
+            }
+            return h;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return __uint_as_float(0x7fc00000u);
+}
+
+// The place of a workgroup: its tile, and for rows of several blocks its block by ticket.
+struct RecPlace {
+    int tile;
+    int64_t entry;   // several blocks: of w_words and w_lam; else the workgroup along the rows
+    int row, block;  // several blocks (row < 0: none; block past its row's: nothing to do but say so)
+};
+template <bool BACK>
+__device__ __forceinline__ RecPlace rec_place(const RecParams& p, uint32_t* shared, int64_t& first, int& len) {
+    const RecPlan& q = p.plan;
+    RecPlace at;
+    at.tile = blockIdx.x % (unsigned)q.tiles;
+    const unsigned rest = blockIdx.x / (unsigned)q.tiles;
+    const unsigned g = rest % (unsigned)q.groups;
+    const int block = q.nt * kRecChunk;
+    if (threadIdx.x < 64) {  // (a whole wave: rows are searched by 64 lanes)
+        uint32_t ticket = 0;
+        if (threadIdx.x == 0)
+            ticket = __hip_atomic_fetch_add(p.w_tickets + 16 * ((int64_t)at.tile * q.groups + g), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+        ticket = __builtin_amdgcn_readfirstlane(ticket);
+        if (p.offsets) shared[1] = rec_row_of(p, BACK ? q.entries - 1 - ticket : ticket, block, threadIdx.x);
+        shared[0] = ticket;
+    }
+    __syncthreads();
+    const uint32_t ticket = __builtin_amdgcn_readfirstlane(shared[0]);
+    if (!p.offsets) {
+        // equal rows: the rows of a group side by side, block after block
+        const uint32_t rows = ((unsigned)p.rows + q.groups - 1) / q.groups;
+        const int j = (int)(ticket / rows);
+        at.row = (int)(ticket % rows) * q.groups + (int)g;
+        if (at.row >= p.rows) at.row = -1;
+        at.block = BACK ? q.blocks - 1 - j : j;
+        at.entry = (int64_t)at.row * q.blocks + at.block;
+        first = (int64_t)at.row * p.L;
+        len = p.L;
+    } else {
+        at.entry = BACK ? q.entries - 1 - ticket : ticket;
+        at.row = (int)__builtin_amdgcn_readfirstlane(shared[1]);
+        rec_row(p, at.row, first, len);
+        const int64_t j = at.entry - rec_entry(p, at.row, block);
+        at.block = j < 0 || j > 1 << 24 ? 1 << 24 : (int)j;  // (j < 0: offsets that fall, a caller's mistake)
+    }
+    return at;
+}
+
+}  // namespace sfm

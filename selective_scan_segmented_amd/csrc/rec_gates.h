@@ -28,8 +28,11 @@ __device__ __forceinline__ float rec_sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// -c softplus(lam) log2(e), a channel's constant.
-__device__ __forceinline__ float rec_rate(float lam, float c) { return -c * softplus_log2e(lam); }
+// -c softplus(lam) log2(e), a channel's constant; finite, so that a shut gate keeps the state at any rate.
+__device__ __forceinline__ float rec_rate(float lam, float c) {
+    const float rate = -c * softplus_log2e(lam);
+    return rate < -3e38f ? -3e38f : rate;
+}
 
 // 1 - a^2 from la2 = log2(a) <= 0 and a itself.  The series' first omitted term and the rounding of 1 - a a meet at
 // the threshold: EXACT (float32 tensors) z = 2 la > -1/2, eight terms, 2^-26 and 2^-22; else z > -1/16, four terms,

@@ -6,6 +6,20 @@
 
 namespace sfm {
 
+// How a call's rows are cut (plan_rec): a workgroup is nr rows x nt chunks of kRecChunk tokens x nc lanes of `lane`
+// channels.  Rows longer than nt chunks are cut into blocks of that many, a workgroup each, which hand their states on
+// through the workspace.
+constexpr int kRecChunk = 8;
+struct RecPlan {
+    int lane, nc, nt, nr, tiles;  // tiles: workgroups side by side over the channels
+    int multi;                    // rows of several blocks
+    int blocks;                   // equal rows: blocks to a row (1 with packed rows)
+    int groups;                   // several blocks: ticket counters to a tile
+    int64_t entries;              // blocks of all rows; one block: workgroups along the rows
+    int64_t launch;               // workgroups
+    int64_t bytes_words, bytes;   // workspace: tickets and words; with the backward's parts of dlam
+};
+
 // One call's rows, channels and strides (forward, backward and the step).
 struct RecParams {
     const void* x;           // token t, channel d: x + t * ldx + d (elements)
@@ -26,26 +40,17 @@ struct RecParams {
     void *dx, *dr, *di;      // [tokens][D]
     float* dlam;             // [D]
     float* dh0;              // [rows][D] or null
-    float* w_lam;            // workspace: [rows][D], every row's part of dlam
+    // workspace
+    uint32_t* w_tickets;     // [tiles][groups], 64 bytes apart
+    uint64_t* w_words;       // [entries][tiles * nc * lane]: what a block makes of a state (rec_block.h)
+    float* w_lam;            // [entries][D]: parts of dlam
+    RecPlan plan;
 };
 
-// first token and length of row s; offsets outside the tokens (a caller's mistake) are cut to them
-__device__ __forceinline__ void rec_row(const RecParams& p, int s, int64_t& first, int& len) {
-    if (!p.offsets) {
-        first = (int64_t)s * p.L;
-        len = p.L;
-        return;
-    }
-    int64_t lo = p.offsets[s], hi = p.offsets[s + 1];
-    lo = lo < 0 ? 0 : (lo > p.tokens ? p.tokens : lo);
-    hi = hi < lo ? lo : (hi > p.tokens ? p.tokens : hi);
-    first = lo;
-    len = hi - lo > p.L ? p.L : (int)(hi - lo);
-}
-
-// Workspace bytes of the calls.
-int64_t plan_rec_fwd(int64_t rows, int64_t L, int64_t tokens, int64_t D, int io_dtype);
-int64_t plan_rec_bwd(int64_t rows, int64_t L, int64_t tokens, int64_t D, int io_dtype);
+// Cuts a call; `lane`: channels to a lane (rec_wide, or one).
+RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, int lane, bool back);
+// Channels to a lane: 4 bytes where the sizes, strides and addresses allow it, else one.
+inline int rec_wide(int io_dtype) { return io_dtype == 0 ? 1 : 2; }
 hipError_t launch_rec_fwd(const RecParams& p, int io_dtype, hipStream_t s);
 hipError_t launch_rec_bwd(const RecParams& p, int io_dtype, hipStream_t s);
 hipError_t launch_rec_step(const RecParams& p, int io_dtype, hipStream_t s);

@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "sfm_api_util.h"
 #include "sfm_rec.h"
 
@@ -20,11 +22,44 @@ sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, 
     if (!packed && tokens != rows * L)
         return fail(SFM_ERR_SHAPE, "%s: %lld tokens are not rows=%lld of L=%lld", fn, (long long)tokens,
                     (long long)rows, (long long)L);
-    // a launch holds fewer than 2^32 work items
+    // a launch holds fewer than 2^32 work items (the step's: 256 channels of a row to a workgroup; the rows': plan)
     if (rows * ((D + 255) / 256) >= 1 << 24)
         return fail(SFM_ERR_SHAPE, "%s: rows=%lld of %lld channels are more workgroups than a launch holds", fn,
                     (long long)rows, (long long)D);
     return SFM_OK;
+}
+
+// The workspace of a call, wide or not (which the alignment of its tensors decides); -1: more than a launch holds.
+int64_t need_of(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, int io_dtype, bool back) {
+    int64_t need = 0;
+    for (int lane : {1, sfm::rec_wide(io_dtype)}) {
+        if (D % lane) continue;
+        const sfm::RecPlan q = sfm::plan_rec(rows, L, tokens, D, packed, lane, back);
+        if (q.launch * (q.nr * q.nt * q.nc) >= 1LL << 32 || q.bytes_words >= 1LL << 40) return -1;
+        if (q.bytes > need) need = q.bytes;
+    }
+    return need;
+}
+
+// The size queries do not say whether rows are packed: the larger of both.
+int64_t need_of_either(int64_t rows, int64_t L, int64_t tokens, int64_t D, int io_dtype, bool back) {
+    const int64_t a = need_of(rows, L, tokens, D, true, io_dtype, back);
+    const int64_t b = tokens == rows * L ? need_of(rows, L, tokens, D, false, io_dtype, back) : 0;
+    return a < 0 || b < 0 ? -1 : a > b ? a : b;
+}
+
+sfm_status too_large(const char* fn, int64_t rows, int64_t tokens, int64_t D) {
+    return fail(SFM_ERR_SHAPE, "%s: rows=%lld of %lld tokens and %lld channels are more workgroups than a launch holds", fn,
+                (long long)rows, (long long)tokens, (long long)D);
+}
+
+// Cuts the call and gives it its workspace.
+void take_plan(sfm::RecParams& p, bool wide, int io_dtype, bool back, void* workspace) {
+    p.plan = sfm::plan_rec(p.rows, p.L, p.tokens, p.D, p.offsets != nullptr, wide ? sfm::rec_wide(io_dtype) : 1, back);
+    char* at = static_cast<char*>(workspace);
+    p.w_tickets = reinterpret_cast<uint32_t*>(at);
+    p.w_words = reinterpret_cast<uint64_t*>(at + (int64_t)p.plan.tiles * p.plan.groups * 64);
+    p.w_lam = reinterpret_cast<float*>(at + p.plan.bytes_words);
 }
 
 sfm_status check_inputs(const char* fn, const void* x, const void* r, const void* i, const float* lam, int64_t tokens,
@@ -39,6 +74,15 @@ sfm_status check_inputs(const char* fn, const void* x, const void* r, const void
     if (!aligned_to(x, e) || !aligned_to(r, e) || !aligned_to(i, e) || !aligned_to(lam, 4))
         return fail(SFM_ERR_ALIGN, "%s: an input is not aligned to its element", fn);
     return SFM_OK;
+}
+
+// Whether every token's channels can be taken 8 bytes at a time.
+bool wide_tokens(std::initializer_list<const void*> tensors, std::initializer_list<int64_t> strides, int io_dtype) {
+    for (const void* t : tensors)
+        if (!aligned_to(t, 8)) return false;
+    for (int64_t ld : strides)
+        if (ld % sfm::rec_wide(io_dtype)) return false;
+    return true;
 }
 
 struct Ranges {
@@ -98,7 +142,9 @@ sfm_status sfm_gated_recurrence_fwd_ws_size(int64_t rows, int64_t L, int64_t tok
     if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
     const sfm_status st = check_sizes(fn, rows, L, tokens, true, D, io_dtype);
     if (st != SFM_OK) return st;
-    *bytes = sfm::plan_rec_fwd(rows, L, tokens, D, io_dtype);
+    const int64_t need = need_of_either(rows, L, tokens, D, io_dtype, false);
+    if (need < 0) return too_large(fn, rows, tokens, D);
+    *bytes = need;
     return ok();
 }
 
@@ -108,7 +154,9 @@ sfm_status sfm_gated_recurrence_bwd_ws_size(int64_t rows, int64_t L, int64_t tok
     if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
     const sfm_status st = check_sizes(fn, rows, L, tokens, true, D, io_dtype);
     if (st != SFM_OK) return st;
-    *bytes = sfm::plan_rec_bwd(rows, L, tokens, D, io_dtype);
+    const int64_t need = need_of_either(rows, L, tokens, D, io_dtype, true);
+    if (need < 0) return too_large(fn, rows, tokens, D);
+    *bytes = need;
     return ok();
 }
 
@@ -125,7 +173,8 @@ sfm_status sfm_gated_recurrence_fwd(const void* x, const void* r, const void* i,
     const int e = io_bytes(io_dtype);
     if (!aligned_to(h0, 4) || !aligned_to(hT, 4) || !aligned_to(offsets, 4) || !aligned_to(y, e))
         return fail(SFM_ERR_ALIGN, "%s: h0, hT, offsets or y not aligned to its element", fn);
-    const int64_t need = sfm::plan_rec_fwd(rows, L, tokens, D, io_dtype);
+    const int64_t need = need_of(rows, L, tokens, D, offsets != nullptr, io_dtype, false);
+    if (need < 0) return too_large(fn, rows, tokens, D);
     st = check_workspace(fn, workspace, workspace_bytes, need);
     if (st != SFM_OK) return st;
     Ranges in, out;
@@ -139,6 +188,7 @@ sfm_status sfm_gated_recurrence_fwd(const void* x, const void* r, const void* i,
     if (st != SFM_OK) return st;
     sfm::RecParams p = params(x, r, i, lam, rows, L, tokens, D, ldx, ldr, ldi, c);
     p.h0 = h0, p.y = y, p.hT = hT, p.offsets = offsets;
+    take_plan(p, wide_tokens({x, r, i, y}, {ldx, ldr, ldi, D}, io_dtype), io_dtype, false, workspace);
     return hip_status(sfm::launch_rec_fwd(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
 }
 
@@ -159,7 +209,8 @@ sfm_status sfm_gated_recurrence_bwd(const void* x, const void* r, const void* i,
         if (!aligned_to(t, e)) return fail(SFM_ERR_ALIGN, "%s: y, dy or a gradient not aligned to its element", fn);
     for (const void* t : {(const void*)h0, (const void*)dhT, (const void*)dh0, (const void*)dlam, (const void*)offsets})
         if (!aligned_to(t, 4)) return fail(SFM_ERR_ALIGN, "%s: h0, dhT, dh0, dlam or offsets not aligned to its element", fn);
-    const int64_t need = sfm::plan_rec_bwd(rows, L, tokens, D, io_dtype);
+    const int64_t need = need_of(rows, L, tokens, D, offsets != nullptr, io_dtype, true);
+    if (need < 0) return too_large(fn, rows, tokens, D);
     st = check_workspace(fn, workspace, workspace_bytes, need);
     if (st != SFM_OK) return st;
     const int64_t nb = tokens * D * e, sb = rows * D * 4;
@@ -181,7 +232,7 @@ sfm_status sfm_gated_recurrence_bwd(const void* x, const void* r, const void* i,
     sfm::RecParams p = params(x, r, i, lam, rows, L, tokens, D, ldx, ldr, ldi, c);
     p.h0 = h0, p.offsets = offsets, p.y = const_cast<void*>(y), p.dy = dy, p.dhT = dhT;
     p.dx = dx, p.dr = dr, p.di = di, p.dlam = dlam, p.dh0 = dh0;
-    p.w_lam = static_cast<float*>(workspace);
+    take_plan(p, wide_tokens({x, r, i, y, dy, dx, dr, di}, {ldx, ldr, ldi, D}, io_dtype), io_dtype, true, workspace);
     return hip_status(sfm::launch_rec_bwd(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
 }
 
