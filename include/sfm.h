@@ -467,7 +467,7 @@ sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G
  * h float32, zero (or h0) before the row's first token.
  *
  * sfm_gated_recurrence_fwd -- whole rows.
- *   x, r, i  [tokens, D] io        token strides ldx, ldr, ldi (elements, D to 2^22)
+ *   x, r, i  [tokens, D] io        token strides ldx, ldr, ldi (elements, D to 2^20)
  *   lam      [D] f32;  c > 0 (8 is usual)
  *   h0       [rows, D] f32 or NULL (zero)
  *   y        [tokens, D] io, contiguous
@@ -476,8 +476,8 @@ sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G
  *   offsets  as for sfm_gated_delta_fwd: NULL for equal rows (tokens == rows * L), or
  *            int32 [rows + 1] on the device; L bounds the longest row, offsets outside
  *            the tokens are cut to them, tokens of no row and those past L keep their old y
- *   D 1..65536.  Tensors need their element's alignment only; rows on 16 bytes with D a
- *   multiple of 16 bytes are loaded in wider pieces.
+ *   D 1..65536.  Tensors need their element's alignment only; bfloat16 ones of even D and
+ *   strides on 4 bytes are loaded two channels at a time, others one by one.
  * A non-finite value of a token stays in its row and channel.  Repeated calls give the same bits.
  * workspace: at least sfm_gated_recurrence_fwd_ws_size() bytes (may be NULL when that is
  *   0), 16-byte aligned, owned by the caller.

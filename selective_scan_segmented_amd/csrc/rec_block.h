@@ -7,31 +7,42 @@
 
 namespace sfm {
 
+// A run of tokens in memory as a buffer: a lane's byte offset, and a token's, which all lanes share, as the other part of
+// the address, so that a token costs a lane no address of its own.  (The range check is not used: lanes without a
+// token do not load.)
+struct RecBuf {
+    __amdgpu_buffer_rsrc_t r;
+};
+template <typename T>
+__device__ __forceinline__ RecBuf rec_buf(const void* base, int64_t first) {
+    return RecBuf{__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(static_cast<const T*>(base) + first), 0, -1, 0x00027000)};
+}
+
 // `lane` neighbouring channels of a token as they lie in memory: 4 bytes, or one bfloat16 where two are not aligned.
-template <typename T, int C> struct RecPack;
-template <> struct RecPack<__bf16, 2> {
+template <typename T, int C> struct RecPack {
     uint32_t v;
-    static constexpr uint32_t kMinusInf = 0xff80ff80u;
-    __device__ __forceinline__ void load(const __bf16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
-    __device__ __forceinline__ float get(int j) const { return __uint_as_float(j ? v & 0xffff0000u : v << 16); }
-    static __device__ __forceinline__ void store(__bf16* p, const float (&f)[2]) {
-        typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-        *reinterpret_cast<bf2*>(p) = bf2{(__bf16)f[0], (__bf16)f[1]};
+    static constexpr bool kHalf = sizeof(T) * C == 2;
+    static constexpr uint32_t kMinusInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+    __device__ __forceinline__ void load(const RecBuf& b, uint32_t at, uint32_t token) {
+        if constexpr (kHalf)
+            v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b.r, at, token, 0);
+        else
+            v = __builtin_amdgcn_raw_buffer_load_b32(b.r, at, token, 0);
     }
-};
-template <> struct RecPack<__bf16, 1> {
-    uint32_t v;
-    static constexpr uint32_t kMinusInf = 0xff80u;
-    __device__ __forceinline__ void load(const __bf16* p) { v = *reinterpret_cast<const uint16_t*>(p); }
-    __device__ __forceinline__ float get(int) const { return __uint_as_float(v << 16); }
-    static __device__ __forceinline__ void store(__bf16* p, const float (&f)[1]) { *p = (__bf16)f[0]; }
-};
-template <> struct RecPack<float, 1> {
-    uint32_t v;
-    static constexpr uint32_t kMinusInf = 0xff800000u;
-    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const uint32_t*>(p); }
-    __device__ __forceinline__ float get(int) const { return __uint_as_float(v); }
-    static __device__ __forceinline__ void store(float* p, const float (&f)[1]) { *p = f[0]; }
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(v);
+        return __uint_as_float(j ? v & 0xffff0000u : v << 16);
+    }
+    static __device__ __forceinline__ void store(const RecBuf& b, uint32_t at, uint32_t token, const float (&f)[C]) {
+        if constexpr (kHalf) {
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)f[0]), b.r, at, token, 0);
+        } else if constexpr (C == 2) {
+            typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, bf2{(__bf16)f[0], (__bf16)f[1]}), b.r, at, token, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), b.r, at, token, 0);
+        }
+    }
 };
 
 // first token and length of row s; offsets outside the tokens (a caller's mistake) are cut to them
@@ -70,33 +81,33 @@ __device__ __forceinline__ int rec_row_of(const RecParams& p, int64_t entry, int
 
 // A block takes a state h to A h + H.  Its word says so: A's bits (0 <= A <= 1, or NaN) and H's; kRecWhole in A's
 // place: H is the state after the block; all ones: nothing yet.  A word is written and read in one piece, so that no
-// other order of memory matters.
+// other order of memory matters.  A tile's words lie entry by entry, kRecWords to an entry (of the channels side by side in a workgroup, at most 32 lanes').
+template <int C> constexpr int kRecWords = 32 * C;
 constexpr uint32_t kRecEmpty = 0xffffffffu, kRecWhole = 0xbf800000u;  // (the latter -1: no A has its sign)
-template <bool BACK> constexpr int kRecWindow = BACK ? 4 : 8;  // (what the backward holds leaves it fewer registers)
 
 __device__ __forceinline__ void rec_publish(uint64_t* at, uint32_t tag, float h) {
     __hip_atomic_store(at, (uint64_t)__float_as_uint(h) << 32 | tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ uint32_t rec_factor(float a) { return a == a ? __float_as_uint(a) & 0x7fffffffu : 0x7fc00000u; }
 
-// The state before a block from the words of those before it in the walk (`before` of them, `step` apart, the first
-// the nearest; the farthest is always whole in the end).  From the nearest whole one on the words are applied in the
-// order of the walk, one after the other as their owners do: the same bits wherever the whole one is found.
+// The state before a block from the words of those before it in the walk (`before` of them, the first the nearest; the
+// farthest is always whole in the end).  From the nearest whole one on the words are applied in the order of the walk,
+// one after the other as their owners do: the same bits wherever the whole one is found.
 // Every wait ends: tickets are drawn in the order of the walk, so the blocks waited for run already or are through, the
 // first waits for none, and every workgroup of packed rows says in the end that its word is whole, whatever a caller's
 // offsets make of its place.  The limit is far beyond any wait; past it the state is NaN.
-template <bool BACK>
-__device__ __forceinline__ float rec_look_back(const uint64_t* near, int64_t step, int before) {
-    const int n = before < kRecWindow<BACK> ? before : kRecWindow<BACK>;
+template <bool BACK, int WINDOW, int WORDS>
+__device__ __forceinline__ float rec_look_back(const uint64_t* word, int before) {
+    const int n = before < WINDOW ? before : WINDOW;
     for (int polls = 0; polls < 1 << 24; ++polls) {
-        uint64_t w[kRecWindow<BACK>];
+        uint64_t w[WINDOW];
 #pragma unroll
-        for (int k = 0; k < kRecWindow<BACK>; ++k)
-            w[k] = k < n ? __hip_atomic_load(near + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : ~0ull;
+        for (int k = 0; k < WINDOW; ++k)
+            w[k] = k < n ? __hip_atomic_load(word + (BACK ? k + 1 : -k - 1) * WORDS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : ~0ull;
         int whole = -1;
         bool open = true;
 #pragma unroll
-        for (int k = 0; k < kRecWindow<BACK>; ++k) {
+        for (int k = 0; k < WINDOW; ++k) {
             const uint32_t tag = (uint32_t)w[k];
             if (open && tag == kRecWhole) whole = k;
             open = open && tag != kRecWhole && tag != kRecEmpty;
@@ -104,7 +115,7 @@ __device__ __forceinline__ float rec_look_back(const uint64_t* near, int64_t ste
         if (whole >= 0) {
             float h = 0.0f;
 #pragma unroll
-            for (int k = kRecWindow<BACK> - 1; k >= 0; --k) {
+            for (int k = WINDOW - 1; k >= 0; --k) {
                 const float H = __uint_as_float((uint32_t)(w[k] >> 32));
                 if (k == whole) h = H;
                 if (k < whole) h = __builtin_fmaf(__uint_as_float((uint32_t)w[k]), h, H);
@@ -116,46 +127,64 @@ __device__ __forceinline__ float rec_look_back(const uint64_t* near, int64_t ste
     return __uint_as_float(0x7fc00000u);
 }
 
-// The place of a workgroup: its tile, and for rows of several blocks its block by ticket.
-struct RecPlace {
+// What a workgroup works on: a block of a row, or nr rows side by side.
+struct RecItem {
     int tile;
-    int64_t entry;   // several blocks: of w_words and w_lam; else the workgroup along the rows
-    int row, block;  // several blocks (row < 0: none; block past its row's: nothing to do but say so)
+    int row;            // the (first) row
+    int block, blocks;  // of the row: which, and how many (one where it has no token; none: a block that no row has)
+    int64_t entry;      // of w_words and w_lam
+    int64_t first;      // the (first) row's first token
+    int len;            // and length
 };
-template <bool BACK>
-__device__ __forceinline__ RecPlace rec_place(const RecParams& p, uint32_t* shared, int64_t& first, int& len) {
+
+// Rows of one block.
+__device__ __forceinline__ RecItem rec_item(const RecParams& p) {
     const RecPlan& q = p.plan;
-    RecPlace at;
-    at.tile = blockIdx.x % (unsigned)q.tiles;
-    const unsigned rest = blockIdx.x / (unsigned)q.tiles;
-    const unsigned g = rest % (unsigned)q.groups;
+    RecItem at;
+    at.tile = (int)(blockIdx.x % (unsigned)q.tiles);
+    at.entry = blockIdx.x / (unsigned)q.tiles;
+    at.row = (int)at.entry * q.nr;
+    at.block = 0, at.blocks = 1;
+    rec_row(p, at.row, at.first, at.len);
+    return at;
+}
+
+// Rows of several blocks: the next block of the walk, by ticket.  (One barrier.)
+template <bool BACK>
+__device__ __forceinline__ RecItem rec_draw(const RecParams& p, uint32_t (&shared)[2]) {
+    const RecPlan& q = p.plan;
+    RecItem at;
+    at.tile = (int)(blockIdx.x % (unsigned)q.tiles);
+    const unsigned group = blockIdx.x / (unsigned)q.tiles % (unsigned)q.groups;
     const int block = q.nt * kRecChunk;
     if (threadIdx.x < 64) {  // (a whole wave: rows are searched by 64 lanes)
         uint32_t ticket = 0;
         if (threadIdx.x == 0)
-            ticket = __hip_atomic_fetch_add(p.w_tickets + 16 * ((int64_t)at.tile * q.groups + g), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+            ticket = __hip_atomic_fetch_add(p.w_tickets + 16 * ((int64_t)at.tile * q.groups + group), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
         ticket = __builtin_amdgcn_readfirstlane(ticket);
         if (p.offsets) shared[1] = rec_row_of(p, BACK ? q.entries - 1 - ticket : ticket, block, threadIdx.x);
         shared[0] = ticket;
     }
-    __syncthreads();
+    lds_barrier();
     const uint32_t ticket = __builtin_amdgcn_readfirstlane(shared[0]);
     if (!p.offsets) {
-        // equal rows: the rows of a group side by side, block after block
+        // equal rows: those of a group side by side, block after block
         const uint32_t rows = ((unsigned)p.rows + q.groups - 1) / q.groups;
         const int j = (int)(ticket / rows);
-        at.row = (int)(ticket % rows) * q.groups + (int)g;
-        if (at.row >= p.rows) at.row = -1;
+        at.row = (int)(ticket % rows) * q.groups + (int)group;
         at.block = BACK ? q.blocks - 1 - j : j;
+        at.blocks = at.row < p.rows ? q.blocks : 0;
         at.entry = (int64_t)at.row * q.blocks + at.block;
-        first = (int64_t)at.row * p.L;
-        len = p.L;
+        at.first = (int64_t)at.row * p.L;
+        at.len = p.L;
     } else {
         at.entry = BACK ? q.entries - 1 - ticket : ticket;
-        at.row = (int)__builtin_amdgcn_readfirstlane(shared[1]);
-        rec_row(p, at.row, first, len);
+        at.row = __builtin_amdgcn_readfirstlane(shared[1]);
+        rec_row(p, at.row, at.first, at.len);
+        at.blocks = at.len > 0 ? (at.len + block - 1) / block : 1;
         const int64_t j = at.entry - rec_entry(p, at.row, block);
-        at.block = j < 0 || j > 1 << 24 ? 1 << 24 : (int)j;  // (j < 0: offsets that fall, a caller's mistake)
+        at.block = (int)j;
+        if (j < 0 || j >= at.blocks) at.block = at.blocks = 0;  // (j < 0: tokens before the first row, or offsets that fall)
     }
     return at;
 }

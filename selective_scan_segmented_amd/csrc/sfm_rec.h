@@ -7,15 +7,15 @@
 namespace sfm {
 
 // How a call's rows are cut (plan_rec): a workgroup is nr rows x nt chunks of kRecChunk tokens x nc lanes of `lane`
-// channels.  Rows longer than nt chunks are cut into blocks of that many, a workgroup each, which hand their states on
-// through the workspace.
+// channels.  Rows longer than nt chunks are cut into blocks of that many, a workgroup each (hand), which hand their
+// states on through the workspace.
 constexpr int kRecChunk = 8;
 struct RecPlan {
     int lane, nc, nt, nr, tiles;  // tiles: workgroups side by side over the channels
-    int multi;                    // rows of several blocks
-    int blocks;                   // equal rows: blocks to a row (1 with packed rows)
-    int groups;                   // several blocks: ticket counters to a tile
-    int64_t entries;              // blocks of all rows; one block: workgroups along the rows
+    int hand;
+    int blocks;                   // hand, equal rows: blocks to a row
+    int groups;                   // hand: ticket counters to a tile
+    int64_t entries;              // hand: blocks of all rows; else: workgroups along the rows
     int64_t launch;               // workgroups
     int64_t bytes_words, bytes;   // workspace: tickets and words; with the backward's parts of dlam
 };
@@ -42,13 +42,14 @@ struct RecParams {
     float* dh0;              // [rows][D] or null
     // workspace
     uint32_t* w_tickets;     // [tiles][groups], 64 bytes apart
-    uint64_t* w_words;       // [entries][tiles * nc * lane]: what a block makes of a state (rec_block.h)
+    uint64_t* w_words;       // [tiles][entries][32 lanes' channels]: what a block makes of a state (rec_block.h)
     float* w_lam;            // [entries][D]: parts of dlam
     RecPlan plan;
 };
 
-// Cuts a call; `lane`: channels to a lane (rec_wide, or one).
-RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, int lane, bool back);
+// Cuts a call; near: the largest token stride is below 2^21 bytes (so that the 2048 tokens of nr rows end below 2^32); lane: channels to a lane (rec_wide, or one).
+RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, bool near, int lane, bool back);
+constexpr int64_t kRecMaxStride = 1 << 20;  // (a block's 512 tokens then end below 2^31 bytes)
 // Channels to a lane: 4 bytes where the sizes, strides and addresses allow it, else one.
 inline int rec_wide(int io_dtype) { return io_dtype == 0 ? 1 : 2; }
 hipError_t launch_rec_fwd(const RecParams& p, int io_dtype, hipStream_t s);

@@ -29,14 +29,16 @@ sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, 
     return SFM_OK;
 }
 
-// The workspace of a call, wide or not (which the alignment of its tensors decides); -1: more than a launch holds.
+// The workspace of a call, wide or near or not (which its tensors' places and strides decide); -1: more than a launch holds.
 int64_t need_of(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, int io_dtype, bool back) {
     int64_t need = 0;
     for (int lane : {1, sfm::rec_wide(io_dtype)}) {
         if (D % lane) continue;
-        const sfm::RecPlan q = sfm::plan_rec(rows, L, tokens, D, packed, lane, back);
-        if (q.launch * (q.nr * q.nt * q.nc) >= 1LL << 32 || q.bytes_words >= 1LL << 40) return -1;
-        if (q.bytes > need) need = q.bytes;
+        for (bool near : {false, true}) {
+            const sfm::RecPlan q = sfm::plan_rec(rows, L, tokens, D, packed, near, lane, back);
+            if (q.launch >= 1LL << 24 || q.bytes_words >= 1LL << 40) return -1;
+            if (q.bytes > need) need = q.bytes;
+        }
     }
     return need;
 }
@@ -55,7 +57,10 @@ sfm_status too_large(const char* fn, int64_t rows, int64_t tokens, int64_t D) {
 
 // Cuts the call and gives it its workspace.
 void take_plan(sfm::RecParams& p, bool wide, int io_dtype, bool back, void* workspace) {
-    p.plan = sfm::plan_rec(p.rows, p.L, p.tokens, p.D, p.offsets != nullptr, wide ? sfm::rec_wide(io_dtype) : 1, back);
+    int64_t most = p.D;
+    for (int64_t ld : {p.ldx, p.ldr, p.ldi}) most = ld > most ? ld : most;
+    const bool near = most * io_bytes(io_dtype) < 1 << 21;
+    p.plan = sfm::plan_rec(p.rows, p.L, p.tokens, p.D, p.offsets != nullptr, near, wide ? sfm::rec_wide(io_dtype) : 1, back);
     char* at = static_cast<char*>(workspace);
     p.w_tickets = reinterpret_cast<uint32_t*>(at);
     p.w_words = reinterpret_cast<uint64_t*>(at + (int64_t)p.plan.tiles * p.plan.groups * 64);
@@ -66,7 +71,7 @@ sfm_status check_inputs(const char* fn, const void* x, const void* r, const void
                         int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, float c, int io_dtype) {
     if (!lam || (tokens > 0 && (!x || !r || !i))) return fail(SFM_ERR_NULL, "%s: x, r, i and lam are required", fn);
     for (int64_t ld : {ldx, ldr, ldi})
-        if (ld < D || ld > 1 << 22)
+        if (ld < D || ld > sfm::kRecMaxStride)
             return fail(SFM_ERR_SHAPE, "%s: token strides %lld, %lld, %lld below D=%lld (or too large)", fn,
                         (long long)ldx, (long long)ldr, (long long)ldi, (long long)D);
     if (!(c > 0.0f && c <= 1e6f)) return fail(SFM_ERR_SHAPE, "%s: c=%g", fn, (double)c);
@@ -76,10 +81,10 @@ sfm_status check_inputs(const char* fn, const void* x, const void* r, const void
     return SFM_OK;
 }
 
-// Whether every token's channels can be taken 8 bytes at a time.
+// Whether every token's channels can be taken 4 bytes at a time.
 bool wide_tokens(std::initializer_list<const void*> tensors, std::initializer_list<int64_t> strides, int io_dtype) {
     for (const void* t : tensors)
-        if (!aligned_to(t, 8)) return false;
+        if (!aligned_to(t, 4)) return false;
     for (int64_t ld : strides)
         if (ld % sfm::rec_wide(io_dtype)) return false;
     return true;
