@@ -467,7 +467,7 @@ sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G
  * h float32, zero (or h0) before the row's first token.
  *
  * sfm_gated_recurrence_fwd -- whole rows.
- *   x, r, i  [tokens, D] io        token strides ldx, ldr, ldi (elements, D to 2^20)
+ *   x, r, i  [tokens, D] io        token strides ldx, ldr, ldi (elements, D to 2^19)
  *   lam      [D] f32;  c > 0 (8 is usual)
  *   h0       [rows, D] f32 or NULL (zero)
  *   y        [tokens, D] io, contiguous

@@ -14,8 +14,9 @@ struct RecBuf {
     __amdgpu_buffer_rsrc_t r;
 };
 template <typename T>
-__device__ __forceinline__ RecBuf rec_buf(const void* base, int64_t first) {
-    return RecBuf{__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(static_cast<const T*>(base) + first), 0, -1, 0x00027000)};
+__device__ __forceinline__ RecBuf rec_buf(const void* base, uint32_t token, uint32_t ld, int back = 0) {
+    const T* at = static_cast<const T*>(base) + (int64_t)((uint64_t)token * ld) - back;
+    return RecBuf{__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, -1, 0x00027000)};
 }
 
 // `lane` neighbouring channels of a token as they lie in memory: 4 bytes, or one bfloat16 where two are not aligned.
@@ -46,28 +47,29 @@ template <typename T, int C> struct RecPack {
 };
 
 // first token and length of row s; offsets outside the tokens (a caller's mistake) are cut to them
-__device__ __forceinline__ void rec_row(const RecParams& p, int s, int64_t& first, int& len) {
+__device__ __forceinline__ void rec_row(const RecParams& p, int s, uint32_t& first, int& len) {
     if (!p.offsets) {
-        first = (int64_t)s * p.L;
+        first = (uint32_t)s * (uint32_t)p.L;
         len = p.L;
         return;
     }
-    int64_t lo = p.offsets[s], hi = p.offsets[s + 1];
-    lo = lo < 0 ? 0 : (lo > p.tokens ? p.tokens : lo);
-    hi = hi < lo ? lo : (hi > p.tokens ? p.tokens : hi);
-    first = lo;
-    len = hi - lo > p.L ? p.L : (int)(hi - lo);
+    int lo = p.offsets[s], hi = p.offsets[s + 1];
+    const int tokens = (int)p.tokens;
+    lo = lo < 0 ? 0 : (lo > tokens ? tokens : lo);
+    hi = hi < lo ? lo : (hi > tokens ? tokens : hi);
+    first = (uint32_t)lo;
+    len = hi - lo > p.L ? p.L : hi - lo;
 }
 
 // Packed rows of several blocks: row s has the entries from first / block + s on, as many as it has blocks and one if it
 // has no token, so that entries of rows never meet and tokens / block + rows of them suffice.  The row of an entry is
 // the last one that starts at it or before, found by 64 lanes at a time.
-__device__ __forceinline__ int64_t rec_entry(const RecParams& p, int s, int block) {
-    int64_t lo = p.offsets[s];
-    lo = lo < 0 ? 0 : (lo > p.tokens ? p.tokens : lo);
-    return lo / block + s;
+__device__ __forceinline__ uint32_t rec_entry(const RecParams& p, int s, int block) {
+    int lo = p.offsets[s];
+    lo = lo < 0 ? 0 : (lo > (int)p.tokens ? (int)p.tokens : lo);
+    return (uint32_t)lo / (uint32_t)block + (uint32_t)s;
 }
-__device__ __forceinline__ int rec_row_of(const RecParams& p, int64_t entry, int block, int lane) {
+__device__ __forceinline__ int rec_row_of(const RecParams& p, uint32_t entry, int block, int lane) {
     int lo = 0, hi = p.rows;  // the row is in [lo, hi)
     while (hi - lo > 1) {
         const int step = (hi - lo + 63) / 64, s = lo + lane * step;
@@ -132,20 +134,27 @@ struct RecItem {
     int tile;
     int row;            // the (first) row
     int block, blocks;  // of the row: which, and how many (one where it has no token; none: a block that no row has)
-    int64_t entry;      // of w_words and w_lam
-    int64_t first;      // the (first) row's first token
+    uint32_t entry;     // of w_words and w_lam
+    uint32_t first;     // the (first) row's first token
     int len;            // and length
 };
 
-// Rows of one block.
+// The workgroup's tile and its number among the tile's.
+__device__ __forceinline__ void rec_tile(const RecPlan& q, int& tile, uint32_t& rest) {
+    rest = (uint32_t)((uint64_t)blockIdx.x * q.by_tiles >> 40);
+    tile = (int)(blockIdx.x - rest * (uint32_t)q.tiles);
+}
+
+// A row (or rows of one block) that the workgroup walks itself: the walk's first block.
+template <bool BACK>
 __device__ __forceinline__ RecItem rec_item(const RecParams& p) {
-    const RecPlan& q = p.plan;
+    const int block = p.plan.block;
     RecItem at;
-    at.tile = (int)(blockIdx.x % (unsigned)q.tiles);
-    at.entry = blockIdx.x / (unsigned)q.tiles;
-    at.row = (int)at.entry * q.nr;
-    at.block = 0, at.blocks = 1;
+    rec_tile(p.plan, at.tile, at.entry);
+    at.row = (int)at.entry * p.plan.nr;
     rec_row(p, at.row, at.first, at.len);
+    at.blocks = at.len <= block ? 1 : (int)(((uint32_t)at.len + block - 1) / (uint32_t)block);
+    at.block = BACK ? at.blocks - 1 : 0;
     return at;
 }
 
@@ -154,36 +163,36 @@ template <bool BACK>
 __device__ __forceinline__ RecItem rec_draw(const RecParams& p, uint32_t (&shared)[2]) {
     const RecPlan& q = p.plan;
     RecItem at;
-    at.tile = (int)(blockIdx.x % (unsigned)q.tiles);
-    const unsigned group = blockIdx.x / (unsigned)q.tiles % (unsigned)q.groups;
-    const int block = q.nt * kRecChunk;
+    uint32_t rest;
+    rec_tile(q, at.tile, rest);
+    const uint32_t group = rest & (uint32_t)(q.groups - 1), last = (uint32_t)q.entries - 1;
+    const int block = q.block;
     if (threadIdx.x < 64) {  // (a whole wave: rows are searched by 64 lanes)
         uint32_t ticket = 0;
         if (threadIdx.x == 0)
-            ticket = __hip_atomic_fetch_add(p.w_tickets + 16 * ((int64_t)at.tile * q.groups + group), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+            ticket = __hip_atomic_fetch_add(p.w_tickets + 16 * (uint32_t)(at.tile * q.groups + group), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
         ticket = __builtin_amdgcn_readfirstlane(ticket);
-        if (p.offsets) shared[1] = rec_row_of(p, BACK ? q.entries - 1 - ticket : ticket, block, threadIdx.x);
+        if (p.offsets) shared[1] = rec_row_of(p, BACK ? last - ticket : ticket, block, threadIdx.x);
         shared[0] = ticket;
     }
     lds_barrier();
     const uint32_t ticket = __builtin_amdgcn_readfirstlane(shared[0]);
     if (!p.offsets) {
         // equal rows: those of a group side by side, block after block
-        const uint32_t rows = ((unsigned)p.rows + q.groups - 1) / q.groups;
-        const int j = (int)(ticket / rows);
-        at.row = (int)(ticket % rows) * q.groups + (int)group;
-        at.block = BACK ? q.blocks - 1 - j : j;
+        const uint32_t rows = ((uint32_t)p.rows + q.groups - 1) / (uint32_t)q.groups, j = ticket / rows;
+        at.row = (int)((ticket - j * rows) * q.groups + group);
+        at.block = (int)(BACK ? q.blocks - 1 - j : j);
         at.blocks = at.row < p.rows ? q.blocks : 0;
-        at.entry = (int64_t)at.row * q.blocks + at.block;
-        at.first = (int64_t)at.row * p.L;
+        at.entry = (uint32_t)(at.row * q.blocks + at.block);
+        at.first = (uint32_t)at.row * (uint32_t)p.L;
         at.len = p.L;
     } else {
-        at.entry = BACK ? q.entries - 1 - ticket : ticket;
+        at.entry = BACK ? last - ticket : ticket;
         at.row = __builtin_amdgcn_readfirstlane(shared[1]);
         rec_row(p, at.row, at.first, at.len);
-        at.blocks = at.len > 0 ? (at.len + block - 1) / block : 1;
-        const int64_t j = at.entry - rec_entry(p, at.row, block);
-        at.block = (int)j;
+        at.blocks = at.len > 0 ? (int)(((uint32_t)at.len + block - 1) / (uint32_t)block) : 1;
+        const int j = (int)(at.entry - rec_entry(p, at.row, block));
+        at.block = j;
         if (j < 0 || j >= at.blocks) at.block = at.blocks = 0;  // (j < 0: tokens before the first row, or offsets that fall)
     }
     return at;

@@ -8,8 +8,8 @@
 //
 // Bound by memory: 8 bytes a bfloat16 value forward, 16 backward, against some 40 and 75 lane operations.  So every
 // value is read once and a row is spread over as many lanes as it takes to keep the card's loads in flight: a lane
-// holds 8 tokens of 4 bytes of channels in registers and finds what they make of a state, h -> A h + H; a lane a
-// channel joins the chunks of a block through LDS; then every lane walks its 8 tokens from its own state.  Rows longer
+// holds 16 tokens (backward 8) of 4 bytes of channels in registers and finds what they make of a state, h -> A h + H; a lane a
+// channel joins the chunks of a block through LDS; then every lane walks its tokens from its own state.  Rows longer
 // than a block hand their states on through words in memory (rec_block.h), so that they too are read once.
 // The backward walks the same way back with u_t = a_{t+1} G_{t+1}: a u + a dy; it makes the gates again for its second
 // look at the tokens, from what it holds in registers as it lies in memory.
@@ -19,59 +19,60 @@ namespace sfm {
 
 namespace {
 
-constexpr int kThreads = 256;  // most to a workgroup of the rows' kernels
+constexpr int kThreads = 512;      // most to a workgroup of the rows' kernels
+constexpr int kHandThreads = 256;  // and to one of rows of several blocks
 
-// A lane's place in its workgroup: row, chunk and channels.
-struct Lane {
+// A lane's place in its workgroup: row, chunk (of TT tokens) and channels.
+template <int TT> struct Lane {
     int rr, tc, ch, slot;
     uint32_t tok;  // its chunk's first token behind the item's
     bool live;     // has channels
     __device__ __forceinline__ Lane(const RecParams& p, int tile, int C) {
         const RecPlan& q = p.plan;
-        const int per_row = q.nc * q.nt;
-        rr = (int)threadIdx.x / per_row;
-        const int rest = (int)threadIdx.x - rr * per_row;
-        tc = rest / q.nc;
+        rr = 0;
+        int rest = (int)threadIdx.x;
+        if (q.nr > 1) {
+            rr = div_small(rest, q.inv_row);
+            rest -= rr * q.nc * q.nt;
+        }
+        tc = div_small(rest, q.inv_nc);
         const int cl = rest - tc * q.nc;
         ch = (tile * q.nc + cl) * C;
-        slot = (rr * q.nt + tc) * q.nc * C + cl * C;
-        tok = (uint32_t)(rr * p.L + tc * kRecChunk);  // (several rows: equal ones)
-        if (q.nr == 1) tok = tc * kRecChunk;
-        live = rr < q.nr && ch < p.D;
+        slot = (int)threadIdx.x * C;  // ([rows][chunks][channels], as the lanes lie)
+        tok = (uint32_t)(rr * p.L + tc * TT);  // (several rows: equal ones)
+        live = rr < q.nr && tc < q.nt && ch < p.D;
     }
 };
 
 // An item's tokens; everything the same for all lanes but n.
 struct Chunk {
-    int64_t base;  // its first token, where the workgroup's buffers start
-    int rest;      // tokens from there to the block's end (of each row)
-    int row, rows; // its first row, and the rows from there on
-    bool first;    // the block is its row's first
-    __device__ __forceinline__ Chunk() : base(0), rest(0), row(0), rows(0), first(false) {}
+    uint32_t base;  // its first token, where the workgroup's buffers start
+    int rest;       // tokens from there to the block's end (of each row)
+    int row, rows;  // its first row, and the rows from there on
+    bool first;     // the block is its row's first
     __device__ __forceinline__ Chunk(const RecParams& p, const RecItem& at) {
-        const int block = p.plan.nt * kRecChunk, skip = at.block * block;
+        const int block = p.plan.block, skip = at.block * block;
         base = at.first + skip;
         rest = at.len - skip < block ? at.len - skip : block;
-        if (at.blocks == 0) rest = 0;
         row = at.row;
         rows = p.rows - at.row;
         first = skip == 0;
     }
-    // tokens of a lane's chunk (as many as are left: 0 or less, none; kRecChunk or more, all)
-    __device__ __forceinline__ int n(const Lane& l) const { return l.live && l.rr < rows ? rest - l.tc * kRecChunk : 0; }
+    // tokens of a lane's chunk (as many as are left: 0 or less, none; TT or more, all)
+    template <int TT> __device__ __forceinline__ int n(const Lane<TT>& l) const { return l.live && l.rr < rows ? rest - l.tc * TT : 0; }
 };
 
-template <typename T, int C>
-__device__ __forceinline__ void load_chunk(RecPack<T, C> (&v)[kRecChunk], const void* from, int64_t ld, const Chunk& c, const Lane& l, uint32_t none) {
-    const RecBuf b = rec_buf<T>(from, c.base * ld);
-    const uint32_t at = (l.tok * (uint32_t)ld + l.ch) * sizeof(T), token = (uint32_t)ld * sizeof(T);
+template <typename T, int C, int TT>
+__device__ __forceinline__ void load_chunk(RecPack<T, C> (&v)[TT], const void* from, uint32_t ld, const Chunk& c, const Lane<TT>& l, uint32_t none) {
+    const RecBuf b = rec_buf<T>(from, c.base, ld);
+    const uint32_t at = (l.tok * ld + l.ch) * sizeof(T), token = ld * sizeof(T);
     const int n = c.n(l);
-    if (n >= kRecChunk) {
+    if (n >= TT) {
 #pragma unroll
-        for (int t = 0; t < kRecChunk; ++t) v[t].load(b, at, t * token);
+        for (int t = 0; t < TT; ++t) v[t].load(b, at, t * token);
     } else if (n > 0) {
 #pragma unroll
-        for (int t = 0; t < kRecChunk; ++t) {
+        for (int t = 0; t < TT; ++t) {
             v[t].v = none;
             if (t < n) v[t].load(b, at, t * token);
         }
@@ -79,9 +80,9 @@ __device__ __forceinline__ void load_chunk(RecPack<T, C> (&v)[kRecChunk], const 
 }
 
 // Joins the chunks' (A, H) of [rows][chunks][channels] in LDS: a lane a row and channel.  In their place: the state
-// before every chunk.  BACK: chunks from the last to the first.
+// before every chunk.  BACK: chunks from the last to the first.  kept: the state after the block, for the row's next.
 template <int C, bool HAND, bool BACK>
-__device__ __forceinline__ void join_chunks(const RecParams& p, float2* agg, const RecItem& at) {
+__device__ __forceinline__ void join_chunks(const RecParams& p, float2* agg, const RecItem& at, float& kept) {
     const RecPlan& q = p.plan;
     const int width = q.nc * C;
     const float* before = BACK ? p.dhT : p.h0;
@@ -92,12 +93,12 @@ __device__ __forceinline__ void join_chunks(const RecParams& p, float2* agg, con
         const int64_t s = at.row + rr;
         if (ch >= p.D || s >= p.rows) continue;
         float2* a = agg + rr * q.nt * width + w;
-        float h = 0.0f;
-        if (starts && before) h = before[s * p.D + ch];
+        float h = kept;
+        if (starts) h = before ? before[s * p.D + ch] : 0.0f;
         if constexpr (HAND) {
             const bool tells = !ends || p.offsets;  // (packed rows: always, rec_look_back)
             if (!starts || tells) {
-                uint64_t* word = p.w_words + (at.tile * q.entries + at.entry) * kRecWords<C> + w;
+                uint64_t* word = p.w_words + ((int64_t)at.tile * q.entries + at.entry) * kRecWords<C> + w;
                 float A = 1.0f, H = 0.0f;
 #pragma unroll 8
                 for (int k = 0; k < q.nt; ++k) {
@@ -107,7 +108,7 @@ __device__ __forceinline__ void join_chunks(const RecParams& p, float2* agg, con
                 }
                 if (!starts) {
                     if (tells) rec_publish(word, rec_factor(A), H);
-                    h = rec_look_back<BACK, 8, kRecWords<C>>(word, BACK ? at.blocks - 1 - at.block : at.block);
+                    h = rec_look_back<BACK, 4, kRecWords<C>>(word, BACK ? at.blocks - 1 - at.block : at.block);
                 }
                 if (tells) rec_publish(word, kRecWhole, __builtin_fmaf(A, h, H));
             }
@@ -119,6 +120,7 @@ __device__ __forceinline__ void join_chunks(const RecParams& p, float2* agg, con
             v->x = h;
             h = __builtin_fmaf(f.x, h, f.y);
         }
+        kept = h;
         if (ends && after) after[s * p.D + ch] = h;
     }
 }
@@ -129,169 +131,178 @@ __device__ __forceinline__ void empty_block(const RecParams& p, const RecItem& a
     if (!p.offsets) return;
     const int width = p.plan.nc * C;
     for (int m = threadIdx.x; m < width; m += blockDim.x) {
-        rec_publish(p.w_words + (at.tile * p.plan.entries + at.entry) * kRecWords<C> + m, kRecWhole, 0.0f);
+        rec_publish(p.w_words + ((int64_t)at.tile * p.plan.entries + at.entry) * kRecWords<C> + m, kRecWhole, 0.0f);
         const int ch = at.tile * width + m;
-        if (BACK && ch < p.D) p.w_lam[at.entry * p.D + ch] = 0.0f;
+        if (BACK && ch < p.D) p.w_lam[(int64_t)at.entry * p.D + ch] = 0.0f;
     }
 }
 
 template <typename T, int C, bool HAND>
-__global__ __launch_bounds__(kThreads, C == 2 ? 7 : 8) void rec_fwd_kernel(const RecParams p) {
+__global__ __launch_bounds__(HAND ? kHandThreads : kThreads, C == 2 ? (HAND ? 5 : 4) : 6) void rec_fwd_kernel(const RecParams p) {
     constexpr bool kExact = sizeof(T) == 4;
-    __shared__ float2 agg[kThreads * C];
+    constexpr int TT = kRecChunk<false>;
+    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? kHandThreads : kThreads) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
     if constexpr (HAND) {
         at = rec_draw<false>(p, shared);
         if (at.blocks == 0) return empty_block<C, false>(p, at);
     } else {
-        at = rec_item(p);
+        at = rec_item<false>(p);
     }
-    const Lane l(p, at.tile, C);
-    const Chunk c(p, at);
-    const int n = c.n(l);
-    float a[kRecChunk][C], b[kRecChunk][C];
-    if (l.live) {
-        float rate[C], A[C], H[C];
+    const Lane<TT> l(p, at.tile, C);
+    float rate[C], kept = 0.0f;
 #pragma unroll
-        for (int j = 0; j < C; ++j) A[j] = 1.0f, H[j] = 0.0f;
+    for (int j = 0; j < C; ++j) rate[j] = l.live ? rec_rate(p.lam[l.ch + j], p.c) : 0.0f;
+    for (int turn = 0;; turn ^= 1) {
+        float2* agg = agg_[HAND ? 0 : turn];
+        const Chunk c(p, at);
+        const int n = c.n(l);
+        float a[TT][C], b[TT][C];
+        if (l.live) {
+            float A[C], H[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) A[j] = 1.0f, H[j] = 0.0f;
+            if (n > 0) {
+                RecPack<T, C> r[TT], i[TT], x[TT];
+                load_chunk<T, C, TT>(r, p.r, p.ldr, c, l, RecPack<T, C>::kMinusInf);
+                load_chunk<T, C, TT>(i, p.i, p.ldi, c, l, 0);
+                load_chunk<T, C, TT>(x, p.x, p.ldx, c, l, 0);
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int j = 0; j < C; ++j) {
+                        const float la2 = rate[j] * rec_sigmoid<kExact>(r[t].get(j));
+                        a[t][j] = exp2_fast(la2);
+                        const float m = __builtin_amdgcn_sqrtf(rec_keep2<kExact>(la2, a[t][j]));
+                        b[t][j] = m * rec_sigmoid<kExact>(i[t].get(j)) * x[t].get(j);
+                        H[j] = __builtin_fmaf(a[t][j], H[j], b[t][j]);
+                        A[j] *= a[t][j];
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], H[j]);
+        }
+        lds_barrier();
+        join_chunks<C, HAND, false>(p, agg, at, kept);
+        lds_barrier();
         if (n > 0) {
-            RecPack<T, C> r[kRecChunk], i[kRecChunk], x[kRecChunk];
-            load_chunk<T, C>(r, p.r, p.ldr, c, l, RecPack<T, C>::kMinusInf);
-            load_chunk<T, C>(i, p.i, p.ldi, c, l, 0);
-            load_chunk<T, C>(x, p.x, p.ldx, c, l, 0);
+            float h[C];
 #pragma unroll
-            for (int j = 0; j < C; ++j) rate[j] = rec_rate(p.lam[l.ch + j], p.c);
+            for (int j = 0; j < C; ++j) h[j] = agg[l.slot + j].x;
+            const RecBuf y = rec_buf<T>(p.y, c.base, p.D);
+            const uint32_t to = (l.tok * (uint32_t)p.D + l.ch) * sizeof(T), token = p.D * sizeof(T);
+            auto walk = [&](auto whole) __attribute__((always_inline)) {
 #pragma unroll
-            for (int t = 0; t < kRecChunk; ++t)
+                for (int t = 0; t < TT; ++t) {
 #pragma unroll
-                for (int j = 0; j < C; ++j) {
-                    const float la2 = rate[j] * rec_sigmoid<kExact>(r[t].get(j));
-                    a[t][j] = exp2_fast(la2);
-                    const float m = __builtin_amdgcn_sqrtf(rec_keep2<kExact>(la2, a[t][j]));
-                    b[t][j] = m * rec_sigmoid<kExact>(i[t].get(j)) * x[t].get(j);
-                    H[j] = __builtin_fmaf(a[t][j], H[j], b[t][j]);
-                    A[j] *= a[t][j];
+                    for (int j = 0; j < C; ++j) h[j] = __builtin_fmaf(a[t][j], h[j], b[t][j]);
+                    if (decltype(whole)::value || t < n) RecPack<T, C>::store(y, to, t * token, h);
                 }
+            };
+            if (n >= TT)
+                walk(std::true_type{});
+            else
+                walk(std::false_type{});
         }
-#pragma unroll
-        for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], H[j]);
+        if (HAND || ++at.block >= at.blocks) break;
     }
-    lds_barrier();
-    join_chunks<C, HAND, false>(p, agg, at);
-    lds_barrier();
-    if (n <= 0) return;
-    float h[C];
-#pragma unroll
-    for (int j = 0; j < C; ++j) h[j] = agg[l.slot + j].x;
-    const RecBuf y = rec_buf<T>(p.y, c.base * p.D);
-    const uint32_t to = (l.tok * (uint32_t)p.D + l.ch) * sizeof(T), token = p.D * sizeof(T);
-    auto walk = [&](auto whole) __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < kRecChunk; ++t) {
-#pragma unroll
-            for (int j = 0; j < C; ++j) h[j] = __builtin_fmaf(a[t][j], h[j], b[t][j]);
-            if (decltype(whole)::value || t < n) RecPack<T, C>::store(y, to, t * token, h);
-        }
-    };
-    if (n >= kRecChunk)
-        walk(std::true_type{});
-    else
-        walk(std::false_type{});
 }
 
 template <typename T, int C, bool HAND>
-__global__ __launch_bounds__(kThreads, 4) void rec_bwd_kernel(const RecParams p) {
+__global__ __launch_bounds__(HAND ? kHandThreads : kThreads, 4) void rec_bwd_kernel(const RecParams p) {
     constexpr bool kExact = sizeof(T) == 4;
-    __shared__ float2 agg[kThreads * C];
-    __shared__ float part[kThreads * C];
+    constexpr int TT = kRecChunk<true>;
+    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? kHandThreads : kThreads) * C];
+    __shared__ float part[(HAND ? kHandThreads : kThreads) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
     if constexpr (HAND) {
         at = rec_draw<true>(p, shared);
         if (at.blocks == 0) return empty_block<C, true>(p, at);
     } else {
-        at = rec_item(p);
+        at = rec_item<true>(p);
     }
     const RecPlan& q = p.plan;
-    const Lane l(p, at.tile, C);
-    const Chunk c(p, at);
-    const int n = c.n(l);
-    const bool start = c.first && l.tc == 0;
-    RecPack<T, C> r[kRecChunk], g[kRecChunk], i[kRecChunk], x[kRecChunk], y[kRecChunk];
-    float rate[C];
-    if (l.live) {
-        float A[C], U[C];
+    const Lane<TT> l(p, at.tile, C);
+    float rate[C], sum[C], kept = 0.0f;
 #pragma unroll
-        for (int j = 0; j < C; ++j) A[j] = 1.0f, U[j] = 0.0f;
-        if (n > 0) {
-            load_chunk<T, C>(r, p.r, p.ldr, c, l, RecPack<T, C>::kMinusInf);
-            load_chunk<T, C>(g, p.dy, p.D, c, l, 0);
-            load_chunk<T, C>(i, p.i, p.ldi, c, l, 0);
-            load_chunk<T, C>(x, p.x, p.ldx, c, l, 0);
-            // the states before the tokens: the outputs one earlier
-            const RecBuf w = rec_buf<T>(p.y, (c.base - 1) * p.D);
-            const uint32_t token = p.D * sizeof(T), from = (l.tok * (uint32_t)p.D + l.ch) * sizeof(T);
-            if (n >= kRecChunk && !start) {
+    for (int j = 0; j < C; ++j) rate[j] = l.live ? rec_rate(p.lam[l.ch + j], p.c) : 0.0f, sum[j] = 0.0f;
+    for (int turn = 0;; turn ^= 1) {
+        float2* agg = agg_[HAND ? 0 : turn];
+        const Chunk c(p, at);
+        const int n = c.n(l);
+        const bool start = c.first && l.tc == 0;
+        RecPack<T, C> r[TT], g[TT], i[TT], x[TT], y[TT];
+        if (l.live) {
+            float A[C], U[C];
 #pragma unroll
-                for (int t = 0; t < kRecChunk; ++t) y[t].load(w, from, t * token);
-            } else {
+            for (int j = 0; j < C; ++j) A[j] = 1.0f, U[j] = 0.0f;
+            if (n > 0) {
+                load_chunk<T, C, TT>(r, p.r, p.ldr, c, l, RecPack<T, C>::kMinusInf);
+                load_chunk<T, C, TT>(g, p.dy, p.D, c, l, 0);
+                load_chunk<T, C, TT>(i, p.i, p.ldi, c, l, 0);
+                load_chunk<T, C, TT>(x, p.x, p.ldx, c, l, 0);
+                // the states before the tokens: the outputs one earlier
+                const RecBuf w = rec_buf<T>(p.y, c.base, p.D, p.D);
+                const uint32_t token = p.D * sizeof(T), from = (l.tok * (uint32_t)p.D + l.ch) * sizeof(T);
+                if (n >= TT && !start) {
 #pragma unroll
-                for (int t = 0; t < kRecChunk; ++t) {
-                    y[t].v = 0;
-                    if (t < n && !(t == 0 && start)) y[t].load(w, from, t * token);
+                    for (int t = 0; t < TT; ++t) y[t].load(w, from, t * token);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        y[t].v = 0;
+                        if (t < n && !(t == 0 && start)) y[t].load(w, from, t * token);
+                    }
                 }
+#pragma unroll
+                for (int t = TT - 1; t >= 0; --t)
+#pragma unroll
+                    for (int j = 0; j < C; ++j) {
+                        const float a = exp2_fast(rate[j] * rec_sigmoid<kExact>(r[t].get(j)));
+                        U[j] = a * (U[j] + g[t].get(j));
+                        A[j] *= a;
+                    }
             }
 #pragma unroll
-            for (int j = 0; j < C; ++j) rate[j] = rec_rate(p.lam[l.ch + j], p.c);
-#pragma unroll
-            for (int t = kRecChunk - 1; t >= 0; --t)
-#pragma unroll
-                for (int j = 0; j < C; ++j) {
-                    const float a = exp2_fast(rate[j] * rec_sigmoid<kExact>(r[t].get(j)));
-                    U[j] = a * (U[j] + g[t].get(j));
-                    A[j] *= a;
-                }
+            for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], U[j]);
         }
-#pragma unroll
-        for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], U[j]);
-    }
-    lds_barrier();
-    join_chunks<C, HAND, true>(p, agg, at);
-    lds_barrier();
-    float sum[C];
-#pragma unroll
-    for (int j = 0; j < C; ++j) sum[j] = 0.0f;
-    if (n > 0) {
-        float u[C], h0[C];
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            u[j] = agg[l.slot + j].x;
-            h0[j] = p.h0 && start ? p.h0[(int64_t)(c.row + l.rr) * p.D + l.ch + j] : 0.0f;
-        }
-        const uint32_t to = (l.tok * (uint32_t)p.D + l.ch) * sizeof(T), token = p.D * sizeof(T);
-#pragma unroll
-        for (int t = kRecChunk - 1; t >= 0; --t) {
-            if (t >= n) continue;
-            float dx[C], dr[C], di[C];
+        lds_barrier();
+        join_chunks<C, HAND, true>(p, agg, at, kept);
+        lds_barrier();
+        if (n > 0) {
+            float u[C], h0[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                const float sr = rec_sigmoid<kExact>(r[t].get(j)), si = rec_sigmoid<kExact>(i[t].get(j));
-                const float la2 = rate[j] * sr, a = exp2_fast(la2), em = rec_keep2<kExact>(la2, a);
-                const float rs = em > 0.0f ? __builtin_amdgcn_rsqf(em) : em == em ? 0.0f : em;
-                const float G = g[t].get(j) + u[j], xv = x[t].get(j);
-                const float before = t == 0 && start ? h0[j] : y[t].get(j);
-                const float P = G * (a * (la2 * kLn2)) * (before - a * rs * si * xv);
-                dx[j] = G * (em * rs) * si;
-                di[j] = dx[j] * xv * (1.0f - si);
-                dr[j] = P * (1.0f - sr);
-                sum[j] += P;
-                u[j] = a * G;
+                u[j] = agg[l.slot + j].x;
+                h0[j] = p.h0 && start ? p.h0[(int64_t)(c.row + l.rr) * p.D + l.ch + j] : 0.0f;
             }
-            RecPack<T, C>::store(rec_buf<T>(p.dx, c.base * p.D), to, t * token, dx);
-            RecPack<T, C>::store(rec_buf<T>(p.dr, c.base * p.D), to, t * token, dr);
-            RecPack<T, C>::store(rec_buf<T>(p.di, c.base * p.D), to, t * token, di);
+            const uint32_t to = (l.tok * (uint32_t)p.D + l.ch) * sizeof(T), token = p.D * sizeof(T);
+#pragma unroll
+            for (int t = TT - 1; t >= 0; --t) {
+                if (t >= n) continue;
+                float dx[C], dr[C], di[C];
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    const float sr = rec_sigmoid<kExact>(r[t].get(j)), si = rec_sigmoid<kExact>(i[t].get(j));
+                    const float la2 = rate[j] * sr, a = exp2_fast(la2), em = rec_keep2<kExact>(la2, a);
+                    const float rs = em > 0.0f ? __builtin_amdgcn_rsqf(em) : em == em ? 0.0f : em;
+                    const float G = g[t].get(j) + u[j], xv = x[t].get(j);
+                    const float before = t == 0 && start ? h0[j] : y[t].get(j);
+                    const float P = G * (a * (la2 * kLn2)) * (before - a * rs * si * xv);
+                    dx[j] = G * (em * rs) * si;
+                    di[j] = dx[j] * xv * (1.0f - si);
+                    dr[j] = P * (1.0f - sr);
+                    sum[j] += P;
+                    u[j] = a * G;
+                }
+                RecPack<T, C>::store(rec_buf<T>(p.dx, c.base, p.D), to, t * token, dx);
+                RecPack<T, C>::store(rec_buf<T>(p.dr, c.base, p.D), to, t * token, dr);
+                RecPack<T, C>::store(rec_buf<T>(p.di, c.base, p.D), to, t * token, di);
+            }
         }
+        if (HAND || --at.block < 0) break;
     }
     if (l.live)
 #pragma unroll
@@ -304,7 +315,7 @@ __global__ __launch_bounds__(kThreads, 4) void rec_bwd_kernel(const RecParams p)
         float all = 0.0f;
 #pragma unroll 8
         for (int k = 0; k < q.nr * q.nt; ++k) all += part[k * width + m];
-        p.w_lam[at.entry * p.D + ch] = all;
+        p.w_lam[(int64_t)at.entry * p.D + ch] = all;
     }
 }
 
@@ -393,22 +404,39 @@ hipError_t launch_rows(const RecParams& p, hipStream_t s) {
 
 }  // namespace
 
+// Whether rows of several blocks are handed on or walked by a workgroup each.  Handing on costs a launch that clears the
+// words (5 us) and a wait a block; walking leaves the card to the rows and tiles there are, and packed rows to the
+// longest of them.  bfloat16, 2048 channels in 32 tiles, walked / handed on:
+//     forward, 16 rows of 600: 34 / 37 us, 8 rows: 27 / 23 us, 16 rows of 2400: 145 / 148 us, 8 rows: 94 / 73 us;
+//     three blocks (300 tokens), 2 rows: 14 / 15 us, 8 rows: 15.5 / 16 us, 4 rows: 15 / 13 us;
+//     backward, 32 rows of 600: 153 / 164 us, 16 rows: 90 / 84 us;
+//     packed to 600 in 16 tiles, 256 rows: 156 / 166 us (back 317 / 343), 128 rows: 89 / 94 us (194 / 191);
+//     packed to 2000, 64 rows: 165 / 136 us (back 333 / 285).
+static bool hands_on(int64_t rows, int64_t L, int64_t tokens, int tiles, int blocks, bool packed, bool back) {
+    if (packed) return rows * tiles < 4096 || L * rows > 4 * tokens;  // (one far longer than the others, or no bound)
+    return rows * tiles < (back ? 1024 : 512) && (back || blocks > 3);
+}
+
 RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, bool near, int lane, bool back) {
     RecPlan q{};
     q.lane = lane;
     const int lanes = (int)((D + lane - 1) / lane);
-    const int64_t chunks = (L + kRecChunk - 1) / kRecChunk;
+    const int chunk = back ? kRecChunk<true> : kRecChunk<false>;
+    const int64_t chunks = (L + chunk - 1) / chunk;
     const int least = lanes < 32 ? lanes : 32;  // lanes side by side: 128 bytes where there are so many
-    const int most = kThreads / least < 64 ? kThreads / least : 64;
-    q.hand = chunks > (most > 16 ? most : 16);
-    q.nt = q.hand ? most : (int)chunks;
-    if (q.hand && !packed) {  // (equal rows: equal blocks)
+    const int most = kHandThreads / least < 64 ? kHandThreads / least : 64;
+    const bool several = chunks > (most > 16 ? most : 16);
+    q.nt = several ? most : (int)chunks;
+    q.blocks = 1, q.groups = 1;
+    if (several && !packed) {  // (equal rows: equal blocks)
         q.blocks = (int)((chunks + most - 1) / most);
         q.nt = (int)((chunks + q.blocks - 1) / q.blocks);
         q.blocks = (int)((chunks + q.nt - 1) / q.nt);
     }
+    q.block = q.nt * chunk;
     // one block: as wide as the workgroup allows in whole 128 bytes, down to half that where it leaves fewer lanes idle
-    int nc = q.hand ? least : kThreads / q.nt;
+    const int budget = q.nt * least > kHandThreads ? kThreads : kHandThreads;
+    int nc = several ? least : budget / q.nt;
     if (nc >= lanes) {
         nc = lanes;
     } else if (nc >= 32) {
@@ -419,23 +447,25 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     }
     q.nc = nc;
     q.tiles = (lanes + nc - 1) / nc;
-    q.nr = q.hand || packed || q.tiles > 1 || !near ? 1 : kThreads / (q.nt * nc);
+    q.hand = several && hands_on(rows, L, tokens, q.tiles, q.blocks, packed, back);
+    q.nr = several || packed || q.tiles > 1 || !near ? 1 : budget / (q.nt * nc);
     if (q.nr > rows) q.nr = (int)rows;
-    q.groups = 1;
     if (!q.hand) {
         q.entries = (rows + q.nr - 1) / q.nr;
         q.launch = q.entries * q.tiles;
     } else if (packed) {
-        q.entries = tokens / (q.nt * kRecChunk) + rows;
+        q.entries = tokens / q.block + rows;
         q.launch = q.entries * q.tiles;
     } else {
-        q.groups = rows < 8 ? (int)rows : 8;
+        q.groups = rows < 2 ? 1 : rows < 4 ? 2 : rows < 8 ? 4 : 8;
         q.entries = rows * q.blocks;
         q.launch = (rows + q.groups - 1) / q.groups * q.groups * q.blocks * q.tiles;
     }
     q.bytes_words = q.hand ? (int64_t)q.tiles * q.groups * 64 + q.entries * q.tiles * 32 * lane * 8 : 0;
     q.bytes_words = (q.bytes_words + 15) / 16 * 16;
     q.bytes = q.bytes_words + (back ? q.entries * D * 4 : 0);
+    q.by_tiles = ((1ULL << 40) + q.tiles - 1) / q.tiles;
+    q.inv_nc = 1.0f / (float)q.nc, q.inv_row = 1.0f / (float)(q.nc * q.nt);
     return q;
 }
 

@@ -6,18 +6,21 @@
 
 namespace sfm {
 
-// How a call's rows are cut (plan_rec): a workgroup is nr rows x nt chunks of kRecChunk tokens x nc lanes of `lane`
-// channels.  Rows longer than nt chunks are cut into blocks of that many, a workgroup each (hand), which hand their
-// states on through the workspace.
-constexpr int kRecChunk = 8;
+// How a call's rows are cut (plan_rec): a workgroup is nr rows x nt chunks of tokens x nc lanes of `lane` channels.
+// Rows longer than nt chunks are cut into blocks of that many: one after the other by one workgroup, or (hand) a
+// workgroup each, which hand their states on through the workspace.
+template <bool BACK> constexpr int kRecChunk = BACK ? 8 : 16;  // tokens to a lane (recurrence.hip)
 struct RecPlan {
     int lane, nc, nt, nr, tiles;  // tiles: workgroups side by side over the channels
+    int block;                    // tokens to a block
     int hand;
-    int blocks;                   // hand, equal rows: blocks to a row
-    int groups;                   // hand: ticket counters to a tile
+    int blocks;                   // equal rows: blocks to a row
+    int groups;                   // hand: ticket counters to a tile, a power of two
     int64_t entries;              // hand: blocks of all rows; else: workgroups along the rows
     int64_t launch;               // workgroups
     int64_t bytes_words, bytes;   // workspace: tickets and words; with the backward's parts of dlam
+    uint64_t by_tiles;            // 2^40 / tiles, rounded up: n by_tiles / 2^40 is n / tiles for n < 2^24
+    float inv_nc, inv_row;        // 1 / nc, 1 / (nc nt)
 };
 
 // One call's rows, channels and strides (forward, backward and the step).
@@ -47,9 +50,9 @@ struct RecParams {
     RecPlan plan;
 };
 
-// Cuts a call; near: the largest token stride is below 2^21 bytes (so that the 2048 tokens of nr rows end below 2^32); lane: channels to a lane (rec_wide, or one).
+// Cuts a call; near: the largest token stride is below 2^19 bytes (so that the 8192 tokens of nr rows end below 2^32); lane: channels to a lane (rec_wide, or one).
 RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, bool near, int lane, bool back);
-constexpr int64_t kRecMaxStride = 1 << 20;  // (a block's 512 tokens then end below 2^31 bytes)
+constexpr int64_t kRecMaxStride = 1 << 19;  // (a block's 1024 tokens then end below 2^31 bytes)
 // Channels to a lane: 4 bytes where the sizes, strides and addresses allow it, else one.
 inline int rec_wide(int io_dtype) { return io_dtype == 0 ? 1 : 2; }
 hipError_t launch_rec_fwd(const RecParams& p, int io_dtype, hipStream_t s);

@@ -59,7 +59,7 @@ sfm_status too_large(const char* fn, int64_t rows, int64_t tokens, int64_t D) {
 void take_plan(sfm::RecParams& p, bool wide, int io_dtype, bool back, void* workspace) {
     int64_t most = p.D;
     for (int64_t ld : {p.ldx, p.ldr, p.ldi}) most = ld > most ? ld : most;
-    const bool near = most * io_bytes(io_dtype) < 1 << 21;
+    const bool near = most * io_bytes(io_dtype) < 1 << 19;
     p.plan = sfm::plan_rec(p.rows, p.L, p.tokens, p.D, p.offsets != nullptr, near, wide ? sfm::rec_wide(io_dtype) : 1, back);
     char* at = static_cast<char*>(workspace);
     p.w_tickets = reinterpret_cast<uint32_t*>(at);

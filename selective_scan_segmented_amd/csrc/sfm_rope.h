@@ -18,6 +18,8 @@ struct RopeSide {
     float* dw;        // backward: [d] or null (not wanted)
     int64_t ld;
     int heads;
+    int run;          // tokens that a workgroup takes at a time
+    int64_t groups;   // workgroups; backward: no more than kRopeParts
 };
 
 struct RopeParams {
@@ -29,12 +31,17 @@ struct RopeParams {
     int ends[kRopeMaxAxes];    // pair j goes by the first axis a with j < ends[a]
     float eps;
     int norm, neighbours;      // neighbours: pairs (2j, 2j + 1), else (j, j + rot / 2)
-    // workspace (backward with weights): [2][parts][d]
-    float* part;
-    int parts;
+    // plan (plan_rope)
+    int vec;                   // neighbouring values to a load
+    int slots, lanes;          // of two vec to a head; lanes: to a head, a power of two
+    int threads;
+    float* part;               // workspace (backward with weights): [2][kRopeParts][d]
 };
 
-int64_t plan_rope_bwd(RopeParams& p, bool want);
+constexpr int kRopeParts = 1024;  // most parts of dw to a side
+
+// Fills the plan; align: bytes that every tensor's rows are aligned to (16, 8, 4 or 2).
+void plan_rope(RopeParams& p, int io_bytes, int align, bool back);
 hipError_t launch_rope_fwd(const RopeParams& p, int io_dtype, hipStream_t s);
 hipError_t launch_rope_bwd(const RopeParams& p, int io_dtype, hipStream_t s);
 

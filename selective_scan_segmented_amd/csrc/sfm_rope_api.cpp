@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "sfm_api_util.h"
 #include "sfm_rope.h"
 
@@ -63,6 +65,13 @@ sfm_status fill(const char* fn, sfm::RopeParams& p, const void* q, const void* k
     return SFM_OK;
 }
 
+// Bytes that all addresses are a multiple of, at most 16.
+int alignment(std::initializer_list<const void*> tensors) {
+    uintptr_t all = 16;
+    for (const void* t : tensors) all |= reinterpret_cast<uintptr_t>(t);
+    return (int)(all & -all);
+}
+
 struct Ranges {
     Range of[8];
     int n = 0;
@@ -116,6 +125,7 @@ sfm_status sfm_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, c
     st = check_ranges(fn, in, out);
     if (st != SFM_OK) return st;
     p.side[0].y = qo, p.side[1].y = ko;
+    sfm::plan_rope(p, e, alignment({q, k, qo, ko}), false);
     return hip_status(sfm::launch_rope_fwd(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
 }
 
@@ -125,9 +135,7 @@ sfm_status sfm_qk_norm_rope_bwd_ws_size(int64_t tokens, int64_t Hq, int64_t Hk, 
     if (!bytes) return fail(SFM_ERR_NULL, "%s: bytes is required", fn);
     const sfm_status st = check_sizes(fn, tokens, Hq, Hk, d, io_dtype);
     if (st != SFM_OK) return st;
-    sfm::RopeParams p{};
-    p.tokens = tokens, p.side[0].heads = (int)Hq, p.side[1].heads = (int)Hk, p.d = (int)d;
-    *bytes = sfm::plan_rope_bwd(p, want_weights != 0);
+    *bytes = want_weights ? 2 * (int64_t)sfm::kRopeParts * d * 4 : 0;
     return ok();
 }
 
@@ -147,7 +155,7 @@ sfm_status sfm_qk_norm_rope_bwd(const void* dqo, const void* dko, const void* q,
     for (const void* t : {dqo, dko, (const void*)dq, (const void*)dk})
         if (!aligned_to(t, e)) return fail(SFM_ERR_ALIGN, "%s: a gradient is not aligned to its element", fn);
     if (!aligned_to(dwq, 4) || !aligned_to(dwk, 4)) return fail(SFM_ERR_ALIGN, "%s: dwq or dwk not aligned to its element", fn);
-    const int64_t need = sfm::plan_rope_bwd(p, dwq || dwk);
+    const int64_t need = dwq || dwk ? 2 * (int64_t)sfm::kRopeParts * d * 4 : 0;
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(SFM_ERR_SHAPE, "%s: workspace of %lld bytes needed, %lld given", fn, (long long)need,
                     (long long)(workspace ? workspace_bytes : 0));
@@ -167,6 +175,7 @@ sfm_status sfm_qk_norm_rope_bwd(const void* dqo, const void* dko, const void* q,
     if (tokens == 0 && !dwq && !dwk) return ok();
     p.side[0].dy = dqo, p.side[1].dy = dko, p.side[0].y = dq, p.side[1].y = dk, p.side[0].dw = dwq, p.side[1].dw = dwk;
     p.part = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    sfm::plan_rope(p, e, alignment({q, k, dqo, dko, dq, dk}), true);
     return hip_status(sfm::launch_rope_bwd(p, io_dtype, static_cast<hipStream_t>(stream)), fn);
 }
 

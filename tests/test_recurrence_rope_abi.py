@@ -43,7 +43,7 @@ def step(lib, **kw):
 
 
 SHARED = [(dict(x=None), NULL), (dict(i=None), NULL), (dict(lam=None), NULL), (dict(y=None), NULL), (dict(io=2), DTYPE),
-          (dict(D=0), SHAPE), (dict(D=65537, ldx=65537, ldr=65537, ldi=65537), SHAPE), (dict(ldx=63), SHAPE), (dict(ldi=(1 << 20) + 1), SHAPE),
+          (dict(D=0), SHAPE), (dict(D=65537, ldx=65537, ldr=65537, ldi=65537), SHAPE), (dict(ldx=63), SHAPE), (dict(ldi=(1 << 19) + 1), SHAPE),
           (dict(rows=0), SHAPE), (dict(c=0.0), SHAPE), (dict(c=-8.0), SHAPE), (dict(c=float("nan")), SHAPE), (dict(c=float("inf")), SHAPE),
           (dict(x=P + 1), ALIGN), (dict(lam=4 * P + 2), ALIGN), (dict(y=5 * P + 1), ALIGN)]
 ROWS = [(dict(tokens=1999), SHAPE), (dict(L=0), SHAPE), (dict(tokens=-1, off=7 * P), SHAPE), (dict(off=7 * P + 2), ALIGN),
