@@ -467,7 +467,8 @@ sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G
  * h float32, zero (or h0) before the row's first token.
  *
  * sfm_gated_recurrence_fwd -- whole rows.
- *   x, r, i  [tokens, D] io        token strides ldx, ldr, ldi (elements, D to 2^19)
+ *   x, r, i  [tokens, D] io        token strides ldx, ldr, ldi (elements, from D on; min(L, 1024)
+ *            tokens of one have to lie within 2^31 bytes)
  *   lam      [D] f32;  c > 0 (8 is usual)
  *   h0       [rows, D] f32 or NULL (zero)
  *   y        [tokens, D] io, contiguous
@@ -508,8 +509,8 @@ sfm_status sfm_gated_recurrence_bwd_ws_size(int64_t rows, int64_t L, int64_t tok
 
 /*
  * sfm_gated_recurrence_step -- one token of each of `rows` requests (serving) on a pool
- * of states, updated in place: x, r, i [rows, D] io with strides as above; state
- * [pool, D] f32; slots and y as for sfm_gated_delta_step.
+ * of states, updated in place: x, r, i [rows, D] io with any strides from D to 2^36;
+ * state [pool, D] f32; slots and y as for sfm_gated_delta_step.
  */
 sfm_status sfm_gated_recurrence_step(const void* x, const void* r, const void* i, const float* lam, float* state,
                                      const int32_t* slots, void* y, int64_t rows, int64_t pool, int64_t D,
@@ -524,7 +525,7 @@ sfm_status sfm_gated_recurrence_step(const void* x, const void* r, const void* i
  *   position * freqs[j] (taken in 64 bits); values from rot on stay z.
  *
  * sfm_qk_norm_rope_fwd:
- *   q [tokens, Hq, d], k [tokens, Hk, d] io   token strides ldq, ldk (heads' width to 2^22)
+ *   q [tokens, Hq, d], k [tokens, Hk, d] io   token strides ldq, ldk (heads' width to 2^29)
  *   positions  int32 [period, axes] on the device: token t has row t mod period (period
  *              divides tokens: rows that share their positions give them once)
  *   freqs      [rot / 2] f32 on the device

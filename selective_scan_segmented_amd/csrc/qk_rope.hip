@@ -372,7 +372,8 @@ void plan_rope(RopeParams& p, int io_bytes, int align, bool back) {
         const int64_t holds = kTable / (p.slots * V), few = p.tokens / 512;
         if (run > holds) run = holds;
         if (run > few) run = few;
-        if (run > 128) run = 128;  // (whose bytes stay below 2^31)
+        const int64_t near = (1LL << 31) / (q.ld * io_bytes);  // (whose bytes stay below 2^31)
+        if (run > near) run = near;
         q.run = run < 1 ? 1 : (int)run;
         q.groups = (p.tokens + q.run - 1) / q.run;
         const int64_t most = back ? kRopeParts : 1 << 20;  // (a launch holds fewer than 2^32 work items)

@@ -52,7 +52,8 @@ struct RecParams {
 
 // Cuts a call; near: the largest token stride is below 2^19 bytes (so that the 8192 tokens of nr rows end below 2^32); lane: channels to a lane (rec_wide, or one).
 RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, bool near, int lane, bool back);
-constexpr int64_t kRecMaxStride = 1 << 19;  // (a block's 1024 tokens then end below 2^31 bytes)
+// Largest token strides: the tokens of a block (at most 1024, and no more than a row has) end below 2^31 bytes.
+inline int64_t rec_max_stride(int64_t L, int io_bytes) { return (1LL << 31) / ((L < 1024 ? L : 1024) * io_bytes); }
 // Channels to a lane: 4 bytes where the sizes, strides and addresses allow it, else one.
 inline int rec_wide(int io_dtype) { return io_dtype == 0 ? 1 : 2; }
 hipError_t launch_rec_fwd(const RecParams& p, int io_dtype, hipStream_t s);

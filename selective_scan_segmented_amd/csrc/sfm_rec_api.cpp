@@ -68,12 +68,12 @@ void take_plan(sfm::RecParams& p, bool wide, int io_dtype, bool back, void* work
 }
 
 sfm_status check_inputs(const char* fn, const void* x, const void* r, const void* i, const float* lam, int64_t tokens,
-                        int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, float c, int io_dtype) {
+                        int64_t D, int64_t ldx, int64_t ldr, int64_t ldi, int64_t most, float c, int io_dtype) {
     if (!lam || (tokens > 0 && (!x || !r || !i))) return fail(SFM_ERR_NULL, "%s: x, r, i and lam are required", fn);
     for (int64_t ld : {ldx, ldr, ldi})
-        if (ld < D || ld > sfm::kRecMaxStride)
-            return fail(SFM_ERR_SHAPE, "%s: token strides %lld, %lld, %lld below D=%lld (or too large)", fn,
-                        (long long)ldx, (long long)ldr, (long long)ldi, (long long)D);
+        if (ld < D || ld > most)
+            return fail(SFM_ERR_SHAPE, "%s: token strides %lld, %lld, %lld below D=%lld or above %lld", fn,
+                        (long long)ldx, (long long)ldr, (long long)ldi, (long long)D, (long long)most);
     if (!(c > 0.0f && c <= 1e6f)) return fail(SFM_ERR_SHAPE, "%s: c=%g", fn, (double)c);
     const uintptr_t e = io_bytes(io_dtype);
     if (!aligned_to(x, e) || !aligned_to(r, e) || !aligned_to(i, e) || !aligned_to(lam, 4))
@@ -172,7 +172,7 @@ sfm_status sfm_gated_recurrence_fwd(const void* x, const void* r, const void* i,
     static const char* fn = "sfm_gated_recurrence_fwd";
     sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, D, io_dtype);
     if (st != SFM_OK) return st;
-    st = check_inputs(fn, x, r, i, lam, tokens, D, ldx, ldr, ldi, c, io_dtype);
+    st = check_inputs(fn, x, r, i, lam, tokens, D, ldx, ldr, ldi, sfm::rec_max_stride(L, io_bytes(io_dtype)), c, io_dtype);
     if (st != SFM_OK) return st;
     if (tokens > 0 && !y) return fail(SFM_ERR_NULL, "%s: y is required", fn);
     const int e = io_bytes(io_dtype);
@@ -205,7 +205,7 @@ sfm_status sfm_gated_recurrence_bwd(const void* x, const void* r, const void* i,
     static const char* fn = "sfm_gated_recurrence_bwd";
     sfm_status st = check_sizes(fn, rows, L, tokens, offsets != nullptr, D, io_dtype);
     if (st != SFM_OK) return st;
-    st = check_inputs(fn, x, r, i, lam, tokens, D, ldx, ldr, ldi, c, io_dtype);
+    st = check_inputs(fn, x, r, i, lam, tokens, D, ldx, ldr, ldi, sfm::rec_max_stride(L, io_bytes(io_dtype)), c, io_dtype);
     if (st != SFM_OK) return st;
     if (!dlam || (tokens > 0 && (!y || !dy || !dx || !dr || !di)))
         return fail(SFM_ERR_NULL, "%s: y, dy, dx, dr, di and dlam are required", fn);
@@ -247,7 +247,7 @@ sfm_status sfm_gated_recurrence_step(const void* x, const void* r, const void* i
     static const char* fn = "sfm_gated_recurrence_step";
     sfm_status st = check_sizes(fn, rows, 1, rows, false, D, io_dtype);
     if (st != SFM_OK) return st;
-    st = check_inputs(fn, x, r, i, lam, rows, D, ldx, ldr, ldi, c, io_dtype);
+    st = check_inputs(fn, x, r, i, lam, rows, D, ldx, ldr, ldi, 1LL << 36, c, io_dtype);
     if (st != SFM_OK) return st;
     if (!state || !y) return fail(SFM_ERR_NULL, "%s: state and y are required", fn);
     if (!sane(pool, 1 << 24)) return fail(SFM_ERR_SHAPE, "%s: a pool of %lld states", fn, (long long)pool);

@@ -34,7 +34,7 @@ sfm_status fill(const char* fn, sfm::RopeParams& p, const void* q, const void* k
     if (tokens > 0 && (!q || !k)) return fail(SFM_ERR_NULL, "%s: q and k are required", fn);
     if (rot > 0 && (!freqs || (tokens > 0 && !positions)))
         return fail(SFM_ERR_NULL, "%s: positions and freqs are required with a rotation", fn);
-    if (ldq < Hq * d || ldk < Hk * d || ldq > 1 << 22 || ldk > 1 << 22)
+    if (ldq < Hq * d || ldk < Hk * d || ldq > 1 << 29 || ldk > 1 << 29)
         return fail(SFM_ERR_SHAPE, "%s: token strides %lld, %lld below the heads' widths (or too large)", fn,
                     (long long)ldq, (long long)ldk);
     if (!(flags & SFM_QK_NORM) && (wq || wk)) return fail(SFM_ERR_SHAPE, "%s: weights without the norm", fn);

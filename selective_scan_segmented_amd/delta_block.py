@@ -4,6 +4,7 @@ The block stands beside the mixer block around the scan (block.py), on the same
 channel-last tokens X [B, L, C]:
 
     q, k, v = X W_qkv                         one projection, read in place as its slices
+    q, k    = rotated norms of q and k        sfm_qk_norm_rope_fwd (with rot > 0: learned weights, positions)
     g       = A softplus(X W_a + bias)        log decay per head, A < 0
     beta    = sigmoid(X W_b)                  gate per head
     o, S    = gated delta rule(q, k, v, g, beta)        sfm_gated_delta_fwd, unit queries and keys
@@ -27,6 +28,7 @@ class DeltaSizes:
     Hk: int           # query and key heads; H is a multiple
     dk: int
     dv: int
+    rot: int = 0      # values of a key head that the position rotates; 0: neither norm nor rotation
 
     @property
     def qkv(self) -> int:
@@ -49,6 +51,17 @@ class DeltaBlock:
         dt = torch.exp(math.log(1e-3) + torch.rand(z.H, generator=gen) * math.log(100.0))
         self.bias = torch.log(torch.expm1(dt)).to(device)
         self.norm_w, self.norm_b = (1 + 0.1 * rnd(z.H * z.dv)).to(device), (0.1 * rnd(z.H * z.dv)).to(device)
+        if z.rot:
+            self.wq, self.wk = (1 + 0.1 * rnd(z.dk)).to(device), (1 + 0.1 * rnd(z.dk)).to(device)
+            self.freqs = (10000.0 ** (-torch.arange(z.rot // 2, dtype=torch.float64) * 2 / z.rot)).float().to(device)
+
+    def _rotation(self, positions):
+        return dict(wq=self.wq, wk=self.wk, positions=positions, freqs=self.freqs)
+
+    def _turned(self, q, k, positions):
+        """The queries and keys that the delta rule takes."""
+        import selective_scan_segmented_amd as sfm
+        return sfm.sfm_qk_norm_rope_fwd(q, k, **self._rotation(positions)) if self.z.rot else (q, k)
 
     def _heads(self, X):
         """q, k, v as slices of one projection, and the raw gates."""
@@ -70,12 +83,16 @@ class DeltaBlock:
         z = self.z
         return sfm.sfm_group_norm_fwd(o.reshape(-1, 1, z.H * z.dv), z.H, self.norm_w, self.norm_b, act="silu")
 
-    def forward(self, X, state=None, return_state=False, keep=False):
-        """X [B, L, C] -> out [B, L, C], and the heads' states if asked for.  keep: what backward() takes."""
+    def forward(self, X, state=None, return_state=False, keep=False, positions=None):
+        """X [B, L, C] -> out [B, L, C], and the heads' states if asked for.  keep: what backward() takes.
+        positions (with rot): int32 [B, L] or [L], None: 0 .. L - 1."""
         import torch
 
         import selective_scan_segmented_amd as sfm
-        q, k, v, g, beta, raw = self._heads(X)
+        if self.z.rot and positions is None:
+            positions = torch.arange(X.shape[1], dtype=torch.int32, device=X.device)
+        q0, k0, v, g, beta, raw = self._heads(X)
+        q, k = self._turned(q0, k0, positions)
         r = sfm.sfm_gated_delta_fwd(q, k, v, g, beta, h0=state, l2norm=True, return_state=return_state)
         o, S = r if return_state else (r, None)
         y, mean, rstd = self._norm(o)
@@ -83,20 +100,23 @@ class DeltaBlock:
         out = torch.matmul(y, self.W_out)
         if keep:
             self.kept = (X, q, k, v, g, beta, raw, state, o, y, mean, rstd)
+            self.kept_raw = (q0, k0, positions)
         return (out, S) if return_state else out
 
-    def step(self, x, state, slots=None):
-        """One token of each request: x [R, C]; state [pool, H, dk, dv] float32, updated in place."""
+    def step(self, x, state, slots=None, positions=None):
+        """One token of each request: x [R, C]; state [pool, H, dk, dv] float32, updated in place; positions (with rot)
+        int32 [R]."""
         import torch
 
         import selective_scan_segmented_amd as sfm
         q, k, v, g, beta, _ = self._heads(x)
+        q, k = self._turned(q, k, positions)
         o = sfm.sfm_gated_delta_step(q, k, v, g, beta, state, slots=slots, l2norm=True)
         return torch.matmul(self._norm(o)[0].view(x.shape[0], -1), self.W_out)
 
     def backward(self, dout, dstate=None):
         """Gradients of the last forward(keep=True) for dout [B, L, C]: a dict of dX, dW_qkv, dW_a, dW_b, dW_out,
-        dA, dbias, dnorm_w, dnorm_b (and dstate0 if it had a state)."""
+        dA, dbias, dnorm_w, dnorm_b (dwq and dwk with rot, dstate0 if it had a state)."""
         import torch
 
         import selective_scan_segmented_amd as sfm
@@ -111,6 +131,11 @@ class DeltaBlock:
         d = sfm.sfm_gated_delta_bwd(q, k, v, g, beta, n["dx"].view(o.shape), h0=state, dstate=dstate, l2norm=True)
         if state is not None:
             grads["dstate0"] = d["dh0"]
+        if z.rot:
+            q0, k0, positions = self.kept_raw
+            t = sfm.sfm_qk_norm_rope_bwd(d["dq"], d["dk"], q0, k0, **self._rotation(positions))
+            grads.update(dwq=t["dwq"], dwk=t["dwk"])
+            d.update(dq=t["dq"], dk=t["dk"])
         dp = torch.cat([d["dq"].flatten(-2), d["dk"].flatten(-2), d["dv"].flatten(-2)], -1)
         dg, sig = d["dg"].float(), torch.sigmoid(raw)
         draw = dg * self.A * sig

@@ -43,10 +43,10 @@ def step(lib, **kw):
 
 
 SHARED = [(dict(x=None), NULL), (dict(i=None), NULL), (dict(lam=None), NULL), (dict(y=None), NULL), (dict(io=2), DTYPE),
-          (dict(D=0), SHAPE), (dict(D=65537, ldx=65537, ldr=65537, ldi=65537), SHAPE), (dict(ldx=63), SHAPE), (dict(ldi=(1 << 19) + 1), SHAPE),
+          (dict(D=0), SHAPE), (dict(D=65537, ldx=65537, ldr=65537, ldi=65537), SHAPE), (dict(ldx=63), SHAPE), (dict(ldi=(1 << 36) + 1), SHAPE),
           (dict(rows=0), SHAPE), (dict(c=0.0), SHAPE), (dict(c=-8.0), SHAPE), (dict(c=float("nan")), SHAPE), (dict(c=float("inf")), SHAPE),
           (dict(x=P + 1), ALIGN), (dict(lam=4 * P + 2), ALIGN), (dict(y=5 * P + 1), ALIGN)]
-ROWS = [(dict(tokens=1999), SHAPE), (dict(L=0), SHAPE), (dict(tokens=-1, off=7 * P), SHAPE), (dict(off=7 * P + 2), ALIGN),
+ROWS = [(dict(tokens=1999), SHAPE), (dict(ldr=(1 << 31) // 2000 + 1), SHAPE), (dict(L=0), SHAPE), (dict(tokens=-1, off=7 * P), SHAPE), (dict(off=7 * P + 2), ALIGN),
         (dict(h0=11 * P + 2), ALIGN), (dict(rows=1 << 24, L=1, tokens=1 << 24), SHAPE)]
 
 
@@ -99,7 +99,7 @@ ROPE = [(dict(q=None), NULL), (dict(k=None), NULL), (dict(pos=None), NULL), (dic
         (dict(flags=4), SHAPE), (dict(flags=0), SHAPE), (dict(tokens=-1), SHAPE), (dict(period=3), SHAPE), (dict(period=0), SHAPE),
         (dict(Hq=0), SHAPE), (dict(Hk=0), SHAPE), (dict(d=257, ldq=2000, ldk=2000), SHAPE), (dict(rot=63), SHAPE), (dict(rot=66), SHAPE),
         (dict(rot=-2), SHAPE), (dict(axes=0), SHAPE), (dict(axes=5), SHAPE), (dict(axes=2), SHAPE), (dict(axes=2, sections=sections(16, 15)), SHAPE),
-        (dict(axes=2, sections=sections(33, -1)), SHAPE), (dict(ldq=255), SHAPE), (dict(ldk=(1 << 22) + 1), SHAPE), (dict(eps=0.0), SHAPE),
+        (dict(axes=2, sections=sections(33, -1)), SHAPE), (dict(ldq=255), SHAPE), (dict(ldk=(1 << 29) + 1), SHAPE), (dict(eps=0.0), SHAPE),
         (dict(eps=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE), (dict(q=P + 1), ALIGN), (dict(wk=4 * P + 2), ALIGN),
         (dict(pos=5 * P + 2), ALIGN)]
 
