@@ -928,23 +928,25 @@ def _rope_args(q, k, wq, wk, positions, freqs, sections, interleaved, norm):
     tokens = lead.numel()
     rot, axes, period, parts = 0, 1, 1, None
     if freqs is not None:
-        _dev(freqs, "freqs", torch.float32)
-        _dev(positions, "positions", torch.int32)
-        if positions is None or freqs.dim() != 1 or not freqs.numel():
+        pairs = freqs.numel()
+        _want(freqs, "freqs", torch.float32, (pairs,))
+        if positions is None or not pairs:
             raise ValueError("a rotation takes positions and freqs [rot / 2]")
-        rot = 2 * freqs.numel()
-        sections = (freqs.numel(),) if sections is None else tuple(int(n) for n in sections)
-        axes = len(sections)
-        parts = (ctypes.c_int64 * max(1, axes))(*sections)
-        shape, last = tuple(positions.shape), (axes,)
-        if axes == 1 and shape in (tuple(lead), tuple(lead[-1:])):  # one axis: without a dimension of its own
+        rot = 2 * pairs
+        if sections is not None:
+            axes = len(sections)
+            if axes != 1 or sections[0] != pairs:
+                parts = (ctypes.c_int64 * max(1, axes))(*(int(n) for n in sections))
+        shape, last = positions.shape, (axes,)
+        if axes == 1 and (shape == lead or shape == lead[-1:]):  # one axis: without a dimension of its own
             last = ()
-        if shape == tuple(lead) + last:
+        if shape == lead + last:
             period = tokens
-        elif len(lead) == 2 and shape == tuple(lead[-1:]) + last:  # rows that share their positions
+        elif len(lead) == 2 and shape == lead[-1:] + last:  # rows that share their positions
             period = lead[-1]
         else:
-            raise ValueError(f"positions must be {tuple(lead)} or {tuple(lead[-1:])} with {axes} axes, got {shape}")
+            raise ValueError(f"positions must be {tuple(lead)} or {tuple(lead[-1:])} with {axes} axes, got {tuple(shape)}")
+        _want(positions, "positions", torch.int32, shape)
     elif positions is not None or sections is not None:
         raise ValueError("positions and sections without freqs")
     flags = (SFM_QK_NORM if norm else 0) | (SFM_QK_NEIGHBOURS if interleaved else 0)

@@ -156,7 +156,7 @@ def test_positions(calls, lead, shape, sections, want):  # noqa: F811
     rope(*heads(lead), positions=Stub(*shape, dtype=I32), sections=sections, **ROT)
     name, a = calls[-1]
     assert name == "sfm_qk_norm_rope_fwd" and (a[8], a[9], a[14]) == want and a[13] == 32
-    assert list(a[15]) == list(sections or (16,))
+    assert a[15] is None if want[2] == 1 else list(a[15]) == list(sections)
 
 
 def test_norm_alone(calls):  # noqa: F811
