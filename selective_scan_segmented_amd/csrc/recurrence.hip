@@ -233,12 +233,14 @@ __global__ __launch_bounds__(HAND ? kHandThreads : kThreads, 4) void rec_bwd_ker
         const Chunk c(p, at);
         const int n = c.n(l);
         const bool start = c.first && l.tc == 0;
-        RecPack<T, C> r[TT], g[TT], i[TT], x[TT], y[TT];
+        RecPack<T, C> g[TT], i[TT], x[TT], y[TT];
+        float sr[TT][C];
         if (l.live) {
             float A[C], U[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) A[j] = 1.0f, U[j] = 0.0f;
             if (n > 0) {
+                RecPack<T, C> r[TT];
                 load_chunk<T, C, TT>(r, p.r, p.ldr, c, l, RecPack<T, C>::kMinusInf);
                 load_chunk<T, C, TT>(g, p.dy, p.D, c, l, 0);
                 load_chunk<T, C, TT>(i, p.i, p.ldi, c, l, 0);
@@ -260,7 +262,8 @@ __global__ __launch_bounds__(HAND ? kHandThreads : kThreads, 4) void rec_bwd_ker
                 for (int t = TT - 1; t >= 0; --t)
 #pragma unroll
                     for (int j = 0; j < C; ++j) {
-                        const float a = exp2_fast(rate[j] * rec_sigmoid<kExact>(r[t].get(j)));
+                        sr[t][j] = rec_sigmoid<kExact>(r[t].get(j));
+                        const float a = exp2_fast(rate[j] * sr[t][j]);
                         U[j] = a * (U[j] + g[t].get(j));
                         A[j] *= a;
                     }
@@ -285,17 +288,18 @@ __global__ __launch_bounds__(HAND ? kHandThreads : kThreads, 4) void rec_bwd_ker
                 float dx[C], dr[C], di[C];
 #pragma unroll
                 for (int j = 0; j < C; ++j) {
-                    const float sr = rec_sigmoid<kExact>(r[t].get(j)), si = rec_sigmoid<kExact>(i[t].get(j));
-                    const float la2 = rate[j] * sr, a = exp2_fast(la2), em = rec_keep2<kExact>(la2, a);
-                    const float rs = em > 0.0f ? __builtin_amdgcn_rsqf(em) : em == em ? 0.0f : em;
-                    const float G = g[t].get(j) + u[j], xv = x[t].get(j);
-                    const float before = t == 0 && start ? h0[j] : y[t].get(j);
-                    const float P = G * (a * (la2 * kLn2)) * (before - a * rs * si * xv);
-                    dx[j] = G * (em * rs) * si;
-                    di[j] = dx[j] * xv * (1.0f - si);
-                    dr[j] = P * (1.0f - sr);
-                    sum[j] += P;
+                    const float si = rec_sigmoid<kExact>(i[t].get(j)), xv = x[t].get(j);
+                    const float la2 = rate[j] * sr[t][j], la = (rate[j] * kLn2) * sr[t][j];
+                    const float a = exp2_fast(la2), em = rec_keep2<kExact>(la2, a);
+                    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(em, 0x1p-120f));  // (a = 1: la is 0 beside it)
+                    const float G = g[t].get(j) + u[j], before = t == 0 && start ? h0[j] : y[t].get(j);
                     u[j] = a * G;
+                    const float P = u[j] * (la * __builtin_fmaf(-a, rs * (si * xv), before));
+                    dx[j] = G * (em * rs * si);
+                    const float s = dx[j] * xv;
+                    di[j] = __builtin_fmaf(-s, si, s);
+                    dr[j] = __builtin_fmaf(-P, sr[t][j], P);
+                    sum[j] += P;
                 }
                 RecPack<T, C>::store(rec_buf<T>(p.dx, c.base, p.D), to, t * token, dx);
                 RecPack<T, C>::store(rec_buf<T>(p.dr, c.base, p.D), to, t * token, dr);
