@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTable = 2048;  // sines and cosines that a workgroup holds
+constexpr int kPositions = 512;  // and positions
 constexpr float kRopeDown = 0x1p-96f;
 constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
 
@@ -69,14 +70,18 @@ template <typename T, int V> struct RopeRun {
     }
 };
 
-// cos and sin of position * frequency: the product in turns and in 64 bits, its fraction to 32.
-__device__ __forceinline__ float2 rope_angle(const RopeParams& p, int64_t row, int j) {
-    int axis = 0;
-    for (int a = 0; a + 1 < p.axes; ++a) axis += j >= p.ends[a];
-    const double turns = (double)p.positions[row * p.axes + axis] * ((double)p.freqs[j] * kTurn);
-    const double f = turns - __builtin_rint(turns);
+// cos and sin of position * frequency: the product in turns and in 64 bits, its fraction to 32.  Beside bfloat16 values
+// the hardware's functions of turns are exact enough (of sines and cosines alone, 1 in 10000 rounds to the neighbour of
+// the exact value's); float32 ones take the library's.
+template <bool EXACT>
+__device__ __forceinline__ float2 rope_angle(int position, float freq) {
+    const double turns = (double)position * ((double)freq * kTurn);
+    const float f = (float)(turns - __builtin_rint(turns));
     float2 cs;
-    sincospif((float)(2.0 * f), &cs.y, &cs.x);
+    if constexpr (EXACT)
+        sincospif(2.0f * f, &cs.y, &cs.x);
+    else
+        cs = make_float2(__builtin_amdgcn_cosf(f), __builtin_amdgcn_sinf(f));
     return cs;
 }
 
@@ -114,14 +119,16 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2*
 }
 
 // Heads that a lane has in flight: as many as registers allow (forward of 2 x 8192 tokens x 24 heads of 128: 40 us with
-// four, 42 with two, 58 with one).
-constexpr int in_flight(int V, int S, bool back) { return S > 1 ? 1 : back ? 2 : 4; }
+// four, 42 with two, 58 with one; backward of 2 x 4002 x 12: 23.2 us with one, 24 with two).
+constexpr int in_flight(int V, int S, bool back) { return S > 1 || back ? 1 : 4; }
 
 // S: slots to a lane.
 template <typename T, int V, int S, bool NEIGH, bool BACK>
 __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
     constexpr int U = in_flight(V, S, BACK);
     __shared__ __align__(16) float2 table[kTable];
+    __shared__ int positions[kPositions];
+    __shared__ float freqs[kRopeMaxD / 2];
     const int sd = blockIdx.y, tid = threadIdx.x;
     const RopeSide& q = p.side[sd];
     if ((int64_t)blockIdx.x >= q.groups) return;
@@ -141,7 +148,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
             s1[s][v] = s2[s][v] = 0.0f;
         }
     }
-    const float inv_heads = 1.0f / (float)q.heads, inv_d = 1.0f / (float)p.d;
+    const float inv_heads = 1.0f / (float)q.heads, inv_d = 1.0f / (float)p.d, inv_width = 1.0f / (float)width;
+    const float inv_axes = 1.0f / (float)p.axes;
+    if (tid < half) freqs[tid] = p.freqs[tid];
+    const uint32_t period = (uint32_t)p.period;
     for (int64_t run = blockIdx.x; run * q.run < p.tokens; run += q.groups) {
         const int64_t tok0 = run * q.run;
         const int tokens = p.tokens - tok0 < q.run ? (int)(p.tokens - tok0) : q.run, rows = tokens * q.heads;
@@ -149,7 +159,19 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
         const int64_t out = tok0 * q.heads * p.d;
         const __amdgpu_buffer_rsrc_t yb = __builtin_amdgcn_make_buffer_rsrc(static_cast<T*>(q.y) + out, 0, -1, 0x00027000);
         const __amdgpu_buffer_rsrc_t gb = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(static_cast<const T*>(BACK ? q.dy : q.x) + (BACK ? out : 0)), 0, -1, 0x00027000);
-        bool first = true;
+        // the run's positions: asked for before its first heads, so that they are there first
+        int at[kPositions / kThreads];
+        const uint32_t base = (uint32_t)tok0 % period;  // (the same for all lanes)
+#pragma unroll
+        for (int e = 0; e < kPositions / kThreads; ++e) {
+            at[e] = 0;
+            const int k = tid + e * kThreads;
+            if (!half || k >= tokens * p.axes) continue;
+            const int t = div_small(k, inv_axes);
+            uint32_t row = base + (uint32_t)t;
+            if (row >= period) row = row - period < period ? row - period : row % period;
+            at[e] = p.positions[(int64_t)row * p.axes + (k - t * p.axes)];
+        }
         for (int r0 = 0; r0 < rows; r0 += groups * U) {
             RopeRun<T, V> x1[U][S], x2[U][S], g1[U][S], g2[U][S];
             int tok[U];
@@ -174,13 +196,17 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
                         }
                     }
             }
-            if (first) {  // the run's sines and cosines; values behind the rotation keep their place
-                for (int k = tid; k < tokens * width; k += blockDim.x) {
-                    const int t = k / width, j = k - t * width;
-                    table[k] = j < half ? rope_angle(p, (tok0 + t) % p.period, j) : make_float2(1.0f, 0.0f);
+            if (r0 == 0) {  // the run's sines and cosines; values behind the rotation keep their place
+#pragma unroll
+                for (int e = 0; e < kPositions / kThreads; ++e) positions[tid + e * kThreads] = at[e];
+                lds_barrier();
+                for (int k = tid; k < tokens * width; k += kThreads) {
+                    const int t = div_small(k, inv_width), j = k - t * width;
+                    int axis = 0;
+                    for (int a = 0; a + 1 < p.axes; ++a) axis += j >= p.ends[a];
+                    table[k] = j < half ? rope_angle<sizeof(T) == 4>(positions[t * p.axes + axis], freqs[j]) : make_float2(1.0f, 0.0f);
                 }
                 lds_barrier();
-                first = false;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -364,12 +390,13 @@ void plan_rope(RopeParams& p, int io_bytes, int align, bool back) {
     p.slots = (p.d + 2 * V - 1) / (2 * V);
     p.lanes = 1;
     while (p.lanes < p.slots && p.lanes < 64) p.lanes *= 2;
-    const int per = in_flight(V, p.slots > 64 ? 2 : 1, back) * (back ? 2 : 1);
+    const int per = in_flight(V, p.slots > 64 ? 2 : 1, back) * (back ? 8 : 1);
     p.threads = kThreads;
     for (RopeSide& q : p.side) {
         // tokens whose heads give every lane that many, as far as the table holds them and enough workgroups are left
         int64_t run = (int64_t)(kThreads / p.lanes) * per / q.heads;
-        const int64_t holds = kTable / (p.slots * V), few = p.tokens / 512;
+        const int64_t of_table = kTable / (p.slots * V), of_positions = kPositions / p.axes;
+        const int64_t holds = of_table < of_positions ? of_table : of_positions, few = p.tokens / 512;
         if (run > holds) run = holds;
         if (run > few) run = few;
         const int64_t near = (1LL << 31) / (q.ld * io_bytes);  // (whose bytes stay below 2^31)
