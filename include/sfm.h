@@ -479,6 +479,8 @@ sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G
  *            the tokens are cut to them, tokens of no row and those past L keep their old y
  *   D 1..65536.  Tensors need their element's alignment only; bfloat16 ones of even D and
  *   strides on 4 bytes are loaded two channels at a time, others one by one.
+ *   Rows and channels that make more workgroups than a launch holds (2^24, rows of 128 channels
+ *   one each) are SFM_ERR_SHAPE.
  * A non-finite value of a token stays in its row and channel.  Repeated calls give the same bits.
  * workspace: at least sfm_gated_recurrence_fwd_ws_size() bytes (may be NULL when that is
  *   0), 16-byte aligned, owned by the caller.

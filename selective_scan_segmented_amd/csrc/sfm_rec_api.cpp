@@ -36,7 +36,8 @@ int64_t need_of(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed,
         if (D % lane) continue;
         for (bool near : {false, true}) {
             const sfm::RecPlan q = sfm::plan_rec(rows, L, tokens, D, packed, near, lane, back);
-            if (q.launch >= 1LL << 24 || q.bytes_words >= 1LL << 40) return -1;
+            const int64_t threads = (q.nr * q.nt * q.nc + 63) / 64 * 64;
+            if (q.launch >= 1LL << 24 || q.launch * threads >= 1LL << 32) return -1;
             if (q.bytes > need) need = q.bytes;
         }
     }
