@@ -767,10 +767,11 @@ def _channels(t, name, dtype, shape):
     st = t.stride()
     single = len(shape) == 3 and shape[1] == 1  # rows of one token: the tokens are the rows'
     ld = st[0] if single else st[-2]
-    if (D > 1 and st[-1] != 1) or (len(shape) == 3 and not single and shape[0] > 1 and st[0] != shape[1] * ld) or \
-            (ld < D and shape.numel() > D):
+    if shape.numel() <= D:
+        ld = D  # (one token, or none: its stride says nothing)
+    if (D > 1 and st[-1] != 1) or (len(shape) == 3 and not single and shape[0] > 1 and st[0] != shape[1] * ld) or ld < D:
         raise ValueError(f"{name}: channels must be contiguous and tokens evenly strided, got strides {st}")
-    return max(ld, D)
+    return ld
 
 
 def _recurrence_args(x, r, i, lam, packed, dims, form):

@@ -93,6 +93,9 @@ def test_slices_of_a_projection_are_taken_in_place(calls):  # noqa: F811
     t[:3] = [Stub(B, 1, D, stride=(5000, 7, 1)) for _ in range(3)]
     fwd(t)
     assert calls[-1][1][12:15] == (5000,) * 3
+    t[:3] = [Stub(1, 1, D, stride=(1 << 40, 7, 1)) for _ in range(3)]  # one token in all: its strides say nothing
+    fwd(t)
+    assert calls[-1][1][12:15] == (D,) * 3
 
 
 def test_a_step_takes_two_dimensions(calls):  # noqa: F811
