@@ -242,3 +242,43 @@ def test_duplicate_work_of_no_request():
     slots = torch.tensor([-7, 0, 9, 1], dtype=torch.int32, device="cuda")
     y = sfm.sfm_gated_recurrence_step(x[:, 0], r[:, 0], i[:, 0], lam, pool, slots=slots)
     assert y[1].any() and not y[0].any() and not y[2:].any()
+
+
+def test_tensors_past_32_bits():
+    """2^32 elements and more: the last rows, tokens and heads are what they are by themselves."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    B, L, D = 16387, 64, 4096
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    lam = torch.log(torch.expm1(-torch.log(0.9 + 0.099 * torch.rand(D, generator=gen, device="cuda"))))
+    x = torch.empty(B, L, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    assert x.numel() > 1 << 32
+    S = torch.empty(B, D, device="cuda")
+    y = sfm.sfm_gated_recurrence_fwd(x, x, x, lam, state=S)
+    g = sfm.sfm_gated_recurrence_bwd(x, x, x, lam, y, x)
+    last = x[-3:].clone()
+    y1, S1 = sfm.sfm_gated_recurrence_fwd(last, last, last, lam, return_state=True)
+    g1 = sfm.sfm_gated_recurrence_bwd(last, last, last, lam, y1, last)
+    assert torch.equal(y[-3:], y1) and torch.equal(S[-3:], S1)
+    for n in ("dx", "dr", "di"):
+        assert torch.equal(g[n][-3:], g1[n]), n
+    del g
+    # one long row (handed on), and its end: decays are below 0.999^(8 sigmoid(r)), so 4000 tokens keep e^-16 of a state;
+    # blocks fall elsewhere, where a block's decay is a product of up to 1024 factors: 2^-14 of states below 4
+    x = x.view(1, B * L, D)
+    y = sfm.sfm_gated_recurrence_fwd(x, x, x, lam, y=y.view(1, B * L, D))
+    end = x[:, -4000:].contiguous()
+    y1 = sfm.sfm_gated_recurrence_fwd(end, end, end, lam)
+    assert torch.allclose(y[:, -64:].float(), y1[:, -64:].float(), rtol=2.0 ** -7, atol=2.0 ** -12)
+    # heads
+    H, d = 128, 128
+    q, k = x.view(-1, H, d), x.view(-1, H, d)[:, :1]
+    pos, freqs = torch.arange(q.shape[0], dtype=torch.int32, device="cuda"), torch.rand(d // 2, generator=gen, device="cuda")
+    form = dict(wq=lam[:d].contiguous(), wk=lam[:d].contiguous(), freqs=freqs)
+    qo, ko = sfm.sfm_qk_norm_rope_fwd(q, k, positions=pos, qo=y.view(q.shape), **form)
+    g = sfm.sfm_qk_norm_rope_bwd(q, ko, q, k, positions=pos, **form)
+    a, b, p = q[-100:].clone(), k[-100:].clone(), pos[-100:].clone()
+    qo1, ko1 = sfm.sfm_qk_norm_rope_fwd(a, b, positions=p, **form)
+    g1 = sfm.sfm_qk_norm_rope_bwd(a, ko1, a, b, positions=p, **form)
+    assert torch.equal(qo[-100:], qo1) and torch.equal(ko[-100:], ko1)
+    assert torch.equal(g["dq"][-100:], g1["dq"]) and torch.equal(g["dk"][-100:], g1["dk"])
