@@ -301,3 +301,79 @@ def test_long_row_of_slow_decays():
     """One row of 70000 tokens: blocks by the hundred."""
     check_forward(1, [70000], 8, "f32", c=1.0)
     check_backward(1, [70000], 8, "bf16")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,L", [(3, 700), (4, 300), (5, 1100), (9, 530), (11, 260), (17, 400)])
+def test_numbers_of_long_rows(rows, L, io):
+    """Blocks handed on by rows that are no whole groups."""
+    check_forward(rows, [L] * rows, 72, io)
+    check_backward(rows, [L] * rows, 72, io)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_many_packed_rows(io):
+    """Packed rows of several blocks that a workgroup walks each, some of them empty."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    rng = np.random.default_rng(4)
+    D, n = 33, 4200
+    lens = rng.integers(100, 300, n)
+    lens[[0, 7, 8, n - 1]] = 0
+    ends = np.cumsum(lens)
+    x, r, i, lam, s0, dy, dhT = ref.recurrence_inputs(4, int(ends[-1]), n, D, io)
+    t = [dev(v, io).view(1, -1, D) for v in (x, r, i)] + [dev(lam, "f32")]
+    off = torch.tensor(np.concatenate([[0], ends]), dtype=torch.int32).cuda()
+    rows = dict(h0=dev(s0, "f32"), offsets=off, max_len=300)
+    y, state = sfm.sfm_gated_recurrence_fwd(*t, return_state=True, **rows)
+    g = sfm.sfm_gated_recurrence_bwd(*t, y, dev(dy, io).view(y.shape), dstate=dev(dhT, "f32"), **rows)
+    yh = from_dev(y)[0]
+    for s in (0, 1, 7, 9, 1000, 2500, n - 2, n - 1):
+        at, one = slice(ends[s] - lens[s], ends[s]), slice(s, s + 1)
+        wy, wh = ref.recurrence(x[at], r[at], i[at], lam, s0[one], [lens[s]], 8.0)
+        close(yh[at], wy, io, "y", FORWARD[io])
+        close(from_dev(state)[one], wh, "f32", "state", FORWARD["f32"])
+        w = ref.recurrence_bwd(x[at], r[at], i[at], lam, s0[one], yh[at], [lens[s]], 8.0, dy[at], dhT[one])
+        for k in ("dx", "dr", "di"):
+            close(from_dev(g[k])[0, at], w[k], io, k, BACKWARD[io])
+        close(from_dev(g["dh0"])[one], w["dh0"], "f32", "dh0", BACKWARD["f32"])
+    # dr is the terms of dlam times 1 - sigmoid(r), each rounded to its type once
+    lam = t[3].double()
+    terms = g["dr"][0].double() / torch.sigmoid(-t[1][0].double()) * (torch.sigmoid(lam) / torch.nn.functional.softplus(lam))
+    step = 2.0 ** -8 if io == "bf16" else 2.0 ** -24
+    assert ((g["dlam"].double() - terms.sum(0)).abs() <= (step + 1e-5) * terms.abs().sum(0)).all()
+
+
+def test_replays_of_packed_rows_read_their_offsets():
+    """A captured call of packed rows takes the offsets that its tensor holds at each replay."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    D, tokens, most = 72, 2000, 900
+    x, r, i, lam, s0, dy, _ = ref.recurrence_inputs(6, tokens, 5, D, "bf16")
+    t = [dev(v, "bf16").view(1, tokens, D) for v in (x, r, i)] + [dev(lam, "f32")]
+    dy, h0 = dev(dy, "bf16").view(1, tokens, D), dev(s0, "f32")
+    off = torch.zeros(6, dtype=torch.int32, device="cuda")
+
+    def both(y=None, grads=None):
+        form = dict(h0=h0, offsets=off, max_len=most)
+        y, state = sfm.sfm_gated_recurrence_fwd(*t, y=y, return_state=True, **form)
+        return y, state, sfm.sfm_gated_recurrence_bwd(*t, y, dy, grads=grads, **form)
+
+    outs = lambda: (torch.zeros_like(dy), {n: torch.zeros_like(dy) for n in ("dx", "dr", "di")})
+    held = outs()
+    both(*held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, state, g = both(*held)
+    for ends in ([0, 900, 900, 1000, 1900, 2000], [0, 0, 0, 0, 0, 0], [5, 300, 600, 900, 1200, 1700], [0, 900, 900, 1000, 1900, 2000]):
+        off.copy_(torch.tensor(ends, dtype=torch.int32))
+        wy, ws, wg = both(*outs())
+        for v in (held[0], *held[1].values()):
+            v.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, wy) and torch.equal(state, ws)
+        for n in wg:
+            assert torch.equal(g[n], wg[n]), n
