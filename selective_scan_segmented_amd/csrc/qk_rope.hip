@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
     }
 }
 
-// dw from the workgroups' parts: 16 values to a workgroup, every 64th part to a lane.
+// dw from the workgroups' parts: 16 values to a workgroup, every 64th part to a lane, all asked for together.
 __global__ __launch_bounds__(1024) void rope_weights_kernel(const RopeParams p) {
     __shared__ float part[64][17];
     const int w = threadIdx.x & 15, g = threadIdx.x >> 4, j = blockIdx.x * 16 + w;
@@ -336,8 +336,12 @@ __global__ __launch_bounds__(1024) void rope_weights_kernel(const RopeParams p) 
     float sum = 0.0f;
     if (j < p.d) {
         const float* v = p.part + (int64_t)blockIdx.y * kRopeParts * p.d + j;
-#pragma unroll 4
-        for (int64_t k = g; k < q.groups; k += 64) sum += v[k * p.d];
+        const int n = (int)q.groups;
+        float f[kRopeParts / 64];
+#pragma unroll
+        for (int m = 0; m < kRopeParts / 64; ++m) f[m] = m * 64 + g < n ? v[(m * 64 + g) * p.d] : 0.0f;
+#pragma unroll
+        for (int m = 0; m < kRopeParts / 64; ++m) sum += f[m];
     }
     part[g][w] = sum;
     lds_barrier();
