@@ -19,8 +19,8 @@ namespace sfm {
 
 namespace {
 
-constexpr int kThreads = 512;      // most to a workgroup of the rows' kernels
-constexpr int kHandThreads = 256;  // and to one of rows of several blocks
+constexpr int kThreads = 512;     // most to a workgroup
+constexpr int kFewThreads = 256;  // and to one that walks rows of several blocks (plan_rec)
 
 // A lane's place in its workgroup: row, chunk (of TT tokens) and channels.
 template <int TT> struct Lane {
@@ -137,11 +137,12 @@ __device__ __forceinline__ void empty_block(const RecParams& p, const RecItem& a
     }
 }
 
-template <typename T, int C, bool HAND>
-__global__ __launch_bounds__(HAND ? kHandThreads : kThreads, C == 2 ? (HAND ? 5 : 4) : 6) void rec_fwd_kernel(const RecParams p) {
+// HAND: threads to a workgroup where blocks are handed on, else 0.
+template <typename T, int C, int HAND>
+__global__ __launch_bounds__(HAND ? HAND : kThreads, C == 2 ? (HAND == kFewThreads ? 5 : 4) : 6) void rec_fwd_kernel(const RecParams p) {
     constexpr bool kExact = sizeof(T) == 4;
     constexpr int TT = kRecChunk<false>;
-    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? kHandThreads : kThreads) * C];
+    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? HAND : kThreads) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
     if constexpr (HAND) {
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(HAND ? kHandThreads : kThreads, C == 2 ? (HAND ? 5 
             for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], H[j]);
         }
         lds_barrier();
-        join_chunks<C, HAND, false>(p, agg, at, kept);
+        join_chunks<C, HAND != 0, false>(p, agg, at, kept);
         lds_barrier();
         if (n > 0) {
             float h[C];
@@ -209,12 +210,12 @@ __global__ __launch_bounds__(HAND ? kHandThreads : kThreads, C == 2 ? (HAND ? 5 
     }
 }
 
-template <typename T, int C, bool HAND>
-__global__ __launch_bounds__(HAND ? kHandThreads : kThreads, 4) void rec_bwd_kernel(const RecParams p) {
+template <typename T, int C, int HAND>
+__global__ __launch_bounds__(HAND ? HAND : kThreads, 4) void rec_bwd_kernel(const RecParams p) {
     constexpr bool kExact = sizeof(T) == 4;
     constexpr int TT = kRecChunk<true>;
-    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? kHandThreads : kThreads) * C];
-    __shared__ float part[(HAND ? kHandThreads : kThreads) * C];
+    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? HAND : kThreads) * C];
+    __shared__ float part[(HAND ? HAND : kThreads) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
     if constexpr (HAND) {
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(HAND ? kHandThreads : kThreads, 4) void rec_bwd_ker
             for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], U[j]);
         }
         lds_barrier();
-        join_chunks<C, HAND, true>(p, agg, at, kept);
+        join_chunks<C, HAND != 0, true>(p, agg, at, kept);
         lds_barrier();
         if (n > 0) {
             float u[C], h0[C];
@@ -400,8 +401,9 @@ hipError_t launch_rows(const RecParams& p, hipStream_t s) {
         else                                                                                   \
             hipLaunchKernelGGL((rec_fwd_kernel<T, C, HAND>), grid, threads, 0, s, p);          \
     }
-    SFM_REC_LAUNCH(1, 0) SFM_REC_LAUNCH(1, 1)
-    if constexpr (sizeof(T) == 2) { SFM_REC_LAUNCH(2, 0) SFM_REC_LAUNCH(2, 1) }
+    SFM_REC_LAUNCH(1, 0) SFM_REC_LAUNCH(1, kThreads)
+    if constexpr (sizeof(T) == 2) { SFM_REC_LAUNCH(2, 0) SFM_REC_LAUNCH(2, kThreads) }
+    if constexpr (sizeof(T) == 2 && !BACK) { SFM_REC_LAUNCH(2, kFewThreads) }
 #undef SFM_REC_LAUNCH
     return hipGetLastError();
 }
@@ -428,18 +430,36 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     const int chunk = back ? kRecChunk<true> : kRecChunk<false>;
     const int64_t chunks = (L + chunk - 1) / chunk;
     const int least = lanes < 32 ? lanes : 32;  // lanes side by side: 128 bytes where there are so many
-    const int most = kHandThreads / least < 64 ? kHandThreads / least : 64;
-    const bool several = chunks > (most > 16 ? most : 16);
-    q.nt = several ? most : (int)chunks;
-    q.blocks = 1, q.groups = 1;
-    if (several && !packed) {  // (equal rows: equal blocks)
-        q.blocks = (int)((chunks + most - 1) / most);
-        q.nt = (int)((chunks + q.blocks - 1) / q.blocks);
-        q.blocks = (int)((chunks + q.nt - 1) / q.nt);
+    const int chains = (lanes + least - 1) / least;
+    // cuts rows for workgroups of so many threads; whether they then are of several blocks
+    const auto cut = [&](int threads) {
+        const int most = threads / least < 64 ? threads / least : 64;
+        const bool several = chunks > (most > 16 ? most : 16);
+        q.nt = several ? most : (int)chunks;
+        q.blocks = 1;
+        if (several && !packed) {  // (equal rows: equal blocks)
+            q.blocks = (int)((chunks + most - 1) / most);
+            q.nt = (int)((chunks + q.blocks - 1) / q.blocks);
+            q.blocks = (int)((chunks + q.nt - 1) / q.nt);
+        }
+        return several;
+    };
+    bool several = cut(kFewThreads);
+    if (several && hands_on(rows, L, tokens, chains, q.blocks, packed, back)) {
+        // Workgroups that hand on: wide ones make fewer blocks to wait for, small ones more waits at once.  256 / 512 threads:
+        //     backward, float32: 1 x 70000 x 320: 267 / 176 us, 16 x 4002 x 320: 148 / 146 us, 2 x 8192 x 2048: 247 / 249 us;
+        //     backward, bfloat16: 1 x 20000 x 1024: 108 / 96 us, 2 x 8192 x 2048: 140 / 138 us, 24 packed to 2048 x 1024: 125 / 121 us;
+        //     forward, float32: 1 x 70000 x 320: 138 / 90 us, 2 x 8192 x 2048: 121 / 119 us;
+        //     forward, bfloat16: 1 x 32768 x 320 (5 rows' tiles): 67 / 42 us, 1 x 8192 x 1024 (16): 28 / 23 us, x 2048 (32):
+        //     41 / 40 us, 3 x 8192 x 1024 (48): 62 / 64 us, 2 x 8192 x 2048 (64): 69 / 70 us, packed to 2048: 63 / 66 us.
+        const int threads = lane == 1 || back || rows * chains <= 32 ? kThreads : kFewThreads;
+        several = cut(threads);
+        q.hand = several ? threads : 0;
     }
+    q.groups = 1;
     q.block = q.nt * chunk;
     // one block: as wide as the workgroup allows in whole 128 bytes, down to half that where it leaves fewer lanes idle
-    const int budget = q.nt * least > kHandThreads ? kThreads : kHandThreads;
+    const int budget = q.nt * least > kFewThreads ? kThreads : kFewThreads;
     int nc = several ? least : budget / q.nt;
     if (nc >= lanes) {
         nc = lanes;
@@ -451,7 +471,6 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     }
     q.nc = nc;
     q.tiles = (lanes + nc - 1) / nc;
-    q.hand = several && hands_on(rows, L, tokens, q.tiles, q.blocks, packed, back);
     q.nr = several || packed || q.tiles > 1 || !near ? 1 : budget / (q.nt * nc);
     if (q.nr > rows) q.nr = (int)rows;
     if (!q.hand) {

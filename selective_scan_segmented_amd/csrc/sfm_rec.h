@@ -13,7 +13,7 @@ template <bool BACK> constexpr int kRecChunk = BACK ? 8 : 16;  // tokens to a la
 struct RecPlan {
     int lane, nc, nt, nr, tiles;  // tiles: workgroups side by side over the channels
     int block;                    // tokens to a block
-    int hand;
+    int hand;                     // threads to a workgroup that hands on, else 0
     int blocks;                   // equal rows: blocks to a row
     int groups;                   // hand: ticket counters to a tile, a power of two
     int64_t entries;              // hand: blocks of all rows; else: workgroups along the rows
