@@ -34,28 +34,20 @@ __device__ __forceinline__ float rec_rate(float lam, float c) {
     return rate < -3e38f ? -3e38f : rate;
 }
 
-// 1 - a^2 = 1 - 4^la2 from la2 = log2(a) <= 0 and a itself: the series of it in la2 (terms -z^k / k! with z = la2 ln 4),
-// or 1 - a a.  The series' first omitted term and the rounding of 1 - a a meet at the threshold: EXACT (float32 tensors)
-// z = -1/2, eight terms, 2^-26 and 2^-22; else z = -1/16, four terms, 2^-23 and 2^-19.6, both of which the root halves.
+// 1 - a^2 from la2 = log2(a) <= 0 and a itself: a (1/a - a) = 2 a sinh(w), w = -la2 ln 2, by the series of sinh, or 1 - a a.
+// The series' first omitted term and an ulp of a in 1 - a a meet at the threshold.  What they leave in the root: EXACT
+// (float32 tensors), w = 1/4, three terms: 2^-25 and 2^-22.4; else w = 1/16, two terms: 2^-24 and 2^-20.4.
 template <bool EXACT>
 __device__ __forceinline__ float rec_keep2(float la2, float a) {
-    constexpr double z = 1.3862943611198906;  // ln 4
-    constexpr double z2 = z * z, z4 = z2 * z2;
-    float s;
-    if constexpr (EXACT) {
-        s = __builtin_fmaf(la2, (float)(-z4 * z4 / 40320), (float)(-z4 * z2 * z / 5040));
-        s = __builtin_fmaf(la2, s, (float)(-z4 * z2 / 720));
-        s = __builtin_fmaf(la2, s, (float)(-z4 * z / 120));
-        s = __builtin_fmaf(la2, s, (float)(-z4 / 24));
-    } else {
-        s = (float)(-z4 / 24);
-    }
-    s = __builtin_fmaf(la2, s, (float)(-z2 * z / 6));
-    s = __builtin_fmaf(la2, s, (float)(-z2 / 2));
-    s = __builtin_fmaf(la2, s, (float)-z);
-    float series = la2 * s, direct = __builtin_fmaf(-a, a, 1.0f);
+    constexpr double w = 0.69314718055994531;  // ln 2
+    constexpr double w3 = w * w * w;
+    const float q = la2 * la2;
+    float s = (float)(-w3 / 3);
+    if constexpr (EXACT) s = __builtin_fmaf(q, (float)(-w3 * w * w / 60), s);
+    s = __builtin_fmaf(q, s, (float)(-2 * w));
+    float series = la2 * a * s, direct = __builtin_fmaf(-a, a, 1.0f);
     asm("" : "+v"(series), "+v"(direct));  // (both are made: a choice of lanes, not a branch for each value)
-    return la2 > (float)((EXACT ? -0.5 : -0.0625) / z) ? series : direct;
+    return la2 > (float)((EXACT ? -0.25 : -0.0625) / w) ? series : direct;
 }
 
 }  // namespace sfm
