@@ -6,9 +6,8 @@
  * Plain C: extern "C", only pointers, integers and enums; no C++ exception and
  * no torch type crosses it.  Device pointers point to memory the CALLER owns:
  * the library never allocates, frees or keeps a reference to device memory.
- * The backward and the split-row forward (sfm_selective_scan_bwd,
- * sfm_selective_scan_fwd_ws) take a caller-owned workspace;
- * sfm_selective_scan_fwd_noalloc uses the library's static per-GPU scratch
+ * Entry points with a workspace argument take a caller-owned one, whose size a
+ * query of theirs tells; sfm_selective_scan_fwd_noalloc uses the library's static per-GPU scratch
  * array instead; every other entry point needs no device memory beyond its
  * inputs and outputs.  Every entry point that touches the GPU only
  * enqueues work on `stream` (a hipStream_t; NULL = the null stream) and

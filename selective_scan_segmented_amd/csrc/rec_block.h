@@ -98,6 +98,8 @@ __device__ __forceinline__ uint32_t rec_factor(float a) { return a == a ? __floa
 // Every wait ends: tickets are drawn in the order of the walk, so the blocks waited for run already or are through, the
 // first waits for none, and every workgroup of packed rows says in the end that its word is whole, whatever a caller's
 // offsets make of its place.  The limit is far beyond any wait; past it the state is NaN.
+// Four words at a time: eight or sixteen find the whole one no sooner (the waits are for blocks whose tokens are still on
+// their way), as do longer sleeps and looking at the nearest word alone (68.3 to 68.9 us at 2 x 8192 x 2048 forward).
 template <bool BACK, int WINDOW, int WORDS>
 __device__ __forceinline__ float rec_look_back(const uint64_t* word, int before) {
     const int n = before < WINDOW ? before : WINDOW;
