@@ -86,6 +86,16 @@ __device__ __forceinline__ void load_chunk(RecPack<T, C> (&v)[TT], const void* f
     }
 }
 
+// A wave's priority among those of its unit: waves that ask for tokens go first and those that make gates last, where that
+// was seen to help.  Without / with it: forward in bfloat16, 40 x 600 x 1024: 54.4 / 51.6 us, 32 x 4002 x 1024:
+// 239 / 230 us, packed to 2048: 62.5 / 61.6 us; backward walked, bfloat16, 256 x 198 x 320: 62.3 / 60.0 us, float32, 32 x 4002
+// x 1024: 943 / 931 us.  Not elsewhere: forward in float32, 2 x 8192 x 2048: 120 / 124 us, 64 x 198 x 640: 26.8 / 28.1 us;
+// backward handed on, 16 x 4002 x 320 float32: 146.7 / 147.6 us, 32 x 4002 x 1024 bfloat16: 495 / 498 us; nor in rows of one
+// block, 256 x 51 x 640 forward: 16.8 / 17.0 us.
+template <bool ON, int LEVEL> __device__ __forceinline__ void priority() {
+    if constexpr (ON) __builtin_amdgcn_s_setprio(LEVEL);
+}
+
 // Joins the chunks' (A, H) of [rows][chunks][channels] in LDS: a lane a row and channel.  In their place: the state
 // before every chunk.  BACK: chunks from the last to the first.  kept: the state after the block, for the row's next.
 template <int C, bool HAND, bool BACK>
@@ -144,12 +154,17 @@ __device__ __forceinline__ void empty_block(const RecParams& p, const RecItem& a
     }
 }
 
-// HAND: threads to a workgroup where blocks are handed on, else 0.
-template <typename T, int C, int HAND>
-__global__ __launch_bounds__(HAND ? HAND : kThreads, C == 2 ? (HAND == kFewThreads ? 5 : 4) : 6) void rec_fwd_kernel(const RecParams p) {
+// FORM: rows of one block, of several that a workgroup walks, or handed on: by workgroups of so many threads.
+constexpr int kOne = 0, kWalk = 1;
+constexpr int threads_of(int form) { return form > kWalk ? form : form == kWalk ? kFewThreads : kThreads; }  // (at most)
+
+template <typename T, int C, int FORM>
+__global__ __launch_bounds__(threads_of(FORM), C == 2 ? (threads_of(FORM) == kFewThreads ? 5 : 4) : 6) void rec_fwd_kernel(const RecParams p) {
+    constexpr bool HAND = FORM > kWalk;
     constexpr bool kExact = sizeof(T) == 4;
     constexpr int TT = kRecChunk<false>;
-    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? HAND : kThreads) * C];
+    constexpr bool kUrgent = C == 2 && FORM != kOne;
+    __shared__ float2 agg_[FORM == kWalk ? 2 : 1][threads_of(FORM) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
     if constexpr (HAND) {
@@ -163,7 +178,7 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, C == 2 ? (HAND == kFewThrea
 #pragma unroll
     for (int j = 0; j < C; ++j) rate[j] = l.live ? rec_rate(p.lam[l.ch + j], p.c) : 0.0f;
     for (int turn = 0;; turn ^= 1) {
-        float2* agg = agg_[HAND ? 0 : turn];
+        float2* agg = agg_[FORM == kWalk ? turn : 0];
         const Chunk c(p, at);
         const int n = c.n(l);
         float a[TT][C], b[TT][C];
@@ -173,9 +188,11 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, C == 2 ? (HAND == kFewThrea
             for (int j = 0; j < C; ++j) A[j] = 1.0f, H[j] = 0.0f;
             if (n > 0) {
                 RecPack<T, C> r[TT], i[TT], x[TT];
+                priority<kUrgent, 3>();
                 load_chunk<T, C, TT>(r, p.r, p.ldr, c, l, RecPack<T, C>::kMinusInf);
                 load_chunk<T, C, TT>(i, p.i, p.ldi, c, l, 0);
                 load_chunk<T, C, TT>(x, p.x, p.ldx, c, l, 0);
+                priority<kUrgent, 0>();
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -192,7 +209,8 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, C == 2 ? (HAND == kFewThrea
             for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], H[j]);
         }
         lds_barrier();
-        join_chunks<C, HAND != 0, false>(p, agg, at, kept);
+        priority<kUrgent, 1>();
+        join_chunks<C, HAND, false>(p, agg, at, kept);
         lds_barrier();
         if (n > 0) {
             float h[C];
@@ -213,16 +231,18 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, C == 2 ? (HAND == kFewThrea
             else
                 walk(std::false_type{});
         }
-        if (HAND || ++at.block >= at.blocks) break;
+        if (FORM != kWalk || ++at.block >= at.blocks) break;
     }
 }
 
-template <typename T, int C, int HAND>
-__global__ __launch_bounds__(HAND ? HAND : kThreads, 4) void rec_bwd_kernel(const RecParams p) {
+template <typename T, int C, int FORM>
+__global__ __launch_bounds__(threads_of(FORM), 4) void rec_bwd_kernel(const RecParams p) {
+    constexpr bool HAND = FORM > kWalk;
     constexpr bool kExact = sizeof(T) == 4;
     constexpr int TT = kRecChunk<true>;
-    __shared__ float2 agg_[HAND ? 1 : 2][(HAND ? HAND : kThreads) * C];
-    __shared__ float part[(HAND ? HAND : kThreads) * C];
+    constexpr bool kUrgent = FORM == kWalk;
+    __shared__ float2 agg_[FORM == kWalk ? 2 : 1][threads_of(FORM) * C];
+    __shared__ float part[threads_of(FORM) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
     if constexpr (HAND) {
@@ -237,7 +257,7 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, 4) void rec_bwd_kernel(cons
 #pragma unroll
     for (int j = 0; j < C; ++j) rate[j] = l.live ? rec_rate(p.lam[l.ch + j], p.c) : 0.0f, sum[j] = 0.0f;
     for (int turn = 0;; turn ^= 1) {
-        float2* agg = agg_[HAND ? 0 : turn];
+        float2* agg = agg_[FORM == kWalk ? turn : 0];
         const Chunk c(p, at);
         const int n = c.n(l);
         const bool start = c.first && l.tc == 0;
@@ -249,6 +269,7 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, 4) void rec_bwd_kernel(cons
             for (int j = 0; j < C; ++j) A[j] = 1.0f, U[j] = 0.0f;
             if (n > 0) {
                 RecPack<T, C> r[TT];
+                priority<kUrgent, 3>();
                 load_chunk<T, C, TT>(r, p.r, p.ldr, c, l, RecPack<T, C>::kMinusInf);
                 load_chunk<T, C, TT>(g, p.dy, p.D, c, l, 0);
                 load_chunk<T, C, TT>(i, p.i, p.ldi, c, l, 0);
@@ -266,6 +287,7 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, 4) void rec_bwd_kernel(cons
                         if (t < n && !(t == 0 && start)) y[t].load(w, from, t * token);
                     }
                 }
+                priority<kUrgent, 0>();
 #pragma unroll
                 for (int t = TT - 1; t >= 0; --t)
 #pragma unroll
@@ -280,7 +302,8 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, 4) void rec_bwd_kernel(cons
             for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], U[j]);
         }
         lds_barrier();
-        join_chunks<C, HAND != 0, true>(p, agg, at, kept);
+        priority<kUrgent, 1>();
+        join_chunks<C, HAND, true>(p, agg, at, kept);
         lds_barrier();
         if (n > 0) {
             float u[C], h0[C];
@@ -314,7 +337,7 @@ __global__ __launch_bounds__(HAND ? HAND : kThreads, 4) void rec_bwd_kernel(cons
                 RecPack<T, C>::store(rec_buf<T>(p.di, c.base, p.D), to, t * token, di);
             }
         }
-        if (HAND || --at.block < 0) break;
+        if (FORM != kWalk || --at.block < 0) break;
     }
     if (l.live)
 #pragma unroll
@@ -402,15 +425,16 @@ hipError_t launch_rows(const RecParams& p, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     const dim3 grid((unsigned)q.launch), threads((unsigned)(q.nr * q.nt * q.nc + 63) / 64 * 64);  // (whole waves)
-#define SFM_REC_LAUNCH(C, HAND)                                                                \
-    if (q.lane == C && q.hand == HAND) {                                                       \
-        if constexpr (BACK)                                                                    \
-            hipLaunchKernelGGL((rec_bwd_kernel<T, C, HAND>), grid, threads, 0, s, p);          \
-        else                                                                                   \
-            hipLaunchKernelGGL((rec_fwd_kernel<T, C, HAND>), grid, threads, 0, s, p);          \
+    const int form = q.hand ? q.hand : p.L > q.block ? kWalk : kOne;
+#define SFM_REC_LAUNCH(C, FORM)                                                       \
+    if (q.lane == C && form == FORM) {                                                \
+        if constexpr (BACK)                                                           \
+            hipLaunchKernelGGL((rec_bwd_kernel<T, C, FORM>), grid, threads, 0, s, p); \
+        else                                                                          \
+            hipLaunchKernelGGL((rec_fwd_kernel<T, C, FORM>), grid, threads, 0, s, p); \
     }
-    SFM_REC_LAUNCH(1, 0) SFM_REC_LAUNCH(1, kThreads)
-    if constexpr (sizeof(T) == 2) { SFM_REC_LAUNCH(2, 0) SFM_REC_LAUNCH(2, kThreads) }
+    SFM_REC_LAUNCH(1, kOne) SFM_REC_LAUNCH(1, kWalk) SFM_REC_LAUNCH(1, kThreads)
+    if constexpr (sizeof(T) == 2) { SFM_REC_LAUNCH(2, kOne) SFM_REC_LAUNCH(2, kWalk) SFM_REC_LAUNCH(2, kThreads) }
     if constexpr (sizeof(T) == 2 && !BACK) { SFM_REC_LAUNCH(2, kFewThreads) }
 #undef SFM_REC_LAUNCH
     return hipGetLastError();
