@@ -159,11 +159,15 @@ constexpr int kOne = 0, kWalk = 1;
 constexpr int threads_of(int form) { return form > kWalk ? form : form == kWalk ? kFewThreads : kThreads; }  // (at most)
 
 template <typename T, int C, int FORM>
-__global__ __launch_bounds__(threads_of(FORM), C == 2 ? (threads_of(FORM) == kFewThreads ? 5 : 4) : 6) void rec_fwd_kernel(const RecParams p) {
+__global__ __launch_bounds__(threads_of(FORM), C == 2 ? (FORM == kFewThreads ? 5 : 4) : 6) void rec_fwd_kernel(const RecParams p) {
     constexpr bool HAND = FORM > kWalk;
     constexpr bool kExact = sizeof(T) == 4;
     constexpr int TT = kRecChunk<false>;
     constexpr bool kUrgent = C == 2 && FORM != kOne;
+    // Gates of so many tokens at a time: those behind the row's end are left out, and fewer values are held at once.  All 16 /
+    // 4 / 2: one block, 256 x 51 x 640 bfloat16: 17.0 / 15.5 / 15.5 us, 64 x 198 x 640 float32: 26.7 / 24.5 / 24.5 us; handed on,
+    // 2 x 8192 x 2048: 69.0 / 68.1 / 67.3 us; walked, bfloat16, 256 x 300 x 512: 75.7 / 72.0 / 75.9 us; float32: 141 / 150 / 158 us.
+    constexpr int kGates = HAND ? 2 : FORM == kWalk && C == 1 ? TT : 4;
     __shared__ float2 agg_[FORM == kWalk ? 2 : 1][threads_of(FORM) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
@@ -194,16 +198,20 @@ __global__ __launch_bounds__(threads_of(FORM), C == 2 ? (threads_of(FORM) == kFe
                 load_chunk<T, C, TT>(x, p.x, p.ldx, c, l, 0);
                 priority<kUrgent, 0>();
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
+                for (int t0 = 0; t0 < TT; t0 += kGates) {
+                    if (kGates < TT && t0 >= n) continue;
 #pragma unroll
-                    for (int j = 0; j < C; ++j) {
-                        const float la2 = rate[j] * rec_sigmoid<kExact>(r[t].get(j));
-                        a[t][j] = exp2_fast(la2);
-                        const float m = __builtin_amdgcn_sqrtf(rec_keep2<kExact>(la2, a[t][j]));
-                        b[t][j] = m * rec_sigmoid<kExact>(i[t].get(j)) * x[t].get(j);
-                        H[j] = __builtin_fmaf(a[t][j], H[j], b[t][j]);
-                        A[j] *= a[t][j];
-                    }
+                    for (int t = t0; t < t0 + kGates; ++t)
+#pragma unroll
+                        for (int j = 0; j < C; ++j) {
+                            const float la2 = rate[j] * rec_sigmoid<kExact>(r[t].get(j));
+                            a[t][j] = exp2_fast(la2);
+                            const float m = __builtin_amdgcn_sqrtf(rec_keep2<kExact>(la2, a[t][j]));
+                            b[t][j] = m * rec_sigmoid<kExact>(i[t].get(j)) * x[t].get(j);
+                            H[j] = __builtin_fmaf(a[t][j], H[j], b[t][j]);
+                            A[j] *= a[t][j];
+                        }
+                }
             }
 #pragma unroll
             for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], H[j]);
@@ -489,6 +497,16 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
         q.hand = several ? threads : 0;
     }
     q.groups = 1;
+    // Many packed rows of one block, most far shorter than the longest: lanes for the average's chunks (forward), or for no
+    // more than a small workgroup's (backward), walk the longer ones.  One block / this: forward, bfloat16, 4096 rows to 100 x
+    // 1024: 404 / 346 us, 512 to 250 x 2048: 259 / 237 us; float32, 2048 to 200 x 320: 194 / 198 us (left out); backward,
+    // bfloat16, 4096 to 100 x 1024: 955 / 890 us, float32, 2048 to 100 x 320: 266 / 246 us; rows of 90 to 100 x 320: 406 / 448 us.
+    if (packed && !several && rows * chains >= 4096 && 3 * tokens <= 2 * rows * L && (back || lane == 2)) {
+        int64_t nt = back ? chunks : (tokens / rows + chunk - 1) / chunk;
+        if (nt < lane) nt = lane;  // (a lane of the join to a channel)
+        if (nt > kFewThreads / least) nt = kFewThreads / least;
+        if (nt < chunks) q.nt = (int)nt;
+    }
     q.block = q.nt * chunk;
     // one block: as wide as the workgroup allows in whole 128 bytes, down to half that where it leaves fewer lanes idle
     const int budget = q.nt * least > kFewThreads ? kThreads : kFewThreads;
