@@ -249,6 +249,7 @@ __global__ __launch_bounds__(threads_of(FORM), 4) void rec_bwd_kernel(const RecP
     constexpr bool kExact = sizeof(T) == 4;
     constexpr int TT = kRecChunk<true>;
     constexpr bool kUrgent = FORM == kWalk;
+    constexpr int kGates = FORM == kOne ? 4 : TT;  // (8 / 4: 8192 x 2 x 320 bfloat16: 47 / 44 us, 256 x 51 x 640: 33.8 / 33.6 us)
     __shared__ float2 agg_[FORM == kWalk ? 2 : 1][threads_of(FORM) * C];
     __shared__ float part[threads_of(FORM) * C];
     __shared__ uint32_t shared[2];
@@ -297,14 +298,18 @@ __global__ __launch_bounds__(threads_of(FORM), 4) void rec_bwd_kernel(const RecP
                 }
                 priority<kUrgent, 0>();
 #pragma unroll
-                for (int t = TT - 1; t >= 0; --t)
+                for (int t0 = TT - kGates; t0 >= 0; t0 -= kGates) {
+                    if (kGates < TT && t0 >= n) continue;
 #pragma unroll
-                    for (int j = 0; j < C; ++j) {
-                        sr[t][j] = rec_sigmoid<kExact>(r[t].get(j));
-                        const float a = exp2_fast(rate[j] * sr[t][j]);
-                        U[j] = a * (U[j] + g[t].get(j));
-                        A[j] *= a;
-                    }
+                    for (int t = t0 + kGates - 1; t >= t0; --t)
+#pragma unroll
+                        for (int j = 0; j < C; ++j) {
+                            sr[t][j] = rec_sigmoid<kExact>(r[t].get(j));
+                            const float a = exp2_fast(rate[j] * sr[t][j]);
+                            U[j] = a * (U[j] + g[t].get(j));
+                            A[j] *= a;
+                        }
+                }
             }
 #pragma unroll
             for (int j = 0; j < C; ++j) agg[l.slot + j] = make_float2(A[j], U[j]);

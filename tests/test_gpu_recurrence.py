@@ -312,19 +312,21 @@ def test_numbers_of_long_rows(rows, L, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-def test_many_packed_rows(io):
-    """Packed rows of several blocks that a workgroup walks each, some of them empty."""
+@pytest.mark.parametrize("D,low,high,most", [(33, 100, 300, 300), (34, 1, 60, 125), (66, 1, 20, 70)])
+def test_many_packed_rows(D, low, high, most, io):
+    """Packed rows that a workgroup walks each, some of them empty, some far longer than the others."""
     import torch
     import selective_scan_segmented_amd as sfm
     rng = np.random.default_rng(4)
-    D, n = 33, 4200
-    lens = rng.integers(100, 300, n)
+    n = 4200
+    lens = rng.integers(low, high, n)
     lens[[0, 7, 8, n - 1]] = 0
+    lens[[1, 1000, 3000]] = most
     ends = np.cumsum(lens)
     x, r, i, lam, s0, dy, dhT = ref.recurrence_inputs(4, int(ends[-1]), n, D, io)
     t = [dev(v, io).view(1, -1, D) for v in (x, r, i)] + [dev(lam, "f32")]
     off = torch.tensor(np.concatenate([[0], ends]), dtype=torch.int32).cuda()
-    rows = dict(h0=dev(s0, "f32"), offsets=off, max_len=300)
+    rows = dict(h0=dev(s0, "f32"), offsets=off, max_len=most)
     y, state = sfm.sfm_gated_recurrence_fwd(*t, return_state=True, **rows)
     g = sfm.sfm_gated_recurrence_bwd(*t, y, dev(dy, io).view(y.shape), dstate=dev(dhT, "f32"), **rows)
     yh = from_dev(y)[0]
