@@ -127,9 +127,10 @@ def test_workspace_sizes(lib):
         assert f(2, 100, 200, 0, 1, ctypes.byref(out)) == SHAPE
         assert f(2, 100, 200, 64, 2, ctypes.byref(out)) == DTYPE
         assert f(2, 100, 200, 64, 1, ctypes.byref(out)) == OK and out.value >= 0
-        # workgroups of 512 lanes: a launch holds 2^32 lanes
-        assert f((1 << 23) - 8, 256 if f is lib.sfm_gated_recurrence_fwd_ws_size else 128, 0, 32, 0, ctypes.byref(out)) == OK
-        assert f((1 << 23) + 8, 256 if f is lib.sfm_gated_recurrence_fwd_ws_size else 128, 0, 32, 0, ctypes.byref(out)) == SHAPE
+        # workgroups of 512 lanes (rows nearly as long as the longest): a launch holds 2^32 lanes
+        L, tokens = (256, (1 << 31) - 1) if f is lib.sfm_gated_recurrence_fwd_ws_size else (128, 1 << 30)
+        assert f((1 << 23) - 8, L, tokens, 32, 0, ctypes.byref(out)) == OK
+        assert f((1 << 23) + 8, L, tokens, 32, 0, ctypes.byref(out)) == SHAPE
     f = lib.sfm_qk_norm_rope_bwd_ws_size
     assert f(100, 4, 2, 64, 1, 1, None) == NULL
     assert f(100, 4, 2, 257, 1, 1, ctypes.byref(out)) == SHAPE
