@@ -15,10 +15,10 @@
 // u_t = a_{t+1} G_{t+1}: a u + a dy; it makes the gates again for its second look at the tokens, from what it holds in
 // registers as it lies in memory.
 //
-// Measured (a call; rate of the bytes that have to move, of 5.1 TB/s that a large copy reaches):
-//     forward, bfloat16: 256 x 51 x 640: 16.8 us, 4.0 TB/s (a copy as large 17); 2 x 8192 x 2048: 69 us, 3.9 TB/s, of
-//     which 5 are the words' clearing and 8 the waits for states before; 24 rows packed to 2048 x 1024: 62 us, 3.4 TB/s;
-//     backward: bfloat16, 256 x 198 x 320: 62 us, 4.2 TB/s; float32, 16 x 4002 x 320: 146 us, 4.5 TB/s;
+// Measured (calls back to back; rate of the bytes that have to move, of 5.1 TB/s that a large copy reaches):
+//     forward, bfloat16: 256 x 51 x 640: 15.7 us, 4.3 TB/s (a copy as large 17); 2 x 8192 x 2048: 67.5 us, 4.0 TB/s, of
+//     which 5 are the words' clearing and 8 the waits for states before; 24 rows packed to 2048 x 1024: 61 us, 3.5 TB/s;
+//     backward: bfloat16, 256 x 198 x 320: 60 us, 4.3 TB/s; float32, 16 x 4002 x 320: 147 us, 4.5 TB/s;
 //     step: 256 requests x 2048: 3.7 us on the card.
 #include "rec_block.h"
 
