@@ -457,15 +457,19 @@ hipError_t launch_rows(const RecParams& p, hipStream_t s) {
 
 // Whether rows of several blocks are handed on or walked by a workgroup each.  Handing on costs a launch that clears the
 // words (5 us) and a wait a block; walking leaves the card to the rows and tiles there are, and packed rows to the
-// longest of them.  bfloat16, 2048 channels in 32 tiles, walked / handed on:
-//     forward, 16 rows of 600: 34 / 37 us, 8 rows: 27 / 23 us, 16 rows of 2400: 145 / 148 us, 8 rows: 94 / 73 us;
+// longest of them.  32 tiles, walked / handed on:
+//     forward, bfloat16, 16 rows of 600: 38 / 44 us, 12 rows: 32 / 32 us, 8 rows of 2400: 98 / 77 us, 16 rows: 139 / 149 us;
 //     three blocks (300 tokens), 2 rows: 14 / 15 us, 8 rows: 15.5 / 16 us, 4 rows: 15 / 13 us;
-//     backward, 32 rows of 600: 153 / 164 us, 16 rows: 90 / 84 us;
-//     packed to 600 in 16 tiles, 256 rows: 156 / 166 us (back 317 / 343), 128 rows: 89 / 94 us (194 / 191);
+//     float32, 16 rows of 600: 41 / 43 us, of 2400: 152 / 144 us, of 8000: 496 / 454 us, 24 rows of 2400: 215 / 211 us;
+//     backward, bfloat16, 16 rows of 600: 89 / 87 us, of 2400: 316 / 296 us, 24 rows of 600: 114 / 127 us, of 2400: 409 / 437
+//     us; float32, 16 rows of 600: 85 / 83 us, 24 rows: 112 / 121 us; five blocks (300 tokens), 16 rows: 49 / 53 us, 6 rows:
+//     31 / 24 us;
+//     packed to 600 in 16 tiles, bfloat16, 256 rows: 156 / 166 us (back 317 / 343), 128 rows: 89 / 94 us (194 / 191);
 //     packed to 2000, 64 rows: 165 / 136 us (back 333 / 285).
-static bool hands_on(int64_t rows, int64_t L, int64_t tokens, int tiles, int blocks, bool packed, bool back) {
+static bool hands_on(int64_t rows, int64_t L, int64_t tokens, int tiles, int blocks, bool packed, bool narrow, bool back) {
     if (packed) return rows * tiles < 4096 || L * rows > 4 * tokens;  // (one far longer than the others, or no bound)
-    return rows * tiles < (back ? 1024 : 512) && (back || blocks > 3);
+    if (back) return rows * tiles < 640;
+    return rows * tiles < (narrow && blocks > 8 ? 800 : 512) && blocks > 3;
 }
 
 RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed, bool near, int lane, bool back) {
@@ -490,7 +494,7 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
         return several;
     };
     bool several = cut(kFewThreads);
-    if (several && hands_on(rows, L, tokens, chains, q.blocks, packed, back)) {
+    if (several && hands_on(rows, L, tokens, chains, q.blocks, packed, lane == 1, back)) {
         // Workgroups that hand on: wide ones make fewer blocks to wait for, small ones more waits at once.  256 / 512 threads:
         //     backward, float32: 1 x 70000 x 320: 267 / 176 us, 16 x 4002 x 320: 148 / 146 us, 2 x 8192 x 2048: 247 / 249 us;
         //     backward, bfloat16: 1 x 20000 x 1024: 108 / 96 us, 2 x 8192 x 2048: 140 / 138 us, 24 packed to 2048 x 1024: 125 / 121 us;
