@@ -464,10 +464,16 @@ hipError_t launch_rows(const RecParams& p, hipStream_t s) {
 //     backward, bfloat16, 16 rows of 600: 89 / 87 us, of 2400: 316 / 296 us, 24 rows of 600: 114 / 127 us, of 2400: 409 / 437
 //     us; float32, 16 rows of 600: 85 / 83 us, 24 rows: 112 / 121 us; five blocks (300 tokens), 16 rows: 49 / 53 us, 6 rows:
 //     31 / 24 us;
-//     packed to 600 in 16 tiles, bfloat16, 256 rows: 156 / 166 us (back 317 / 343), 128 rows: 89 / 94 us (194 / 191);
-//     packed to 2000, 64 rows: 165 / 136 us (back 333 / 285).
+//     packed in 16 tiles, bfloat16 (back): to 300, 128 rows: 44 / 47 us (99 / 111); to 600, 64 rows: 44 / 42 us (100 / 95), 128
+//     rows: 92 / 95 us (189 / 193); to 2000, 128 rows: 291 / 284 us (595 / 581), 256 rows: 539 / 549 us (1091 / 1126); of 500
+//     to 600, 64 rows: 61 / 72 us (141 / 158); float32, to 600, 128 rows: 86 / 89 us (183 / 181), 256 rows: 160 / 157 us (323 /
+//     321); to 2000, 256 rows: 533 / 496 us (1095 / 1051).
 static bool hands_on(int64_t rows, int64_t L, int64_t tokens, int tiles, int blocks, bool packed, bool narrow, bool back) {
-    if (packed) return rows * tiles < 4096 || L * rows > 4 * tokens;  // (one far longer than the others, or no bound)
+    if (packed) {
+        if (L * rows > 4 * tokens) return true;  // (one far longer than the others, or no bound)
+        const bool even = 3 * tokens > 2 * rows * L;
+        return rows * tiles < (narrow ? 6144 : even ? 1024 : L <= 1024 ? 2048 : 4096);
+    }
     if (back) return rows * tiles < 640;
     return rows * tiles < (narrow && blocks > 8 ? 800 : 512) && blocks > 3;
 }
