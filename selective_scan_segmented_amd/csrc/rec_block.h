@@ -83,8 +83,12 @@ __device__ __forceinline__ int rec_row_of(const RecParams& p, uint32_t entry, in
 
 // A block takes a state h to A h + H.  Its word says so: A's bits (0 <= A <= 1, or NaN) and H's; kRecWhole in A's
 // place: H is the state after the block; all ones: nothing yet.  A word is written and read in one piece, so that no
-// other order of memory matters.  A tile's words lie entry by entry, kRecWords to an entry (of the channels side by side in a workgroup, at most 32 lanes').
+// other order of memory matters.  The words of 32 lanes' channels lie entry by entry, kRecWords to an entry.
 template <int C> constexpr int kRecWords = 32 * C;
+template <int C> __device__ __forceinline__ uint64_t* rec_words(const RecParams& p, int tile, uint32_t entry, int w) {
+    const int64_t run = tile * p.plan.subs + w / kRecWords<C>;
+    return p.w_words + (run * p.plan.entries + entry) * kRecWords<C> + w % kRecWords<C>;
+}
 constexpr uint32_t kRecEmpty = 0xffffffffu, kRecWhole = 0xbf800000u;  // (the latter -1: no A has its sign)
 
 __device__ __forceinline__ void rec_publish(uint64_t* at, uint32_t tag, float h) {

@@ -115,7 +115,7 @@ __device__ __forceinline__ void join_chunks(const RecParams& p, float2* agg, con
         if constexpr (HAND) {
             const bool tells = !ends || p.offsets;  // (packed rows: always, rec_look_back)
             if (!starts || tells) {
-                uint64_t* word = p.w_words + ((int64_t)at.tile * q.entries + at.entry) * kRecWords<C> + w;
+                uint64_t* word = rec_words<C>(p, at.tile, at.entry, w);
                 float A = 1.0f, H = 0.0f;
 #pragma unroll 8
                 for (int k = 0; k < q.nt; ++k) {
@@ -148,7 +148,7 @@ __device__ __forceinline__ void empty_block(const RecParams& p, const RecItem& a
     if (!p.offsets) return;
     const int width = p.plan.nc * C;
     for (int m = threadIdx.x; m < width; m += blockDim.x) {
-        rec_publish(p.w_words + ((int64_t)at.tile * p.plan.entries + at.entry) * kRecWords<C> + m, kRecWhole, 0.0f);
+        rec_publish(rec_words<C>(p, at.tile, at.entry, m), kRecWhole, 0.0f);
         const int ch = at.tile * width + m;
         if (BACK && ch < p.D) p.w_lam[(int64_t)at.entry * p.D + ch] = 0.0f;
     }
@@ -512,6 +512,16 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
         q.hand = several ? threads : 0;
     }
     q.groups = 1;
+    // No bound of the rows, or one that few come near, and rows of few tokens on average: handed on as long ones, but by
+    // workgroups of 32 or 64 tokens and so many more channels.  Without / with it, no bound: forward (back), bfloat16, 4096 rows
+    // to 16 x 2048: 763 / 275 us (1762 / 588), to 100 x 1024: 591 / 466 us (1328 / 1002; with 32 tokens 436 and 903); one row of
+    // 50000 among 2048 to 16 x 320, float32: 222 / 218 us (378 / 319; with 32 tokens 339 and 410).
+    const bool loose = q.hand && packed && lanes > least && L * rows > 4 * tokens && tokens < 100 * rows;
+    if (loose) {
+        int64_t nt = (tokens < 24 * rows ? 32 : 64) / chunk;
+        if (nt < q.hand / lanes) nt = q.hand / lanes;
+        if (nt < q.nt) q.nt = (int)nt;
+    }
     // Many packed rows of one block, most far shorter than the longest: lanes for the average's chunks (forward), or for no
     // more than a small workgroup's (backward), walk the longer ones.  One block / this: forward, bfloat16, 4096 rows to 100 x
     // 1024: 404 / 346 us, 512 to 250 x 2048: 259 / 237 us; float32, 2048 to 200 x 320: 194 / 198 us (left out); backward,
@@ -525,7 +535,7 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     q.block = q.nt * chunk;
     // one block: as wide as the workgroup allows in whole 128 bytes, down to half that where it leaves fewer lanes idle
     const int budget = q.nt * least > kFewThreads ? kThreads : kFewThreads;
-    int nc = several ? least : budget / q.nt;
+    int nc = loose ? q.hand / q.nt : several ? least : budget / q.nt;
     if (nc >= lanes) {
         nc = lanes;
     } else if (nc >= 32) {
@@ -536,6 +546,7 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     }
     q.nc = nc;
     q.tiles = (lanes + nc - 1) / nc;
+    q.subs = (nc + 31) / 32;
     q.nr = several || packed || q.tiles > 1 || !near ? 1 : budget / (q.nt * nc);
     if (q.nr > rows) q.nr = (int)rows;
     if (!q.hand) {
@@ -549,7 +560,7 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
         q.entries = rows * q.blocks;
         q.launch = (rows + q.groups - 1) / q.groups * q.groups * q.blocks * q.tiles;
     }
-    q.bytes_words = q.hand ? (int64_t)q.tiles * q.groups * 64 + q.entries * q.tiles * 32 * lane * 8 : 0;
+    q.bytes_words = q.hand ? (int64_t)q.tiles * q.groups * 64 + q.entries * q.tiles * q.subs * 32 * lane * 8 : 0;
     q.bytes_words = (q.bytes_words + 15) / 16 * 16;
     q.bytes = q.bytes_words + (back ? q.entries * D * 4 : 0);
     q.by_tiles = ((1ULL << 40) + q.tiles - 1) / q.tiles;

@@ -16,6 +16,7 @@ struct RecPlan {
     int hand;                     // threads to a workgroup that hands on, else 0
     int blocks;                   // equal rows: blocks to a row
     int groups;                   // hand: ticket counters to a tile, a power of two
+    int subs;                     // hand: runs of 32 lanes to a tile
     int64_t entries;              // hand: blocks of all rows; else: workgroups along the rows
     int64_t launch;               // workgroups
     int64_t bytes_words, bytes;   // workspace: tickets and words; with the backward's parts of dlam
@@ -45,7 +46,7 @@ struct RecParams {
     float* dh0;              // [rows][D] or null
     // workspace
     uint32_t* w_tickets;     // [tiles][groups], 64 bytes apart
-    uint64_t* w_words;       // [tiles][entries][32 lanes' channels]: what a block makes of a state (rec_block.h)
+    uint64_t* w_words;       // [tiles x subs][entries][32 lanes' channels]: what a block makes of a state (rec_block.h)
     float* w_lam;            // [entries][D]: parts of dlam
     RecPlan plan;
 };

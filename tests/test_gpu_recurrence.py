@@ -34,7 +34,7 @@ def side_by_side(parts, io):
     return torch.split(p, [a.shape[-1] for a in parts], -1)
 
 
-def call(seed, lens, D, io, slices=False, h0=True):
+def call(seed, lens, D, io, slices=False, h0=True, bound=True):
     """Inputs of a call: the float64 ones, the GPU's, and the row arguments."""
     import torch
     packed = lens in PACKED or len(set(lens)) > 1
@@ -46,7 +46,7 @@ def call(seed, lens, D, io, slices=False, h0=True):
     gates = [t.unflatten(0, lead) if t.numel() else t.view(*lead, D) for t in gates]
     rows = dict(h0=dev(s0, "f32") if h0 else None)
     if packed:
-        rows.update(offsets=torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda(), max_len=max(lens))
+        rows.update(offsets=torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda(), max_len=max(lens) if bound else None)
     return (x, r, i, lam, s0, dy, dhT), gates + [dev(lam, "f32")], rows, np.cumsum(lens), lead
 
 
@@ -379,3 +379,11 @@ def test_replays_of_packed_rows_read_their_offsets():
         assert torch.equal(y, wy) and torch.equal(state, ws)
         for n in wg:
             assert torch.equal(g[n], wg[n]), n
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [8, 72, 200, 640])
+@pytest.mark.parametrize("lens", [[3, 1, 0, 7, 2, 5, 0, 4] * 6, [3, 1, 0, 7, 2, 5, 0, 4, 700] * 4, [40, 90, 1, 60, 0, 77] * 5], ids=["short", "outliers", "middling"])
+def test_packed_rows_without_a_bound(lens, D, io):
+    check_forward(len(lens), lens, D, io, bound=False)
+    check_backward(len(lens), lens, D, io, bound=False)
