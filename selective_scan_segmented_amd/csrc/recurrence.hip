@@ -168,6 +168,10 @@ __global__ __launch_bounds__(threads_of(FORM), C == 2 ? (FORM == kFewThreads ? 5
     // 4 / 2: one block, 256 x 51 x 640 bfloat16: 17.0 / 15.5 / 15.5 us, 64 x 198 x 640 float32: 26.7 / 24.5 / 24.5 us; handed on,
     // 2 x 8192 x 2048: 69.0 / 68.1 / 67.3 us; walked, bfloat16, 256 x 300 x 512: 75.7 / 72.0 / 75.9 us; float32: 141 / 150 / 158 us.
     constexpr int kGates = HAND ? 2 : FORM == kWalk && C == 1 ? TT : 4;
+    // Outputs that stay in the cache for their reader / do not: 256 x 51 x 640 bfloat16: 15.7 / 14.1 us, between a writer of x
+    // and a reader of y 28.0 / 28.3 us; handed on, 2 x 8192 x 2048: 66.4 / 64.7 us, so placed 109 / 112 us; float32, 256 x 200 x
+    // 1024: 159 / 165 us.
+    constexpr int kPolicy = FORM == kOne && C == 2 ? kStreamed : 0;
     __shared__ float2 agg_[FORM == kWalk ? 2 : 1][threads_of(FORM) * C];
     __shared__ uint32_t shared[2];
     RecItem at;
@@ -231,7 +235,7 @@ __global__ __launch_bounds__(threads_of(FORM), C == 2 ? (FORM == kFewThreads ? 5
                 for (int t = 0; t < TT; ++t) {
 #pragma unroll
                     for (int j = 0; j < C; ++j) h[j] = __builtin_fmaf(a[t][j], h[j], b[t][j]);
-                    if (decltype(whole)::value || t < n) RecPack<T, C>::store(y, to, t * token, h);
+                    if (decltype(whole)::value || t < n) RecPack<T, C>::template store<kPolicy>(y, to, t * token, h);
                 }
             };
             if (n >= TT)
