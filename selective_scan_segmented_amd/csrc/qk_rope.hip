@@ -50,6 +50,7 @@ template <typename T, int V> struct RopeRun {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
         return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
     }
+    template <int POLICY>
     static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at, const float (&f)[V]) {
         uint32_t w[kWords];
 #pragma unroll
@@ -62,13 +63,13 @@ template <typename T, int V> struct RopeRun {
             }
         }
         if constexpr (kBytes == 16)
-            __builtin_amdgcn_raw_buffer_store_b128(w4{w[0], w[1], w[2], w[3]}, b, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(w4{w[0], w[1], w[2], w[3]}, b, at, 0, POLICY);
         else if constexpr (kBytes == 8)
-            __builtin_amdgcn_raw_buffer_store_b64(w2{w[0], w[1]}, b, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(w2{w[0], w[1]}, b, at, 0, POLICY);
         else if constexpr (kBytes == 4)
-            __builtin_amdgcn_raw_buffer_store_b32(w[0], b, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(w[0], b, at, 0, POLICY);
         else
-            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)w[0], b, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)w[0], b, at, 0, POLICY);
     }
 };
 
@@ -293,12 +294,19 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
                             for (int v = 0; v < V; ++v) a[s][v] = e[s][v], b[s][v] = f[s][v];
                     }
                 }
-                if (live)
+                auto put = [&](auto policy) __attribute__((always_inline)) {
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
-                        if (one[s] < p.d) RopeRun<T, V>::store(yb, to[u] + one[s] * sizeof(T), a[s]);
-                        if (two[s] < p.d) RopeRun<T, V>::store(yb, to[u] + two[s] * sizeof(T), b[s]);
+                        if (one[s] < p.d) RopeRun<T, V>::template store<decltype(policy)::value>(yb, to[u] + one[s] * sizeof(T), a[s]);
+                        if (two[s] < p.d) RopeRun<T, V>::template store<decltype(policy)::value>(yb, to[u] + two[s] * sizeof(T), b[s]);
                     }
+                };
+                if (live) {
+                    if (!BACK && !NEIGH && V > 1 && p.lines)
+                        put(std::integral_constant<int, 2>{});  // (nontemporal)
+                    else
+                        put(std::integral_constant<int, 0>{});
+                }
             }
         }
         lds_barrier();  // (the next run's table)
@@ -398,6 +406,10 @@ void plan_rope(RopeParams& p, int io_bytes, int align, bool back) {
     while (p.lanes < p.slots && p.lanes < 64) p.lanes *= 2;
     const int per = in_flight(V, p.slots > 64 ? 2 : 1, back) * (back ? 8 : 1);
     p.threads = kThreads;
+    // Outputs whose halves are whole lines of 128 bytes are written past the cache (without / with it: 2 x 8192 tokens x 24 heads
+    // of 128 among other work: 44 / 38 us, between a writer of q and k and a reader of both outputs 113 / 112 us).  Not others:
+    // 256 x 198 x 10 heads of 64, so placed: 75 / 80 us; nor the backward, 8 x 8192 x 24 heads of 128: 526 / 538 us.
+    p.lines = !back && !p.neighbours && p.rot == p.d && p.d / 2 * io_bytes % 128 == 0;
     for (RopeSide& q : p.side) {
         // tokens whose heads give every lane that many, as far as the table holds them and enough workgroups are left
         int64_t run = (int64_t)(kThreads / p.lanes) * per / q.heads;

@@ -35,6 +35,7 @@ struct RopeParams {
     int vec;                   // neighbouring values to a load
     int slots, lanes;          // of two vec to a head; lanes: to a head, a power of two
     int threads;
+    int lines;                 // outputs written past the cache
     float* part;               // workspace (backward with weights): [2][kRopeParts][d]
 };
 
