@@ -11,8 +11,8 @@
 // half a rotation on, or 2 x 16 bytes side by side), so that the rotation stays in a lane and the mean square is one sum
 // over a few.  A workgroup takes a run of tokens with all heads of queries or of keys: it makes the tokens' sines and
 // cosines once, into LDS, while its first heads are on their way.
-// Measured, bfloat16: forward, 256 x 198 tokens x 10 heads of 64: 28 us, 4.6 TB/s; 2 x 8192 x 24 heads of 128: 40 us, 5.1
-// TB/s; backward, 2 x 4002 x 12 heads of 128: 23 us, 3.2 TB/s, of which 4 are the weights' join (a copy of its 74 MB: 19).
+// Measured, bfloat16: forward, 256 x 198 tokens x 10 heads of 64: 28 us, 4.6 TB/s; 2 x 8192 x 24 heads of 128: 38 us, 5.2
+// TB/s; backward, 2 x 4002 x 12 heads of 128: 21 us, 3.5 TB/s, of which 4 are the weights' join (a copy of its 74 MB: 19).
 #include "sfm_device.h"
 #include "sfm_rope.h"
 

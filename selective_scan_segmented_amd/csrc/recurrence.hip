@@ -16,9 +16,10 @@
 // registers as it lies in memory.
 //
 // Measured (calls back to back; rate of the bytes that have to move, of 5.1 TB/s that a large copy reaches):
-//     forward, bfloat16: 256 x 51 x 640: 15.7 us, 4.3 TB/s (a copy as large 17); 2 x 8192 x 2048: 67.5 us, 4.0 TB/s, of
-//     which 5 are the words' clearing and 8 the waits for states before; 24 rows packed to 2048 x 1024: 61 us, 3.5 TB/s;
-//     backward: bfloat16, 256 x 198 x 320: 60 us, 4.3 TB/s; float32, 16 x 4002 x 320: 147 us, 4.5 TB/s;
+//     forward, bfloat16: 256 x 51 x 640: 15 us, 4.4 TB/s (a copy as large 17); 2 x 8192 x 2048: 67 us, 4.0 TB/s, of
+//     which 5 are the words' clearing and 8 the waits for states before; 24 rows packed to 2048 x 1024: 60 us, 3.5 TB/s;
+//     backward: bfloat16, 256 x 198 x 320: 60 us, 4.3 TB/s; float32, 16 x 4002 x 320: 127 us, 5.2 TB/s (143 us, 4.6 TB/s
+//     where nothing of its outputs is left on the card);
 //     step: 256 requests x 2048: 3.7 us on the card.
 #include "rec_block.h"
 
@@ -27,7 +28,7 @@ namespace sfm {
 namespace {
 
 constexpr int kThreads = 512;     // most to a workgroup
-constexpr int kFewThreads = 256;  // and to one that walks rows of several blocks (plan_rec)
+constexpr int kFewThreads = 256;  // and to one that walks rows (plan_rec)
 
 // A lane's place in its workgroup: row, chunk (of TT tokens) and channels.
 template <int TT> struct Lane {
