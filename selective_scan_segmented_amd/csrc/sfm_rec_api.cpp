@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cstring>
 #include <initializer_list>
 
 #include "sfm_api_util.h"
@@ -107,12 +108,16 @@ struct Ranges {
     }
 };
 
-// No output on an input (but `same`, which may be the input of exactly that place) or on another output.
-sfm_status check_ranges(const char* fn, const Ranges& in, const Ranges& out, const void* same = nullptr) {
+// No output on an input or on another output, but hT on the whole of h0: that input by its name, since other inputs can
+// have the same place and size (lam, with one row).
+sfm_status check_ranges(const char* fn, const Ranges& in, const Ranges& out) {
+    const auto in_place = [](const Range& o, const Range& i) {
+        return !strcmp(o.name, "hT") && !strcmp(i.name, "h0") && o.lo == i.lo && o.hi == i.hi;
+    };
     for (int j = 0; j < out.n; ++j) {
         const Range& o = out.of[j];
         for (int k = 0; k < in.n; ++k)
-            if (overlap(o, in.of[k]) && !(same && o.lo == reinterpret_cast<uintptr_t>(same) && in.of[k].lo == o.lo && in.of[k].hi == o.hi))
+            if (overlap(o, in.of[k]) && !in_place(o, in.of[k]))
                 return fail(SFM_ERR_ALIAS, "%s: %s overlaps %s", fn, o.name, in.of[k].name);
         for (int k = 0; k < j; ++k)
             if (overlap(o, out.of[k])) return fail(SFM_ERR_ALIAS, "%s: %s overlaps %s", fn, o.name, out.of[k].name);
@@ -190,7 +195,7 @@ sfm_status sfm_gated_recurrence_fwd(const void* x, const void* r, const void* i,
     out.add("y", y, tokens * D * e);
     out.add("hT", hT, rows * D * 4);
     out.add("workspace", workspace, need);
-    st = check_ranges(fn, in, out, hT);
+    st = check_ranges(fn, in, out);
     if (st != SFM_OK) return st;
     sfm::RecParams p = params(x, r, i, lam, rows, L, tokens, D, ldx, ldr, ldi, c);
     p.h0 = h0, p.y = y, p.hT = hT, p.offsets = offsets;
