@@ -138,12 +138,14 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
     const int lane = tid & (p.lanes - 1), group = tid / p.lanes, groups = (int)blockDim.x / p.lanes;
     const int half = p.rot >> 1, width = p.slots * V;
     int one[S], two[S];
+    bool pairs[S];  // the slot's values are rotated; others stay as they are, whatever stands beside them
     float w1[S][V], w2[S][V], s1[S][V], s2[S][V];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const int slot = lane + 64 * s;
         one[s] = slot * V, two[s] = half + slot * V;
-        if (NEIGH || slot * V >= half) one[s] = 2 * slot * V, two[s] = one[s] + V;
+        pairs[s] = slot * V < half;
+        if (NEIGH || !pairs[s]) one[s] = 2 * slot * V, two[s] = one[s] + V;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             w1[s][v] = q.w && one[s] < p.d ? q.w[one[s] + v] : 1.0f;
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
                         }
                     }
             }
-            if (r0 == 0) {  // the run's sines and cosines; values behind the rotation keep their place
+            if (r0 == 0) {  // the run's sines and cosines (places of values behind the rotation are left empty)
 #pragma unroll
                 for (int e = 0; e < kPositions / kThreads; ++e) positions[tid + e * kThreads] = at[e];
                 lds_barrier();
@@ -207,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
                     const int t = div_small(k, inv_width), j = k - t * width;
                     int axis = 0;
                     for (int a = 0; a + 1 < p.axes; ++a) axis += j >= p.ends[a];
-                    table[k] = j < half ? rope_angle<sizeof(T) == 4>(positions[t * p.axes + axis], freqs[j]) : make_float2(1.0f, 0.0f);
+                    if (j < half) table[k] = rope_angle<sizeof(T) == 4>(positions[t * p.axes + axis], freqs[j]);
                 }
                 lds_barrier();
             }
@@ -252,10 +254,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
                 if constexpr (!BACK) {
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
-                        if (one[s] >= p.d) continue;
 #pragma unroll
                         for (int v = 0; v < V; ++v) a[s][v] *= w1[s][v], b[s][v] *= w2[s][v];
-                        turn<V, NEIGH>(a[s], b[s], cs + (lane + 64 * s) * V, 1.0f);
+                        if (pairs[s]) turn<V, NEIGH>(a[s], b[s], cs + (lane + 64 * s) * V, 1.0f);
                     }
                 } else {
                     float e[S][V], f[S][V], dot = 0.0f;
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p) {
                             e[s][v] = live && one[s] < p.d ? g1[u][s].get(v) : 0.0f;
                             f[s][v] = live && two[s] < p.d ? g2[u][s].get(v) : 0.0f;
                         }
-                        if (one[s] < p.d) turn<V, NEIGH>(e[s], f[s], cs + (lane + 64 * s) * V, -1.0f);
+                        if (pairs[s]) turn<V, NEIGH>(e[s], f[s], cs + (lane + 64 * s) * V, -1.0f);
 #pragma unroll
                         for (int v = 0; v < V; ++v) {
                             s1[s][v] = __builtin_fmaf(e[s][v], a[s][v], s1[s][v]);
