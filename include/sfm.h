@@ -476,10 +476,10 @@ sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G
  *   offsets  as for sfm_gated_delta_fwd: NULL for equal rows (tokens == rows * L), or
  *            int32 [rows + 1] on the device; L bounds the longest row, offsets outside
  *            the tokens are cut to them, tokens of no row and those past L keep their old y
- *   D 1..65536.  Tensors need their element's alignment only; bfloat16 ones of even D and
+ *   rows 1..2^24, L 1..2^31 - 1, tokens to 2^31 - 1, D 1..65536.  Tensors need their element's alignment only; bfloat16 ones of even D and
  *   strides on 4 bytes are loaded two channels at a time, others one by one.
- *   Rows and channels that make more workgroups than a launch holds (2^24, rows of 128 channels
- *   one each) are SFM_ERR_SHAPE.
+ *   Rows, tokens and channels that make more workgroups than a launch holds (2^24, or 2^32 lanes;
+ *   short rows of 128 channels are one each, long ones one for 128 tokens or more) are SFM_ERR_SHAPE.
  * A non-finite value of a token stays in its row and channel.  Repeated calls give the same bits.
  * workspace: at least sfm_gated_recurrence_fwd_ws_size() bytes (may be NULL when that is
  *   0), 16-byte aligned, owned by the caller.

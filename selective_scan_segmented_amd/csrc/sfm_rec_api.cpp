@@ -17,7 +17,8 @@ bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t
 
 sfm_status check_sizes(const char* fn, int64_t rows, int64_t L, int64_t tokens, bool packed, int64_t D, int io_dtype) {
     if (io_dtype != SFM_F32 && io_dtype != SFM_BF16) return fail(SFM_ERR_DTYPE, "%s: io_dtype %d", fn, io_dtype);
-    if (!sane(rows, 1 << 24) || !sane(L, 1 << 24) || tokens < 0 || tokens > (1LL << 31) - 1 || !sane(D, 1 << 16))
+    constexpr int64_t most = (1LL << 31) - 1;  // (a bound of all the tokens is one, whatever the rows' lengths)
+    if (!sane(rows, 1 << 24) || !sane(L, most) || tokens < 0 || tokens > most || !sane(D, 1 << 16))
         return fail(SFM_ERR_SHAPE, "%s: rows=%lld L=%lld tokens=%lld D=%lld out of range", fn, (long long)rows,
                     (long long)L, (long long)tokens, (long long)D);
     if (!packed && tokens != rows * L)
