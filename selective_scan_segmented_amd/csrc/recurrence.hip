@@ -340,10 +340,12 @@ __global__ __launch_bounds__(threads_of(FORM), 4) void rec_bwd_kernel(const RecP
                     const float si = rec_sigmoid<kExact>(i[t].get(j)), xv = x[t].get(j);
                     const float la2 = rate[j] * sr[t][j], la = (rate[j] * kLn2) * sr[t][j];
                     const float a = exp2_fast(la2), em = rec_keep2<kExact>(la2, a);
-                    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(em, 0x1p-120f));  // (a = 1: la is 0 beside it)
+                    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(em, 0x1p-126f));  // (a = 1: la is 0 beside it)
                     const float G = g[t].get(j) + u[j], before = t == 0 && start ? h0[j] : y[t].get(j);
                     u[j] = a * G;
-                    const float P = u[j] * (la * __builtin_fmaf(-a, rs * (si * xv), before));
+                    // (u la before all else: 0 where a is, whatever la; and la / m before x, which a shut gate may find large)
+                    const float ula = u[j] * la;
+                    const float P = __builtin_fmaf(ula, before, -(ula * rs) * (a * (si * xv)));
                     dx[j] = G * (em * rs * si);
                     const float s = dx[j] * xv;
                     di[j] = __builtin_fmaf(-s, si, s);
