@@ -1,6 +1,7 @@
-"""Gradients of the gated recurrence beside gates that are shut and rates past any use: large inputs that a shut gate
-keeps out, states beside a decay of zero.  Each gradient is a sum of products; float32 may be off by its part of their
-magnitudes (1e-4: the tests' own for gradients), however small or large they are, and nothing turns into NaN."""
+"""The gated recurrence beside gates that are shut and rates past any use: states that are kept, gradients of large
+inputs that a shut gate keeps out, states beside a decay of zero.  Each gradient is a sum of products; float32 may be off
+by its part of their magnitudes (1e-4: the tests' own for gradients), however small or large they are, and nothing turns
+into NaN."""
 import numpy as np
 import pytest
 
@@ -72,3 +73,25 @@ def test_states_beside_decays_of_zero(rate, io):
     lam[::3] = np.float32(rate)
     x[:, ::3] *= 1024.0
     run(x, r, i, lam, s0, dy, dhT, io)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_shut_gates_keep_states_to_the_bit_within_a_chunk(io):
+    """Gates shut from token 4 to token 20; a lane walks tokens 0 to 15, another one 16 on."""
+    import torch
+    import selective_scan_segmented_amd as sfm
+    x, r, i, lam, s0, _, _ = ref.recurrence_inputs(13, L, 1, D, io)
+    r[4:21:2], r[5:21:2] = -np.inf, -200.0
+    t = [dev(v, io).view(1, L, D) for v in (x, r, i)] + [dev(lam, "f32")]
+    h0 = dev(s0, "f32")
+    y = sfm.sfm_gated_recurrence_fwd(*t, h0=h0)[0]
+    for tok in range(4, 16):
+        assert torch.equal(y[tok], y[3]), tok
+    for tok in range(17, 21):
+        assert torch.equal(y[tok], y[16]), tok
+    # Token 15 is 16 fused steps from h0.  Token 16 is A h0 + H: A of 16 products, H of 16 fused steps, each of these rounded
+    # by 2^-24 of a state (H: of twice the largest, since H = h - A h0), and the last step: (16 + 16 + 2 16 + 2) 2^-24 apart.
+    states = sfm.sfm_gated_recurrence_fwd(*[v[:, :16].float() for v in t[:3]], t[3], h0=h0)[0]
+    largest = torch.cat([h0, states]).abs().max(0).values
+    step = 66 * 2.0 ** -24 * largest + (2.0 ** -7 * y[3].float().abs() if io == "bf16" else 0)
+    assert ((y[15].float() - y[16].float()).abs() <= step).all()
