@@ -465,20 +465,33 @@ hipError_t launch_rows(const RecParams& p, hipStream_t s) {
 // Whether rows of several blocks are handed on or walked by a workgroup each.  Handing on costs a launch that clears the
 // words (5 us) and a wait a block; walking leaves the card to the rows and tiles there are, and packed rows to the
 // longest of them.  32 tiles, walked / handed on:
-//     forward, bfloat16, 16 rows of 600: 38 / 44 us, 12 rows: 32 / 32 us, 8 rows of 2400: 98 / 77 us, 16 rows: 139 / 149 us;
-//     three blocks (300 tokens), 2 rows: 14 / 15 us, 8 rows: 15.5 / 16 us, 4 rows: 15 / 13 us;
-//     float32, 16 rows of 600: 41 / 43 us, of 2400: 152 / 144 us, of 8000: 496 / 454 us, 24 rows of 2400: 215 / 211 us;
-//     backward, bfloat16, 16 rows of 600: 89 / 87 us, of 2400: 316 / 296 us, 24 rows of 600: 114 / 127 us, of 2400: 409 / 437
-//     us; float32, 16 rows of 600: 85 / 83 us, 24 rows: 112 / 121 us; five blocks (300 tokens), 16 rows: 49 / 53 us, 6 rows:
-//     31 / 24 us;
-//     packed in 16 tiles, bfloat16 (back): to 300, 128 rows: 44 / 47 us (99 / 111); to 600, 64 rows: 44 / 42 us (100 / 95), 128
-//     rows: 92 / 95 us (189 / 193); to 2000, 128 rows: 291 / 284 us (595 / 581), 256 rows: 539 / 549 us (1091 / 1126); of 500
-//     to 600, 64 rows: 61 / 72 us (141 / 158); float32, to 600, 128 rows: 86 / 89 us (183 / 181), 256 rows: 160 / 157 us (323 /
-//     321); to 2000, 256 rows: 533 / 496 us (1095 / 1051).
+//     forward, bfloat16, 12 rows of 600: 33 / 33 us, 16 rows: 37 / 43 us, 8 rows of 2400: 98 / 74 us, 16 rows: 131 / 141 us;
+//     three blocks (300 tokens), 2 rows: 13 / 16 us, 4 rows: 15 / 16 us, 8 rows: 17 / 17 us;
+//     float32, 16 rows of 600: 40 / 43 us, of 2400: 145 / 135 us, of 8000: 492 / 446 us, 24 rows of 2400: 213 / 206 us;
+//     backward, bfloat16, 16 rows of 600: 89 / 82 us, of 2400: 311 / 297 us, 20 rows of 600: 102 / 102 us, of 2400: 377 / 369
+//     us, 24 rows of 600: 111 / 122 us, of 2400: 415 / 443 us; five blocks (300 tokens), 8 rows: 38 / 27 us, 16 rows: 49 / 52
+//     us (the loss is taken); float32, 16 rows of 600: 81 / 77 us, 24 rows: 111 / 119 us, of 300, 12 rows: 43 / 40 us, 16
+//     rows: 47 / 47 us.
+// Packed, rows of 1 to the length stated, in 16 tiles where no other width is given; forward, and after the semicolon
+// backward.  Short ones, walked / handed on:
+//     to 300, bfloat16, 16 rows: 16 / 16 us; 36 / 25, 64 rows: 29 / 30; 55 / 57, 128 rows: 44 / 48; 87 / 95; float32, 32 rows:
+//     16 / 19; 40 / 34, 64 rows: 25 / 29; 53 / 54, 128 rows: 39 / 49; 76 / 87; bfloat16 x 511 (one channel to a lane), 64 rows:
+//     27 / 32; 51 / 60; to 400, 128 rows, bfloat16: 54 / 60; 112 / 120, float32: 52 / 60; 103 / 109; 500 rows x 64 bfloat16: 23 /
+//     34; 57 / 47; of 350 to 400, forward, 8 rows, bfloat16: 18 / 14, float32: 16 / 14 (of 250 to 300: 16 / 14 and 13 / 14), 32
+//     rows: 27 / 33 and 27 / 32; 48 rows x 333 bfloat16 (528 tiles): 36 / 32 (the loss is taken).
+// Even ones (500 to 600): bfloat16, 16 rows: 29 / 26; 63 / 49, 32 rows: 35 / 43; 85 / 84, 64 rows: 68 / 77; 141 / 151; float32,
+//     16 rows: 24 / 23; 57 / 47, 32 rows: 35 / 43; 78 / 78, 64 rows: 67 / 74; 139 / 143 (backward, the loss is taken), 200 x 320:
+//     105 / 115; 260 / 236.
+// Others: to 600, bfloat16, 64 rows: 45 / 46; 103 / 91, 128 rows: 75 / 79; 169 / 159, 256 rows: 138 / 149; 298 / 306; float32, 64
+//     rows: 45 / 45; 98 / 83, 128 rows: 72 / 75; 154 / 148, 256 rows: 136 / 142; 299 / 284, 384 rows: 201 / 204; 424 / 415; to 2000,
+//     bfloat16, 128 rows: 266 / 242; 564 / 495, 256 rows: 474 / 458; 975 / 946; float32, 256 rows: 469 / 423; 981 / 894; 1500 to
+//     2000, 64 rows, bfloat16: 224 / 220; 447 / 448, float32: 216 / 200; 439 / 426.
 static bool hands_on(int64_t rows, int64_t L, int64_t tokens, int tiles, int blocks, bool packed, bool narrow, bool back) {
     if (packed) {
         if (L * rows > 4 * tokens) return true;  // (one far longer than the others, or no bound)
+        if (L <= 400) return rows * tiles < (back ? 1024 : 256);
         const bool even = 3 * tokens > 2 * rows * L;
+        if (even && L <= 1024 && !back) return rows * tiles < 384;
         return rows * tiles < (narrow ? 6144 : even ? 1024 : L <= 1024 ? 2048 : 4096);
     }
     if (back) return rows * tiles < 640;

@@ -1,7 +1,7 @@
 """Rows that a workgroup walks block after block, forward and backward: every output against the definition in float64.
 
 A row is walked where rows and their tiles of 32 lanes fill the card: equal rows backward from 640 of them on (forward
-from 512), packed ones from 1024 to 6144 on.  Blocks are of up to 128 tokens forward and 64 backward."""
+from 512), packed ones from 256 to 6144 on, by their lengths.  Blocks are of up to 128 tokens forward and 64 backward."""
 import numpy as np
 import pytest
 
