@@ -472,11 +472,12 @@ sfm_status sfm_group_norm_bwd_ws_size(int64_t N, int64_t L, int64_t C, int64_t G
  *   h0       [rows, D] f32 or NULL (zero)
  *   y        [tokens, D] io, contiguous
  *   hT       [rows, D] f32 or NULL: the states after each row (a row without tokens:
- *            its h0); hT == h0 is allowed
+ *            its h0); hT == h0 is allowed, no other input in its place
  *   offsets  as for sfm_gated_delta_fwd: NULL for equal rows (tokens == rows * L), or
  *            int32 [rows + 1] on the device; L bounds the longest row, offsets outside
  *            the tokens are cut to them, tokens of no row and those past L keep their old y
- *   rows 1..2^24, L 1..2^31 - 1, tokens to 2^31 - 1, D 1..65536.  Tensors need their element's alignment only; bfloat16 ones of even D and
+ *   rows 1..2^24, L 1..2^31 - 1 (all the tokens where no bound is known), tokens to 2^31 - 1,
+ *   D 1..65536.  Tensors need their element's alignment only; bfloat16 ones of even D and
  *   strides on 4 bytes are loaded two channels at a time, others one by one.
  *   Rows, tokens and channels that make more workgroups than a launch holds (2^24, or 2^32 lanes;
  *   short rows of 128 channels are one each, long ones one for 128 tokens or more) are SFM_ERR_SHAPE.
@@ -523,7 +524,7 @@ sfm_status sfm_gated_recurrence_step(const void* x, const void* r, const void* i
  *   z = w x / sqrt(mean(x^2) + eps)   with SFM_QK_NORM (w: wq or wk, [d] f32 or NULL: 1), else z = x;
  *   the first rot values are rot / 2 pairs, (j, j + rot / 2) or with SFM_QK_NEIGHBOURS
  *   (2j, 2j + 1), and pair j becomes (z1 cos - z2 sin, z2 cos + z1 sin) of the angle
- *   position * freqs[j] (taken in 64 bits); values from rot on stay z.
+ *   position * freqs[j] (taken in 64 bits); values from rot on stay z, each by itself.
  *
  * sfm_qk_norm_rope_fwd:
  *   q [tokens, Hq, d], k [tokens, Hk, d] io   token strides ldq, ldk (heads' width to 2^29)

@@ -823,7 +823,8 @@ def sfm_gated_recurrence_fwd(x, r, i, lam, c=8.0, h0=None, offsets=None, max_len
 
     x, r, i: [B, L, D] float32 or bfloat16 (r and i before their sigmoids; slices of one projection are taken in
     place); lam: [D] float32; h0: [B, D] float32 states before the rows, or None.  offsets, max_len: packed rows as
-    for sfm_gated_delta_fwd, tensors [1, tokens, D].  Tokens of no row, and those past max_len in one, are not
+    for sfm_gated_delta_fwd, tensors [1, tokens, D] of up to 2^31 - 1 tokens; without max_len rows are taken as long ones,
+    which costs where they are many and short.  Tokens of no row, and those past max_len in one, are not
     written: a new output holds anything there.  Returns y [B, L, D], and with return_state the float32 states after
     the rows.  `state`, if given, takes those in either case (h0 itself is allowed)."""
     torch = _torch()

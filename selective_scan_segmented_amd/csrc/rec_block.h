@@ -20,10 +20,11 @@ __device__ __forceinline__ RecBuf rec_buf(const void* base, uint32_t token, uint
 }
 
 // Cache policy of a buffer access: nontemporal (its lines are the first to go).  The inputs are read that way: they are not
-// read again here, and their lines leave the outputs' room (without / with it: forward, 2 x 8192 x 2048 bfloat16: 67.7 / 66.9
-// us, float32: 119 / 107 us; backward, 16 x 4002 x 320 float32: 144 / 127 us, 32 x 600 x 2048 bfloat16: 150 / 133 us; with a
-// writer of the inputs before and a reader of the outputs behind, 2 x 8192 x 2048: 115 / 109 us, back 225 / 216 us; rows of
-// two to four tokens: 15.8 / 17.6 us).
+// read again here, and their lines leave the outputs' room.  Without / with it, alone: forward, 2 x 8192 x 2048 bfloat16: 69.6 /
+// 66.6 us, float32: 120 / 108 us, 512 x 100 x 640: 102 / 92 us; backward, 16 x 4002 x 320 float32: 144 / 142 us, 2 x 8192 x 2048
+// bfloat16: 138 / 133 us, 1024 x 32 x 640: 72 / 64 us; 8192 x 2 x 320 (too small to need the room): 25.7 / 26.9 us, back 43.8 /
+// 48.8 us.  With a writer of the inputs before and a reader of the outputs behind: 2 x 8192 x 2048 bfloat16: 115 / 109 us, back
+// 225 / 215 us, float32: 215 / 194 us; 8192 x 2 x 320: 36.8 / 37.5 us, back 67.8 / 65.6 us.
 constexpr int kStreamed = 2;
 
 // `lane` neighbouring channels of a token as they lie in memory: 4 bytes, or one bfloat16 where two are not aligned.
@@ -110,8 +111,10 @@ __device__ __forceinline__ uint32_t rec_factor(float a) { return a == a ? __floa
 // Every wait ends: tickets are drawn in the order of the walk, so the blocks waited for run already or are through, the
 // first waits for none, and every workgroup of packed rows says in the end that its word is whole, whatever a caller's
 // offsets make of its place.  The limit is far beyond any wait; past it the state is NaN.
-// Four words at a time: eight or sixteen find the whole one no sooner (the waits are for blocks whose tokens are still on
-// their way), as do longer sleeps and looking at the nearest word alone (68.3 to 68.9 us at 2 x 8192 x 2048 forward).
+// Words to a look, 1 / 4 / 8 / 16: where rows' waits are for tokens that are still on their way, 2 x 8192 x 2048 bfloat16
+// forward: 75 / 66 / 74 / 128 us (more ask for more at once, and take registers), 3 x 8192 x 1024: 69 / 60 / 67 / 113 us, back 119 /
+// 117 / 133 / 135 us; one long row, which is waited for hop by hop: 1 x 32768 x 320: 85 / 44 / 39 / 41 us, back 168 / 77 / 62 / 59 us,
+// 1 x 65536 x 64: 143 / 55 / 41 / 35 us, 1 x 70000 x 320 float32: 186 / 84 / 79 / 86 us.  Four everywhere.
 template <bool BACK, int WINDOW, int WORDS>
 __device__ __forceinline__ float rec_look_back(const uint64_t* word, int before) {
     const int n = before < WINDOW ? before : WINDOW;

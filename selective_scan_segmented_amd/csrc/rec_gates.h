@@ -2,9 +2,9 @@
 //
 //     la = -c softplus(lam) sigmoid(r),  a = exp(la),  m = sqrt(1 - a^2)
 //
-// The decay is kept as its base-2 logarithm, so that a is one exponential.  1 - a^2 = -expm1(2 la) cancels where a is
-// near 1, which is where the recurrence remembers and where training starts (a from 0.9 to 0.999): there it is the
-// series of expm1, elsewhere 1 - a a.
+// The decay is kept as its base-2 logarithm, so that a is one exponential.  The difference 1 - a^2 cancels where a is
+// near 1, which is where the recurrence remembers and where training starts (a from 0.9 to 0.999): there it is a series
+// of sinh (rec_keep2), elsewhere 1 - a a.
 #pragma once
 
 #include "sfm_device.h"

@@ -16,10 +16,10 @@
 // registers as it lies in memory.
 //
 // Measured (calls back to back; rate of the bytes that have to move, of 5.1 TB/s that a large copy reaches):
-//     forward, bfloat16: 256 x 51 x 640: 15 us, 4.4 TB/s (a copy as large 17); 2 x 8192 x 2048: 67 us, 4.0 TB/s, of
+//     forward, bfloat16: 256 x 51 x 640: 14.5 us, 4.6 TB/s (a copy as large 17); 2 x 8192 x 2048: 67 us, 4.0 TB/s, of
 //     which 5 are the words' clearing and 8 the waits for states before; 24 rows packed to 2048 x 1024: 60 us, 3.5 TB/s;
-//     backward: bfloat16, 256 x 198 x 320: 60 us, 4.3 TB/s; float32, 16 x 4002 x 320: 127 us, 5.2 TB/s (143 us, 4.6 TB/s
-//     where nothing of its outputs is left on the card);
+//     backward: bfloat16, 256 x 198 x 320: 60 us, 4.3 TB/s, 2 x 8192 x 2048: 133 us, 4.0 TB/s; float32, 16 x 4002 x 320: 142
+//     us, 4.6 TB/s (128 us, 5.1 TB/s, where its outputs take the place of the last call's and part of them is still on the card);
 //     step: 256 requests x 2048: 3.7 us on the card.
 #include "rec_block.h"
 
@@ -88,11 +88,11 @@ __device__ __forceinline__ void load_chunk(RecPack<T, C> (&v)[TT], const void* f
 }
 
 // A wave's priority among those of its unit: waves that ask for tokens go first and those that make gates last, where that
-// was seen to help.  Without / with it: forward in bfloat16, 40 x 600 x 1024: 54.4 / 51.6 us, 32 x 4002 x 1024:
-// 239 / 230 us, packed to 2048: 62.5 / 61.6 us; backward walked, bfloat16, 256 x 198 x 320: 62.3 / 60.0 us, float32, 32 x 4002
-// x 1024: 943 / 931 us.  Not elsewhere: forward in float32, 2 x 8192 x 2048: 120 / 124 us, 64 x 198 x 640: 26.8 / 28.1 us;
-// backward handed on, 16 x 4002 x 320 float32: 146.7 / 147.6 us, 32 x 4002 x 1024 bfloat16: 495 / 498 us; nor in rows of one
-// block, 256 x 51 x 640 forward: 16.8 / 17.0 us.
+// was seen to help.  Without / with it: forward in bfloat16, 40 x 600 x 1024: 54.2 / 51.1 us, 32 x 4002 x 1024: 247 / 229 us,
+// packed to 2048: 60.6 / 60.0 us; backward walked, bfloat16, 256 x 198 x 320: 61.9 / 60.1 us, float32, 32 x 4002 x 1024: 962 /
+// 952 us.  Not elsewhere: forward in float32, 2 x 8192 x 2048: 108.1 / 111.9 us, 64 x 198 x 640: 25.7 / 27.3 us; backward handed
+// on, 16 x 4002 x 320 float32: 141.8 / 142.1 us, 2 x 8192 x 2048 bfloat16: 134.2 / 134.4 us; nor in rows of one block, 256 x 51
+// x 640 forward: 14.3 / 14.3 us.
 template <bool ON, int LEVEL> __device__ __forceinline__ void priority() {
     if constexpr (ON) __builtin_amdgcn_s_setprio(LEVEL);
 }
@@ -166,12 +166,12 @@ __global__ __launch_bounds__(threads_of(FORM), C == 2 ? (FORM == kFewThreads ? 5
     constexpr int TT = kRecChunk<false>;
     constexpr bool kUrgent = C == 2 && FORM != kOne;
     // Gates of so many tokens at a time: those behind the row's end are left out, and fewer values are held at once.  All 16 /
-    // 4 / 2: one block, 256 x 51 x 640 bfloat16: 17.0 / 15.5 / 15.5 us, 64 x 198 x 640 float32: 26.7 / 24.5 / 24.5 us; handed on,
-    // 2 x 8192 x 2048: 69.0 / 68.1 / 67.3 us; walked, bfloat16, 256 x 300 x 512: 75.7 / 72.0 / 75.9 us; float32: 141 / 150 / 158 us.
+    // 4 / 2: one block, 256 x 51 x 640 bfloat16: 15.4 / 14.7 / 14.0 us, 64 x 198 x 640 float32: 25.8 / 25.6 / 25.6 us; handed on,
+    // 2 x 8192 x 2048: 67.5 / 66.7 / 66.3 us; walked, 256 x 300 x 512, bfloat16: 71.0 / 66.7 / 74.5 us; float32: 134 / 143 / 148 us.
     constexpr int kGates = HAND ? 2 : FORM == kWalk && C == 1 ? TT : 4;
-    // Outputs that stay in the cache for their reader / do not: 256 x 51 x 640 bfloat16: 15.7 / 14.1 us, between a writer of x
-    // and a reader of y 28.0 / 28.3 us; handed on, 2 x 8192 x 2048: 66.4 / 64.7 us, so placed 109 / 112 us; float32, 256 x 200 x
-    // 1024: 159 / 165 us.
+    // Outputs that stay in the cache for their reader / do not, alone, and between a writer of x and a reader of y: 256 x 51 x 640
+    // bfloat16: 16.2 / 14.7 us, 28.0 / 28.0 us; not where rows are handed on, 2 x 8192 x 2048: 66.8 / 64.9 us, 108.6 / 112.1 us,
+    // walked, 32 x 600 x 2048: 126.2 / 132.3 us so placed, nor in float32, 256 x 200 x 1024: 172 / 165 us, 305 / 308 us.
     constexpr int kPolicy = FORM == kOne && C == 2 ? kStreamed : 0;
     __shared__ float2 agg_[FORM == kWalk ? 2 : 1][threads_of(FORM) * C];
     __shared__ uint32_t shared[2];
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(threads_of(FORM), 4) void rec_bwd_kernel(const RecP
     constexpr bool kExact = sizeof(T) == 4;
     constexpr int TT = kRecChunk<true>;
     constexpr bool kUrgent = FORM == kWalk;
-    constexpr int kGates = FORM == kOne ? 4 : TT;  // (8 / 4: 8192 x 2 x 320 bfloat16: 47 / 44 us, 256 x 51 x 640: 33.8 / 33.6 us)
+    constexpr int kGates = FORM == kOne ? 4 : TT;  // (8 / 4: 8192 x 2 x 320 bfloat16: 51.6 / 48.8 us, 256 x 51 x 640: 34.4 / 34.2 us)
     __shared__ float2 agg_[FORM == kWalk ? 2 : 1][threads_of(FORM) * C];
     __shared__ float part[threads_of(FORM) * C];
     __shared__ uint32_t shared[2];
@@ -522,11 +522,11 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     bool several = cut(kFewThreads);
     if (several && hands_on(rows, L, tokens, chains, q.blocks, packed, lane == 1, back)) {
         // Workgroups that hand on: wide ones make fewer blocks to wait for, small ones more waits at once.  256 / 512 threads:
-        //     backward, float32: 1 x 70000 x 320: 267 / 176 us, 16 x 4002 x 320: 148 / 146 us, 2 x 8192 x 2048: 247 / 249 us;
-        //     backward, bfloat16: 1 x 20000 x 1024: 108 / 96 us, 2 x 8192 x 2048: 140 / 138 us, 24 packed to 2048 x 1024: 125 / 121 us;
-        //     forward, float32: 1 x 70000 x 320: 138 / 90 us, 2 x 8192 x 2048: 121 / 119 us;
-        //     forward, bfloat16: 1 x 32768 x 320 (5 rows' tiles): 67 / 42 us, 1 x 8192 x 1024 (16): 28 / 23 us, x 2048 (32):
-        //     41 / 40 us, 3 x 8192 x 1024 (48): 62 / 64 us, 2 x 8192 x 2048 (64): 69 / 70 us, packed to 2048: 63 / 66 us.
+        //     backward, float32: 1 x 70000 x 320: 260 / 168 us, 16 x 4002 x 320: 145 / 145 us, 2 x 8192 x 2048: 246 / 247 us;
+        //     backward, bfloat16: 1 x 20000 x 1024: 104 / 89 us, 2 x 8192 x 2048: 135 / 134 us, 24 packed to 2048 x 1024: 120 / 116 us;
+        //     forward, float32: 1 x 70000 x 320: 134 / 84 us, 2 x 8192 x 2048: 110 / 108 us;
+        //     forward, bfloat16: 1 x 32768 x 320 (5 rows' tiles): 68 / 44 us, 1 x 8192 x 1024 (16): 27 / 24 us, x 2048 (32):
+        //     39 / 39 us, 3 x 8192 x 1024 (48): 60 / 66 us, 2 x 8192 x 2048 (64): 67 / 72 us, packed to 2048: 60 / 63 us.
         const int threads = lane == 1 || back || rows * chains <= 32 ? kThreads : kFewThreads;
         several = cut(threads);
         q.hand = several ? threads : 0;
@@ -534,8 +534,9 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     q.groups = 1;
     // No bound of the rows, or one that few come near, and rows of few tokens on average: handed on as long ones, but by
     // workgroups of 32 or 64 tokens and so many more channels.  Without / with it, no bound: forward (back), bfloat16, 4096 rows
-    // to 16 x 2048: 763 / 275 us (1762 / 588), to 100 x 1024: 591 / 466 us (1328 / 1002; with 32 tokens 436 and 903); one row of
-    // 50000 among 2048 to 16 x 320, float32: 222 / 218 us (378 / 319; with 32 tokens 339 and 410).
+    // to 16 x 2048: 746 / 264 us (1741 / 561), to 100 x 1024: 572 / 433 us (1261 / 935; with 32 tokens 395 and 836); one row of
+    // 50000 among 2048 to 16 x 320, float32: 220 / 214 us (371 / 310; with 32 tokens 348 and 417).  With the bound the first two
+    // take 112 and 308 us (234 and 824).
     const bool loose = q.hand && packed && lanes > least && L * rows > 4 * tokens && tokens < 100 * rows;
     if (loose) {
         int64_t nt = (tokens < 24 * rows ? 32 : 64) / chunk;
@@ -544,8 +545,8 @@ RecPlan plan_rec(int64_t rows, int64_t L, int64_t tokens, int64_t D, bool packed
     }
     // Many packed rows of one block, most far shorter than the longest: lanes for the average's chunks (forward), or for no
     // more than a small workgroup's (backward), walk the longer ones.  One block / this: forward, bfloat16, 4096 rows to 100 x
-    // 1024: 404 / 346 us, 512 to 250 x 2048: 259 / 237 us; float32, 2048 to 200 x 320: 194 / 198 us (left out); backward,
-    // bfloat16, 4096 to 100 x 1024: 955 / 890 us, float32, 2048 to 100 x 320: 266 / 246 us; rows of 90 to 100 x 320: 406 / 448 us.
+    // 1024: 382 / 309 us, 512 to 250 x 2048: 241 / 217 us; float32, 2048 to 200 x 320: 179 / 189 us (left out); backward,
+    // bfloat16, 4096 to 100 x 1024: 897 / 824 us, float32, 2048 to 100 x 320: 258 / 228 us; rows of 90 to 100 x 320: 395 / 433 us.
     if (packed && !several && rows * chains >= 4096 && 3 * tokens <= 2 * rows * L && (back || lane == 2)) {
         int64_t nt = back ? chunks : (tokens / rows + chunk - 1) / chunk;
         if (nt < lane) nt = lane;  // (a lane of the join to a channel)

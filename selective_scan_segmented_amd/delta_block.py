@@ -11,7 +11,9 @@ channel-last tokens X [B, L, C]:
     y       = silu(group norm(o))             sfm_group_norm_fwd, every token by itself, a group a head
     out     = y W_out
 
-The projections and the gates' elementwise functions are PyTorch; weights are random (seeded).
+The delta rule takes unit queries and keys, so that only their direction counts: of the
+rotated norms the weights and the rotation, not the norm's own scale.  The projections
+and the gates' elementwise functions are PyTorch; weights are random (seeded).
 
     python -m selective_scan_segmented_amd.delta_block     # times one block on the GPU
 """
